@@ -132,7 +132,7 @@ def _prep_tables(c, seed):
     free[:F - total] = pages[total:]
     i32 = torch.int32
     return dict(c=c, rows=rows.to(i32).to(DEV), new=new.to(i32).to(DEV), lens=lens.to(i32).to(DEV), table=table.to(DEV),
-                free=free.to(DEV), nfree=torch.tensor([F - total], dtype=i32, device=DEV))
+                free=free.to(DEV), nfree=torch.tensor([F - total], dtype=i32, device=DEV), kept=None)
 
 
 def _prep_rope(c, seed):
@@ -206,9 +206,14 @@ def run(s):
 def _own_tables(s):
     import attention_attn_varlen_gb300 as av
     c = s["c"]
-    t = av.step_tables(s["rows"], s["new"], s["lens"], s["table"], s["free"], s["nfree"], c["bs"], c["T"])
+    if s["kept"] is None:   # buffers that the program keeps from step to step
+        ws = torch.empty(av.lib().attn_step_tables_workspace_size(c["B"]), dtype=torch.uint8, device=DEV)
+        s["kept"] = av.StepTables.empty(c["B"], c["M"], c["T"], DEV), ws
+    t, ws = s["kept"]
+    av.step_tables(s["rows"], s["new"], s["lens"], s["table"], s["free"], s["nfree"], c["bs"], c["T"], out=t,
+                   workspace=ws)
     # the step's tokens are taken back: the pool is as before
-    av.trim_pages(s["rows"], t.context_lens, s["lens"], s["table"], s["free"], s["nfree"], c["bs"])
+    av.trim_pages(s["rows"], t.context_lens, s["lens"], s["table"], s["free"], s["nfree"], c["bs"], workspace=ws)
     return dict(block_table=t.block_table, slot_mapping=t.slot_mapping, positions=t.positions, cu_q=t.cu_seqlens_q,
                 cu_k=t.cu_seqlens_k, cache_seqlens=t.cache_seqlens, context_lens=t.context_lens, lens=s["lens"],
                 table=s["table"], free=s["free"], nfree=s["nfree"])
