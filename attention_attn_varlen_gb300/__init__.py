@@ -15,6 +15,11 @@ Entry points (the C ABI's names):
     attn_padded_fwd         a padded [B, S, H, D] batch with per-sequence lengths
     store_kvcache           slot_mapping scatter into the caches (optionally also V/16 in fp16)
     softmax_rows            row softmax (attn_softmax_rows)
+    step_tables             a step's block table, slot mapping, positions and offsets from request lengths
+    trim_pages              cut requests to fewer tokens, giving their pages back
+    rope_store_kvcache      rotary positions (several axes) on q and k, fused with the paged store
+    linear_attn_varlen_fwd  linear attention with a decay per head over packed prompts, fp32 state cache
+    linear_attn_decode      the same for one token per sequence
     get_last_device_error   the device error word (index, range and timeout checks)
     selftest_bounded_wait   the failure-detection self-test
 and the layer-shaped dispatcher in :mod:`attention_attn_varlen_gb300.attention`.
@@ -25,6 +30,7 @@ import ctypes
 import math
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -32,13 +38,15 @@ from ._build import LIB as _LIB_PATH
 from ._build import build
 
 __all__ = ["attn_varlen_fwd", "attn_varlen_fwd_host", "host_staging", "attn_decode_paged", "attn_with_kvcache",
-           "attn_padded_fwd", "softmax_rows", "store_kvcache", "get_last_device_error", "selftest_bounded_wait",
+           "attn_padded_fwd", "softmax_rows", "store_kvcache", "step_tables", "trim_pages", "StepTables",
+           "rope_store_kvcache", "linear_attn_varlen_fwd", "linear_attn_decode", "linear_attn_workspace_size", "get_last_device_error", "selftest_bounded_wait",
            "lib", "build", "AttnError", "exported_symbols", "set_kernel_events", "decode_num_splits",
            "decode_workspace_size"]
 
 ATTN_OK = 0
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "launch failed",
-           5: "device timeout", 6: "device index out of range", 7: "no device", 8: "input value out of range"}
+           5: "device timeout", 6: "device index out of range", 7: "no device", 8: "input value out of range",
+           9: "page pool or table row full"}
 
 
 class AttnError(RuntimeError):
@@ -103,6 +111,21 @@ def lib():
     L.attn_varlen_fwd_host.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32,
                                        _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp, _vp, _vp, _vp, _vp]
     L.attn_varlen_fwd_host.restype = _i32
+    L.attn_step_tables.argtypes = [_vp] * 6 + [_i32, _i32, _i32, _i32, _i64, _i64] + [_vp] * 8 + [_sz, _vp]
+    L.attn_step_tables.restype = _i32
+    L.attn_trim_pages.argtypes = [_vp] * 6 + [_i32, _i32, _i32, _i32, _i64, _vp, _sz, _vp]
+    L.attn_trim_pages.restype = _i32
+    L.attn_step_tables_workspace_size.argtypes = [_i32]
+    L.attn_step_tables_workspace_size.restype = _sz
+    L.attn_rope_store_kvcache.argtypes = [_vp] * 6 + [_i32, _i64, _i32, _i32, _f32] + [_vp] * 6 + [_i64, _i32, _i32,
+                                                                                                _i32] + [_i64] * 6 + [_vp]
+    L.attn_rope_store_kvcache.restype = _i32
+    L.attn_linear_varlen_fwd.argtypes = [_vp] * 9 + [_i32, _i64, _i32, _i32, _i32, _i32, _f32] + [_i64] * 5 + [_vp, _sz, _vp]
+    L.attn_linear_varlen_fwd.restype = _i32
+    L.attn_linear_workspace_size.argtypes = [_i32] * 5
+    L.attn_linear_workspace_size.restype = _sz
+    L.attn_linear_decode.argtypes = [_vp] * 8 + [_i32, _i32, _i32, _i32, _f32] + [_i64] * 5 + [_vp]
+    L.attn_linear_decode.restype = _i32
     _lib = L
     return L
 
@@ -155,6 +178,23 @@ def _bf16_cuda(*named):
 def _int_cuda(name, t, dtype):
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+
+
+def _cuda(dtype, dev, *named):
+    """Each tensor (None allowed) is contiguous, of this dtype and on CUDA device number dev."""
+    for name, t in named:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The tensor's CUDA device, which has to be the current one (the library launches there)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
 
 
 # --------------------------------------------------------------------------
@@ -475,6 +515,238 @@ def store_kvcache(k, v, k_cache, v_cache, slot_mapping, stream=None, v16_cache=N
     st = lib().store_kvcache(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(v16_cache), _ptr(slot_mapping), N,
                              Hkv, D, ks, vs, num_slots, _stream(stream))
     _check(st, "store_kvcache")
+
+
+class StepTables(NamedTuple):
+    """The index tables of one step (see attn_step_tables), all on the device."""
+    block_table: torch.Tensor      # int32 [B, max_blocks]
+    slot_mapping: torch.Tensor     # int64 [max_tokens]
+    positions: torch.Tensor        # int32 [max_tokens]
+    cu_seqlens_q: torch.Tensor     # int32 [B + 1]
+    cu_seqlens_k: torch.Tensor     # int32 [B + 1]
+    cache_seqlens: torch.Tensor    # int32 [B]: cached tokens after the step
+    context_lens: torch.Tensor     # int32 [B]: cached tokens before it
+
+    @classmethod
+    def empty(cls, batch: int, max_blocks: int, max_tokens: int, device=None) -> "StepTables":
+        """Buffers for steps of this size, to keep and pass as `out`."""
+        new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=device or "cuda")  # noqa: E731
+        i32 = torch.int32
+        return cls(new(i32, batch, max_blocks), new(torch.int64, max_tokens), new(i32, max_tokens),
+                   new(i32, batch + 1), new(i32, batch + 1), new(i32, batch), new(i32, batch))
+
+
+def _pool_args(request_rows, lens, seq_lens, page_table, free_pages, num_free, workspace, lens_name):
+    dev = _device(seq_lens, "seq_lens")
+    _cuda(torch.int32, dev, ("request_rows", request_rows), (lens_name, lens), ("seq_lens", seq_lens),
+          ("page_table", page_table), ("free_pages", free_pages), ("num_free", num_free))
+    if page_table.dim() != 2 or seq_lens.dim() != 1 or page_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("page_table must be [num_rows, max_blocks] and seq_lens [num_rows]")
+    if num_free.numel() != 1:
+        raise ValueError("num_free must hold one number")
+    B = lens.numel()
+    if request_rows is not None and request_rows.numel() != B:
+        raise ValueError(f"request_rows and {lens_name} must have the same length")
+    if workspace is None:
+        workspace = torch.empty(lib().attn_step_tables_workspace_size(B), dtype=torch.uint8, device=seq_lens.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return dev, B, workspace
+
+
+def step_tables(request_rows, new_lens, seq_lens, page_table, free_pages, num_free, block_size: int,
+                max_tokens: int, out: StepTables | None = None, workspace=None, stream=None) -> StepTables:
+    """Grow the requests of a step by their new tokens, taking pages off the
+    free list, and build the step's tables on the GPU (no host sync).
+
+    Pool, updated in place: seq_lens int32 [R], page_table int32 [R, M],
+    free_pages int32 [num_pages] (the first num_free entries), num_free int32
+    [1].  Step: request_rows int32 [B] (None: entry b is row b), new_lens int32
+    [B]; max_tokens sizes slot_mapping and positions (entries behind the last
+    token are -1 and 0).  Entries that cannot be served keep their length, get
+    slots of -1 and are reported by get_last_device_error (9: out of pages)."""
+    dev, B, workspace = _pool_args(request_rows, new_lens, seq_lens, page_table, free_pages, num_free, workspace,
+                                   "new_lens")
+    R, M = page_table.shape
+    if out is None:
+        out = StepTables.empty(B, M, int(max_tokens), seq_lens.device)
+    else:
+        _cuda(torch.int32, dev, ("block_table", out.block_table), ("positions", out.positions),
+              ("cu_seqlens_q", out.cu_seqlens_q), ("cu_seqlens_k", out.cu_seqlens_k),
+              ("cache_seqlens", out.cache_seqlens), ("context_lens", out.context_lens))
+        _cuda(torch.int64, dev, ("slot_mapping", out.slot_mapping))
+        if out.block_table.shape != (B, M) or out.slot_mapping.numel() != max_tokens \
+                or out.positions.numel() != max_tokens or out.cu_seqlens_q.numel() != B + 1 \
+                or out.cu_seqlens_k.numel() != B + 1 or out.cache_seqlens.numel() != B or out.context_lens.numel() != B:
+            raise ValueError("out was made for other sizes")
+    st = lib().attn_step_tables(_ptr(request_rows), _ptr(new_lens), _ptr(seq_lens), _ptr(page_table),
+                                _ptr(free_pages), _ptr(num_free), B, R, M, int(block_size), free_pages.numel(),
+                                int(max_tokens), _ptr(out.block_table), _ptr(out.slot_mapping), _ptr(out.positions),
+                                _ptr(out.cu_seqlens_q), _ptr(out.cu_seqlens_k), _ptr(out.cache_seqlens),
+                                _ptr(out.context_lens), _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "attn_step_tables")
+    return out
+
+
+def trim_pages(request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, block_size: int, workspace=None,
+               stream=None) -> None:
+    """Cut requests to their first keep_lens tokens (int32 [B]; 0 ends a
+    request) and give the pages behind them back to the free list."""
+    _, B, workspace = _pool_args(request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, workspace,
+                                 "keep_lens")
+    R, M = page_table.shape
+    st = lib().attn_trim_pages(_ptr(request_rows), _ptr(keep_lens), _ptr(seq_lens), _ptr(page_table),
+                               _ptr(free_pages), _ptr(num_free), B, R, M, int(block_size), free_pages.numel(),
+                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "attn_trim_pages")
+
+
+def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None, slot_mapping=None, pair_axis=None,
+                       interleaved: bool = False, scale: float = 1.0, q_out=None, k_out=None, return_k: bool = False,
+                       v16_cache=None, stream=None):
+    """Rotary positions on q [N, Hq, D] and k [N, Hkv, D], and the scatter of the
+    rotated k and of v into the caches (as store_kvcache), in one pass.
+
+    positions int32 [N], or [A, N] with pair_axis (a sequence of A-axis numbers,
+    one per pair); inv_freq float32 [rot_dim / 2].  Pair i is elements (i, i +
+    rot_dim / 2), or (2 i, 2 i + 1) if interleaved; elements past rot_dim pass
+    through.  Without caches only q and k are rotated (v may be None).  q_out and
+    k_out may be q and k.  Returns the rotated q, or (q, k) with return_k."""
+    dev = _device(q, "q")
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out)):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev):
+            raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
+    N, Hq, D = q.shape
+    Hkv = k.shape[1]
+    stored = k_cache is not None or v_cache is not None or slot_mapping is not None or v16_cache is not None
+    num_slots = 0
+    if stored:
+        if k_cache is None or v_cache is None or slot_mapping is None or v is None:
+            raise ValueError("storing needs v, k_cache, v_cache and slot_mapping")
+        _cuda(torch.bfloat16, dev, ("k_cache", k_cache), ("v_cache", v_cache))
+        _cuda(torch.float16, dev, ("v16_cache", v16_cache))
+        _cuda(torch.int64, dev, ("slot_mapping", slot_mapping))
+        if k_cache.shape != v_cache.shape or k_cache.shape[-2:] != (Hkv, D) \
+                or (v16_cache is not None and v16_cache.shape != v_cache.shape):
+            raise ValueError("the caches must have one shape [..., Hkv, D], k's heads and head_dim")
+        if slot_mapping.numel() != N:
+            raise ValueError("slot_mapping must have one entry per token")
+        num_slots = k_cache.numel() // (Hkv * D)
+    elif k_out is None:
+        return_k = True
+    qs, ks = _rows(q, "q", Hq, D), _rows(k, "k", Hkv, D)
+    vs = _rows(v, "v", Hkv, D) if v is not None else 0
+    if k.shape[0] != N or (v is not None and v.shape[0] != N):
+        raise ValueError("q, k and v must have the same number of tokens")
+    if q_out is None:
+        q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+    if k_out is None and return_k:
+        k_out = torch.empty((N, Hkv, D), dtype=q.dtype, device=q.device)
+    qos = _rows(q_out, "q_out", Hq, D)
+    kos = _rows(k_out, "k_out", Hkv, D) if k_out is not None else 0
+    if q_out.shape[0] != N or (k_out is not None and k_out.shape[0] != N):
+        raise ValueError("q_out and k_out must have one row per token")
+    _cuda(torch.float32, dev, ("inv_freq", inv_freq))
+    if positions.dtype is not torch.int32 or positions.get_device() != dev or positions.dim() not in (1, 2) \
+            or positions.shape[-1] != N or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be int32 [{N}] or [axes, {N}] on cuda:{dev}, contiguous along the tokens")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != inv_freq.numel():
+            raise ValueError("pair_axis must have one entry per pair (inv_freq)")
+    elif axes > 1:
+        raise ValueError("positions with several axes need pair_axis")
+    st = lib().attn_rope_store_kvcache(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), pair_axis, axes,
+        positions.stride(0) if axes > 1 else N, 2 * inv_freq.numel(), 1 if interleaved else 0, float(scale),
+        _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(v16_cache), _ptr(slot_mapping), N, Hq, Hkv, D,
+        qs, ks, vs, qos, kos, num_slots, _stream(stream))
+    _check(st, "attn_rope_store_kvcache")
+    return (q_out, k_out) if return_k else q_out
+
+
+def _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out, B):
+    dev = _device(q, "q")
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev):
+            raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must have the same number of tokens")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape[0] != T:
+        raise ValueError("out must have one row per token")
+    _cuda(torch.float32, dev, ("log_decay", log_decay), ("state_cache", state_cache))
+    _cuda(torch.int32, dev, ("state_slots", state_slots), ("context_lens", context_lens))
+    if log_decay.numel() != Hkv:
+        raise ValueError("log_decay must have one entry per key/value head")
+    if (state_cache is None) != (state_slots is None):
+        raise ValueError("state_cache and state_slots go together")
+    slots = 0
+    if state_cache is not None:
+        if state_cache.dim() != 4 or state_cache.shape[1:] != (Hkv, D, D):
+            raise ValueError(f"state_cache must be [num_slots, {Hkv}, {D}, {D}]")
+        slots = state_cache.shape[0]
+        if state_slots.numel() != B:
+            raise ValueError("state_slots must have one entry per sequence")
+    if context_lens is not None and context_lens.numel() != B:
+        raise ValueError("context_lens must have one entry per sequence")
+    return out, T, Hq, Hkv, D, slots, (_rows(q, "q", Hq, D), _rows(k, "k", Hkv, D), _rows(v, "v", Hkv, D),
+                                       _rows(out, "out", Hq, D))
+
+
+def linear_attn_workspace_size(batch: int, num_heads_q: int, num_heads_kv: int, head_dim: int, max_seqlen: int) -> int:
+    return lib().attn_linear_workspace_size(batch, num_heads_q, num_heads_kv, head_dim, max_seqlen)
+
+
+def linear_attn_varlen_fwd(q, k, v, log_decay, cu_seqlens, max_seqlen: int, scale: float | None = None,
+                           state_cache=None, state_slots=None, context_lens=None, out=None, workspace=None,
+                           stream=None):
+    """Linear attention with a decay per head over packed sequences:
+    S_t = exp(log_decay) S_{t-1} + v_t k_t^T, o_t = scale * S_t q_t.
+
+    q [T, Hq, D], k/v [T, Hkv, D] bf16 (D 64 or 128), log_decay float32 [Hkv] <=
+    0, cu_seqlens int32 [B + 1].  state_cache float32 [num_slots, Hkv, Dv, Dk]
+    with state_slots int32 [B] receives the final states; a sequence with
+    context_lens[b] > 0 (int32 [B]) starts from its slot, any other from zero.
+    scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
+    B = cu_seqlens.numel() - 1
+    out, T, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out,
+                                                      B)
+    _cuda(torch.int32, q.get_device(), ("cu_seqlens", cu_seqlens))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    L = lib()
+    ws_bytes = L.attn_linear_workspace_size(B, Hq, Hkv, D, int(max_seqlen))
+    if workspace is None and ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    ws_have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = L.attn_linear_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(log_decay), _ptr(cu_seqlens),
+                                  _ptr(state_cache), _ptr(state_slots), _ptr(context_lens), B, T, int(max_seqlen), Hq,
+                                  Hkv, D, float(scale), slots, *strides, _ptr(workspace), ws_have, _stream(stream))
+    _check(st, "attn_linear_varlen_fwd")
+    return out
+
+
+def linear_attn_decode(q, k, v, log_decay, state_cache, state_slots, scale: float | None = None, context_lens=None,
+                       out=None, stream=None):
+    """linear_attn_varlen_fwd for one token per sequence: q [B, Hq, D], k/v [B,
+    Hkv, D]; the states in state_cache are updated in place.  A slot < 0 stands
+    for a zero state that is not kept; context_lens[b] = 0 starts from zero
+    (None: every slot continues).  Returns out [B, Hq, D]."""
+    out, B, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out,
+                                                      q.shape[0])
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    st = lib().attn_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(log_decay), _ptr(state_cache),
+                                  _ptr(state_slots), _ptr(context_lens), B, Hq, Hkv, D, float(scale), slots, *strides,
+                                  _stream(stream))
+    _check(st, "attn_linear_decode")
+    return out
 
 
 def set_kernel_events(before=None, after=None) -> None:

@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_varlen.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
-SOURCES = ["api.cu", "store_kvcache.cu", "decode.cu", "prefill.cu", "softmax.cu"]
+SOURCES = ["api.cu", "store_kvcache.cu", "decode.cu", "prefill.cu", "softmax.cu", "step_tables.cu",
+           "rope_store.cu", "linear_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

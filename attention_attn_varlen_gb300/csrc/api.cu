@@ -367,6 +367,7 @@ const char *attn_status_string(attn_status s) {
         case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out";
         case ATTN_ERR_DEVICE_INDEX: return "a device-side index was out of range";
         case ATTN_ERR_NO_DEVICE: return "no usable CUDA device";
+        case ATTN_ERR_DEVICE_CAPACITY: return "the page pool or a request's table row is full";
         case ATTN_ERR_DEVICE_RANGE: return "an input value was outside the range a kernel handles";
     }
     return "unknown status";
@@ -397,6 +398,7 @@ attn_status attn_get_last_device_error(void *stream, uint32_t *detail) {
     if (word & ERR_INDEX) return ATTN_ERR_DEVICE_INDEX;
     if (word & ERR_TIMEOUT) return ATTN_ERR_DEVICE_TIMEOUT;
     if (word & ERR_RANGE) return ATTN_ERR_DEVICE_RANGE;
+    if (word & ERR_CAPACITY) return ATTN_ERR_DEVICE_CAPACITY;
     return ATTN_OK;
 }
 
@@ -954,6 +956,276 @@ attn_status store_kvcache(const void *k, const void *v, void *k_cache, void *v_c
         return ATTN_ERR_LAUNCH_FAILED;
     }
     return ATTN_OK;
+}
+
+// ---------------------------------------------------------------------------
+// step tables
+// ---------------------------------------------------------------------------
+
+size_t attn_step_tables_workspace_size(int batch) {
+    if (batch <= 0 || batch > kTablesMaxBatch) return 0;
+    return (size_t)batch * (sizeof(int4) + sizeof(int32_t));
+}
+
+}  // extern "C"
+
+static attn_status tables_params(TablesParams *p, const int32_t *request_rows, const int32_t *lens, int32_t *seq_lens,
+                                 int32_t *page_table, int32_t *free_pages, int32_t *num_free, int batch,
+                                 int num_rows, int max_blocks, int block_size, int64_t num_pages, void *workspace,
+                                 size_t workspace_bytes) {
+    if (!lens || !seq_lens || !page_table || !free_pages || !num_free) return ATTN_ERR_INVALID_ARG;
+    if (batch <= 0 || num_rows <= 0 || max_blocks <= 0 || num_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    if (!request_rows && batch > num_rows) return ATTN_ERR_INVALID_ARG;
+    if (!pow2(block_size) || block_size < 16) return ATTN_ERR_INVALID_ARG;
+    if (batch > kTablesMaxBatch) return ATTN_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks * block_size >= (int64_t)INT32_MAX || num_pages * block_size >= (int64_t)INT32_MAX)
+        return ATTN_ERR_UNSUPPORTED;
+    if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < attn_step_tables_workspace_size(batch)) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    memset(p, 0, sizeof *p);
+    p->rows = request_rows;
+    p->lens = lens;
+    p->seq_lens = seq_lens;
+    p->page_table = page_table;
+    p->free_pages = free_pages;
+    p->num_free = num_free;
+    p->batch = batch;
+    p->num_rows = num_rows;
+    p->max_blocks = max_blocks;
+    while ((1 << p->bs_log2) < block_size) ++p->bs_log2;
+    p->num_pages = (int)num_pages;
+    p->span = reinterpret_cast<int4 *>(workspace);
+    p->page_top = reinterpret_cast<int32_t *>(workspace);   // grow: in the spans' place
+    p->before = reinterpret_cast<int32_t *>(p->span + batch);
+    return ATTN_OK;
+}
+
+static attn_status device_for(DevInfo **d) {
+    attn_status st = dev_info(d);
+    return st != ATTN_OK ? st : check_arch(*d);
+}
+
+static attn_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return ATTN_OK;
+    cudaGetLastError();
+    return ATTN_ERR_LAUNCH_FAILED;
+}
+
+extern "C" {
+
+attn_status attn_step_tables(const int32_t *request_rows, const int32_t *new_lens, int32_t *seq_lens,
+                             int32_t *page_table, const int32_t *free_pages, int32_t *num_free, int batch,
+                             int num_rows, int max_blocks, int block_size, int64_t num_pages, int64_t max_tokens,
+                             int32_t *block_table, int64_t *slot_mapping, int32_t *positions,
+                             int32_t *cu_seqlens_q, int32_t *cu_seqlens_k, int32_t *cache_seqlens,
+                             int32_t *context_lens, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!block_table || !cu_seqlens_q || !cu_seqlens_k || !cache_seqlens || !context_lens)
+        return ATTN_ERR_INVALID_ARG;
+    if (max_tokens < 0 || (max_tokens > 0 && (!slot_mapping || !positions))) return ATTN_ERR_INVALID_ARG;
+    if (max_tokens >= (int64_t)INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    TablesParams p;
+    attn_status st = tables_params(&p, request_rows, new_lens, seq_lens, page_table, const_cast<int32_t *>(free_pages),
+                                   num_free, batch, num_rows, max_blocks, block_size, num_pages, workspace,
+                                   workspace_bytes);
+    if (st != ATTN_OK) return st;
+    DevInfo *d = nullptr;
+    if ((st = device_for(&d)) != ATTN_OK) return st;
+    p.max_tokens = max_tokens;
+    p.block_table = block_table;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.cu_q = cu_seqlens_q;
+    p.cu_k = cu_seqlens_k;
+    p.cache_seqlens = cache_seqlens;
+    p.context_lens = context_lens;
+    p.err = d->err;
+    return launched(launch_step_tables(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_trim_pages(const int32_t *request_rows, const int32_t *keep_lens, int32_t *seq_lens,
+                            int32_t *page_table, int32_t *free_pages, int32_t *num_free, int batch, int num_rows,
+                            int max_blocks, int block_size, int64_t num_pages, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    TablesParams p;
+    attn_status st = tables_params(&p, request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, batch,
+                                   num_rows, max_blocks, block_size, num_pages, workspace, workspace_bytes);
+    if (st != ATTN_OK) return st;
+    DevInfo *d = nullptr;
+    if ((st = device_for(&d)) != ATTN_OK) return st;
+    p.err = d->err;
+    return launched(launch_trim_pages(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// rotary positions fused with the paged store
+// ---------------------------------------------------------------------------
+
+attn_status attn_rope_store_kvcache(const void *q, const void *k, const void *v, const int32_t *positions,
+                                    const float *inv_freq, const uint8_t *pair_axis, int num_axes,
+                                    int64_t axis_stride, int rot_dim, int interleaved, float scale, void *q_out,
+                                    void *k_out, void *k_cache, void *v_cache, void *v16_cache,
+                                    const int64_t *slot_mapping, int64_t num_tokens, int num_heads_q,
+                                    int num_heads_kv, int head_dim, int64_t q_row_stride, int64_t k_row_stride,
+                                    int64_t v_row_stride, int64_t q_out_row_stride, int64_t k_out_row_stride,
+                                    int64_t num_slots, void *stream) {
+    if (num_tokens < 0 || num_heads_q <= 0 || num_heads_kv <= 0 || head_dim <= 0 || num_slots < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (rot_dim <= 0 || rot_dim % 2 || rot_dim > head_dim || head_dim % 2) return ATTN_ERR_INVALID_ARG;
+    if (num_axes <= 0 || !(scale > 0.f) || !isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (rot_dim / 2 > kRopeMaxPairs || num_axes > kRopeMaxAxes) return ATTN_ERR_UNSUPPORTED;
+    if (num_axes > 1 && (!pair_axis || axis_stride < num_tokens)) return ATTN_ERR_INVALID_ARG;
+    const bool cache = k_cache || v_cache || v16_cache || slot_mapping;
+    if (num_tokens > 0 && cache && (!k_cache || !v_cache || !slot_mapping || !v)) return ATTN_ERR_INVALID_ARG;
+    if (num_tokens == 0) return ATTN_OK;
+    if (!cache && !k_out) return ATTN_ERR_INVALID_ARG;   // the rotated k would go nowhere
+    if (!q || !k || !positions || !inv_freq || !q_out) return ATTN_ERR_INVALID_ARG;
+    if ((int64_t)num_heads_q * head_dim > (int64_t)INT32_MAX / 4 || (int64_t)num_heads_kv * head_dim > (int64_t)INT32_MAX / 4)
+        return ATTN_ERR_UNSUPPORTED;
+    if (num_tokens >= (int64_t)INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    RopeParams p;
+    memset(&p, 0, sizeof p);
+    const int64_t qrow = (int64_t)num_heads_q * head_dim, krow = (int64_t)num_heads_kv * head_dim;
+    p.q_stride = q_row_stride ? q_row_stride : qrow;
+    p.k_stride = k_row_stride ? k_row_stride : krow;
+    p.v_stride = v_row_stride ? v_row_stride : krow;
+    p.q_out_stride = q_out_row_stride ? q_out_row_stride : qrow;
+    p.k_out_stride = k_out_row_stride ? k_out_row_stride : krow;
+    if (p.q_stride < qrow || p.q_out_stride < qrow || p.k_stride < krow || p.k_out_stride < krow || p.v_stride < krow)
+        return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        p.axis[i] = pair_axis ? pair_axis[i] : 0;
+        if (p.axis[i] >= num_axes) return ATTN_ERR_INVALID_ARG;
+    }
+    DevInfo *d = nullptr;
+    attn_status st = device_for(&d);
+    if (st != ATTN_OK) return st;
+    p.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p.k = reinterpret_cast<const __nv_bfloat16 *>(k);
+    p.v = cache ? reinterpret_cast<const __nv_bfloat16 *>(v) : nullptr;
+    p.q_out = reinterpret_cast<__nv_bfloat16 *>(q_out);
+    p.k_out = reinterpret_cast<__nv_bfloat16 *>(k_out);
+    p.k_cache = reinterpret_cast<__nv_bfloat16 *>(k_cache);
+    p.v_cache = reinterpret_cast<__nv_bfloat16 *>(v_cache);
+    p.v16_cache = reinterpret_cast<__half *>(v16_cache);
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.axis_stride = axis_stride;
+    p.num_tokens = num_tokens;
+    p.num_slots = num_slots;
+    p.Hq = num_heads_q;
+    p.Hkv = num_heads_kv;
+    p.D = head_dim;
+    p.half = rot_dim / 2;
+    p.num_axes = num_axes;
+    p.interleaved = interleaved ? 1 : 0;
+    p.scale = scale;
+    p.err = d->err;
+    const bool vec = head_dim % 16 == 0 && p.half % 8 == 0 && p.q_stride % 8 == 0 && p.k_stride % 8 == 0 &&
+                     p.v_stride % 8 == 0 && p.q_out_stride % 8 == 0 && p.k_out_stride % 8 == 0 && aligned16(q) &&
+                     aligned16(k) && aligned16(v) && aligned16(q_out) && aligned16(k_out) && aligned16(k_cache) &&
+                     aligned16(v_cache) && aligned16(v16_cache);
+    return launched(launch_rope_store(p, vec, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// linear attention
+// ---------------------------------------------------------------------------
+
+size_t attn_linear_workspace_size(int batch, int num_heads_q, int num_heads_kv, int head_dim, int max_seqlen) {
+    (void)batch, (void)num_heads_q, (void)num_heads_kv, (void)head_dim, (void)max_seqlen;
+    return 0;
+}
+
+}  // extern "C"
+
+// Host checks shared by the two linear-attention entries.
+static attn_status linear_params(LinearParams *p, const void *q, const void *k, const void *v, void *out,
+                                 const float *log_decay, float *state_cache, const int32_t *state_slots,
+                                 const int32_t *context_lens, int batch, int64_t total_tokens, int num_heads_q,
+                                 int num_heads_kv, int head_dim, float scale, int64_t num_slots, int64_t q_row_stride,
+                                 int64_t k_row_stride, int64_t v_row_stride, int64_t out_row_stride) {
+    if (batch <= 0 || total_tokens < 0 || num_heads_q <= 0 || num_heads_kv <= 0 || num_heads_q % num_heads_kv)
+        return ATTN_ERR_INVALID_ARG;
+    if (!log_decay || (total_tokens > 0 && (!q || !k || !v || !out))) return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (state_cache ? !state_slots || num_slots <= 0 : state_slots != nullptr) return ATTN_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (batch > 65535 || num_heads_q > 65535 || total_tokens >= (int64_t)INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state_cache))
+        return ATTN_ERR_INVALID_ARG;
+    if (!fix_stride(&q_row_stride, (int64_t)num_heads_q * head_dim) ||
+        !fix_stride(&out_row_stride, (int64_t)num_heads_q * head_dim) ||
+        !fix_stride(&k_row_stride, (int64_t)num_heads_kv * head_dim) ||
+        !fix_stride(&v_row_stride, (int64_t)num_heads_kv * head_dim))
+        return ATTN_ERR_INVALID_ARG;
+    memset(p, 0, sizeof *p);
+    p->q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p->k = reinterpret_cast<const __nv_bfloat16 *>(k);
+    p->v = reinterpret_cast<const __nv_bfloat16 *>(v);
+    p->out = reinterpret_cast<__nv_bfloat16 *>(out);
+    p->log_decay = log_decay;
+    p->state = state_cache;
+    p->slots = state_slots;
+    p->context_lens = context_lens;
+    p->q_stride = q_row_stride;
+    p->k_stride = k_row_stride;
+    p->v_stride = v_row_stride;
+    p->out_stride = out_row_stride;
+    p->total_tokens = total_tokens;
+    p->num_slots = num_slots;
+    p->batch = batch;
+    p->Hq = num_heads_q;
+    p->Hkv = num_heads_kv;
+    p->G = num_heads_q / num_heads_kv;
+    p->D = head_dim;
+    p->scale = scale;
+    return ATTN_OK;
+}
+
+extern "C" {
+
+attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                                   const int32_t *cu_seqlens, float *state_cache, const int32_t *state_slots,
+                                   const int32_t *context_lens, int batch, int64_t total_tokens, int max_seqlen,
+                                   int num_heads_q, int num_heads_kv, int head_dim, float scale, int64_t num_slots,
+                                   int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                                   int64_t out_row_stride, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!cu_seqlens || max_seqlen < 0) return ATTN_ERR_INVALID_ARG;
+    LinearParams p;
+    attn_status st = linear_params(&p, q, k, v, out, log_decay, state_cache, state_slots, context_lens, batch,
+                                   total_tokens, num_heads_q, num_heads_kv, head_dim, scale, num_slots, q_row_stride,
+                                   k_row_stride, v_row_stride, out_row_stride);
+    if (st != ATTN_OK) return st;
+    const size_t need = attn_linear_workspace_size(batch, num_heads_q, num_heads_kv, head_dim, max_seqlen);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (total_tokens == 0) return ATTN_OK;
+    DevInfo *d = nullptr;
+    if ((st = device_for(&d)) != ATTN_OK) return st;
+    p.cu = cu_seqlens;
+    p.max_seqlen = max_seqlen;
+    p.start_zero = context_lens == nullptr;
+    p.err = d->err;
+    return launched(launch_linear_varlen(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_linear_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                               float *state_cache, const int32_t *state_slots, const int32_t *context_lens, int batch,
+                               int num_heads_q, int num_heads_kv, int head_dim, float scale, int64_t num_slots,
+                               int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                               int64_t out_row_stride, void *stream) {
+    if (!state_cache) return ATTN_ERR_INVALID_ARG;
+    LinearParams p;
+    attn_status st = linear_params(&p, q, k, v, out, log_decay, state_cache, state_slots, context_lens, batch, batch,
+                                   num_heads_q, num_heads_kv, head_dim, scale, num_slots, q_row_stride, k_row_stride,
+                                   v_row_stride, out_row_stride);
+    if (st != ATTN_OK) return st;
+    DevInfo *d = nullptr;
+    if ((st = device_for(&d)) != ATTN_OK) return st;
+    p.max_seqlen = 1;
+    p.err = d->err;
+    return launched(launch_linear_decode(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -18,10 +18,14 @@ enum : uint32_t {
     ERR_INDEX = 1u << 0,      // an index read from device memory was out of range
     ERR_TIMEOUT = 1u << 1,    // a bounded wait ran out
     ERR_RANGE = 1u << 2,      // an input value outside the range the kernel handles (clamped)
+    ERR_CAPACITY = 1u << 3,   // the page pool or a request's table row is full
     SRC_STORE = 1u << 8,
     SRC_DECODE = 1u << 9,
     SRC_COMBINE = 1u << 10,
     SRC_PREFILL = 1u << 11,
+    SRC_TABLES = 1u << 14,
+    SRC_ROPE = 1u << 15,
+    SRC_LINEAR = 1u << 16,
 };
 
 __device__ __forceinline__ void record_error(uint32_t *err, uint32_t code) {

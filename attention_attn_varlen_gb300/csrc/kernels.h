@@ -92,6 +92,70 @@ cudaError_t launch_padded_cu(int batch, int seqlen_q, int seqlen_k, int32_t *cu_
 cudaError_t launch_kvcache_cu(const int32_t *cache_seqlens, int batch, int seqlen_q, int max_cache_seqlen,
                               int32_t *cu_q, int32_t *cu_k, uint32_t *err, cudaStream_t stream);
 
+// step_tables.cu: growing and trimming page tables on the GPU
+constexpr int kTablesMaxBatch = 65535;
+struct TablesParams {
+    const int32_t *rows;         // null (entry b is row b), or [batch]: request row of each entry
+    const int32_t *lens;         // [batch]: new tokens (grow) or tokens to keep (trim)
+    int32_t *seq_lens;           // [num_rows]: cached tokens of each request
+    int32_t *page_table;         // [num_rows, max_blocks]
+    int32_t *free_pages;         // [num_pages]: the first *num_free entries are free pages
+    int32_t *num_free;
+    int batch, num_rows, max_blocks, bs_log2, num_pages;
+    int64_t max_tokens;          // grow: entries of slot_mapping and positions
+    int32_t *block_table;        // grow, outputs: [batch, max_blocks]
+    int64_t *slot_mapping;       //   [max_tokens]
+    int32_t *positions;          //   [max_tokens]
+    int32_t *cu_q, *cu_k;        //   [batch + 1]
+    int32_t *cache_seqlens;      //   [batch]: tokens after the step
+    int32_t *context_lens;       //   [batch]: tokens before it
+    int32_t *before;             // workspace [batch]: length found for the entry, -1: unusable
+    int32_t *page_top;           // workspace [batch] (grow)
+    int4 *span;                  // workspace [batch] (trim): kept pages, pages before, place, row
+    uint32_t *err;
+};
+cudaError_t launch_step_tables(const TablesParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_trim_pages(const TablesParams &p, int num_sms, cudaStream_t stream);
+
+// rope_store.cu: rotary positions fused with the paged store
+constexpr int kRopeMaxPairs = 128;
+constexpr int kRopeMaxAxes = 4;
+struct RopeParams {
+    const __nv_bfloat16 *q, *k, *v;   // [N, H, D]; row strides below; v null: nothing of V is stored
+    __nv_bfloat16 *q_out, *k_out;     // k_out null: k goes to the cache only
+    __nv_bfloat16 *k_cache, *v_cache; // null: no cache
+    __half *v16_cache;
+    const int64_t *slot_mapping;
+    const int32_t *positions;         // axis a of token t at positions[a * axis_stride + t]
+    const float *inv_freq;            // [half]
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, axis_stride;
+    int64_t num_tokens, num_slots;
+    int Hq, Hkv, D, half, num_axes;
+    int interleaved;
+    float scale;
+    uint8_t axis[kRopeMaxPairs];      // position axis of each pair
+    uint32_t *err;
+};
+cudaError_t launch_rope_store(const RopeParams &p, bool vec, int num_sms, cudaStream_t stream);
+
+// linear_attn.cu: linear attention with a decay for each head
+struct LinearParams {
+    const __nv_bfloat16 *q, *k, *v;   // [T, H, D] with row strides
+    __nv_bfloat16 *out;
+    const float *log_decay;           // [Hkv]
+    const int32_t *cu;                // [batch + 1]; null: one token per sequence (decode)
+    float *state;                     // [num_slots, Hkv, D, D], rows along the value dimension; null: none kept
+    const int32_t *slots;             // [batch]; < 0: no state
+    const int32_t *context_lens;      // [batch] or null; 0: the sequence starts from a zero state
+    int64_t q_stride, k_stride, v_stride, out_stride, total_tokens, num_slots;
+    int batch, Hq, Hkv, G, D, max_seqlen;
+    int start_zero;                   // context_lens is null and every sequence starts from zero
+    float scale;
+    uint32_t *err;
+};
+cudaError_t launch_linear_varlen(const LinearParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_decode(const LinearParams &p, int num_sms, cudaStream_t stream);
+
 cudaError_t launch_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                            const CUtensorMap &omap, const PrefillParams &p, int head_dim, cudaStream_t stream);
 

@@ -66,8 +66,10 @@ typedef enum attn_status {
     ATTN_ERR_DEVICE_TIMEOUT = 5,     /* a kernel's bounded wait ran out (reported by the error word) */
     ATTN_ERR_DEVICE_INDEX = 6,       /* a device-side index was out of range (reported by the error word) */
     ATTN_ERR_NO_DEVICE = 7,          /* no CUDA device, or the device query failed */
-    ATTN_ERR_DEVICE_RANGE = 8        /* an input value outside the range a kernel handles (reported by the
+    ATTN_ERR_DEVICE_RANGE = 8,       /* an input value outside the range a kernel handles (reported by the
                                         error word; see attn_varlen_fwd) */
+    ATTN_ERR_DEVICE_CAPACITY = 9     /* the page pool or a request's table row is full (reported by the error
+                                        word; see attn_step_tables) */
 } attn_status;
 
 /* ------------------------------------------------------------------------
@@ -400,6 +402,153 @@ ATTN_API attn_status attn_softmax_rows(const void *x, void *y, int64_t rows, int
                                        int64_t y_row_stride, int dtype, void *stream);
 
 /* ------------------------------------------------------------------------
+ * attn_step_tables -- the index tables of one serving step, built on the GPU
+ * from request lengths: every request of the step grows by its new tokens,
+ * taking pages from a free list, and the tables that store_kvcache,
+ * attn_varlen_fwd (paged), attn_decode_paged and attn_kvcache_fwd read come out.
+ *
+ * The pool, kept by the caller on the device and updated in place:
+ *   seq_lens     int32 [num_rows]: cached tokens of each request row
+ *   page_table   int32 [num_rows, max_blocks]: pages of each request row
+ *   free_pages   int32 [num_pages]: entries 0 .. *num_free - 1 are the free
+ *                pages; pages are taken from the end (read, not changed here)
+ *   num_free     int32 [1]
+ * The step:
+ *   request_rows nullable int32 [batch]: the request row of each entry (NULL:
+ *                entry b is row b); naming a row twice is a caller error: the
+ *                first entry is served, later ones are reported and not served
+ *   new_lens     int32 [batch] >= 0: new tokens of each entry
+ *   block_size   a power of two >= 16
+ * Outputs:
+ *   block_table   [batch, max_blocks]: the entry's pages, -1 behind them
+ *   slot_mapping  int64 [max_tokens]: cache slot (page * block_size + offset)
+ *                 of each new token, packed in entry order; -1 behind the last
+ *                 one (a padded batch) and for entries that are not served
+ *   positions     int32 [max_tokens]: position of each new token in its
+ *                 request; 0 behind the last one
+ *   cu_seqlens_q  int32 [batch + 1]: prefix sums of new_lens (at most max_tokens)
+ *   cu_seqlens_k  int32 [batch + 1]: prefix sums of cache_seqlens
+ *   cache_seqlens int32 [batch]: cached tokens after the step
+ *   context_lens  int32 [batch]: cached tokens before it
+ * Entries are served in order.  An entry is not served, and its request stays
+ * as it was (cache_seqlens = context_lens), when the pages it and the entries
+ * before it need exceed the free ones or its row has no room for its pages
+ * (ATTN_ERR_DEVICE_CAPACITY), or when its row, its request's length or its
+ * tokens (negative, or past max_tokens) are out of range
+ * (ATTN_ERR_DEVICE_INDEX).  An entry that needs no new page is always served.
+ * workspace: attn_step_tables_workspace_size(batch) bytes, 16-byte aligned.
+ * Limits: batch <= 65535; fewer than 2^31 cache slots, row slots and tokens.
+ * ------------------------------------------------------------------------ */
+ATTN_API attn_status attn_step_tables(const int32_t *request_rows, const int32_t *new_lens, int32_t *seq_lens,
+                                      int32_t *page_table, const int32_t *free_pages, int32_t *num_free, int batch,
+                                      int num_rows, int max_blocks, int block_size, int64_t num_pages,
+                                      int64_t max_tokens, int32_t *block_table, int64_t *slot_mapping,
+                                      int32_t *positions, int32_t *cu_seqlens_q, int32_t *cu_seqlens_k,
+                                      int32_t *cache_seqlens, int32_t *context_lens, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* attn_trim_pages -- cut every named request to its first keep_lens[b] cached
+ * tokens (0: the request has ended; rejected speculative tokens: the accepted
+ * length; at least its length: nothing happens).  Pages that hold no kept token
+ * go back to the free list and their page_table entries become -1.  The order
+ * is the reverse of attn_step_tables', so growing and trimming by the same
+ * amounts restores the list.  Entries with a row out of range or named before,
+ * a negative keep_lens (taken as 0) or more pages than the pool has left room
+ * for (left as they were) are reported as ATTN_ERR_DEVICE_INDEX.  Same
+ * workspace as attn_step_tables. */
+ATTN_API attn_status attn_trim_pages(const int32_t *request_rows, const int32_t *keep_lens, int32_t *seq_lens,
+                                     int32_t *page_table, int32_t *free_pages, int32_t *num_free, int batch,
+                                     int num_rows, int max_blocks, int block_size, int64_t num_pages,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two calls above (0 for invalid sizes). */
+ATTN_API size_t attn_step_tables_workspace_size(int batch);
+
+/* ------------------------------------------------------------------------
+ * attn_rope_store_kvcache -- rotary positions on q and k, and store_kvcache of
+ * the rotated k and of v, in one pass over q, k and v.
+ *
+ * Pair i of a head turns by angle = positions[axis(i)][token] * inv_freq[i]:
+ *   (a, b) -> scale * (a cos - b sin, a sin + b cos),
+ * computed in fp32 from an angle exact to 2^-31 of half a turn at any position,
+ * rounded once to bf16.
+ *
+ *   q, k, v      [num_tokens, num_heads_q | num_heads_kv, head_dim]
+ *   positions    int32 [num_axes][num_tokens], axes axis_stride elements apart
+ *                (unused with one axis); negative positions are allowed
+ *   inv_freq     float32 [rot_dim / 2]
+ *   pair_axis    HOST array [rot_dim / 2], the axis of each pair (for instance
+ *                time, height and width of image and video tokens); NULL: axis 0
+ *   rot_dim      even, <= head_dim: elements past it pass through unchanged
+ *   interleaved  0: pair i is elements (i, i + rot_dim / 2); else (2 i, 2 i + 1)
+ *   scale        > 0, multiplies the rotated elements
+ *   q_out        [num_tokens, num_heads_q, head_dim]; may be q
+ *   k_out        nullable; the rotated k; may be k
+ *   k_cache, v_cache, v16_cache, slot_mapping, num_slots: as for store_kvcache
+ *                (all NULL: nothing is stored, k_out is required, v may be NULL)
+ * Strides in elements, 0 = packed.  Rows, heads and rotated halves on 16-byte
+ * boundaries (head_dim and rot_dim multiples of 16) take the vector kernel,
+ * anything else one element at a time.  head_dim is any even value here.
+ * |v| >= 2^20 with v16_cache is clamped and reported as ATTN_ERR_DEVICE_RANGE.
+ * Limits: rot_dim <= 256, num_axes <= 4.
+ * ------------------------------------------------------------------------ */
+ATTN_API attn_status attn_rope_store_kvcache(const void *q, const void *k, const void *v, const int32_t *positions,
+                                             const float *inv_freq, const uint8_t *pair_axis, int num_axes,
+                                             int64_t axis_stride, int rot_dim, int interleaved, float scale,
+                                             void *q_out, void *k_out, void *k_cache, void *v_cache,
+                                             void *v16_cache, const int64_t *slot_mapping, int64_t num_tokens,
+                                             int num_heads_q, int num_heads_kv, int head_dim, int64_t q_row_stride,
+                                             int64_t k_row_stride, int64_t v_row_stride, int64_t q_out_row_stride,
+                                             int64_t k_out_row_stride, int64_t num_slots, void *stream);
+
+/* ------------------------------------------------------------------------
+ * attn_linear_varlen_fwd -- linear attention with a decay for each head over
+ * packed sequences (prompts, chunks of prompts):
+ *   S_t = e^g S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t
+ * with g = log_decay of the KV head and S [head_dim, head_dim] in fp32, rows
+ * along v.  Query head h reads KV head h / (num_heads_q / num_heads_kv).
+ *
+ *   q, k, v, out [total_tokens, num_heads_q | num_heads_kv, head_dim]; sequence
+ *                b owns rows [cu_seqlens[b], cu_seqlens[b + 1]); rows behind the
+ *                last sequence are left as they were
+ *   log_decay    float32 [num_heads_kv], <= 0 (0: no decay; -inf: only the token
+ *                itself); a positive or NaN value is taken as 0 and reported as
+ *                ATTN_ERR_DEVICE_RANGE
+ *   state_cache  nullable; float32 [num_slots, num_heads_kv, head_dim, head_dim]
+ *   state_slots  int32 [batch] with state_cache: the slot that receives the
+ *                sequence's final state; < 0: none is kept.  Naming a slot
+ *                twice is a caller error (its state is then undefined)
+ *   context_lens nullable int32 [batch]: tokens of the sequence already in its
+ *                state; 0: the sequence starts from a zero state, whatever the
+ *                slot holds.  NULL: every sequence starts from zero
+ *   max_seqlen   host-side upper bound of the lengths (a longer sequence is cut
+ *                to it and reported as ATTN_ERR_DEVICE_INDEX)
+ * A sequence of length 0 leaves its slot as it was.
+ * workspace: attn_linear_workspace_size(...) bytes, 256-byte aligned.
+ * ------------------------------------------------------------------------ */
+ATTN_API attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, void *out,
+                                            const float *log_decay, const int32_t *cu_seqlens, float *state_cache,
+                                            const int32_t *state_slots, const int32_t *context_lens, int batch,
+                                            int64_t total_tokens, int max_seqlen, int num_heads_q, int num_heads_kv,
+                                            int head_dim, float scale, int64_t num_slots, int64_t q_row_stride,
+                                            int64_t k_row_stride, int64_t v_row_stride, int64_t out_row_stride,
+                                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes attn_linear_varlen_fwd needs (0 for invalid sizes, and where it needs none). */
+ATTN_API size_t attn_linear_workspace_size(int batch, int num_heads_q, int num_heads_kv, int head_dim, int max_seqlen);
+
+/* attn_linear_decode -- the recurrent form: one token per sequence, q, out
+ * [batch, num_heads_q, head_dim], k, v [batch, num_heads_kv, head_dim]; the
+ * states are read and updated in place.  state_slots[b] < 0: a zero state,
+ * nothing is kept.  context_lens nullable: 0 starts from a zero state; NULL:
+ * every sequence with a slot continues from it. */
+ATTN_API attn_status attn_linear_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                                        float *state_cache, const int32_t *state_slots, const int32_t *context_lens,
+                                        int batch, int num_heads_q, int num_heads_kv, int head_dim, float scale,
+                                        int64_t num_slots, int64_t q_row_stride, int64_t k_row_stride,
+                                        int64_t v_row_stride, int64_t out_row_stride, void *stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics
  * ------------------------------------------------------------------------ */
 
@@ -408,8 +557,8 @@ ATTN_API const char *attn_status_string(attn_status status);
 
 /* Synchronises `stream`, then reads and clears the device error word of the
  * current device.  Returns ATTN_OK if no kernel recorded a problem since the
- * last call, else ATTN_ERR_DEVICE_INDEX, ATTN_ERR_DEVICE_TIMEOUT or
- * ATTN_ERR_DEVICE_RANGE (in that order of precedence), or
+ * last call, else ATTN_ERR_DEVICE_INDEX, ATTN_ERR_DEVICE_TIMEOUT,
+ * ATTN_ERR_DEVICE_RANGE or ATTN_ERR_DEVICE_CAPACITY (in that order of precedence), or
  * ATTN_ERR_LAUNCH_FAILED if the stream itself reports a CUDA error.  *detail (nullable) receives the raw error word. */
 ATTN_API attn_status attn_get_last_device_error(void *stream, uint32_t *detail);
 
