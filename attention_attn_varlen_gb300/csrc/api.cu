@@ -1132,9 +1132,62 @@ attn_status attn_rope_store_kvcache(const void *q, const void *k, const void *v,
 // linear attention
 // ---------------------------------------------------------------------------
 
+}  // extern "C"
+
+// Segments of the prompt form.  One CTA runs a (sequence, query head) chunk after
+// chunk, so a sequence much longer than a fair share of the tokens (total x heads
+// / SMs) would run on after the others.  Such sequences are cut into segments
+// that run side by side, after a pass that computes each segment's own state from
+// k and v alone: half the main pass's bytes again, plus about 12 us of launches
+// and setup (a segment of 512 tokens).  Without that pass where it does not pay.
+constexpr int kLinearSms = 152;
+static int64_t round64(int64_t x) { return (x + 63) & ~(int64_t)63; }
+
+static int linear_seg_len(int64_t total_tokens, int num_heads_q, int max_seqlen) {
+    const int64_t whole = round64(max_seqlen > 0 ? max_seqlen : 1);
+    int64_t share = total_tokens * num_heads_q / kLinearSms;
+    if (share < 1) share = 1;
+    const int64_t n = max_seqlen / share;
+    if (n < 2) return (int)whole;
+    int64_t seg = round64((max_seqlen + n - 1) / n);
+    if (seg < 512) seg = 512;
+    return max_seqlen > seg + (3 * seg) / 5 + 512 ? (int)seg : (int)whole;
+}
+
+// Segments beyond the first of all sequences together: each stands for at least a
+// fair share of the tokens.
+static int linear_extra_segments(int num_heads_q) { return kLinearSms / num_heads_q + 1; }
+
+static int64_t linear_state_rows(int batch, int num_heads_q, int num_heads_kv, bool copies) {
+    // a start for every segment of a cut sequence (at most twice its extra ones); where
+    // query heads share a state, a copy of every sequence's
+    return 2 * linear_extra_segments(num_heads_q) + (copies && num_heads_q > num_heads_kv ? batch : 0);
+}
+
+struct LinearLayout {
+    size_t units, decay, states, bytes;
+};
+static LinearLayout linear_layout(int batch, int num_heads_q, int num_heads_kv, int head_dim) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    LinearLayout l;
+    l.units = 256;   // the count in front
+    l.decay = l.units + up(sizeof(int4) * ((size_t)batch + linear_extra_segments(num_heads_q)));
+    l.states = l.decay + up(sizeof(float) * (size_t)num_heads_kv * kLinearDecayRow);
+    l.bytes = l.states + sizeof(float) * (size_t)linear_state_rows(batch, num_heads_q, num_heads_kv, true) *
+                             num_heads_kv * head_dim * head_dim;
+    return l;
+}
+
+static bool linear_sizes(int batch, int num_heads_q, int num_heads_kv, int head_dim) {
+    return batch > 0 && batch <= 65535 && num_heads_kv > 0 && num_heads_q > 0 && num_heads_q <= 65535 &&
+           num_heads_q % num_heads_kv == 0 && (head_dim == 64 || head_dim == 128);
+}
+
+extern "C" {
+
 size_t attn_linear_workspace_size(int batch, int num_heads_q, int num_heads_kv, int head_dim, int max_seqlen) {
-    (void)batch, (void)num_heads_q, (void)num_heads_kv, (void)head_dim, (void)max_seqlen;
-    return 0;
+    if (!linear_sizes(batch, num_heads_q, num_heads_kv, head_dim) || max_seqlen < 0) return 0;
+    return linear_layout(batch, num_heads_q, num_heads_kv, head_dim).bytes;
 }
 
 }  // extern "C"
@@ -1200,14 +1253,33 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
     const size_t need = attn_linear_workspace_size(batch, num_heads_q, num_heads_kv, head_dim, max_seqlen);
     if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return ATTN_ERR_INVALID_ARG;
     if (workspace_bytes < need) return ATTN_ERR_WORKSPACE_TOO_SMALL;
-    if (total_tokens == 0) return ATTN_OK;
+    if (total_tokens == 0 || max_seqlen == 0) return ATTN_OK;
     DevInfo *d = nullptr;
     if ((st = device_for(&d)) != ATTN_OK) return st;
     p.cu = cu_seqlens;
     p.max_seqlen = max_seqlen;
     p.start_zero = context_lens == nullptr;
     p.err = d->err;
-    return launched(launch_linear_varlen(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+    p.seg_len = linear_seg_len(total_tokens, num_heads_q, max_seqlen);
+    const bool split = p.seg_len < max_seqlen;
+    const int64_t units = (int64_t)batch + (split ? linear_extra_segments(num_heads_q) : 0);
+    if (units * num_heads_q > (int64_t)INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    p.max_units = (int)units;
+    const bool copies = state_cache && context_lens;
+    p.state_rows = (int)(linear_state_rows(batch, num_heads_q, num_heads_kv, copies) -
+                         (split ? 0 : 2 * linear_extra_segments(num_heads_q)));
+    const LinearLayout l = linear_layout(batch, num_heads_q, num_heads_kv, head_dim);
+    char *ws = reinterpret_cast<char *>(workspace);
+    p.unit_count = reinterpret_cast<int *>(ws);
+    p.units = reinterpret_cast<int4 *>(ws + l.units);
+    p.decay = reinterpret_cast<float *>(ws + l.decay);
+    p.states = reinterpret_cast<float *>(ws + l.states);
+    CUtensorMap qmap, kmap, vmap;
+    if (!make_map(&qmap, q, total_tokens, num_heads_q, head_dim, p.q_stride, 1, 64) ||
+        !make_map(&kmap, k, total_tokens, num_heads_kv, head_dim, p.k_stride, 1, 64) ||
+        !make_map(&vmap, v, total_tokens, num_heads_kv, head_dim, p.v_stride, 1, 64))
+        return ATTN_ERR_LAUNCH_FAILED;
+    return launched(launch_linear_varlen(qmap, kmap, vmap, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_linear_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,
@@ -1225,7 +1297,7 @@ attn_status attn_linear_decode(const void *q, const void *k, const void *v, void
     if ((st = device_for(&d)) != ATTN_OK) return st;
     p.max_seqlen = 1;
     p.err = d->err;
-    return launched(launch_linear_decode(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+    return launched(launch_linear_decode(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

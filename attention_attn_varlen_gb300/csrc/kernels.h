@@ -151,10 +151,19 @@ struct LinearParams {
     int batch, Hq, Hkv, G, D, max_seqlen;
     int start_zero;                   // context_lens is null and every sequence starts from zero
     float scale;
+    // prompts: the work list and the states at segment starts, in the workspace
+    int seg_len;                      // a longer sequence is cut into segments of this many tokens (a multiple of 64)
+    int max_units, state_rows;        // entries of units, rows of states
+    int4 *units;                      // (sequence, segment, first row of states or -1, segments)
+    int *unit_count;
+    float *decay;                     // [Hkv, kLinearDecayRow]
+    float *states;                    // [state_rows, Hkv, D, D]
     uint32_t *err;
 };
-cudaError_t launch_linear_varlen(const LinearParams &p, int num_sms, cudaStream_t stream);
-cudaError_t launch_linear_decode(const LinearParams &p, int num_sms, cudaStream_t stream);
+constexpr int kLinearDecayRow = 136;
+cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const LinearParams &p, cudaStream_t stream);
+cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream);
 
 cudaError_t launch_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                            const CUtensorMap &omap, const PrefillParams &p, int head_dim, cudaStream_t stream);

@@ -3,6 +3,8 @@
 //   o_t = scale * S_t q_t
 // over packed sequences (a prompt) or one token per sequence (decode), with a
 // cache of states.
+#include <mutex>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -135,16 +137,713 @@ cudaError_t launch_tokens(const LinearParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Prompts, in chunks of 64 tokens on the tensor cores.
+//
+// With n tokens in a chunk, i and j counting them from 0 and S_0 the state before:
+//   o_i = scale * sum_{j <= i} e^{(i-j) g} (q_i . k_j) v_j + scale * e^{(i+1) g} S_0 q_i
+//   S_n = e^{n g} S_0 + sum_j e^{(n-1-j) g} v_j k_j^T
+// Every exponent is <= 0: nothing overflows whatever the decay.
+//
+// As matrices with the value dimension in the 128 TMEM lanes (so that all but
+// the first have M = 128, and both S and V are A operands read from TMEM):
+//   QK     [i, j]   = Q K^T                 shared x shared
+//   QS     [dv, i]  = S_0 Q^T               TMEM (S_0 as two bf16 parts) x shared
+//   PV     [dv, i]  = V^T P^T               TMEM (V^T, exact) x shared (P as two bf16 parts)
+//   KV     [dv, dk] = (w_j V)^T K           TMEM (three bf16 parts) x shared
+// with P = scale * e^{(i-j) g} QK (masked) and w_j = e^{(n-1-j) g}.
+//
+// Precision.  q, k and v are bf16 and exact.  P and S_0 only reach the bf16 output:
+// two parts leave 2^-16 of each term, against the output's own 2^-8.  The state is
+// fp32 and returned: w_j v_j in three parts is the fp32 product (2^-24); one
+// or two parts would leave 1.7e-3 or 2.8e-6 of it.  S itself stays in fp32 registers;
+// e^{64 g} multiplies it as hi + lo, so its rounding does not add up over chunks.
+//
+// Bound by HBM: 1 KB per token and head at head_dim 128 (q, k, v read, out
+// written), 65,536 / 152 SMs of it per chunk in 1.49 us; the products above are
+// 12.6 MFLOP there, about 1 us of one SM's tensor core.
+//
+// Roles (20 warps): V preparation (transposes V into TMEM, plain and weighted),
+// state (fp32 registers; adds KV, writes S_0's two parts), output rows, P, one
+// thread issuing every MMA, one thread issuing the loads.
+// ---------------------------------------------------------------------------
+
+constexpr int LC = 64;                       // tokens of a chunk
+constexpr int kChunkThreads = 640;
+constexpr int kChunkPanel = LC * 128;        // 64 rows x 128 bytes
+constexpr uint32_t TC_S = 0;                 // TMEM columns: QK, then PV (the P warps have read QK by then)
+constexpr uint32_t TC_INTER = 64;            // QS
+constexpr uint32_t TC_KV = 128;              // KV
+constexpr uint32_t TC_STATE = 256;           // S_0: hi 64 columns, lo 64 (D / 2 used of each)
+constexpr uint32_t TC_V = 384;               // V^T
+constexpr uint32_t TC_W = 416;               // (w V)^T, three parts of 32
+constexpr int kDecayRow = kLinearDecayRow;   // floats of a head's decay table: e^{m g} for m = 0..64, the part
+                                             // below fp32 of each, then e^{seg_len g} in two parts
+constexpr int kBuckets = 256;
+
+template <int D>
+struct ChunkSmem {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kQkPanel = 2 * kChunkPanel;             // 64 Q rows, then 64 K rows
+    static constexpr int kVOff = kPanels * kQkPanel;
+    static constexpr int kStageBytes = kVOff + kPanels * kChunkPanel;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kPOff = kStages * kStageBytes;          // P: hi, lo
+    static constexpr int kOutOff = kPOff + 2 * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
+    static constexpr int kTabOff = kOutOff + 4 * LC * 64;
+    // scale e^{m g} m = 0..64 (68 floats); w of a full chunk, of the last chunk; first bad token per dv, two chunks
+    static constexpr int kTabBytes = 68 * 4 + 2 * LC * 4 + 2 * 128 * 4;
+    static constexpr int kBarOff = kTabOff + kTabBytes;
+    static constexpr int kNumBars = 2 * kStages + 9;
+    static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// x0, x1 -> their bf16 part (packed); x0, x1 become what is left (exact)
+__device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) {
+    const uint32_t h = pack_bf16x2(x0, x1);
+    x0 -= __uint_as_float(h << 16);
+    x1 -= __uint_as_float(h & 0xFFFF0000u);
+    return h;
+}
+
+// Tokens of unit `u` and the segment's place in its sequence.
+struct ChunkUnit {
+    int b, n, row;      // n tokens, state row in the workspace (-1: none)
+    int64_t t0;
+    bool last;          // holds the sequence's last token
+};
+
+__device__ __forceinline__ ChunkUnit chunk_unit(const LinearParams &p, const int4 e) {
+    ChunkUnit u;
+    int len;
+    linear_rows(p, e.x, u.t0, len, false);
+    u.b = e.x;
+    u.row = e.z < 0 ? -1 : e.z + e.y;
+    const int at = e.y * p.seg_len;
+    u.t0 += at;
+    u.n = min(len - at, p.seg_len);
+    u.last = at + u.n == len;
+    return u;
+}
+
+// The work list: a unit is a sequence, or a segment of seg_len tokens of a longer
+// one; units with the most chunks come first (the hardware starts CTAs in order,
+// so the long ones do not end up alone at the end).  Entry: (sequence, segment,
+// state rows in the workspace or -1, segments).  CTA 0 writes the list, the others
+// the heads' decay tables (in 64 bits: 132 exponentials per head and call).
+__global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const int h = (blockIdx.x - 1) * 8 + (tid >> 7), m = tid & 127;
+        if (h >= p.Hkv || m > LC + 1) return;
+        const double g = (double)linear_log_decay(p, h, m == 0);
+        float *row = p.decay + (int64_t)h * kDecayRow;
+        const int steps = m <= LC ? m : p.seg_len;
+        const double x = steps == 0 ? 1.0 : exp(g * steps);
+        const float hi = (float)x, lo = (float)(x - (double)hi);
+        if (m <= LC) {
+            row[m] = hi;
+            row[LC + 1 + m] = lo;
+        } else {
+            row[2 * LC + 2] = hi;
+            row[2 * LC + 3] = lo;
+        }
+        return;
+    }
+    __shared__ int count[kBuckets], rows_s;
+    for (int i = tid; i < kBuckets; i += 1024) count[i] = 0;
+    if (tid == 0) rows_s = 0;
+    __syncthreads();
+    const int most = max(1, min(p.seg_len, p.max_seqlen));
+    auto bucket = [&](int tokens) { return kBuckets - 1 - (int)((int64_t)tokens * (kBuckets - 1) / most); };
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int b = tid; b < p.batch; b += 1024) {
+            int64_t t0;
+            int n;
+            linear_rows(p, b, t0, n, pass == 0);
+            if (n == 0) continue;
+            const int segs = (n + p.seg_len - 1) / p.seg_len, tail = n - (segs - 1) * p.seg_len;
+            if (pass == 0) {
+                if (segs > 1) atomicAdd(&count[bucket(p.seg_len)], segs - 1);
+                atomicAdd(&count[bucket(tail)], 1);
+            } else {
+                bool from;
+                linear_state(p, b, 0, from, true);
+                // a state of its own for every segment's start; heads that share a state
+                // read a copy, since one of them writes the new one
+                const bool rows = segs > 1 || (from && p.G > 1);
+                int row = rows ? atomicAdd(&rows_s, segs) : -1;
+                // offsets that overlap can ask for more than the workspace was sized for
+                bool fits = row + segs <= p.state_rows;
+                if (!fits) row = -1;
+                for (int i = 0; i < segs; ++i) {
+                    const int at = atomicAdd(&count[bucket(i < segs - 1 ? p.seg_len : tail)], 1);
+                    if (at < p.max_units) p.units[at] = make_int4(b, i, row, segs);
+                    else fits = false;
+                }
+                if (!fits) record_error(p.err, ERR_INDEX | SRC_LINEAR);
+            }
+        }
+        __syncthreads();
+        if (pass == 0 && tid < 32) {
+            // counts -> first places
+            int base = 0;
+            for (int i = 0; i < kBuckets; i += 32) {
+                const int c = count[i + tid];
+                int inc = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (tid >= o) inc += v;
+                }
+                count[i + tid] = base + inc - c;
+                base += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (tid == 0) *p.unit_count = min(base, p.max_units);
+        }
+        __syncthreads();
+    }
+}
+
+// The states at the starts of a sequence's segments, in place of the segments'
+// own sums that the state-only pass left there:
+//   start_0 = the cached state or 0,  start_{s+1} = e^{seg_len g} start_s + own_s
+__global__ void __launch_bounds__(256) linear_scan_kernel(const LinearParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if ((int)blockIdx.x >= *p.unit_count) return;
+    const int4 e = p.units[blockIdx.x];
+    if (e.y != 0 || e.z < 0) return;
+    const int h = blockIdx.y, D2 = p.D * p.D;
+    bool from;
+    const float *state = linear_state(p, e.x, h, from, false);
+    const float *t = p.decay + (int64_t)h * kDecayRow + 2 * LC + 2;
+    const float hi = t[0], lo = t[1];
+    const int x = (blockIdx.z * 256 + threadIdx.x) * 4;
+    if (x >= D2) return;
+    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (from) run = *reinterpret_cast<const float4 *>(state + x);
+    for (int s = 0; s < e.w; ++s) {
+        float4 *at = reinterpret_cast<float4 *>(p.states + ((int64_t)(e.z + s) * p.Hkv + h) * D2 + x);
+        const float4 own = s + 1 < e.w ? *at : run;
+        *at = run;
+        run.x = fmaf(hi, run.x, fmaf(lo, run.x, own.x));
+        run.y = fmaf(hi, run.y, fmaf(lo, run.y, own.y));
+        run.z = fmaf(hi, run.z, fmaf(lo, run.z, own.z));
+        run.w = fmaf(hi, run.w, fmaf(lo, run.w, own.w));
+    }
+}
+
+// LOCAL: the state-only pass over the segments that have a successor: their own
+// sums (from a zero state) go to the workspace.
+template <int D, bool LOCAL>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    linear_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, const LinearParams p) {
+    using S = ChunkSmem<D>;
+    constexpr int ST = S::kStages, PAN = S::kPanels;
+    extern __shared__ __align__(1024) uint8_t lsmem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int heads = LOCAL ? p.Hkv : p.Hq;
+    const int at = blockIdx.x / heads, h = blockIdx.x - at * heads;
+    if (at >= *p.unit_count) return;
+    const int4 entry = p.units[at];
+    if (LOCAL && entry.y + 1 >= entry.w) return;
+    const ChunkUnit u = chunk_unit(p, entry);
+    const int hk = LOCAL ? h : h / p.G;
+    const int chunks = (u.n + LC - 1) / LC;
+    const int n_last = u.n - (chunks - 1) * LC;
+
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lsmem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
+    uint64_t *full = bars, *empty = bars + ST;
+    uint64_t *v_ready = bars + 2 * ST;       // V^T and (w V)^T of the chunk are in TMEM
+    uint64_t *v_free = v_ready + 1;          // PV and KV have read them
+    uint64_t *s_ready = v_ready + 2;         // QK done
+    uint64_t *p_ready = v_ready + 3;         // P in shared memory, QK's columns free
+    uint64_t *o_ready = v_ready + 4;         // QS and PV done
+    uint64_t *o_free = v_ready + 5;          // the output warps have read both
+    uint64_t *kv_ready = v_ready + 6;        // KV done (and QS has read S_0)
+    uint64_t *st_ready = v_ready + 7;        // S_0 of the next chunk in TMEM, KV's columns free
+    uint64_t *drain = v_ready + 8;           // every MMA done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *tab = reinterpret_cast<float *>(sm + S::kTabOff);   // scale e^{m g}
+    float *w_full = tab + 68, *w_last = w_full + LC;
+    int *bad_at = reinterpret_cast<int *>(w_last + LC);        // [2][128]
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 5);         // the MMAs, the four V warps
+        }
+        mbar_init(v_ready, 4);
+        mbar_init(v_free, 1);
+        mbar_init(s_ready, 1);
+        mbar_init(p_ready, 2);
+        mbar_init(o_ready, 1);
+        mbar_init(o_free, 4);
+        mbar_init(kv_ready, 1);
+        mbar_init(st_ready, 8);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    const float *decay = p.decay + (int64_t)hk * kDecayRow;
+    for (int i = threadIdx.x; i <= LC; i += kChunkThreads) tab[i] = p.scale * decay[i];
+    if (threadIdx.x < LC) {
+        const int j = threadIdx.x;
+        w_full[j] = decay[LC - 1 - j];
+        w_last[j] = j < n_last ? decay[n_last - 1 - j] : 0.f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // a warp's wait: every lane gets the same answer
+    auto wait = [&](uint64_t *bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, p.err, SRC_LINEAR)) != 0;
+    };
+
+    if (warp < 4) {
+        // ============================================================ V preparation: thread = value dimension
+        const int dv = warp * 32 + lane;
+        const bool real = dv < D;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c % ST, n = c + 1 < chunks ? LC : n_last;
+            const float *w = c + 1 < chunks ? w_full : w_last;
+            uint8_t *stage = sm + s * S::kStageBytes;
+            if (!wait(&full[s], c / ST)) break;
+            const uint8_t *v = stage + S::kVOff + ((dv & (D - 1)) >> 6) * kChunkPanel;
+            const uint32_t col = (uint32_t)(dv & 7) * 2, ch = (uint32_t)(dv & 63) >> 3;
+            if (n < LC) {
+                // rows behind the sequence's end: K's are zeroed (a weight of 0 would not
+                // cancel a NaN there), V's are left out below
+                for (int x = threadIdx.x; x < (LC - n) * 8 * PAN; x += 128) {
+                    const int pan = x / ((LC - n) * 8), r = x - pan * (LC - n) * 8;
+                    *reinterpret_cast<uint4 *>(stage + pan * S::kQkPanel + kChunkPanel + n * 128 + r * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            int bad = LC;
+            bool waited = true;
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                uint32_t raw[8], hi[8], mid[8], lo[8];
+                uint32_t big = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = part * 16 + 2 * i;
+                    uint32_t a = *reinterpret_cast<const uint16_t *>(v + j * 128 + ((ch ^ (j & 7)) << 4) + col);
+                    uint32_t b = *reinterpret_cast<const uint16_t *>(v + (j + 1) * 128 + ((ch ^ ((j + 1) & 7)) << 4) + col);
+                    if (n < LC) {
+                        a = j < n ? a : 0u;
+                        b = j + 1 < n ? b : 0u;
+                    }
+                    raw[i] = a | (b << 16);
+                    big = __vmaxu2(big, raw[i] & 0x7FFF7FFFu);
+                    const float2 wj = *reinterpret_cast<const float2 *>(w + j);
+                    float x0 = __uint_as_float(a << 16) * wj.x, x1 = __uint_as_float(b << 16) * wj.y;
+                    hi[i] = take_bf16(x0, x1);
+                    mid[i] = take_bf16(x0, x1);
+                    lo[i] = pack_bf16x2(x0, x1);
+                }
+                if (!LOCAL && ((big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u)) {
+                    // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
+                    // left out there and the output warps write NaN from its token on
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if ((raw[i] & 0x7F80u) == 0x7F80u) {
+                            bad = min(bad, part * 16 + 2 * i);
+                            raw[i] &= 0xFFFF0000u;
+                        }
+                        if ((raw[i] & 0x7F800000u) == 0x7F800000u) {
+                            bad = min(bad, part * 16 + 2 * i + 1);
+                            raw[i] &= 0xFFFFu;
+                        }
+                    }
+                }
+                if (part == 0 && c > 0) waited = wait(v_free, c - 1);
+                if (!waited) break;
+                if (!LOCAL) tmem_st8(lane_base + TC_V + part * 8, raw);
+                tmem_st8(lane_base + TC_W + part * 8, hi);
+                tmem_st8(lane_base + TC_W + 32 + part * 8, mid);
+                tmem_st8(lane_base + TC_W + 64 + part * 8, lo);
+            }
+            if (!waited) break;
+            if (!LOCAL && real) bad_at[(c & 1) * 128 + dv] = bad;
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(v_ready);
+                mbar_arrive(&empty[s]);
+            }
+        }
+    } else if (warp < 12) {
+        // ============================================================ state: thread = value dimension, half of dk
+        const int grp = warp & 3, half = (warp - 4) >> 2, dv = grp * 32 + lane;
+        const bool real = grp * 32 < D;      // warp-uniform
+        const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
+        constexpr int N = D / 2;             // columns per thread
+        float St[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) St[i] = 0.f;
+        bool from = false;
+        float *state = linear_state(p, u.b, hk, from, false);
+        if (!LOCAL && real) {
+            const float *src = nullptr;
+            if (u.row >= 0) src = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
+            else if (from) src = state;
+            if (src) {
+#pragma unroll
+                for (int i = 0; i < N; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src + dv * D + half * N + i);
+                    St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
+                }
+            }
+        }
+        auto publish = [&]() {               // S_0's two parts to TMEM
+#pragma unroll
+            for (int i = 0; i < N; i += 16) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float x0 = St[i + 2 * k], x1 = St[i + 2 * k + 1];
+                    hi[k] = take_bf16(x0, x1);
+                    lo[k] = pack_bf16x2(x0, x1);
+                }
+                tmem_st8(lane_base + TC_STATE + (half * N + i) / 2, hi);
+                tmem_st8(lane_base + TC_STATE + 64 + (half * N + i) / 2, lo);
+            }
+            tc_wait_st();
+        };
+        if (!LOCAL && real) publish();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(st_ready);
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const int n = c + 1 < chunks ? LC : n_last;
+            const float a = decay[n], a_lo = decay[LC + 1 + n];
+            if (!wait(kv_ready, c)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (real) {
+#pragma unroll
+                for (int i = 0; i < N; i += 16) {
+                    uint32_t kv[16];
+                    tmem_ld16(lane_base + TC_KV + half * N + i, kv);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        St[i + k] = fmaf(a, St[i + k], fmaf(a_lo, St[i + k], __uint_as_float(kv[k])));
+                }
+                if (!LOCAL && c + 1 < chunks) publish();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(st_ready);
+        }
+        float *dst = nullptr;
+        if (LOCAL) dst = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
+        else if (u.last && h % p.G == 0) dst = state;
+        if (ok && real && dst && (!LOCAL || u.row >= 0)) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4 *>(dst + dv * D + half * N + i) =
+                    make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
+        }
+    } else if (warp < 16) {
+        // ============================================================ output rows: thread = value dimension
+        if (!LOCAL) {
+            const int grp = warp & 3, dv = grp * 32 + lane;
+            const bool real = grp * 32 < D;
+            const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
+            uint8_t *stg = sm + S::kOutOff + grp * LC * 64;
+            for (int c = 0; c < chunks; ++c) {
+                const int n = c + 1 < chunks ? LC : n_last;
+                if (!wait(o_ready, c)) break;
+                tc_fence_after();
+                if (real) {
+                    const int bad = bad_at[(c & 1) * 128 + dv];
+#pragma unroll
+                    for (int part = 0; part < 4; ++part) {
+                        uint32_t x[16], y[16];
+                        tmem_ld16(lane_base + TC_S + part * 16, x);
+                        tmem_ld16(lane_base + TC_INTER + part * 16, y);
+                        tc_wait_ld();
+                        if (part == 3) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(o_free);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const int t = part * 16 + i;
+                            float o0 = fmaf(tab[t + 1], __uint_as_float(y[i]), __uint_as_float(x[i]));
+                            float o1 = fmaf(tab[t + 2], __uint_as_float(y[i + 1]), __uint_as_float(x[i + 1]));
+                            if (t >= bad) o0 = __int_as_float(0x7fc00000);
+                            if (t + 1 >= bad) o1 = __int_as_float(0x7fc00000);
+                            const uint32_t r = pack_bf16x2(o0, o1);
+                            *reinterpret_cast<uint16_t *>(stg + t * 64 + lane * 2) = (uint16_t)r;
+                            *reinterpret_cast<uint16_t *>(stg + (t + 1) * 64 + lane * 2) = (uint16_t)(r >> 16);
+                        }
+                    }
+                    __syncwarp();
+                    __nv_bfloat16 *out = p.out + (u.t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
+#pragma unroll
+                    for (int i = 0; i < LC / 8; ++i) {
+                        const int t = i * 8 + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * 64 + (lane & 3) * 16);
+                        if (t < n) *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) = v;
+                    }
+                    __syncwarp();
+                } else {
+                    if (lane == 0) mbar_arrive(o_free);
+                }
+            }
+        }
+    } else if (warp < 18) {
+        // ============================================================ P: thread = query token
+        if (!LOCAL) {
+            const int half = warp - 16, i = half * 32 + lane;
+            const uint32_t lane_base = tmem + ((uint32_t)(half * 32) << 16);
+            uint8_t *ph = sm + S::kPOff, *pl = ph + kChunkPanel;
+            if (half == 0) {
+                // tokens 0..31 see no key behind 31: those halves of their rows stay zero
+#pragma unroll
+                for (int k = 4; k < 8; ++k) {
+                    *reinterpret_cast<uint4 *>(ph + sw128_off(i, k)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(pl + sw128_off(i, k)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            for (int c = 0; c < chunks; ++c) {
+                if (!wait(s_ready, c)) break;
+                tc_fence_after();
+                for (int part = 0; part <= half; ++part) {
+                    uint32_t s[32];
+                    tmem_ld32(lane_base + TC_S + part * 32, s);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = part * 32 + k * 8 + e * 2;
+                            float x0 = j <= i ? __uint_as_float(s[k * 8 + e * 2]) * tab[max(i - j, 0)] : 0.f;
+                            float x1 = j + 1 <= i ? __uint_as_float(s[k * 8 + e * 2 + 1]) * tab[max(i - j - 1, 0)] : 0.f;
+                            hi[e] = take_bf16(x0, x1);
+                            lo[e] = pack_bf16x2(x0, x1);
+                        }
+                        *reinterpret_cast<uint4 *>(ph + sw128_off(i, part * 4 + k)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(pl + sw128_off(i, part * 4 + k)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready);
+            }
+        }
+    } else if (warp == 18) {
+        // ============================================================ MMA
+        bool ok = true;
+        for (int c = 0; c < chunks && ok; ++c) {
+            const int s = c % ST;
+            const uint32_t qk = smem_u32(sm + s * S::kStageBytes), pb = smem_u32(sm + S::kPOff);
+            ok = wait(&full[s], c / ST);
+            if (ok && !LOCAL && c > 0) ok = wait(o_free, c - 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (!LOCAL && lane == 0) {
+                // rows 64..127 of A are K's: a product nobody reads, in exchange for M = 128
+                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * S::kQkPanel + (k % 4) * 32;
+                    tc_mma_ss(tmem + TC_S, sw128_desc(qk + off, 16, 1024), sw128_desc(qk + kChunkPanel + off, 16, 1024),
+                              id, k > 0);
+                }
+                tc_commit(s_ready);
+            }
+            __syncwarp();
+            ok = wait(st_ready, c);
+            if (!ok) break;
+            tc_fence_after();
+            if (!LOCAL && lane == 0) {
+                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + k * 8,
+                                  sw128_desc(qk + (k / 4) * S::kQkPanel + (k % 4) * 32, 16, 1024), id, part + k > 0);
+                }
+            }
+            __syncwarp();
+            ok = wait(v_ready, c);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                    for (int k = 0; k < LC / 16; ++k)
+                        tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8,
+                                  sw128_desc(qk + kChunkPanel + k * 16 * 128, S::kQkPanel, 1024), id, part + k > 0);
+                }
+                tc_commit(kv_ready);
+                if (LOCAL) {
+                    tc_commit(v_free);
+                    tc_commit(&empty[s]);
+                }
+            }
+            __syncwarp();
+            if (!LOCAL) {
+                ok = wait(p_ready, c);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                        for (int k = 0; k < LC / 16; ++k)
+                            tc_mma_ts(tmem + TC_S, tmem + TC_V + k * 8,
+                                      sw128_desc(pb + part * kChunkPanel + k * 32, 16, 1024), id, part + k > 0);
+                    }
+                    tc_commit(o_ready);
+                    tc_commit(v_free);
+                    tc_commit(&empty[s]);
+                }
+                __syncwarp();
+            }
+        }
+        // nothing of this CTA's is left in the tensor core when TMEM goes back
+        if (lane == 0) {
+            tc_commit(drain);
+            mbar_wait(drain, 0u, nullptr, p.err, SRC_LINEAR);
+        }
+        __syncwarp();
+    } else {
+        // ============================================================ loads
+        if (lane == 0) {
+            if (!LOCAL) tma_prefetch_desc(&qmap);
+            tma_prefetch_desc(&kmap);
+            tma_prefetch_desc(&vmap);
+            int c = 0;
+            for (; c < chunks; ++c) {
+                const int s = c % ST;
+                if (c >= ST && !mbar_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag, p.err, SRC_LINEAR)) break;
+                uint8_t *stage = sm + s * S::kStageBytes;
+                const int row = (int)(u.t0 + (int64_t)c * LC);
+                mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
+#pragma unroll
+                for (int x = 0; x < PAN; ++x) {
+                    if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, h, row);
+                    tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
+                    tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
+                }
+            }
+            // copies still in flight (after a wait that gave up) land before the CTA ends
+            for (int d = max(0, c - ST); d < c; ++d) mbar_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, nullptr, p.err, SRC_LINEAR);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// kernel<<<grid, block, smem>>> as the programmatic dependent of the launch before it
+template <typename... K, typename... A>
+cudaError_t launch_after(void (*k)(K...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const A &...a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a...);
+}
+
+template <int D>
+cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                          const LinearParams &p, cudaStream_t stream) {
+    using S = ChunkSmem<D>;
+    static std::once_flag once[kMaxDev];
+    static cudaError_t attr_err[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        attr_err[dev] = cudaFuncSetAttribute(linear_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             S::kBytes);
+        if (attr_err[dev] == cudaSuccess)
+            attr_err[dev] = cudaFuncSetAttribute(linear_chunk_kernel<D, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    });
+    if (attr_err[dev] != cudaSuccess) return attr_err[dev];
+    linear_plan_kernel<<<1 + (p.Hkv + 7) / 8, 1024, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const bool split = p.seg_len < p.max_seqlen;
+    if (split) {
+        e = launch_after(linear_chunk_kernel<D, true>, dim3((unsigned)p.max_units * p.Hkv), kChunkThreads, S::kBytes,
+                         stream, qmap, kmap, vmap, p);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.state_rows > 0) {
+        e = launch_after(linear_scan_kernel, dim3(p.max_units, p.Hkv, D * D / 1024), 256, 0, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    main_kernel_event_before(stream);
+    e = launch_after(linear_chunk_kernel<D, false>, dim3((unsigned)p.max_units * p.Hq), kChunkThreads, S::kBytes,
+                     stream, qmap, kmap, vmap, p);
+    main_kernel_event_after(stream);
+    return e;
+}
+
 }  // namespace
 
-cudaError_t launch_linear_varlen(const LinearParams &p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    return launch_tokens(p, stream);
+cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const LinearParams &p, cudaStream_t stream) {
+    return p.D == 128 ? launch_chunks<128>(qmap, kmap, vmap, p, stream) : launch_chunks<64>(qmap, kmap, vmap, p, stream);
 }
 
-cudaError_t launch_linear_decode(const LinearParams &p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    return launch_tokens(p, stream);
-}
+cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream) { return launch_tokens(p, stream); }
 
 }  // namespace attn
