@@ -191,10 +191,11 @@ struct ChunkSmem {
     static constexpr int kPOff = kStages * kStageBytes;          // P: hi, lo
     static constexpr int kOutOff = kPOff + 2 * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
     static constexpr int kTabOff = kOutOff + 4 * LC * 64;
-    // scale e^{m g} m = 0..64 (68 floats); w of a full chunk, of the last chunk; first bad token per dv, two chunks
-    static constexpr int kTabBytes = 68 * 4 + 2 * LC * 4 + 2 * 128 * 4;
+    // scale e^{m g}: zeros for m = -64..-1, then m = 0..63; m = 1..64; w of a full chunk, of the last chunk;
+    // first non-finite token per dv, two chunks
+    static constexpr int kTabBytes = 5 * LC * 4 + 2 * 128 * 4;
     static constexpr int kBarOff = kTabOff + kTabBytes;
-    static constexpr int kNumBars = 2 * kStages + 9;
+    static constexpr int kNumBars = 2 * kStages + 12;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -214,11 +215,45 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// 16 lanes x 32 columns of 32 bits in the 8x8 matrix fragment layout: thread t holds (lane
+// t / 4, column t % 4) and (lane t / 4 + 8, same column) of each group of four columns
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// 16 lanes x 32 columns: thread t gets, of each group of eight columns, (lane t / 4, columns
+// 2 (t % 4) and + 1) and the same of lane t / 4 + 8
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// one lane of the warp, the same every time; the operands of what it issues stay warp-uniform
+// values to the compiler, which one of `lane == 0` does not give: 30 against 50 clocks per
+// tcgen05.mma issued
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// four transposed 8x8 b16 matrices to shared memory (row addresses from lanes 8 m .. 8 m + 7)
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
+}
+
 // x0, x1 -> their bf16 part (packed); x0, x1 become what is left (exact)
 __device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) {
     const uint32_t h = pack_bf16x2(x0, x1);
-    x0 -= __uint_as_float(h << 16);
-    x1 -= __uint_as_float(h & 0xFFFF0000u);
+    fma2(x0, x1, __uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u), -1.f, -1.f, x0, x1);
     return h;
 }
 
@@ -375,33 +410,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lsmem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *full = bars, *empty = bars + ST;
-    uint64_t *v_ready = bars + 2 * ST;       // V^T and (w V)^T of the chunk are in TMEM
-    uint64_t *v_free = v_ready + 1;          // PV and KV have read them
-    uint64_t *s_ready = v_ready + 2;         // QK done
-    uint64_t *p_ready = v_ready + 3;         // P in shared memory, QK's columns free
-    uint64_t *o_ready = v_ready + 4;         // QS and PV done
-    uint64_t *o_free = v_ready + 5;          // the output warps have read both
-    uint64_t *kv_ready = v_ready + 6;        // KV done (and QS has read S_0)
-    uint64_t *st_ready = v_ready + 7;        // S_0 of the next chunk in TMEM, KV's columns free
-    uint64_t *drain = v_ready + 8;           // every MMA done
+    uint64_t *w_ready = bars + 2 * ST;       // (w V)^T of the chunk is in TMEM
+    uint64_t *w_free = w_ready + 1;          // ... and KV has read it
+    uint64_t *v_ready = w_ready + 2;         // V^T is in TMEM
+    uint64_t *s_ready = w_ready + 3;         // QK done
+    uint64_t *p_ready = w_ready + 4;         // P in shared memory, QK's columns free
+    uint64_t *o_ready = w_ready + 5;         // QS and PV done (V^T read)
+    uint64_t *o_free = w_ready + 6;          // the output warps have read both
+    uint64_t *kv_ready = w_ready + 7;        // KV done
+    uint64_t *kv_free = w_ready + 8;         // the state warps have read it
+    uint64_t *qs_done = w_ready + 9;         // QS has read S_0
+    uint64_t *st_ready = w_ready + 10;       // the next S_0 is in TMEM
+    uint64_t *drain = w_ready + 11;          // every MMA done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *tab = reinterpret_cast<float *>(sm + S::kTabOff);   // scale e^{m g}
-    float *w_full = tab + 68, *w_last = w_full + LC;
-    int *bad_at = reinterpret_cast<int *>(w_last + LC);        // [2][128]
+    float *tab = reinterpret_cast<float *>(sm + S::kTabOff) + LC;   // scale e^{m g}, zeros in front
+    float *tab1 = tab + LC;                                         // scale e^{(m + 1) g}
+    float *w_full = tab1 + LC, *w_last = w_full + LC;
+    int *bad_at = reinterpret_cast<int *>(w_last + LC);             // [2][128]
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 5);         // the MMAs, the four V warps
         }
+        mbar_init(w_ready, 4);
+        mbar_init(w_free, 1);
         mbar_init(v_ready, 4);
-        mbar_init(v_free, 1);
         mbar_init(s_ready, 1);
         mbar_init(p_ready, 2);
         mbar_init(o_ready, 1);
         mbar_init(o_free, 4);
         mbar_init(kv_ready, 1);
+        mbar_init(kv_free, 8);
+        mbar_init(qs_done, 1);
         mbar_init(st_ready, 8);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -412,9 +454,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tmem_relinquish();
     }
     const float *decay = p.decay + (int64_t)hk * kDecayRow;
-    for (int i = threadIdx.x; i <= LC; i += kChunkThreads) tab[i] = p.scale * decay[i];
     if (threadIdx.x < LC) {
         const int j = threadIdx.x;
+        tab[j - LC] = 0.f;
+        tab[j] = p.scale * decay[j];
+        tab1[j] = p.scale * decay[j + 1];
         w_full[j] = decay[LC - 1 - j];
         w_last[j] = j < n_last ? decay[n_last - 1 - j] : 0.f;
     }
@@ -428,17 +472,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
 
     if (warp < 4) {
-        // ============================================================ V preparation: thread = value dimension
-        const int dv = warp * 32 + lane;
-        const bool real = dv < D;
+        // ============================================================ V preparation: a warp per 32 value dimensions
+        // In 8x8 fragments: ldmatrix transposes 8 tokens x 8 dv, a thread then holds two neighbouring tokens of
+        // one dv, which is a 32-bit column of the A operand.
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const int q2 = (lane & 3) * 2;           // its tokens: 8 g + q2, + 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c % ST, n = c + 1 < chunks ? LC : n_last;
-            const float *w = c + 1 < chunks ? w_full : w_last;
+            const float *w = (c + 1 < chunks ? w_full : w_last) + q2;
             uint8_t *stage = sm + s * S::kStageBytes;
             if (!wait(&full[s], c / ST)) break;
-            const uint8_t *v = stage + S::kVOff + ((dv & (D - 1)) >> 6) * kChunkPanel;
-            const uint32_t col = (uint32_t)(dv & 7) * 2, ch = (uint32_t)(dv & 63) >> 3;
             if (n < LC) {
                 // rows behind the sequence's end: K's are zeroed (a weight of 0 would not
                 // cancel a NaN there), V's are left out below
@@ -449,59 +492,106 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 fence_proxy_async_smem();
             }
-            int bad = LC;
-            bool waited = true;
+            // r[2 g + x] of part (hl, 4 groups): dv 16 hl + 8 x + lane / 4, tokens 8 g + q2, + 1
+            auto load = [&](int part, uint32_t (&r)[8]) {
+                // head_dim 64: warps 2 and 3 repeat 0 and 1 (lanes 64..127 reach no output)
+                const int d8 = ((warp * 32) & (D - 1)) / 8 + (part & 2) + ((lane >> 3) & 1);
+                const uint32_t panel = smem_u32(stage + S::kVOff) + (d8 >> 3) * kChunkPanel;
+                const uint32_t row = ((part & 1) * 4 + (lane >> 4)) * 8 + (lane & 7);
+                ldsm_x4_t(panel + sw128_off(row, d8 & 7), r[0], r[1], r[2], r[3]);
+                ldsm_x4_t(panel + sw128_off(row + 16, d8 & 7), r[4], r[5], r[6], r[7]);
+                if (n < LC) {
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = ((part & 1) * 4 + (i >> 1)) * 8 + q2;
+                        r[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+                    }
+                }
+            };
+            bool waited = true;
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
                 uint32_t raw[8], hi[8], mid[8], lo[8];
-                uint32_t big = 0;
+                load(part, raw);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int j = part * 16 + 2 * i;
-                    uint32_t a = *reinterpret_cast<const uint16_t *>(v + j * 128 + ((ch ^ (j & 7)) << 4) + col);
-                    uint32_t b = *reinterpret_cast<const uint16_t *>(v + (j + 1) * 128 + ((ch ^ ((j + 1) & 7)) << 4) + col);
-                    if (n < LC) {
-                        a = j < n ? a : 0u;
-                        b = j + 1 < n ? b : 0u;
-                    }
-                    raw[i] = a | (b << 16);
-                    big = __vmaxu2(big, raw[i] & 0x7FFF7FFFu);
-                    const float2 wj = *reinterpret_cast<const float2 *>(w + j);
-                    float x0 = __uint_as_float(a << 16) * wj.x, x1 = __uint_as_float(b << 16) * wj.y;
+                    const float2 wj = *reinterpret_cast<const float2 *>(w + ((part & 1) * 4 + i / 2) * 8);
+                    float x0, x1;
+                    fma2(x0, x1, __uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xFFFF0000u), wj.x, wj.y, 0.f,
+                         0.f);
                     hi[i] = take_bf16(x0, x1);
                     mid[i] = take_bf16(x0, x1);
                     lo[i] = pack_bf16x2(x0, x1);
                 }
-                if (!LOCAL && ((big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u)) {
-                    // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
-                    // left out there and the output warps write NaN from its token on
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if ((raw[i] & 0x7F80u) == 0x7F80u) {
-                            bad = min(bad, part * 16 + 2 * i);
-                            raw[i] &= 0xFFFF0000u;
-                        }
-                        if ((raw[i] & 0x7F800000u) == 0x7F800000u) {
-                            bad = min(bad, part * 16 + 2 * i + 1);
-                            raw[i] &= 0xFFFFu;
-                        }
-                    }
+                if (part == 0 && c > 0) {
+                    waited = wait(w_free, c - 1);
+                    tc_fence_after();
                 }
-                if (part == 0 && c > 0) waited = wait(v_free, c - 1);
                 if (!waited) break;
-                if (!LOCAL) tmem_st8(lane_base + TC_V + part * 8, raw);
-                tmem_st8(lane_base + TC_W + part * 8, hi);
-                tmem_st8(lane_base + TC_W + 32 + part * 8, mid);
-                tmem_st8(lane_base + TC_W + 64 + part * 8, lo);
+                const uint32_t at = lane_base + ((uint32_t)(part >> 1) << 20) + TC_W + (part & 1) * 16;
+                tmem_st_16x128b_x4(at, hi);
+                tmem_st_16x128b_x4(at + 32, mid);
+                tmem_st_16x128b_x4(at + 64, lo);
             }
             if (!waited) break;
-            if (!LOCAL && real) bad_at[(c & 1) * 128 + dv] = bad;
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(v_ready);
-                mbar_arrive(&empty[s]);
+                mbar_arrive(w_ready);
+                if (LOCAL) mbar_arrive(&empty[s]);
+            }
+            if (!LOCAL) {
+                if (c > 0 && !wait(o_ready, c - 1)) break;
+                tc_fence_after();
+                int bad0 = LC, bad1 = LC;
+#pragma unroll 1
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t raw[8], big = 0;
+                    load(part, raw);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) big = __vmaxu2(big, raw[i] & 0x7FFF7FFFu);
+                    if (__any_sync(0xffffffffu, (big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u)) {
+                        // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
+                        // left out there and the output warps write NaN from its token on
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = ((part & 1) * 4 + (i >> 1)) * 8 + q2;
+                            int first = LC;
+                            if ((raw[i] & 0x7F800000u) == 0x7F800000u) {
+                                first = j + 1;
+                                raw[i] &= 0xFFFFu;
+                            }
+                            if ((raw[i] & 0x7F80u) == 0x7F80u) {
+                                first = j;
+                                raw[i] &= 0xFFFF0000u;
+                            }
+                            if (i & 1) bad1 = min(bad1, first);
+                            else bad0 = min(bad0, first);
+                        }
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            bad0 = min(bad0, __shfl_xor_sync(0xffffffffu, bad0, o));
+                            bad1 = min(bad1, __shfl_xor_sync(0xffffffffu, bad1, o));
+                        }
+                    }
+                    tmem_st_16x128b_x4(lane_base + ((uint32_t)(part >> 1) << 20) + TC_V + (part & 1) * 16, raw);
+                    if (part & 1) {
+                        if ((lane & 3) == 0) {
+                            int *at = bad_at + (c & 1) * 128 + warp * 32 + (part & 2) * 8 + (lane >> 2);
+                            at[0] = bad0;
+                            at[8] = bad1;
+                        }
+                        bad0 = bad1 = LC;
+                    }
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(v_ready);
+                    mbar_arrive(&empty[s]);
+                }
             }
         }
     } else if (warp < 12) {
@@ -541,19 +631,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tmem_st8(lane_base + TC_STATE + 64 + (half * N + i) / 2, lo);
             }
             tc_wait_st();
+            tc_fence_before();
         };
-        if (!LOCAL && real) publish();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(st_ready);
+        if (!LOCAL) {
+            if (real) publish();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(st_ready);
+        }
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             const int n = c + 1 < chunks ? LC : n_last;
             const float a = decay[n], a_lo = decay[LC + 1 + n];
-            if (!wait(kv_ready, c)) {
-                ok = false;
-                break;
-            }
+            if (!(ok = wait(kv_ready, c))) break;
             tc_fence_after();
             if (real) {
 #pragma unroll
@@ -562,14 +651,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     tmem_ld16(lane_base + TC_KV + half * N + i, kv);
                     tc_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        St[i + k] = fmaf(a, St[i + k], fmaf(a_lo, St[i + k], __uint_as_float(kv[k])));
+                    for (int k = 0; k < 16; k += 2) {
+                        float x0, x1;
+                        fma2(x0, x1, a_lo, a_lo, St[i + k], St[i + k + 1], __uint_as_float(kv[k]),
+                             __uint_as_float(kv[k + 1]));
+                        fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
+                    }
                 }
-                if (!LOCAL && c + 1 < chunks) publish();
+                tc_fence_before();
             }
-            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(st_ready);
+            if (lane == 0) mbar_arrive(kv_free);
+            if (!LOCAL && c + 1 < chunks) {
+                if (!(ok = wait(qs_done, c))) break;
+                tc_fence_after();
+                if (real) publish();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(st_ready);
+            }
         }
         float *dst = nullptr;
         if (LOCAL) dst = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
@@ -581,9 +680,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
         }
     } else if (warp < 16) {
-        // ============================================================ output rows: thread = value dimension
+        // ============================================================ output rows: a warp per 32 value dimensions
+        // In 8x8 fragments (thread: two neighbouring tokens of one dv), transposed by stmatrix into the warp's
+        // own [64 tokens][32 dv] tile, 16-byte chunks swizzled by token pair.
         if (!LOCAL) {
-            const int grp = warp & 3, dv = grp * 32 + lane;
+            const int grp = warp & 3, q2 = (lane & 3) * 2;
             const bool real = grp * 32 < D;
             const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
             uint8_t *stg = sm + S::kOutOff + grp * LC * 64;
@@ -591,43 +692,58 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const int n = c + 1 < chunks ? LC : n_last;
                 if (!wait(o_ready, c)) break;
                 tc_fence_after();
-                if (real) {
-                    const int bad = bad_at[(c & 1) * 128 + dv];
-#pragma unroll
-                    for (int part = 0; part < 4; ++part) {
-                        uint32_t x[16], y[16];
-                        tmem_ld16(lane_base + TC_S + part * 16, x);
-                        tmem_ld16(lane_base + TC_INTER + part * 16, y);
-                        tc_wait_ld();
-                        if (part == 3) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(o_free);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const int t = part * 16 + i;
-                            float o0 = fmaf(tab[t + 1], __uint_as_float(y[i]), __uint_as_float(x[i]));
-                            float o1 = fmaf(tab[t + 2], __uint_as_float(y[i + 1]), __uint_as_float(x[i + 1]));
-                            if (t >= bad) o0 = __int_as_float(0x7fc00000);
-                            if (t + 1 >= bad) o1 = __int_as_float(0x7fc00000);
-                            const uint32_t r = pack_bf16x2(o0, o1);
-                            *reinterpret_cast<uint16_t *>(stg + t * 64 + lane * 2) = (uint16_t)r;
-                            *reinterpret_cast<uint16_t *>(stg + (t + 1) * 64 + lane * 2) = (uint16_t)(r >> 16);
-                        }
-                    }
-                    __syncwarp();
-                    __nv_bfloat16 *out = p.out + (u.t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
-#pragma unroll
-                    for (int i = 0; i < LC / 8; ++i) {
-                        const int t = i * 8 + (lane >> 2);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * 64 + (lane & 3) * 16);
-                        if (t < n) *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) = v;
-                    }
-                    __syncwarp();
-                } else {
+                if (!real) {
                     if (lane == 0) mbar_arrive(o_free);
+                    continue;
                 }
+                const int *bad_row = bad_at + (c & 1) * 128 + grp * 32;
+                const bool any_bad = __any_sync(0xffffffffu, bad_row[lane] < LC);
+#pragma unroll 1
+                for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
+                    const int hl = part >> 1, g0 = (part & 1) * 4;
+                    const uint32_t at = lane_base + ((uint32_t)hl << 20) + (part & 1) * 32;
+                    uint32_t x[16], y[16], r[8];
+                    tmem_ld_16x256b_x4(at + TC_S, x);
+                    tmem_ld_16x256b_x4(at + TC_INTER, y);
+                    int bad[2] = {LC, LC};
+                    if (any_bad) {
+                        bad[0] = bad_row[hl * 16 + (lane >> 2)];
+                        bad[1] = bad_row[hl * 16 + 8 + (lane >> 2)];
+                    }
+                    tc_wait_ld();
+                    if (part == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_free);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {           // group g0 + i / 2, dv + 8 (i % 2)
+                        const float2 e = *reinterpret_cast<const float2 *>(tab1 + (g0 + i / 2) * 8 + q2);
+                        float o0, o1;
+                        fma2(o0, o1, e.x, e.y, __uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]),
+                             __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                        if (any_bad) {
+                            const int t = (g0 + i / 2) * 8 + q2;
+                            if (t >= bad[i & 1]) o0 = __int_as_float(0x7fc00000);
+                            if (t + 1 >= bad[i & 1]) o1 = __int_as_float(0x7fc00000);
+                        }
+                        r[i] = pack_bf16x2(o0, o1);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const int t = (g0 + i / 2 + (lane >> 4)) * 8 + (lane & 7), ch = hl * 2 + ((lane >> 3) & 1);
+                        stsm_x4_t(smem_u32(stg) + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4), r[i], r[i + 1], r[i + 2], r[i + 3]);
+                    }
+                }
+                __syncwarp();
+                __nv_bfloat16 *out = p.out + (u.t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
+#pragma unroll 4
+                for (int i = 0; i < LC / 8; ++i) {
+                    const int t = i * 8 + (lane >> 2);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                    if (t < n) *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) = v;
+                }
+                __syncwarp();
             }
         }
     } else if (warp < 18) {
@@ -647,23 +763,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int c = 0; c < chunks; ++c) {
                 if (!wait(s_ready, c)) break;
                 tc_fence_after();
-                for (int part = 0; part <= half; ++part) {
-                    uint32_t s[32];
-                    tmem_ld32(lane_base + TC_S + part * 32, s);
+#pragma unroll 1
+                for (int part = 0; part < 2 + 2 * half; ++part) {      // 16 keys
+                    uint32_t s[16];
+                    tmem_ld16(lane_base + TC_S + part * 16, s);
+                    const float *e = tab + i - part * 16;
                     tc_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = part * 32 + k * 8 + e * 2;
-                            float x0 = j <= i ? __uint_as_float(s[k * 8 + e * 2]) * tab[max(i - j, 0)] : 0.f;
-                            float x1 = j + 1 <= i ? __uint_as_float(s[k * 8 + e * 2 + 1]) * tab[max(i - j - 1, 0)] : 0.f;
-                            hi[e] = take_bf16(x0, x1);
-                            lo[e] = pack_bf16x2(x0, x1);
+                        for (int x = 0; x < 4; ++x) {
+                            const int j = k * 8 + x * 2;
+                            float x0 = __uint_as_float(s[j]) * e[-j];
+                            float x1 = __uint_as_float(s[j + 1]) * e[-j - 1];
+                            // masked by choice, not by the table's zeros, which would keep a NaN
+                            x0 = part * 16 + j <= i ? x0 : 0.f;
+                            x1 = part * 16 + j + 1 <= i ? x1 : 0.f;
+                            hi[x] = take_bf16(x0, x1);
+                            lo[x] = pack_bf16x2(x0, x1);
                         }
-                        *reinterpret_cast<uint4 *>(ph + sw128_off(i, part * 4 + k)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(pl + sw128_off(i, part * 4 + k)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        const uint32_t at = sw128_off(i, part * 2 + k);
+                        *reinterpret_cast<uint4 *>(ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(pl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -674,22 +796,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else if (warp == 18) {
         // ============================================================ MMA
+        // KV first: it runs while the output warps read the chunk before.
         bool ok = true;
         for (int c = 0; c < chunks && ok; ++c) {
             const int s = c % ST;
             const uint32_t qk = smem_u32(sm + s * S::kStageBytes), pb = smem_u32(sm + S::kPOff);
-            ok = wait(&full[s], c / ST);
-            if (ok && !LOCAL && c > 0) ok = wait(o_free, c - 1);
+            ok = wait(w_ready, c) && (c == 0 || wait(kv_free, c - 1)) && wait(&full[s], c / ST);
             if (!ok) break;
             tc_fence_after();
-            if (!LOCAL && lane == 0) {
+            if (elect_one()) {
+                constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
+                const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                    for (int k = 0; k < LC / 16; ++k)
+                        tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8, kd + k * (16 * 128 >> 4), id, part + k > 0);
+                }
+                tc_commit(kv_ready);
+                tc_commit(w_free);
+                if (LOCAL) tc_commit(&empty[s]);
+            }
+            __syncwarp();
+            if (LOCAL) continue;
+            ok = c == 0 || wait(o_free, c - 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
                 // rows 64..127 of A are K's: a product nobody reads, in exchange for M = 128
                 constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+                const uint64_t qd = sw128_desc(qk, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * S::kQkPanel + (k % 4) * 32;
-                    tc_mma_ss(tmem + TC_S, sw128_desc(qk + off, 16, 1024), sw128_desc(qk + kChunkPanel + off, 16, 1024),
-                              id, k > 0);
+                for (int pan = 0; pan < PAN; ++pan) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
+                        tc_mma_ss(tmem + TC_S, d, d + (kChunkPanel >> 4), id, pan + k > 0);
+                    }
                 }
                 tc_commit(s_ready);
             }
@@ -697,55 +840,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             ok = wait(st_ready, c);
             if (!ok) break;
             tc_fence_after();
-            if (!LOCAL && lane == 0) {
+            if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+                const uint64_t qd = sw128_desc(qk, 16, 1024);
+#pragma unroll
+                for (int x = 0; x < 2 * PAN; ++x) {      // part, panel
+                    const int pan = x & (PAN - 1), part = x / PAN;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + (pan * 4 + k) * 8,
+                                  qd + pan * (S::kQkPanel >> 4) + k * 2, id, x + k > 0);
+                }
+                tc_commit(qs_done);
+                tc_commit(&empty[s]);
+            }
+            __syncwarp();
+            ok = wait(p_ready, c) && wait(v_ready, c);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+                const uint64_t pd = sw128_desc(pb, 16, 1024);
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + k * 8,
-                                  sw128_desc(qk + (k / 4) * S::kQkPanel + (k % 4) * 32, 16, 1024), id, part + k > 0);
-                }
-            }
-            __syncwarp();
-            ok = wait(v_ready, c);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-                constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-#pragma unroll
                     for (int k = 0; k < LC / 16; ++k)
-                        tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8,
-                                  sw128_desc(qk + kChunkPanel + k * 16 * 128, S::kQkPanel, 1024), id, part + k > 0);
+                        tc_mma_ts(tmem + TC_S, tmem + TC_V + k * 8, pd + part * (kChunkPanel >> 4) + k * 2, id, part + k > 0);
                 }
-                tc_commit(kv_ready);
-                if (LOCAL) {
-                    tc_commit(v_free);
-                    tc_commit(&empty[s]);
-                }
+                tc_commit(o_ready);
             }
             __syncwarp();
-            if (!LOCAL) {
-                ok = wait(p_ready, c);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                        for (int k = 0; k < LC / 16; ++k)
-                            tc_mma_ts(tmem + TC_S, tmem + TC_V + k * 8,
-                                      sw128_desc(pb + part * kChunkPanel + k * 32, 16, 1024), id, part + k > 0);
-                    }
-                    tc_commit(o_ready);
-                    tc_commit(v_free);
-                    tc_commit(&empty[s]);
-                }
-                __syncwarp();
-            }
         }
         // nothing of this CTA's is left in the tensor core when TMEM goes back
         if (lane == 0) {

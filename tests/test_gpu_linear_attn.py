@@ -266,3 +266,50 @@ def test_no_tokens_leaves_the_states():
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
     out = av.linear_attn_varlen_fwd(q, q, q, _decay(2).cuda(), i32(0, 0, 0), 0, state_cache=sd, state_slots=i32(0, 1))
     assert out.shape == q.shape and sd.eq(1).all() and av.get_last_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([2500, 70], 2, 1, 64), ([3000], 2, 2, 128), ([1, 1900, 0, 2300], 3, 3, 64)])
+@pytest.mark.parametrize("cached", [False, True])
+def test_long_sequences_cut_into_segments(lens, Hq, Hkv, D, cached):
+    """Few heads and long sequences: segments side by side, from states that a first
+    pass over k and v prepares."""
+    B, T = len(lens), sum(lens)
+    (q, k, v), dev, gen = _inputs(T, T, Hq, Hkv, D)
+    g, cu = torch.tensor([-0.002, -0.2, 0.0])[:Hkv], cu_of(lens)
+    state = torch.randn(B, Hkv, D, D, generator=gen)
+    ctx = torch.ones(B, dtype=torch.int32) if cached else torch.zeros(B, dtype=torch.int32)
+    sd = state.cuda()
+    av.get_last_device_error()
+    out = av.linear_attn_varlen_fwd(*dev, g.cuda(), cu.cuda(), max(lens), 0.1, state_cache=sd,
+                                    state_slots=torch.arange(B, dtype=torch.int32, device="cuda"),
+                                    context_lens=ctx.cuda())
+    torch.cuda.synchronize()
+    assert av.get_last_device_error()[0] == 0
+    ref, finals, weight = linear(q, k, v, g, cu, 0.1, [state[b].double() if cached else None for b in range(B)])
+    _check(out, ref, weight, "out")
+    for b in range(B):
+        if lens[b]:
+            _check_state(sd[b], *finals[b], f"state {b}", lens[b])
+
+
+@pytest.mark.parametrize("D,bad", [(64, float("nan")), (128, float("inf")), (128, float("nan"))])
+def test_a_non_finite_value_reaches_its_own_token_and_later_ones_only(D, bad):
+    """One entry of v, k or q: other value dimensions, heads and the earlier tokens,
+    those of the same chunk among them, are what they are without it."""
+    T, H, t, d = 200, 2, 101, 37
+    _, dev, _ = _inputs(77, T, H, H, D, strided=False)
+    g, cu = _decay(H).cuda(), cu_of([T]).cuda()
+    clean = av.linear_attn_varlen_fwd(*dev, g, cu, T)
+    for which in range(3):
+        x = [y.clone() for y in dev]
+        x[which][t, 1, d] = bad
+        out = av.linear_attn_varlen_fwd(*x, g, cu, T)
+        assert torch.equal(out[:t], clean[:t]) and torch.equal(out[:, 0], clean[:, 0])
+        if which == 2:      # v: one value dimension, from its token on
+            others = [i for i in range(D) if i != d]
+            assert torch.equal(out[:, 1][:, others], clean[:, 1][:, others])
+            assert not out[t:, 1, d].isfinite().any()
+        elif which == 1:    # k: the whole head from its token on
+            assert not out[t:, 1].isfinite().any()
+        else:               # q: its own token
+            assert not out[t, 1].isfinite().any() and torch.equal(out[t + 1:], clean[t + 1:])
