@@ -169,14 +169,15 @@ cudaError_t launch_tokens(const LinearParams &p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 
 constexpr int LC = 64;                       // tokens of a chunk
-constexpr int kChunkThreads = 640;
+constexpr int kChunkThreads = 768;
 constexpr int kChunkPanel = LC * 128;        // 64 rows x 128 bytes
-constexpr uint32_t TC_S = 0;                 // TMEM columns: QK, then PV (the P warps have read QK by then)
-constexpr uint32_t TC_INTER = 64;            // QS
-constexpr uint32_t TC_KV = 128;              // KV
-constexpr uint32_t TC_STATE = 256;           // S_0: hi 64 columns, lo 64 (D / 2 used of each)
-constexpr uint32_t TC_V = 384;               // V^T
-constexpr uint32_t TC_W = 416;               // (w V)^T, three parts of 32
+constexpr uint32_t TC_S = 0;                 // TMEM columns: QK
+constexpr uint32_t TC_INTRA = 64;            // PV
+constexpr uint32_t TC_INTER = 128;           // QS
+constexpr uint32_t TC_KV = 192;              // KV
+constexpr uint32_t TC_STATE = 320;           // S_0: hi, lo (D / 2 of 64 columns each)
+constexpr uint32_t TC_W = 448;               // (w V)^T: hi, mid (32 columns each)
+constexpr uint32_t kAMnMajor = 1u << 15;     // instruction descriptor: A along M in its 128-byte rows
 constexpr int kDecayRow = kLinearDecayRow;   // floats of a head's decay table: e^{m g} for m = 0..64, the part
                                              // below fp32 of each, then e^{seg_len g} in two parts
 constexpr int kBuckets = 256;
@@ -188,14 +189,15 @@ struct ChunkSmem {
     static constexpr int kVOff = kPanels * kQkPanel;
     static constexpr int kStageBytes = kVOff + kPanels * kChunkPanel;
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kPOff = kStages * kStageBytes;          // P: hi, lo
-    static constexpr int kOutOff = kPOff + 2 * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
+    static constexpr int kPOff = kStages * kStageBytes;          // two chunks' P: hi, lo
+    static constexpr int kLoOff = kPOff + 4 * kChunkPanel;       // the third part of w V, laid out like V
+    static constexpr int kOutOff = kLoOff + kPanels * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
     static constexpr int kTabOff = kOutOff + 4 * LC * 64;
     // scale e^{m g}: zeros for m = -64..-1, then m = 0..63; m = 1..64; w of a full chunk, of the last chunk;
-    // first non-finite token per dv, two chunks
-    static constexpr int kTabBytes = 5 * LC * 4 + 2 * 128 * 4;
+    // first non-finite token per dv, four chunks
+    static constexpr int kTabBytes = 5 * LC * 4 + 4 * 128 * 4;
     static constexpr int kBarOff = kTabOff + kTabBytes;
-    static constexpr int kNumBars = 2 * kStages + 12;
+    static constexpr int kNumBars = 3 * kStages + 11;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -215,11 +217,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// A tcgen05.ld or .st takes about 40 clocks of its warp whatever its width: wide shapes.
 // 16 lanes x 32 columns of 32 bits in the 8x8 matrix fragment layout: thread t holds (lane
 // t / 4, column t % 4) and (lane t / 4 + 8, same column) of each group of four columns
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
 
@@ -232,6 +237,18 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+// Registers of the calling warpgroup.  The kernel is launched with 80 a thread; the six
+// warpgroups' shares add up to that: V 2 x 80, state 2 x kStateRegs, output rows
+// kOutRegs, the others kRestRegs.
+constexpr int kStateRegs = 96, kOutRegs = 72, kRestRegs = 56;
+static_assert(2 * 80 + 2 * kStateRegs + kOutRegs + kRestRegs == 6 * 80, "register shares");
+template <int N> __device__ __forceinline__ void more_regs() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_regs() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // one lane of the warp, the same every time; the operands of what it issues stay warp-uniform
@@ -255,6 +272,25 @@ __device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) {
     const uint32_t h = pack_bf16x2(x0, x1);
     fma2(x0, x1, __uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u), -1.f, -1.f, x0, x1);
     return h;
+}
+
+// mbar_wait without its out-of-line part: with a call in the kernel the warpgroups cannot be
+// given register shares of their own.
+__device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *err) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if (it & 63u) continue;
+        if (abort && *abort) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            record_error(err, ERR_TIMEOUT | SRC_LINEAR);
+            if (abort) *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // Tokens of unit `u` and the segment's place in its sequence.
@@ -281,18 +317,25 @@ __device__ __forceinline__ ChunkUnit chunk_unit(const LinearParams &p, const int
 // one; units with the most chunks come first (the hardware starts CTAs in order,
 // so the long ones do not end up alone at the end).  Entry: (sequence, segment,
 // state rows in the workspace or -1, segments).  CTA 0 writes the list, the others
-// the heads' decay tables (in 64 bits: 132 exponentials per head and call).
+// the heads' decay tables.
 __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x;
     if (blockIdx.x > 0) {
         const int h = (blockIdx.x - 1) * 8 + (tid >> 7), m = tid & 127;
         if (h >= p.Hkv || m > LC + 1) return;
-        const double g = (double)linear_log_decay(p, h, m == 0);
+        const float x = linear_log_decay(p, h, m == 0) * (float)(m <= LC ? m : p.seg_len);
+        // near 1, where a state is multiplied many times before it fades, as two parts that are
+        // right to 2^-23 of x; elsewhere the fp32 value. Not 0 * -inf.
+        float hi = 1.f, lo = 0.f;
+        if (m > 0 && x < -0.3f) {
+            hi = expf(x);
+        } else if (m > 0) {
+            const float y = expm1f(x);
+            hi = 1.f + y;
+            lo = y - (hi - 1.f);
+        }
         float *row = p.decay + (int64_t)h * kDecayRow;
-        const int steps = m <= LC ? m : p.seg_len;
-        const double x = steps == 0 ? 1.0 : exp(g * steps);
-        const float hi = (float)x, lo = (float)(x - (double)hi);
         if (m <= LC) {
             row[m] = hi;
             row[LC + 1 + m] = lo;
@@ -374,14 +417,23 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearParams p) 
     if (x >= D2) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (from) run = *reinterpret_cast<const float4 *>(state + x);
-    for (int s = 0; s < e.w; ++s) {
-        float4 *at = reinterpret_cast<float4 *>(p.states + ((int64_t)(e.z + s) * p.Hkv + h) * D2 + x);
-        const float4 own = s + 1 < e.w ? *at : run;
-        *at = run;
-        run.x = fmaf(hi, run.x, fmaf(lo, run.x, own.x));
-        run.y = fmaf(hi, run.y, fmaf(lo, run.y, own.y));
-        run.z = fmaf(hi, run.z, fmaf(lo, run.z, own.z));
-        run.w = fmaf(hi, run.w, fmaf(lo, run.w, own.w));
+    float *at = p.states + ((int64_t)e.z * p.Hkv + h) * D2 + x;
+    const int64_t step = (int64_t)p.Hkv * D2;
+    constexpr int kAhead = 8;   // loads in flight per thread: the sums are read before starts replace them
+    for (int s0 = 0; s0 < e.w; s0 += kAhead) {
+        float4 own[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s0 + k + 1 < e.w) own[k] = *reinterpret_cast<const float4 *>(at + (s0 + k) * step);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s0 + k >= e.w) break;
+            *reinterpret_cast<float4 *>(at + (s0 + k) * step) = run;
+            run.x = fmaf(hi, run.x, fmaf(lo, run.x, own[k].x));
+            run.y = fmaf(hi, run.y, fmaf(lo, run.y, own[k].y));
+            run.z = fmaf(hi, run.z, fmaf(lo, run.z, own[k].z));
+            run.w = fmaf(hi, run.w, fmaf(lo, run.w, own[k].w));
+        }
     }
 }
 
@@ -410,42 +462,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lsmem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *full = bars, *empty = bars + ST;
-    uint64_t *w_ready = bars + 2 * ST;       // (w V)^T of the chunk is in TMEM
+    uint64_t *v_ready = bars + 2 * ST;       // [ST]: the stage's V may be read by PV (tail rows and non-finite
+                                             //   entries are zeroed); per stage, as PV may lag behind KV
+    uint64_t *w_ready = bars + 3 * ST;       // (w V)^T of the chunk is in TMEM
     uint64_t *w_free = w_ready + 1;          // ... and KV has read it
-    uint64_t *v_ready = w_ready + 2;         // V^T is in TMEM
-    uint64_t *s_ready = w_ready + 3;         // QK done
-    uint64_t *p_ready = w_ready + 4;         // P in shared memory, QK's columns free
-    uint64_t *o_ready = w_ready + 5;         // QS and PV done (V^T read)
-    uint64_t *o_free = w_ready + 6;          // the output warps have read both
-    uint64_t *kv_ready = w_ready + 7;        // KV done
-    uint64_t *kv_free = w_ready + 8;         // the state warps have read it
-    uint64_t *qs_done = w_ready + 9;         // QS has read S_0
-    uint64_t *st_ready = w_ready + 10;       // the next S_0 is in TMEM
-    uint64_t *drain = w_ready + 11;          // every MMA done
+    uint64_t *s_ready = w_ready + 2;         // QK done
+    uint64_t *p_ready = w_ready + 3;         // P in shared memory, QK's columns free
+    uint64_t *o_ready = w_ready + 4;         // QS and PV done
+    uint64_t *o_free = w_ready + 5;          // the output warps have read both
+    uint64_t *qs_done = w_ready + 6;         // QS has read S_0
+    uint64_t *st_ready = w_ready + 7;        // the next S_0 is in TMEM
+    uint64_t *kv_ready = w_ready + 8;        // KV done
+    uint64_t *kv_free = w_ready + 9;         // the state warps have read it
+    uint64_t *drain = w_ready + 10;          // every MMA done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *tab = reinterpret_cast<float *>(sm + S::kTabOff) + LC;   // scale e^{m g}, zeros in front
     float *tab1 = tab + LC;                                         // scale e^{(m + 1) g}
     float *w_full = tab1 + LC, *w_last = w_full + LC;
-    int *bad_at = reinterpret_cast<int *>(w_last + LC);             // [2][128]
+    int *bad_at = reinterpret_cast<int *>(w_last + LC);             // [4][128]
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 5);         // the MMAs, the four V warps
+            mbar_init(&v_ready[i], 8);
+            mbar_init(&empty[i], LOCAL ? 9 : 10);   // each MMA thread, the eight V warps
         }
-        mbar_init(w_ready, 4);
+        mbar_init(w_ready, 8);
         mbar_init(w_free, 1);
-        mbar_init(v_ready, 4);
         mbar_init(s_ready, 1);
         mbar_init(p_ready, 2);
-        mbar_init(o_ready, 1);
+        mbar_init(o_ready, 2);               // QS, PV
         mbar_init(o_free, 4);
         mbar_init(kv_ready, 1);
         mbar_init(kv_free, 8);
         mbar_init(qs_done, 1);
         mbar_init(st_ready, 8);
-        mbar_init(drain, 1);
+        mbar_init(drain, 2);                 // each MMA thread
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -468,135 +521,113 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t tmem = *tmem_slot;
     // a warp's wait: every lane gets the same answer
     auto wait = [&](uint64_t *bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, p.err, SRC_LINEAR)) != 0;
+        return __all_sync(0xffffffffu, chunk_wait(bar, (uint32_t)phase & 1u, abort_flag, p.err)) != 0;
     };
 
-    if (warp < 4) {
-        // ============================================================ V preparation: a warp per 32 value dimensions
+    if (warp < 8) {
+        // ============================================================ V preparation: a warp per 16 value dimensions
         // In 8x8 fragments: ldmatrix transposes 8 tokens x 8 dv, a thread then holds two neighbouring tokens of
         // one dv, which is a 32-bit column of the A operand.
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const int grp = warp & 3, hl = warp >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(grp * 32 + hl * 16) << 16);
         const int q2 = (lane & 3) * 2;           // its tokens: 8 g + q2, + 1
+        // head_dim 64: lane groups 2 and 3 repeat 0 and 1 (lanes 64..127 reach no output)
+        const int d8 = ((grp * 32) & (D - 1)) / 8 + 2 * hl + ((lane >> 3) & 1);
+        const uint32_t frag = S::kVOff + (d8 >> 3) * kChunkPanel + sw128_off((lane >> 4) * 8 + (lane & 7), d8 & 7);
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c % ST, n = c + 1 < chunks ? LC : n_last;
             const float *w = (c + 1 < chunks ? w_full : w_last) + q2;
             uint8_t *stage = sm + s * S::kStageBytes;
             if (!wait(&full[s], c / ST)) break;
             if (n < LC) {
-                // rows behind the sequence's end: K's are zeroed (a weight of 0 would not
-                // cancel a NaN there), V's are left out below
-                for (int x = threadIdx.x; x < (LC - n) * 8 * PAN; x += 128) {
-                    const int pan = x / ((LC - n) * 8), r = x - pan * (LC - n) * 8;
-                    *reinterpret_cast<uint4 *>(stage + pan * S::kQkPanel + kChunkPanel + n * 128 + r * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
+                // rows behind the sequence's end are zeroed (a weight of 0 would not cancel a NaN there)
+                const int per = (LC - n) * 8;
+                for (int x = threadIdx.x; x < per * 2 * PAN; x += 256) {
+                    const int tile = x / per, r = x - tile * per, pan = tile >> 1;
+                    uint8_t *at = tile & 1 ? stage + S::kVOff + pan * kChunkPanel
+                                           : stage + pan * S::kQkPanel + kChunkPanel;
+                    *reinterpret_cast<uint4 *>(at + n * 128 + r * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
-            // r[2 g + x] of part (hl, 4 groups): dv 16 hl + 8 x + lane / 4, tokens 8 g + q2, + 1
-            auto load = [&](int part, uint32_t (&r)[8]) {
-                // head_dim 64: warps 2 and 3 repeat 0 and 1 (lanes 64..127 reach no output)
-                const int d8 = ((warp * 32) & (D - 1)) / 8 + (part & 2) + ((lane >> 3) & 1);
-                const uint32_t panel = smem_u32(stage + S::kVOff) + (d8 >> 3) * kChunkPanel;
-                const uint32_t row = ((part & 1) * 4 + (lane >> 4)) * 8 + (lane & 7);
-                ldsm_x4_t(panel + sw128_off(row, d8 & 7), r[0], r[1], r[2], r[3]);
-                ldsm_x4_t(panel + sw128_off(row + 16, d8 & 7), r[4], r[5], r[6], r[7]);
-                if (n < LC) {
+            // raw[2 g + x]: dv 8 x + lane / 4, tokens 8 g + q2, + 1
+            uint32_t raw[16], hi[16], mid[16], lo[16];
+            const uint32_t at = smem_u32(stage) + frag;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int j = ((part & 1) * 4 + (i >> 1)) * 8 + q2;
-                        r[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
-                    }
-                }
-            };
-            bool waited = true;
-#pragma unroll 1
-            for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
-                uint32_t raw[8], hi[8], mid[8], lo[8];
-                load(part, raw);
+            for (int g = 0; g < 8; g += 2)
+                ldsm_x4_t(at + g * 1024, raw[2 * g], raw[2 * g + 1], raw[2 * g + 2], raw[2 * g + 3]);
+            if (n < LC) {                               // (another warp may still be zeroing these rows)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 wj = *reinterpret_cast<const float2 *>(w + ((part & 1) * 4 + i / 2) * 8);
-                    float x0, x1;
-                    fma2(x0, x1, __uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xFFFF0000u), wj.x, wj.y, 0.f,
-                         0.f);
-                    hi[i] = take_bf16(x0, x1);
-                    mid[i] = take_bf16(x0, x1);
-                    lo[i] = pack_bf16x2(x0, x1);
+                for (int i = 0; i < 16; ++i) {
+                    const int j = (i >> 1) * 8 + q2;
+                    raw[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
                 }
-                if (part == 0 && c > 0) {
-                    waited = wait(w_free, c - 1);
-                    tc_fence_after();
-                }
-                if (!waited) break;
-                const uint32_t at = lane_base + ((uint32_t)(part >> 1) << 20) + TC_W + (part & 1) * 16;
-                tmem_st_16x128b_x4(at, hi);
-                tmem_st_16x128b_x4(at + 32, mid);
-                tmem_st_16x128b_x4(at + 64, lo);
             }
-            if (!waited) break;
+            float zero0 = 0.f, zero1 = 0.f;             // NaN once a non-finite v went by
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 wj = *reinterpret_cast<const float2 *>(w + (i >> 1) * 8);
+                const float v0 = __uint_as_float(raw[i] << 16), v1 = __uint_as_float(raw[i] & 0xFFFF0000u);
+                float x0, x1;
+                if (!LOCAL) fma2(zero0, zero1, v0, v1, 0.f, 0.f, zero0, zero1);
+                fma2(x0, x1, v0, v1, wj.x, wj.y, 0.f, 0.f);
+                hi[i] = take_bf16(x0, x1);
+                mid[i] = take_bf16(x0, x1);
+                lo[i] = pack_bf16x2(x0, x1);
+            }
+            if (!LOCAL) {
+                const bool any_bad = __any_sync(0xffffffffu, !(zero0 + zero1 == 0.f));
+                if (any_bad) {
+                    // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
+                    // zeroed there and the output warps write NaN from its token on
+#pragma unroll 1
+                    for (int r = 0; r < 2; ++r) {       // two rows of the fragment: dv 8 r + lane / 4
+                        const int row = grp * 32 + hl * 16 + 8 * r + (lane >> 2);
+                        int first = LC;
+                        if (row < D)
+                            for (int j = q2; j < n; j += (j & 1) ? 7 : 1) {
+                                uint16_t *v = reinterpret_cast<uint16_t *>(
+                                    stage + S::kVOff + (row >> 6) * kChunkPanel + sw128_off(j, (row & 63) >> 3) + (row & 7) * 2);
+                                if ((*v & 0x7F80u) == 0x7F80u) {
+                                    *v = 0;
+                                    first = min(first, j);
+                                }
+                            }
+                        first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+                        first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
+                        if ((lane & 3) == 0 && row < D) bad_at[(c & 3) * 128 + row] = first;
+                    }
+                    fence_proxy_async_smem();
+                } else if (lane < 16) {
+                    bad_at[(c & 3) * 128 + grp * 32 + hl * 16 + lane] = LC;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_ready[s]);
+            }
+            if (c > 0 && !wait(w_free, c - 1)) break;
+            tc_fence_after();
+            tmem_st_16x128b_x8(lane_base + TC_W, hi);
+            tmem_st_16x128b_x8(lane_base + TC_W + 32, mid);
+            if (grp * 32 < D) {
+                const uint32_t to = smem_u32(sm + S::kLoOff) + (frag - S::kVOff);
+#pragma unroll
+                for (int g = 0; g < 8; g += 2)
+                    stsm_x4_t(to + g * 1024, lo[2 * g], lo[2 * g + 1], lo[2 * g + 2], lo[2 * g + 3]);
+                fence_proxy_async_smem();
+            }
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(w_ready);
-                if (LOCAL) mbar_arrive(&empty[s]);
-            }
-            if (!LOCAL) {
-                if (c > 0 && !wait(o_ready, c - 1)) break;
-                tc_fence_after();
-                int bad0 = LC, bad1 = LC;
-#pragma unroll 1
-                for (int part = 0; part < 4; ++part) {
-                    uint32_t raw[8], big = 0;
-                    load(part, raw);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) big = __vmaxu2(big, raw[i] & 0x7FFF7FFFu);
-                    if (__any_sync(0xffffffffu, (big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u)) {
-                        // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
-                        // left out there and the output warps write NaN from its token on
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int j = ((part & 1) * 4 + (i >> 1)) * 8 + q2;
-                            int first = LC;
-                            if ((raw[i] & 0x7F800000u) == 0x7F800000u) {
-                                first = j + 1;
-                                raw[i] &= 0xFFFFu;
-                            }
-                            if ((raw[i] & 0x7F80u) == 0x7F80u) {
-                                first = j;
-                                raw[i] &= 0xFFFF0000u;
-                            }
-                            if (i & 1) bad1 = min(bad1, first);
-                            else bad0 = min(bad0, first);
-                        }
-#pragma unroll
-                        for (int o = 1; o < 4; o <<= 1) {
-                            bad0 = min(bad0, __shfl_xor_sync(0xffffffffu, bad0, o));
-                            bad1 = min(bad1, __shfl_xor_sync(0xffffffffu, bad1, o));
-                        }
-                    }
-                    tmem_st_16x128b_x4(lane_base + ((uint32_t)(part >> 1) << 20) + TC_V + (part & 1) * 16, raw);
-                    if (part & 1) {
-                        if ((lane & 3) == 0) {
-                            int *at = bad_at + (c & 1) * 128 + warp * 32 + (part & 2) * 8 + (lane >> 2);
-                            at[0] = bad0;
-                            at[8] = bad1;
-                        }
-                        bad0 = bad1 = LC;
-                    }
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(v_ready);
-                    mbar_arrive(&empty[s]);
-                }
+                mbar_arrive(&empty[s]);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
+        more_regs<kStateRegs>();
         // ============================================================ state: thread = value dimension, half of dk
-        const int grp = warp & 3, half = (warp - 4) >> 2, dv = grp * 32 + lane;
+        const int grp = warp & 3, half = (warp - 8) >> 2, dv = grp * 32 + lane;
         const bool real = grp * 32 < D;      // warp-uniform
         const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
         constexpr int N = D / 2;             // columns per thread
@@ -639,9 +670,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (lane == 0) mbar_arrive(st_ready);
         }
         bool ok = true;
+        const float a_full = decay[LC], a_full_lo = decay[2 * LC + 1];
+        const float a_last = decay[n_last], a_last_lo = decay[LC + 1 + n_last];
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int n = c + 1 < chunks ? LC : n_last;
-            const float a = decay[n], a_lo = decay[LC + 1 + n];
+            const bool full_chunk = c + 1 < chunks;
+            const float a = full_chunk ? a_full : a_last, a_lo = full_chunk ? a_full_lo : a_last_lo;
             if (!(ok = wait(kv_ready, c))) break;
             tc_fence_after();
             if (real) {
@@ -679,7 +713,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 *reinterpret_cast<float4 *>(dst + dv * D + half * N + i) =
                     make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
+        fewer_regs<kOutRegs>();
         // ============================================================ output rows: a warp per 32 value dimensions
         // In 8x8 fragments (thread: two neighbouring tokens of one dv), transposed by stmatrix into the warp's
         // own [64 tokens][32 dv] tile, 16-byte chunks swizzled by token pair.
@@ -688,6 +723,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const bool real = grp * 32 < D;
             const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
             uint8_t *stg = sm + S::kOutOff + grp * LC * 64;
+            // stmatrix row address: token (lane / 16) * 8 + lane % 8 of its group, dv chunk lane / 8 % 2
+            const int row0 = (lane >> 4) * 8 + (lane & 7), ch0 = (lane >> 3) & 1, sw = (row0 >> 1) & 3;
+            const uint32_t stg_at = smem_u32(stg) + row0 * 64;
+            float2 f[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) f[g] = *reinterpret_cast<const float2 *>(tab1 + g * 8 + q2);
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int n = c + 1 < chunks ? LC : n_last;
                 if (!wait(o_ready, c)) break;
@@ -696,20 +738,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (lane == 0) mbar_arrive(o_free);
                     continue;
                 }
-                const int *bad_row = bad_at + (c & 1) * 128 + grp * 32;
+                const int *bad_row = bad_at + (c & 3) * 128 + grp * 32;
                 const bool any_bad = __any_sync(0xffffffffu, bad_row[lane] < LC);
-#pragma unroll 1
+#pragma unroll
                 for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
                     const int hl = part >> 1, g0 = (part & 1) * 4;
-                    const uint32_t at = lane_base + ((uint32_t)hl << 20) + (part & 1) * 32;
+                    const uint32_t at = lane_base + ((uint32_t)hl << 20) + g0 * 8;
                     uint32_t x[16], y[16], r[8];
-                    tmem_ld_16x256b_x4(at + TC_S, x);
+                    tmem_ld_16x256b_x4(at + TC_INTRA, x);
                     tmem_ld_16x256b_x4(at + TC_INTER, y);
-                    int bad[2] = {LC, LC};
-                    if (any_bad) {
-                        bad[0] = bad_row[hl * 16 + (lane >> 2)];
-                        bad[1] = bad_row[hl * 16 + 8 + (lane >> 2)];
-                    }
                     tc_wait_ld();
                     if (part == 3) {
                         tc_fence_before();
@@ -717,23 +754,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         if (lane == 0) mbar_arrive(o_free);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {           // group g0 + i / 2, dv + 8 (i % 2)
-                        const float2 e = *reinterpret_cast<const float2 *>(tab1 + (g0 + i / 2) * 8 + q2);
+                    for (int i = 0; i < 8; ++i) {           // tokens 8 (g0 + i / 2) + q2, + 1; dv + 8 (i % 2)
+                        const float2 e = f[g0 + i / 2];
                         float o0, o1;
                         fma2(o0, o1, e.x, e.y, __uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]),
                              __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                        if (any_bad) {
-                            const int t = (g0 + i / 2) * 8 + q2;
-                            if (t >= bad[i & 1]) o0 = __int_as_float(0x7fc00000);
-                            if (t + 1 >= bad[i & 1]) o1 = __int_as_float(0x7fc00000);
-                        }
                         r[i] = pack_bf16x2(o0, o1);
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const int t = (g0 + i / 2 + (lane >> 4)) * 8 + (lane & 7), ch = hl * 2 + ((lane >> 3) & 1);
-                        stsm_x4_t(smem_u32(stg) + t * 64 + ((ch ^ ((t >> 1) & 3)) << 4), r[i], r[i + 1], r[i + 2], r[i + 3]);
-                    }
+                    const uint32_t to = stg_at + (uint32_t)(g0 * 512) + (((hl * 2 + ch0) ^ sw) << 4);
+                    stsm_x4_t(to, r[0], r[1], r[2], r[3]);
+                    stsm_x4_t(to + 1024, r[4], r[5], r[6], r[7]);
+                }
+                __syncwarp();
+                if (any_bad) {
+                    // NaN from a dv's first non-finite token on
+                    const int first = bad_row[lane];
+                    for (int t = first; t < LC; ++t)
+                        *reinterpret_cast<uint16_t *>(stg + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + (lane & 7) * 2) =
+                            0x7FC0;
                 }
                 __syncwarp();
                 __nv_bfloat16 *out = p.out + (u.t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
@@ -746,161 +784,231 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp < 18) {
-        // ============================================================ P: thread = query token
+    } else {
+        fewer_regs<kRestRegs>();
+    if (warp < 22) {
+        // ============================================================ loads (warp 20), P: thread = query token
+        const int half = warp - 20;
+        int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 20)
+        auto load = [&]() {                      // the next chunk's, once its stage is free
+            const int c = loaded, s = c % ST;
+            if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag, p.err)) return false;
+            uint8_t *stage = sm + s * S::kStageBytes;
+            const int row = (int)(u.t0 + (int64_t)c * LC);
+            mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
+#pragma unroll
+            for (int x = 0; x < PAN; ++x) {
+                if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, h, row);
+                tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
+                tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
+            }
+            ++loaded;
+            return true;
+        };
+        if (half == 0 && lane == 0) {
+            const int first = LOCAL ? chunks : min(chunks, ST);
+            while (loaded < first && load()) {
+            }
+        }
+        __syncwarp();
         if (!LOCAL) {
-            const int half = warp - 16, i = half * 32 + lane;
+            const int i = half * 32 + lane;
             const uint32_t lane_base = tmem + ((uint32_t)(half * 32) << 16);
-            uint8_t *ph = sm + S::kPOff, *pl = ph + kChunkPanel;
+            uint8_t *pbuf = sm + S::kPOff;
             if (half == 0) {
                 // tokens 0..31 see no key behind 31: those halves of their rows stay zero
 #pragma unroll
-                for (int k = 4; k < 8; ++k) {
-                    *reinterpret_cast<uint4 *>(ph + sw128_off(i, k)) = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(pl + sw128_off(i, k)) = make_uint4(0u, 0u, 0u, 0u);
-                }
+                for (int k = 0; k < 16; ++k)
+                    *reinterpret_cast<uint4 *>(pbuf + (k >> 2) * kChunkPanel + sw128_off(i, 4 + (k & 3))) =
+                        make_uint4(0u, 0u, 0u, 0u);
             }
+            // 8 keys of a row -> 16-byte chunk `ch` of both parts
+            auto put = [&](uint8_t *ph, int ch, float (&x)[8]) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    hi[k] = take_bf16(x[2 * k], x[2 * k + 1]);
+                    lo[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                }
+                const uint32_t at = sw128_off(i, ch);
+                *reinterpret_cast<uint4 *>(ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(ph + kChunkPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            };
             for (int c = 0; c < chunks; ++c) {
+                uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
                 if (!wait(s_ready, c)) break;
                 tc_fence_after();
+                if (half == 1) {
+                    // keys 0..31, all before these tokens: e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}
+                    const float f = tab[lane + 1];
 #pragma unroll 1
-                for (int part = 0; part < 2 + 2 * half; ++part) {      // 16 keys
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t s[16];
+                        tmem_ld16(lane_base + TC_S + part * 16, s);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + part * 16 + k * 8);
+                            const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + part * 16 + k * 8);
+                            const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                            float x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
+                                fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[k * 8 + e]),
+                                     __uint_as_float(s[k * 8 + e + 1]), 0.f, 0.f);
+                            }
+                            put(ph, part * 2 + k, x);
+                        }
+                    }
+                }
+#pragma unroll 1
+                for (int part = 2 * half; part < 2 * half + 2; ++part) {      // 16 keys around the diagonal
                     uint32_t s[16];
                     tmem_ld16(lane_base + TC_S + part * 16, s);
-                    const float *e = tab + i - part * 16;
+                    const int d = i - part * 16;
                     tc_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint32_t hi[4], lo[4];
+                        float x[8];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int j = k * 8 + x * 2;
-                            float x0 = __uint_as_float(s[j]) * e[-j];
-                            float x1 = __uint_as_float(s[j + 1]) * e[-j - 1];
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = k * 8 + e;
                             // masked by choice, not by the table's zeros, which would keep a NaN
-                            x0 = part * 16 + j <= i ? x0 : 0.f;
-                            x1 = part * 16 + j + 1 <= i ? x1 : 0.f;
-                            hi[x] = take_bf16(x0, x1);
-                            lo[x] = pack_bf16x2(x0, x1);
+                            x[e] = j <= d ? __uint_as_float(s[j]) * tab[d - j] : 0.f;
                         }
-                        const uint32_t at = sw128_off(i, part * 2 + k);
-                        *reinterpret_cast<uint4 *>(ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(pl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        put(ph, part * 2 + k, x);
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready);
+                if (lane == 0) {
+                    mbar_arrive(p_ready);
+                    // the stage of the chunk before comes free about now
+                    if (half == 0 && c > 0 && loaded < chunks) load();
+                }
+                __syncwarp();
             }
         }
-    } else if (warp == 18) {
-        // ============================================================ MMA
-        // KV first: it runs while the output warps read the chunk before.
+        // copies still in flight (after a wait that gave up) land before the CTA ends
+        if (half == 0 && lane == 0)
+            for (int d = max(0, loaded - ST); d < loaded; ++d)
+                chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, nullptr, p.err);
+        __syncwarp();
+    } else if (warp == 22) {
+        // ============================================================ MMA: KV and QS
+        // Two threads issue, so that one's waits (about 100 clocks each) fall into the other's
+        // products.  w_ready and p_ready come from threads that saw the chunk's copies land.
         bool ok = true;
-        for (int c = 0; c < chunks && ok; ++c) {
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
             const int s = c % ST;
-            const uint32_t qk = smem_u32(sm + s * S::kStageBytes), pb = smem_u32(sm + S::kPOff);
-            ok = wait(w_ready, c) && (c == 0 || wait(kv_free, c - 1)) && wait(&full[s], c / ST);
+            const uint32_t qk = smem_u32(sm + s * S::kStageBytes);
+            ok = (c == 0 || wait(kv_free, c - 1)) && wait(w_ready, c);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
                 const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
+                const uint64_t ld = sw128_desc(smem_u32(sm + S::kLoOff), PAN == 2 ? kChunkPanel : 0, 1024);
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
+                for (int part = 0; part < 2; ++part) {
 #pragma unroll
                     for (int k = 0; k < LC / 16; ++k)
                         tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8, kd + k * (16 * 128 >> 4), id, part + k > 0);
                 }
+#pragma unroll
+                for (int k = 0; k < LC / 16; ++k)
+                    tc_mma_ss(tmem + TC_KV, ld + k * (16 * 128 >> 4), kd + k * (16 * 128 >> 4), id | kAMnMajor, 1);
                 tc_commit(kv_ready);
                 tc_commit(w_free);
                 if (LOCAL) tc_commit(&empty[s]);
             }
             __syncwarp();
             if (LOCAL) continue;
-            ok = c == 0 || wait(o_free, c - 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                // rows 64..127 of A are K's: a product nobody reads, in exchange for M = 128
-                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
-                const uint64_t qd = sw128_desc(qk, 16, 1024);
-#pragma unroll
-                for (int pan = 0; pan < PAN; ++pan) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
-                        tc_mma_ss(tmem + TC_S, d, d + (kChunkPanel >> 4), id, pan + k > 0);
-                    }
-                }
-                tc_commit(s_ready);
-            }
-            __syncwarp();
-            ok = wait(st_ready, c);
+            ok = (c == 0 || wait(o_free, c - 1)) && wait(st_ready, c);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
                 const uint64_t qd = sw128_desc(qk, 16, 1024);
-#pragma unroll
-                for (int x = 0; x < 2 * PAN; ++x) {      // part, panel
-                    const int pan = x & (PAN - 1), part = x / PAN;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + (pan * 4 + k) * 8,
-                                  qd + pan * (S::kQkPanel >> 4) + k * 2, id, x + k > 0);
-                }
-                tc_commit(qs_done);
-                tc_commit(&empty[s]);
-            }
-            __syncwarp();
-            ok = wait(p_ready, c) && wait(v_ready, c);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
-                const uint64_t pd = sw128_desc(pb, 16, 1024);
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
 #pragma unroll
-                    for (int k = 0; k < LC / 16; ++k)
-                        tc_mma_ts(tmem + TC_S, tmem + TC_V + k * 8, pd + part * (kChunkPanel >> 4) + k * 2, id, part + k > 0);
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + k * 8,
+                                  qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2, id, part + k > 0);
                 }
+                tc_commit(qs_done);
                 tc_commit(o_ready);
+                tc_commit(&empty[s]);
             }
             __syncwarp();
         }
         // nothing of this CTA's is left in the tensor core when TMEM goes back
-        if (lane == 0) {
-            tc_commit(drain);
-            mbar_wait(drain, 0u, nullptr, p.err, SRC_LINEAR);
-        }
+        if (elect_one()) tc_commit(drain);
+        __syncwarp();
+        chunk_wait(drain, 0u, nullptr, p.err);
         __syncwarp();
     } else {
-        // ============================================================ loads
-        if (lane == 0) {
-            if (!LOCAL) tma_prefetch_desc(&qmap);
-            tma_prefetch_desc(&kmap);
-            tma_prefetch_desc(&vmap);
-            int c = 0;
-            for (; c < chunks; ++c) {
-                const int s = c % ST;
-                if (c >= ST && !mbar_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag, p.err, SRC_LINEAR)) break;
-                uint8_t *stage = sm + s * S::kStageBytes;
-                const int row = (int)(u.t0 + (int64_t)c * LC);
-                mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
+        // ============================================================ MMA: QK, a chunk ahead, and PV
+        if (!LOCAL) {
+            bool ok = true;
+            auto issue_qk = [&](int c) {
+                // rows 64..127 of A are K's: a product nobody reads, in exchange for M = 128
+                const uint64_t qd = sw128_desc(smem_u32(sm + (c % ST) * S::kStageBytes), 16, 1024);
+                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < PAN; ++x) {
-                    if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, h, row);
-                    tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
-                    tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
+                    for (int pan = 0; pan < PAN; ++pan) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
+                            tc_mma_ss(tmem + TC_S, d, d + (kChunkPanel >> 4), id, pan + k > 0);
+                        }
+                    }
+                    tc_commit(s_ready);
                 }
+                __syncwarp();
+            };
+            ok = wait(&full[0], 0);
+            tc_fence_after();
+            if (ok) issue_qk(0);
+#pragma unroll 1
+            for (int c = 0; c < chunks && ok; ++c) {
+                ok = (c + 1 >= chunks || wait(&full[(c + 1) % ST], (c + 1) / ST)) && wait(p_ready, c);
+                if (!ok) break;
+                tc_fence_after();
+                if (c + 1 < chunks) issue_qk(c + 1);
+                ok = (c == 0 || wait(o_free, c - 1)) && wait(&v_ready[c % ST], c / ST);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
+                    // 64..127 repeat the one panel
+                    constexpr uint32_t id = idesc_bf16_f32(128, LC, 0) | kAMnMajor;
+                    const uint64_t pd = sw128_desc(smem_u32(sm + S::kPOff + (c & 1) * 2 * kChunkPanel), 16, 1024);
+                    const uint64_t vd = sw128_desc(smem_u32(sm + (c % ST) * S::kStageBytes + S::kVOff),
+                                                   PAN == 2 ? kChunkPanel : 0, 1024);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                        for (int k = 0; k < LC / 16; ++k)
+                            tc_mma_ss(tmem + TC_INTRA, vd + k * (16 * 128 >> 4), pd + part * (kChunkPanel >> 4) + k * 2, id,
+                                      part + k > 0);
+                    }
+                    tc_commit(&empty[c % ST]);
+                    tc_commit(o_ready);
+                }
+                __syncwarp();
             }
-            // copies still in flight (after a wait that gave up) land before the CTA ends
-            for (int d = max(0, c - ST); d < c; ++d) mbar_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, nullptr, p.err, SRC_LINEAR);
         }
+        if (elect_one()) tc_commit(drain);
         __syncwarp();
+        chunk_wait(drain, 0u, nullptr, p.err);
+        __syncwarp();
+    }
     }
     tc_fence_before();
     __syncthreads();
