@@ -169,7 +169,7 @@ cudaError_t launch_tokens(const LinearParams &p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 
 constexpr int LC = 64;                       // tokens of a chunk
-constexpr int kChunkThreads = 768;
+constexpr int kChunkThreads = 1024;
 constexpr int kChunkPanel = LC * 128;        // 64 rows x 128 bytes
 constexpr uint32_t TC_S = 0;                 // TMEM columns: QK
 constexpr uint32_t TC_INTRA = 64;            // PV
@@ -211,6 +211,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -218,13 +224,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 
 // A tcgen05.ld or .st takes about 40 clocks of its warp whatever its width: wide shapes.
-// 16 lanes x 32 columns of 32 bits in the 8x8 matrix fragment layout: thread t holds (lane
+// 16 lanes x 16 columns of 32 bits in the 8x8 matrix fragment layout: thread t holds (lane
 // t / 4, column t % 4) and (lane t / 4 + 8, same column) of each group of four columns
-__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
@@ -239,11 +243,10 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
-// Registers of the calling warpgroup.  The kernel is launched with 80 a thread; the six
-// warpgroups' shares add up to that: V 2 x 80, state 2 x kStateRegs, output rows
-// kOutRegs, the others kRestRegs.
-constexpr int kStateRegs = 96, kOutRegs = 72, kRestRegs = 56;
-static_assert(2 * 80 + 2 * kStateRegs + kOutRegs + kRestRegs == 6 * 80, "register shares");
+// Registers of the calling warpgroup.  The kernel is launched with 64 a thread; the eight
+// warpgroups' shares add up to that: V 2, state 4, output rows 1, the others 1.
+constexpr int kVRegs = 56, kStateRegs = 72, kOutRegs = 64, kRestRegs = 48;
+static_assert(2 * kVRegs + 4 * kStateRegs + kOutRegs + kRestRegs == 8 * 64, "register shares");
 template <int N> __device__ __forceinline__ void more_regs() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -495,9 +498,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(o_ready, 2);               // QS, PV
         mbar_init(o_free, 4);
         mbar_init(kv_ready, 1);
-        mbar_init(kv_free, 8);
+        mbar_init(kv_free, 16);
         mbar_init(qs_done, 1);
-        mbar_init(st_ready, 8);
+        mbar_init(st_ready, 16);
         mbar_init(drain, 2);                 // each MMA thread
         *abort_flag = 0;
         fence_mbar_init();
@@ -528,6 +531,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // ============================================================ V preparation: a warp per 16 value dimensions
         // In 8x8 fragments: ldmatrix transposes 8 tokens x 8 dv, a thread then holds two neighbouring tokens of
         // one dv, which is a 32-bit column of the A operand.
+        fewer_regs<kVRegs>();
         const int grp = warp & 3, hl = warp >> 2;
         const uint32_t lane_base = tmem + ((uint32_t)(grp * 32 + hl * 16) << 16);
         const int q2 = (lane & 3) * 2;           // its tokens: 8 g + q2, + 1
@@ -551,30 +555,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 fence_proxy_async_smem();
             }
-            // raw[2 g + x]: dv 8 x + lane / 4, tokens 8 g + q2, + 1
-            uint32_t raw[16], hi[16], mid[16], lo[16];
-            const uint32_t at = smem_u32(stage) + frag;
+            // in two steps of 32 tokens; raw[2 g + x]: dv 8 x + lane / 4, tokens 32 step + 8 g + q2, + 1
+            float zero0 = 0.f, zero1 = 0.f;             // NaN once a non-finite v went by
+            bool waited = true;
+#pragma unroll 1
+            for (int step = 0; step < 2; ++step) {
+                uint32_t raw[8], hi[8], mid[8], lo[8];
+                const uint32_t at = smem_u32(stage) + frag + step * 4096;
+                ldsm_x4_t(at, raw[0], raw[1], raw[2], raw[3]);
+                ldsm_x4_t(at + 2048, raw[4], raw[5], raw[6], raw[7]);
+                if (n < LC) {                           // (another warp may still be zeroing these rows)
 #pragma unroll
-            for (int g = 0; g < 8; g += 2)
-                ldsm_x4_t(at + g * 1024, raw[2 * g], raw[2 * g + 1], raw[2 * g + 2], raw[2 * g + 3]);
-            if (n < LC) {                               // (another warp may still be zeroing these rows)
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = step * 32 + (i >> 1) * 8 + q2;
+                        raw[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+                    }
+                }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = (i >> 1) * 8 + q2;
-                    raw[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+                for (int i = 0; i < 8; ++i) {
+                    const float2 wj = *reinterpret_cast<const float2 *>(w + step * 32 + (i >> 1) * 8);
+                    const float v0 = __uint_as_float(raw[i] << 16), v1 = __uint_as_float(raw[i] & 0xFFFF0000u);
+                    float x0, x1;
+                    if (!LOCAL) fma2(zero0, zero1, v0, v1, 0.f, 0.f, zero0, zero1);
+                    fma2(x0, x1, v0, v1, wj.x, wj.y, 0.f, 0.f);
+                    hi[i] = take_bf16(x0, x1);
+                    mid[i] = take_bf16(x0, x1);
+                    lo[i] = pack_bf16x2(x0, x1);
+                }
+                if (step == 0 && c > 0) {
+                    waited = wait(w_free, c - 1);
+                    tc_fence_after();
+                }
+                if (!waited) break;
+                tmem_st_16x128b_x4(lane_base + TC_W + step * 16, hi);
+                tmem_st_16x128b_x4(lane_base + TC_W + 32 + step * 16, mid);
+                if (grp * 32 < D) {
+                    const uint32_t to = smem_u32(sm + S::kLoOff) + (frag - S::kVOff) + step * 4096;
+                    stsm_x4_t(to, lo[0], lo[1], lo[2], lo[3]);
+                    stsm_x4_t(to + 2048, lo[4], lo[5], lo[6], lo[7]);
                 }
             }
-            float zero0 = 0.f, zero1 = 0.f;             // NaN once a non-finite v went by
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 wj = *reinterpret_cast<const float2 *>(w + (i >> 1) * 8);
-                const float v0 = __uint_as_float(raw[i] << 16), v1 = __uint_as_float(raw[i] & 0xFFFF0000u);
-                float x0, x1;
-                if (!LOCAL) fma2(zero0, zero1, v0, v1, 0.f, 0.f, zero0, zero1);
-                fma2(x0, x1, v0, v1, wj.x, wj.y, 0.f, 0.f);
-                hi[i] = take_bf16(x0, x1);
-                mid[i] = take_bf16(x0, x1);
-                lo[i] = pack_bf16x2(x0, x1);
+            if (!waited) break;
+            fence_proxy_async_smem();
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(w_ready);
+                if (LOCAL) mbar_arrive(&empty[s]);
             }
             if (!LOCAL) {
                 const bool any_bad = __any_sync(0xffffffffu, !(zero0 + zero1 == 0.f));
@@ -603,34 +631,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     bad_at[(c & 3) * 128 + grp * 32 + hl * 16 + lane] = LC;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&v_ready[s]);
-            }
-            if (c > 0 && !wait(w_free, c - 1)) break;
-            tc_fence_after();
-            tmem_st_16x128b_x8(lane_base + TC_W, hi);
-            tmem_st_16x128b_x8(lane_base + TC_W + 32, mid);
-            if (grp * 32 < D) {
-                const uint32_t to = smem_u32(sm + S::kLoOff) + (frag - S::kVOff);
-#pragma unroll
-                for (int g = 0; g < 8; g += 2)
-                    stsm_x4_t(to + g * 1024, lo[2 * g], lo[2 * g + 1], lo[2 * g + 2], lo[2 * g + 3]);
-                fence_proxy_async_smem();
-            }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(w_ready);
-                mbar_arrive(&empty[s]);
+                if (lane == 0) {
+                    mbar_arrive(&v_ready[s]);
+                    mbar_arrive(&empty[s]);
+                }
             }
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
         more_regs<kStateRegs>();
-        // ============================================================ state: thread = value dimension, half of dk
-        const int grp = warp & 3, half = (warp - 8) >> 2, dv = grp * 32 + lane;
+        // ============================================================ state: thread = value dimension, a quarter of dk
+        const int grp = warp & 3, part = (warp - 8) >> 2, dv = grp * 32 + lane;
         const bool real = grp * 32 < D;      // warp-uniform
         const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
-        constexpr int N = D / 2;             // columns per thread
+        constexpr int N = D / 4;             // columns per thread
         float St[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) St[i] = 0.f;
@@ -643,7 +656,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (src) {
 #pragma unroll
                 for (int i = 0; i < N; i += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src + dv * D + half * N + i);
+                    const float4 x = *reinterpret_cast<const float4 *>(src + dv * D + part * N + i);
                     St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
                 }
             }
@@ -658,8 +671,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     hi[k] = take_bf16(x0, x1);
                     lo[k] = pack_bf16x2(x0, x1);
                 }
-                tmem_st8(lane_base + TC_STATE + (half * N + i) / 2, hi);
-                tmem_st8(lane_base + TC_STATE + 64 + (half * N + i) / 2, lo);
+                tmem_st8(lane_base + TC_STATE + (part * N + i) / 2, hi);
+                tmem_st8(lane_base + TC_STATE + 64 + (part * N + i) / 2, lo);
             }
             tc_wait_st();
             tc_fence_before();
@@ -682,7 +695,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                 for (int i = 0; i < N; i += 16) {
                     uint32_t kv[16];
-                    tmem_ld16(lane_base + TC_KV + half * N + i, kv);
+                    tmem_ld16(lane_base + TC_KV + part * N + i, kv);
                     tc_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
@@ -710,11 +723,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (ok && real && dst && (!LOCAL || u.row >= 0)) {
 #pragma unroll
             for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4 *>(dst + dv * D + half * N + i) =
+                *reinterpret_cast<float4 *>(dst + dv * D + part * N + i) =
                     make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
         }
-    } else if (warp < 20) {
-        fewer_regs<kOutRegs>();
+    } else if (warp < 28) {
         // ============================================================ output rows: a warp per 32 value dimensions
         // In 8x8 fragments (thread: two neighbouring tokens of one dv), transposed by stmatrix into the warp's
         // own [64 tokens][32 dv] tile, 16-byte chunks swizzled by token pair.
@@ -726,9 +738,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // stmatrix row address: token (lane / 16) * 8 + lane % 8 of its group, dv chunk lane / 8 % 2
             const int row0 = (lane >> 4) * 8 + (lane & 7), ch0 = (lane >> 3) & 1, sw = (row0 >> 1) & 3;
             const uint32_t stg_at = smem_u32(stg) + row0 * 64;
-            float2 f[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) f[g] = *reinterpret_cast<const float2 *>(tab1 + g * 8 + q2);
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int n = c + 1 < chunks ? LC : n_last;
@@ -740,13 +749,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 const int *bad_row = bad_at + (c & 3) * 128 + grp * 32;
                 const bool any_bad = __any_sync(0xffffffffu, bad_row[lane] < LC);
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
                     const int hl = part >> 1, g0 = (part & 1) * 4;
                     const uint32_t at = lane_base + ((uint32_t)hl << 20) + g0 * 8;
                     uint32_t x[16], y[16], r[8];
                     tmem_ld_16x256b_x4(at + TC_INTRA, x);
                     tmem_ld_16x256b_x4(at + TC_INTER, y);
+                    const float *e = tab1 + g0 * 8 + q2;
                     tc_wait_ld();
                     if (part == 3) {
                         tc_fence_before();
@@ -755,9 +765,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {           // tokens 8 (g0 + i / 2) + q2, + 1; dv + 8 (i % 2)
-                        const float2 e = f[g0 + i / 2];
+                        const float2 f = *reinterpret_cast<const float2 *>(e + (i / 2) * 8);
                         float o0, o1;
-                        fma2(o0, o1, e.x, e.y, __uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]),
+                        fma2(o0, o1, f.x, f.y, __uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]),
                              __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
                         r[i] = pack_bf16x2(o0, o1);
                     }
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 __syncwarp();
                 __nv_bfloat16 *out = p.out + (u.t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
-#pragma unroll 4
+#pragma unroll 2
                 for (int i = 0; i < LC / 8; ++i) {
                     const int t = i * 8 + (lane >> 2);
                     const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
@@ -786,10 +796,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else {
         fewer_regs<kRestRegs>();
-    if (warp < 22) {
-        // ============================================================ loads (warp 20), P: thread = query token
-        const int half = warp - 20;
-        int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 20)
+    if (warp < 30) {
+        // ============================================================ loads (warp 28), P: thread = query token
+        const int half = warp - 28;
+        int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 28)
         auto load = [&]() {                      // the next chunk's, once its stage is free
             const int c = loaded, s = c % ST;
             if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag, p.err)) return false;
@@ -838,47 +848,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
                 if (!wait(s_ready, c)) break;
                 tc_fence_after();
-                if (half == 1) {
-                    // keys 0..31, all before these tokens: e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}
-                    const float f = tab[lane + 1];
 #pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        uint32_t s[16];
-                        tmem_ld16(lane_base + TC_S + part * 16, s);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + part * 16 + k * 8);
-                            const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + part * 16 + k * 8);
-                            const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-                            float x[8];
-#pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
-                                fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[k * 8 + e]),
-                                     __uint_as_float(s[k * 8 + e + 1]), 0.f, 0.f);
-                            }
-                            put(ph, part * 2 + k, x);
-                        }
-                    }
-                }
-#pragma unroll 1
-                for (int part = 2 * half; part < 2 * half + 2; ++part) {      // 16 keys around the diagonal
-                    uint32_t s[16];
-                    tmem_ld16(lane_base + TC_S + part * 16, s);
-                    const int d = i - part * 16;
+                for (int k = 0; k < 4 + 4 * half; ++k) {        // 8 keys
+                    uint32_t s[8];
+                    tmem_ld8(lane_base + TC_S + k * 8, s);
+                    const int d = i - k * 8;
+                    const float *e = tab + d;
+                    float x[8];
                     tc_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int j = k * 8 + e;
-                            // masked by choice, not by the table's zeros, which would keep a NaN
-                            x[e] = j <= d ? __uint_as_float(s[j]) * tab[d - j] : 0.f;
-                        }
-                        put(ph, part * 2 + k, x);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        // masked by choice, not by the table's zeros, which would keep a NaN
+                        x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
+                    put(ph, k, x);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -896,7 +878,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int d = max(0, loaded - ST); d < loaded; ++d)
                 chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, nullptr, p.err);
         __syncwarp();
-    } else if (warp == 22) {
+    } else if (warp == 30) {
         // ============================================================ MMA: KV and QS
         // Two threads issue, so that one's waits (about 100 clocks each) fall into the other's
         // products.  w_ready and p_ready come from threads that saw the chunk's copies land.
@@ -912,7 +894,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
                 const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
                 const uint64_t ld = sw128_desc(smem_u32(sm + S::kLoOff), PAN == 2 ? kChunkPanel : 0, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
 #pragma unroll
                     for (int k = 0; k < LC / 16; ++k)
@@ -933,7 +915,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
                 const uint64_t qd = sw128_desc(qk, 16, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
