@@ -848,19 +848,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
                 if (!wait(s_ready, c)) break;
                 tc_fence_after();
+                // 8 keys at a time, the next ones loading meanwhile
+                uint32_t s[8];
+                tmem_ld8(lane_base + TC_S, s);
+                tc_wait_ld();
+                if (half == 1) {
+                    // keys 0..31, all before these tokens: e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}
+                    const float f = tab[lane + 1];
 #pragma unroll 1
-                for (int k = 0; k < 4 + 4 * half; ++k) {        // 8 keys
-                    uint32_t s[8];
-                    tmem_ld8(lane_base + TC_S + k * 8, s);
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + k * 8);
+                        const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + k * 8);
+                        const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
+                            fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), 0.f, 0.f);
+                        }
+                        tmem_ld8(lane_base + TC_S + k * 8 + 8, s);
+                        put(ph, k, x);
+                        tc_wait_ld();
+                    }
+                }
+#pragma unroll 1
+                for (int k = 4 * half; k < 4 * half + 4; ++k) {        // the 32 keys around the diagonal
                     const int d = i - k * 8;
                     const float *e = tab + d;
                     float x[8];
-                    tc_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         // masked by choice, not by the table's zeros, which would keep a NaN
                         x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
+                    tmem_ld8(lane_base + TC_S + ((k * 8 + 8) & 63), s);
                     put(ph, k, x);
+                    tc_wait_ld();
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
