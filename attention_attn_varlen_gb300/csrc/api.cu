@@ -1295,6 +1295,7 @@ attn_status attn_linear_decode(const void *q, const void *k, const void *v, void
     if (st != ATTN_OK) return st;
     DevInfo *d = nullptr;
     if ((st = device_for(&d)) != ATTN_OK) return st;
+    if ((int64_t)batch * num_heads_kv * 4 > (int64_t)INT32_MAX) return ATTN_ERR_UNSUPPORTED;   // CTAs of the launch
     p.max_seqlen = 1;
     p.err = d->err;
     return launched(launch_linear_decode(p, reinterpret_cast<cudaStream_t>(stream)));

@@ -11,8 +11,6 @@
 namespace attn {
 namespace {
 
-constexpr int kLinStage = 16;   // tokens staged in shared memory at a time
-
 // Tokens [t0, t0 + n) of sequence b; n = 0 for bad offsets (recorded once by the
 // CTA of head 0).
 __device__ __forceinline__ bool linear_rows(const LinearParams &p, int b, int64_t &t0, int &n, bool report) {
@@ -55,84 +53,84 @@ __device__ __forceinline__ float linear_log_decay(const LinearParams &p, int h, 
     return fminf(g, 0.f);
 }
 
-// One CTA per (sequence, KV head), token after token; the state in registers.
-// Thread (dv, half) holds the float4s 2 m + half of row dv.
+// ---------------------------------------------------------------------------
+// One token per sequence: every state is read and written once, 8 D^2 bytes per
+// sequence and KV head, which bounds it (HBM; 4 operations per 8 bytes).  A lane
+// holds four neighbouring columns of a row, a warp 32 lanes / (D / 4) rows at a
+// time, kDecodeRows loads ahead of anything that uses them (4 KB a warp); the
+// row sums of a warp's rows are reduced together (9 shuffles for 8 rows).
+// ---------------------------------------------------------------------------
+constexpr int kDecodeRows = 8;        // loads in flight per lane
+constexpr int kDecodeWarps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(2 * D) linear_tokens_kernel(const LinearParams p) {
-    __shared__ float ks[kLinStage][D], vs[kLinStage][D], qs[kLinStage][D];
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    const int dv = tid >> 1, half = tid & 1;
-    int64_t t0;
-    int n;
-    linear_rows(p, b, t0, n, h == 0 && tid == 0);
-    if (n == 0) return;   // the state stays as it was
+__global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const LinearParams p) {
+    constexpr int LPR = D / 4;                          // lanes per row
+    constexpr int RPL = 32 / LPR;                       // rows per load
+    constexpr int ROWS = kDecodeRows * RPL;             // rows per warp
+    constexpr int CTAS = D / (ROWS * kDecodeWarps);     // CTAs per state
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.x / CTAS, b = unit / p.Hkv, h = unit - b * p.Hkv;
+    const int row0 = ((blockIdx.x - unit * CTAS) * kDecodeWarps + warp) * ROWS + (lane / LPR) * kDecodeRows;
+    const int col = (lane & (LPR - 1)) * 4;
+    const bool report = h == 0 && threadIdx.x == 0;
     bool from;
-    float *state = linear_state(p, b, h, from, h == 0 && tid == 0);
-    float S[D / 2];
+    float *state = linear_state(p, b, h, from, report);
+    float4 S[kDecodeRows];                              // rows row0 .. row0 + 7, columns col .. col + 3
 #pragma unroll
-    for (int m = 0; m < D / 8; ++m) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (from) x = *reinterpret_cast<const float4 *>(state + dv * D + 4 * (2 * m + half));
-        S[4 * m] = x.x, S[4 * m + 1] = x.y, S[4 * m + 2] = x.z, S[4 * m + 3] = x.w;
+    for (int i = 0; i < kDecodeRows; ++i) {
+        S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from) S[i] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + i) * D + col));
     }
-    const float a = expf(linear_log_decay(p, h, tid == 0));
-    for (int c = 0; c < n; c += kLinStage) {
-        const int m = min(kLinStage, n - c);
-        __syncthreads();
-        for (int x = tid; x < m * D; x += 2 * D) {
-            const int64_t t = t0 + c + x / D;
-            const int d = x % D;
-            ks[x / D][d] = __bfloat162float(p.k[t * p.k_stride + h * D + d]);
-            vs[x / D][d] = __bfloat162float(p.v[t * p.v_stride + h * D + d]);
-        }
-        for (int g = 0; g < p.G; ++g) {
-            // every query head of the group runs over the same tokens; the state advances with the last
-            __syncthreads();
-            const int hq = h * p.G + g;
-            for (int x = tid; x < m * D; x += 2 * D)
-                qs[x / D][x % D] = __bfloat162float(p.q[(t0 + c + x / D) * p.q_stride + hq * D + x % D]);
-            __syncthreads();
-            float R[D / 2];
+    const uint2 kr = *reinterpret_cast<const uint2 *>(p.k + (int64_t)b * p.k_stride + h * D + col);
+    const uint4 vr = *reinterpret_cast<const uint4 *>(p.v + (int64_t)b * p.v_stride + h * D + row0);
+    const float a = expf(linear_log_decay(p, h, b == 0 && threadIdx.x == 0));
+    const float k0 = __uint_as_float(kr.x << 16), k1 = __uint_as_float(kr.x & 0xFFFF0000u);
+    const float k2 = __uint_as_float(kr.y << 16), k3 = __uint_as_float(kr.y & 0xFFFF0000u);
+    const uint32_t vw[4] = {vr.x, vr.y, vr.z, vr.w};
 #pragma unroll
-            for (int i = 0; i < D / 2; ++i) R[i] = S[i];
-            for (int t = 0; t < m; ++t) {
-                const float v = vs[t][dv];
-                float o = 0.f;
+    for (int i = 0; i < kDecodeRows; ++i) {
+        const float v = __uint_as_float(i & 1 ? vw[i / 2] & 0xFFFF0000u : vw[i / 2] << 16);
+        S[i].x = fmaf(v, k0, a * S[i].x);
+        S[i].y = fmaf(v, k1, a * S[i].y);
+        S[i].z = fmaf(v, k2, a * S[i].z);
+        S[i].w = fmaf(v, k3, a * S[i].w);
+        if (state) __stcs(reinterpret_cast<float4 *>(state + (row0 + i) * D + col), S[i]);
+    }
+    for (int g = 0; g < p.G; ++g) {
+        const int hq = h * p.G + g;
+        const uint2 qr = *reinterpret_cast<const uint2 *>(p.q + (int64_t)b * p.q_stride + (int64_t)hq * D + col);
+        const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
+        const float q2 = __uint_as_float(qr.y << 16), q3 = __uint_as_float(qr.y & 0xFFFF0000u);
+        float o[kDecodeRows];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const float4 k4 = *reinterpret_cast<const float4 *>(&ks[t][4 * (2 * i + half)]);
-                    const float4 q4 = *reinterpret_cast<const float4 *>(&qs[t][4 * (2 * i + half)]);
-                    R[4 * i] = fmaf(v, k4.x, a * R[4 * i]);
-                    R[4 * i + 1] = fmaf(v, k4.y, a * R[4 * i + 1]);
-                    R[4 * i + 2] = fmaf(v, k4.z, a * R[4 * i + 2]);
-                    R[4 * i + 3] = fmaf(v, k4.w, a * R[4 * i + 3]);
-                    o = fmaf(R[4 * i], q4.x, o);
-                    o = fmaf(R[4 * i + 1], q4.y, o);
-                    o = fmaf(R[4 * i + 2], q4.z, o);
-                    o = fmaf(R[4 * i + 3], q4.w, o);
-                }
-                o += __shfl_xor_sync(0xffffffffu, o, 1);
-                if (half == 0) p.out[(t0 + c + t) * p.out_stride + hq * D + dv] = __float2bfloat16_rn(o * p.scale);
-            }
-            if (g == p.G - 1) {
+        for (int i = 0; i < kDecodeRows; ++i)
+            o[i] = fmaf(S[i].x, q0, fmaf(S[i].y, q1, fmaf(S[i].z, q2, S[i].w * q3)));
+        // each step halves the rows a lane carries: the last bits of the lane number pick the row
+        int w = LPR / 2;
 #pragma unroll
-                for (int i = 0; i < D / 2; ++i) S[i] = R[i];
+        for (int n = kDecodeRows / 2; n > 0; n /= 2, w /= 2) {
+            const bool up = lane & w;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float give = up ? o[i] : o[i + n], keep = up ? o[i + n] : o[i];
+                o[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
             }
         }
-    }
-    if (state) {
 #pragma unroll
-        for (int m = 0; m < D / 8; ++m)
-            *reinterpret_cast<float4 *>(state + dv * D + 4 * (2 * m + half)) =
-                make_float4(S[4 * m], S[4 * m + 1], S[4 * m + 2], S[4 * m + 3]);
+        for (; w > 0; w /= 2) o[0] += __shfl_xor_sync(0xffffffffu, o[0], w);
+        // row bits: 4, 2, 1 from lane bits LPR / 2, LPR / 4, LPR / 8
+        const int row = (lane & (LPR - 1)) / (LPR / 8);
+        if ((lane & (LPR / 8 - 1)) == 0)
+            p.out[(int64_t)b * p.out_stride + (int64_t)hq * D + row0 + row] = __float2bfloat16_rn(o[0] * p.scale);
     }
 }
 
-cudaError_t launch_tokens(const LinearParams &p, cudaStream_t stream) {
-    const dim3 grid(p.Hkv, p.batch);
+cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
+    const int64_t states = (int64_t)p.batch * p.Hkv;
     main_kernel_event_before(stream);
-    if (p.D == 128) linear_tokens_kernel<128><<<grid, 256, 0, stream>>>(p);
-    else linear_tokens_kernel<64><<<grid, 128, 0, stream>>>(p);
+    if (p.D == 128) linear_decode_kernel<128><<<(unsigned)(states * 4), kDecodeWarps * 32, 0, stream>>>(p);
+    else linear_decode_kernel<64><<<(unsigned)states, kDecodeWarps * 32, 0, stream>>>(p);
     main_kernel_event_after(stream);
     return cudaGetLastError();
 }
@@ -1080,6 +1078,6 @@ cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kma
     return p.D == 128 ? launch_chunks<128>(qmap, kmap, vmap, p, stream) : launch_chunks<64>(qmap, kmap, vmap, p, stream);
 }
 
-cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream) { return launch_tokens(p, stream); }
+cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream) { return launch_decode_kernel(p, stream); }
 
 }  // namespace attn

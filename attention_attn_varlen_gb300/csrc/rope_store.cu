@@ -24,6 +24,7 @@ namespace attn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 3;   // items a thread has in flight
 
 // VEC pairs of one item: two vectors of VEC bf16
 template <int VEC> struct RopeVec;
@@ -91,8 +92,9 @@ struct RopeItem {
 };
 
 template <int VEC, bool INTER>
-__device__ __forceinline__ void rope_load(const RopeParams &p, int64_t t, int it, int per_head, RopeItem<VEC> &r) {
-    r.head = it / per_head;
+__device__ __forceinline__ void rope_load(const RopeParams &p, int64_t t, int it, int per_head, uint32_t head_magic,
+                                          RopeItem<VEC> &r) {
+    r.head = head_magic ? __umulhi(it, head_magic) : it / per_head;
     const int c = it - r.head * per_head;
     const bool is_v = r.head >= p.Hq + p.Hkv;
     const __nv_bfloat16 *row;
@@ -169,34 +171,50 @@ __device__ __forceinline__ void rope_write(const RopeParams &p, int64_t t, int64
 }
 
 // tile_tokens consecutive tokens per CTA; shared memory: their sines and cosines.
+// A thread loads kRopeUnroll items (32 bytes each) before it uses the first; the
+// first ones are in flight while the sines and cosines are computed.
 template <int VEC, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_store_kernel(const RopeParams p, int tile_tokens) {
+__global__ void __launch_bounds__(kRopeThreads) rope_store_kernel(const RopeParams p, int tile_tokens, int per_tok,
+                                                                  uint32_t tok_magic, int per_head,
+                                                                  uint32_t head_magic) {
     extern __shared__ float2 turns[];   // [tile_tokens][half]
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * tile_tokens;
     const int nt = (int)min((int64_t)tile_tokens, p.num_tokens - t0);
-    const int per_head = p.D / (2 * VEC);
-    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
-    const int per_tok = heads * per_head;
-    for (int x = tid; x < nt * p.half; x += kRopeThreads) {
-        const int t = x / p.half;
-        turns[x] = rope_turn(p, t0 + t, x - t * p.half);
-    }
-    __syncthreads();
-    bool bad = false, big = false;
-    for (int x = tid; x < nt * per_tok; x += kRopeThreads) {
-        const int t = x / per_tok;
-        RopeItem<VEC> r;
-        rope_load<VEC, INTER>(p, t0 + t, x - t * per_tok, per_head, r);
-        int64_t slot = -1;
-        if (p.k_cache) {
-            slot = __ldg(p.slot_mapping + t0 + t);
-            if (slot >= p.num_slots) {
-                bad = true;
-                slot = -1;
-            }
+    const int items = nt * per_tok;
+    bool bad = false, big = false, ready = false;
+    for (int x0 = tid; x0 < items || !ready; x0 += kRopeThreads * kRopeUnroll) {
+        RopeItem<VEC> r[kRopeUnroll];
+        int64_t slot[kRopeUnroll];
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            const int x = x0 + u * kRopeThreads;
+            slot[u] = -1;
+            if (x >= items) continue;
+            const int t = tok_magic ? __umulhi(x, tok_magic) : x / per_tok;
+            if (p.k_cache) slot[u] = __ldg(p.slot_mapping + t0 + t);
+            rope_load<VEC, INTER>(p, t0 + t, x - t * per_tok, per_head, head_magic, r[u]);
         }
-        rope_write<VEC, INTER>(p, t0 + t, slot, turns + t * p.half, r, big);
+        if (!ready) {
+            for (int x = tid; x < nt * p.half; x += kRopeThreads) {
+                const int t = x / p.half;
+                turns[x] = rope_turn(p, t0 + t, x - t * p.half);
+            }
+            __syncthreads();
+            ready = true;
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            const int x = x0 + u * kRopeThreads;
+            if (x >= items) continue;
+            const int t = tok_magic ? __umulhi(x, tok_magic) : x / per_tok;
+            int64_t s = slot[u];
+            if (s >= p.num_slots) {
+                bad = true;
+                s = -1;
+            }
+            rope_write<VEC, INTER>(p, t0 + t, s, turns + t * p.half, r[u], big);
+        }
     }
     const unsigned any_bad = __ballot_sync(0xffffffffu, bad), any_big = __ballot_sync(0xffffffffu, big);
     if ((tid & 31) == 0) {
@@ -205,13 +223,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_store_kernel(const RopePara
     }
 }
 
+// ceil(2^32 / d): __umulhi(x, it) is x / d for every x < 2^32 / d (0 for d = 1: divide)
+uint32_t magic_of(int d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0; }
+
 template <int VEC, bool INTER>
 cudaError_t launch(const RopeParams &p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    const int tile = 1;
+    const int per_head = p.D / (2 * VEC), per_tok = (p.Hq + p.Hkv + (p.v ? p.Hkv : 0)) * per_head;
+    // one round of loads per thread, but first of all a CTA for every SM
+    int64_t tile = (int64_t)kRopeUnroll * kRopeThreads / per_tok;
+    if (tile > p.num_tokens / (2 * num_sms)) tile = p.num_tokens / (2 * num_sms);
+    if (tile < 1) tile = 1;
+    const bool magic = tile * (int64_t)per_tok * per_tok < (1ll << 32);
     const int64_t grid = (p.num_tokens + tile - 1) / tile;
     main_kernel_event_before(stream);
-    rope_store_kernel<VEC, INTER><<<(unsigned)grid, kRopeThreads, tile * p.half * sizeof(float2), stream>>>(p, tile);
+    rope_store_kernel<VEC, INTER><<<(unsigned)grid, kRopeThreads, tile * p.half * sizeof(float2), stream>>>(
+        p, (int)tile, per_tok, magic ? magic_of(per_tok) : 0, per_head, magic ? magic_of(per_head) : 0);
     main_kernel_event_after(stream);
     return cudaGetLastError();
 }
