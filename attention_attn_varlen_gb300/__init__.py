@@ -187,6 +187,17 @@ def _cuda(dtype, dev, *named):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
 
 
+def _tokens(t, name, dev, rows, heads, dim) -> int:
+    """Row stride of a bf16 [rows, heads, dim] tensor on cuda:dev whose heads and dim are packed."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
+    stride = t.stride()
+    if t.shape != (rows, heads, dim) or stride[2] != 1 or stride[1] != dim:
+        raise ValueError(f"{name}: expected [{rows}, {heads}, {dim}] with packed heads, got {tuple(t.shape)} "
+                         f"(strides {stride})")
+    return stride[0] if rows > 1 else heads * dim
+
+
 def _device(t: torch.Tensor, name: str) -> int:
     """The tensor's CUDA device, which has to be the current one (the library launches there)."""
     dev = t.get_device()
@@ -195,6 +206,26 @@ def _device(t: torch.Tensor, name: str) -> int:
     if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
     return dev
+
+
+# the current stream's handle without making a Stream object (3 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(workspace, need: int, dev: int, like) -> tuple:
+    """(tensor, address, size) of a caller's workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    if workspace is None:
+        return None, None, 0
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # --------------------------------------------------------------------------
@@ -536,7 +567,7 @@ class StepTables(NamedTuple):
                    new(i32, batch + 1), new(i32, batch + 1), new(i32, batch), new(i32, batch))
 
 
-def _pool_args(request_rows, lens, seq_lens, page_table, free_pages, num_free, workspace, lens_name):
+def _pool_args(request_rows, lens, seq_lens, page_table, free_pages, num_free, lens_name):
     dev = _device(seq_lens, "seq_lens")
     _cuda(torch.int32, dev, ("request_rows", request_rows), (lens_name, lens), ("seq_lens", seq_lens),
           ("page_table", page_table), ("free_pages", free_pages), ("num_free", num_free))
@@ -547,11 +578,7 @@ def _pool_args(request_rows, lens, seq_lens, page_table, free_pages, num_free, w
     B = lens.numel()
     if request_rows is not None and request_rows.numel() != B:
         raise ValueError(f"request_rows and {lens_name} must have the same length")
-    if workspace is None:
-        workspace = torch.empty(lib().attn_step_tables_workspace_size(B), dtype=torch.uint8, device=seq_lens.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    return dev, B, workspace
+    return dev, B
 
 
 def step_tables(request_rows, new_lens, seq_lens, page_table, free_pages, num_free, block_size: int,
@@ -565,8 +592,7 @@ def step_tables(request_rows, new_lens, seq_lens, page_table, free_pages, num_fr
     [B]; max_tokens sizes slot_mapping and positions (entries behind the last
     token are -1 and 0).  Entries that cannot be served keep their length, get
     slots of -1 and are reported by get_last_device_error (9: out of pages)."""
-    dev, B, workspace = _pool_args(request_rows, new_lens, seq_lens, page_table, free_pages, num_free, workspace,
-                                   "new_lens")
+    dev, B = _pool_args(request_rows, new_lens, seq_lens, page_table, free_pages, num_free, "new_lens")
     R, M = page_table.shape
     if out is None:
         out = StepTables.empty(B, M, int(max_tokens), seq_lens.device)
@@ -579,12 +605,14 @@ def step_tables(request_rows, new_lens, seq_lens, page_table, free_pages, num_fr
                 or out.positions.numel() != max_tokens or out.cu_seqlens_q.numel() != B + 1 \
                 or out.cu_seqlens_k.numel() != B + 1 or out.cache_seqlens.numel() != B or out.context_lens.numel() != B:
             raise ValueError("out was made for other sizes")
-    st = lib().attn_step_tables(_ptr(request_rows), _ptr(new_lens), _ptr(seq_lens), _ptr(page_table),
-                                _ptr(free_pages), _ptr(num_free), B, R, M, int(block_size), free_pages.numel(),
-                                int(max_tokens), _ptr(out.block_table), _ptr(out.slot_mapping), _ptr(out.positions),
-                                _ptr(out.cu_seqlens_q), _ptr(out.cu_seqlens_k), _ptr(out.cache_seqlens),
-                                _ptr(out.context_lens), _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(stream))
+    L = lib()
+    workspace, ws, ws_bytes = _bytes(workspace, L.attn_step_tables_workspace_size(B), dev, seq_lens)
+    st = L.attn_step_tables(_address(request_rows), new_lens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
+                            free_pages.data_ptr(), num_free.data_ptr(), B, R, M, int(block_size), free_pages.numel(),
+                            int(max_tokens), out.block_table.data_ptr(), out.slot_mapping.data_ptr(),
+                            out.positions.data_ptr(), out.cu_seqlens_q.data_ptr(), out.cu_seqlens_k.data_ptr(),
+                            out.cache_seqlens.data_ptr(), out.context_lens.data_ptr(), ws, ws_bytes,
+                            _raw_stream(dev) if stream is None else stream.cuda_stream)
     _check(st, "attn_step_tables")
     return out
 
@@ -593,12 +621,13 @@ def trim_pages(request_rows, keep_lens, seq_lens, page_table, free_pages, num_fr
                stream=None) -> None:
     """Cut requests to their first keep_lens tokens (int32 [B]; 0 ends a
     request) and give the pages behind them back to the free list."""
-    _, B, workspace = _pool_args(request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, workspace,
-                                 "keep_lens")
+    dev, B = _pool_args(request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, "keep_lens")
     R, M = page_table.shape
-    st = lib().attn_trim_pages(_ptr(request_rows), _ptr(keep_lens), _ptr(seq_lens), _ptr(page_table),
-                               _ptr(free_pages), _ptr(num_free), B, R, M, int(block_size), free_pages.numel(),
-                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    L = lib()
+    workspace, ws, ws_bytes = _bytes(workspace, L.attn_step_tables_workspace_size(B), dev, seq_lens)
+    st = L.attn_trim_pages(_address(request_rows), keep_lens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
+                           free_pages.data_ptr(), num_free.data_ptr(), B, R, M, int(block_size), free_pages.numel(),
+                           ws, ws_bytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
     _check(st, "attn_trim_pages")
 
 
@@ -614,14 +643,10 @@ def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None,
     through.  Without caches only q and k are rotated (v may be None).  q_out and
     k_out may be q and k.  Returns the rotated q, or (q, k) with return_k."""
     dev = _device(q, "q")
-    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out)):
-        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev):
-            raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
     N, Hq, D = q.shape
     Hkv = k.shape[1]
-    stored = k_cache is not None or v_cache is not None or slot_mapping is not None or v16_cache is not None
     num_slots = 0
-    if stored:
+    if k_cache is not None or v_cache is not None or slot_mapping is not None or v16_cache is not None:
         if k_cache is None or v_cache is None or slot_mapping is None or v is None:
             raise ValueError("storing needs v, k_cache, v_cache and slot_mapping")
         _cuda(torch.bfloat16, dev, ("k_cache", k_cache), ("v_cache", v_cache))
@@ -635,51 +660,43 @@ def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None,
         num_slots = k_cache.numel() // (Hkv * D)
     elif k_out is None:
         return_k = True
-    qs, ks = _rows(q, "q", Hq, D), _rows(k, "k", Hkv, D)
-    vs = _rows(v, "v", Hkv, D) if v is not None else 0
-    if k.shape[0] != N or (v is not None and v.shape[0] != N):
-        raise ValueError("q, k and v must have the same number of tokens")
+    qs, ks = _tokens(q, "q", dev, N, Hq, D), _tokens(k, "k", dev, N, Hkv, D)
+    vs = _tokens(v, "v", dev, N, Hkv, D) if v is not None else 0
     if q_out is None:
         q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
     if k_out is None and return_k:
         k_out = torch.empty((N, Hkv, D), dtype=q.dtype, device=q.device)
-    qos = _rows(q_out, "q_out", Hq, D)
-    kos = _rows(k_out, "k_out", Hkv, D) if k_out is not None else 0
-    if q_out.shape[0] != N or (k_out is not None and k_out.shape[0] != N):
-        raise ValueError("q_out and k_out must have one row per token")
+    qos = _tokens(q_out, "q_out", dev, N, Hq, D)
+    kos = _tokens(k_out, "k_out", dev, N, Hkv, D) if k_out is not None else 0
     _cuda(torch.float32, dev, ("inv_freq", inv_freq))
+    axes = positions.shape[0] if positions.dim() == 2 else 1
     if positions.dtype is not torch.int32 or positions.get_device() != dev or positions.dim() not in (1, 2) \
             or positions.shape[-1] != N or (N > 1 and positions.stride(-1) != 1):
         raise ValueError(f"positions must be int32 [{N}] or [axes, {N}] on cuda:{dev}, contiguous along the tokens")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
+    pairs = inv_freq.numel()
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
-        if len(pair_axis) != inv_freq.numel():
+        if len(pair_axis) != pairs:
             raise ValueError("pair_axis must have one entry per pair (inv_freq)")
     elif axes > 1:
         raise ValueError("positions with several axes need pair_axis")
     st = lib().attn_rope_store_kvcache(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), pair_axis, axes,
-        positions.stride(0) if axes > 1 else N, 2 * inv_freq.numel(), 1 if interleaved else 0, float(scale),
-        _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(v16_cache), _ptr(slot_mapping), N, Hq, Hkv, D,
-        qs, ks, vs, qos, kos, num_slots, _stream(stream))
+        q.data_ptr(), k.data_ptr(), _address(v), positions.data_ptr(), inv_freq.data_ptr(), pair_axis, axes,
+        positions.stride(0) if axes > 1 else N, 2 * pairs, 1 if interleaved else 0, float(scale), q_out.data_ptr(),
+        _address(k_out), _address(k_cache), _address(v_cache), _address(v16_cache), _address(slot_mapping), N, Hq,
+        Hkv, D, qs, ks, vs, qos, kos, num_slots, _raw_stream(dev) if stream is None else stream.cuda_stream)
     _check(st, "attn_rope_store_kvcache")
     return (q_out, k_out) if return_k else q_out
 
 
 def _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out, B):
     dev = _device(q, "q")
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev):
-            raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v must have the same number of tokens")
     if out is None:
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape[0] != T:
-        raise ValueError("out must have one row per token")
+    strides = (_tokens(q, "q", dev, T, Hq, D), _tokens(k, "k", dev, T, Hkv, D), _tokens(v, "v", dev, T, Hkv, D),
+               _tokens(out, "out", dev, T, Hq, D))
     _cuda(torch.float32, dev, ("log_decay", log_decay), ("state_cache", state_cache))
     _cuda(torch.int32, dev, ("state_slots", state_slots), ("context_lens", context_lens))
     if log_decay.numel() != Hkv:
@@ -688,15 +705,14 @@ def _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out
         raise ValueError("state_cache and state_slots go together")
     slots = 0
     if state_cache is not None:
-        if state_cache.dim() != 4 or state_cache.shape[1:] != (Hkv, D, D):
-            raise ValueError(f"state_cache must be [num_slots, {Hkv}, {D}, {D}]")
         slots = state_cache.shape[0]
+        if state_cache.shape != (slots, Hkv, D, D):
+            raise ValueError(f"state_cache must be [num_slots, {Hkv}, {D}, {D}]")
         if state_slots.numel() != B:
             raise ValueError("state_slots must have one entry per sequence")
     if context_lens is not None and context_lens.numel() != B:
         raise ValueError("context_lens must have one entry per sequence")
-    return out, T, Hq, Hkv, D, slots, (_rows(q, "q", Hq, D), _rows(k, "k", Hkv, D), _rows(v, "v", Hkv, D),
-                                       _rows(out, "out", Hq, D))
+    return dev, out, T, Hq, Hkv, D, slots, strides
 
 
 def linear_attn_workspace_size(batch: int, num_heads_q: int, num_heads_kv: int, head_dim: int, max_seqlen: int) -> int:
@@ -715,19 +731,17 @@ def linear_attn_varlen_fwd(q, k, v, log_decay, cu_seqlens, max_seqlen: int, scal
     context_lens[b] > 0 (int32 [B]) starts from its slot, any other from zero.
     scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
     B = cu_seqlens.numel() - 1
-    out, T, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out,
-                                                      B)
-    _cuda(torch.int32, q.get_device(), ("cu_seqlens", cu_seqlens))
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    dev, out, T, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens,
+                                                           out, B)
+    _cuda(torch.int32, dev, ("cu_seqlens", cu_seqlens))
     L = lib()
-    ws_bytes = L.attn_linear_workspace_size(B, Hq, Hkv, D, int(max_seqlen))
-    if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    ws_have = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = L.attn_linear_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(log_decay), _ptr(cu_seqlens),
-                                  _ptr(state_cache), _ptr(state_slots), _ptr(context_lens), B, T, int(max_seqlen), Hq,
-                                  Hkv, D, float(scale), slots, *strides, _ptr(workspace), ws_have, _stream(stream))
+    max_seqlen = int(max_seqlen)
+    workspace, ws, ws_bytes = _bytes(workspace, L.attn_linear_workspace_size(B, Hq, Hkv, D, max_seqlen), dev, q)
+    st = L.attn_linear_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
+                                  cu_seqlens.data_ptr(), _address(state_cache), _address(state_slots),
+                                  _address(context_lens), B, T, max_seqlen, Hq, Hkv, D,
+                                  1.0 / math.sqrt(D) if scale is None else scale, slots, *strides, ws, ws_bytes,
+                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
     _check(st, "attn_linear_varlen_fwd")
     return out
 
@@ -738,13 +752,12 @@ def linear_attn_decode(q, k, v, log_decay, state_cache, state_slots, scale: floa
     Hkv, D]; the states in state_cache are updated in place.  A slot < 0 stands
     for a zero state that is not kept; context_lens[b] = 0 starts from zero
     (None: every slot continues).  Returns out [B, Hq, D]."""
-    out, B, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens, out,
-                                                      q.shape[0])
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    st = lib().attn_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(log_decay), _ptr(state_cache),
-                                  _ptr(state_slots), _ptr(context_lens), B, Hq, Hkv, D, float(scale), slots, *strides,
-                                  _stream(stream))
+    dev, out, B, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens,
+                                                           out, q.shape[0])
+    st = lib().attn_linear_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
+                                  _address(state_cache), _address(state_slots), _address(context_lens), B, Hq, Hkv, D,
+                                  1.0 / math.sqrt(D) if scale is None else scale, slots, *strides,
+                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
     _check(st, "attn_linear_decode")
     return out
 
