@@ -995,7 +995,7 @@ static attn_status tables_params(TablesParams *p, const int32_t *request_rows, c
     while ((1 << p->bs_log2) < block_size) ++p->bs_log2;
     p->num_pages = (int)num_pages;
     p->span = reinterpret_cast<int4 *>(workspace);
-    p->page_top = reinterpret_cast<int32_t *>(workspace);   // grow: in the spans' place
+    p->info = p->span;   // grow: in the spans' place
     p->before = reinterpret_cast<int32_t *>(p->span + batch);
     return ATTN_OK;
 }
@@ -1038,6 +1038,8 @@ attn_status attn_step_tables(const int32_t *request_rows, const int32_t *new_len
     p.cu_k = cu_seqlens_k;
     p.cache_seqlens = cache_seqlens;
     p.context_lens = context_lens;
+    p.vec_rows = max_blocks % 4 == 0 && aligned16(block_table) && aligned16(page_table);
+    p.vec_tokens = aligned16(slot_mapping) && aligned16(positions);
     p.err = d->err;
     return launched(launch_step_tables(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }

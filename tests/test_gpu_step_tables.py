@@ -53,7 +53,8 @@ def _same_tables(t, want):
 
 @pytest.mark.parametrize("B,R,M,bs,new_max,pad", [
     (1, 1, 1, 16, 1, 0), (1, 5, 3, 16, 40, 7), (33, 40, 6, 64, 1, 0), (64, 64, 20, 16, 9, 100),
-    (300, 512, 9, 32, 100, 1), (1025, 1100, 5, 16, 3, 0), (2500, 2500, 700, 16, 30, 13), (7, 9, 1300, 256, 5000, 3)])
+    (300, 512, 9, 32, 100, 1), (1025, 1100, 5, 16, 3, 0), (2500, 2500, 700, 16, 30, 13), (7, 9, 1300, 256, 5000, 3),
+    (6000, 6001, 7, 16, 20, 5), (40, 9000, 8, 16, 30, 2), (5000, 9100, 3, 16, 2, 0)])
 def test_grow_and_trim_match_the_plain_pool(B, R, M, bs, new_max, pad):
     rng = np.random.default_rng(B + M)
     state = _pool(B * 7 + M, R, M, bs)
@@ -153,6 +154,20 @@ def test_bad_entries_are_reported_and_leave_the_others_alone():
     assert st == 6 and word & 1
     av.trim_pages(_i32([0, 0, 77, 4]), _i32([-1, 3, 0, 0]), *dev, 16)
     ref.trim([0, 0, 77, 4], [-1, 3, 0, 0])
+    _same_pool(dev, ref)
+    assert av.get_last_device_error()[0] == 6
+
+
+def test_many_rows_with_rows_named_twice():
+    """More request rows than the claims in shared memory hold."""
+    state = _pool(33, 9000, 3, 16)
+    dev, ref = _device(*state), Pool(*state, 16)
+    rows = np.random.default_rng(4).integers(0, 9000, size=3000)
+    new = np.minimum(2, 48 - state[0][rows])
+    T = int(new.sum())
+    assert len(set(rows.tolist())) < 3000
+    av.get_last_device_error()
+    _same_tables(av.step_tables(_i32(rows), _i32(new), *dev, 16, T), ref.grow(rows, new, T))
     _same_pool(dev, ref)
     assert av.get_last_device_error()[0] == 6
 
