@@ -187,7 +187,8 @@ struct ChunkSmem {
     static constexpr int kVOff = kPanels * kQkPanel;
     static constexpr int kStageBytes = kVOff + kPanels * kChunkPanel;
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kPOff = kStages * kStageBytes;          // two chunks' P: hi, lo
+    static constexpr int kStageOff = kChunkPanel / 2;            // an A operand of QK starts 32 rows before Q
+    static constexpr int kPOff = kStageOff + kStages * kStageBytes;   // two chunks' P: hi, lo
     static constexpr int kLoOff = kPOff + 4 * kChunkPanel;       // the third part of w V, laid out like V
     static constexpr int kOutOff = kLoOff + kPanels * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
     static constexpr int kTabOff = kOutOff + 4 * LC * 64;
@@ -275,23 +276,33 @@ __device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) {
     return h;
 }
 
-// mbar_wait without its out-of-line part: with a call in the kernel the warpgroups cannot be
-// given register shares of their own.
-__device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *err) {
-    uint64_t t0 = 0;
+// mbar_wait in few instructions: the kernel's roles share the instruction cache, and with a call
+// in it the warpgroups could not have register shares of their own.  Gives up after about a
+// second, or once another role has; the kernel's end reports it.
+__device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
 #pragma unroll 1
-    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-        if (it & 63u) continue;
-        if (abort && *abort) return false;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitLimitNs) {
-            record_error(err, ERR_TIMEOUT | SRC_LINEAR);
-            if (abort) *abort = 1;
-            return false;
-        }
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (t - t0 < (uint32_t)kWaitLimitNs && !*abort);
+    *abort = 1;
+    return false;
+}
+
+// 8 keys of token i's row of P -> 16-byte chunk `ch` of both parts
+__device__ __forceinline__ void put_p(uint8_t *ph, int i, int ch, float (&x)[8]) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        hi[k] = take_bf16(x[2 * k], x[2 * k + 1]);
+        lo[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
     }
-    return true;
+    const uint32_t at = sw128_off(i, ch);
+    *reinterpret_cast<uint4 *>(ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(ph + kChunkPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 // Tokens of unit `u` and the segment's place in its sequence.
@@ -447,7 +458,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     using S = ChunkSmem<D>;
     constexpr int ST = S::kStages, PAN = S::kPanels;
     extern __shared__ __align__(1024) uint8_t lsmem_raw[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // values from lane 0 are warp-uniform to the compiler, and so is what is computed from them
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int heads = LOCAL ? p.Hkv : p.Hq;
@@ -457,10 +470,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (LOCAL && entry.y + 1 >= entry.w) return;
     const ChunkUnit u = chunk_unit(p, entry);
     const int hk = LOCAL ? h : h / p.G;
-    const int chunks = (u.n + LC - 1) / LC;
-    const int n_last = u.n - (chunks - 1) * LC;
+    const int chunks = uni((u.n + LC - 1) / LC);
+    const int n_last = uni(u.n - (chunks - 1) * LC);
 
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lsmem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smb = (smem_u32(lsmem_raw) + 1023u) & ~1023u;          // shared-memory address, for descriptors
+    uint8_t *sm = lsmem_raw + (smb - smem_u32(lsmem_raw));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *full = bars, *empty = bars + ST;
     uint64_t *v_ready = bars + 2 * ST;       // [ST]: the stage's V may be read by PV (tail rows and non-finite
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(w_ready, 8);
         mbar_init(w_free, 1);
         mbar_init(s_ready, 1);
-        mbar_init(p_ready, 2);
+        mbar_init(p_ready, 3);
         mbar_init(o_ready, 2);               // QS, PV
         mbar_init(o_free, 4);
         mbar_init(kv_ready, 1);
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(qs_done, 1);
         mbar_init(st_ready, 16);
         mbar_init(drain, 2);                 // each MMA thread
-        *abort_flag = 0;
+        abort_flag[0] = abort_flag[1] = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -519,10 +533,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
+    // waits for what the hardware finishes by itself run to the limit: their flag is their own
+    volatile int &never = *(abort_flag + 1);
     // a warp's wait: every lane gets the same answer
     auto wait = [&](uint64_t *bar, int phase) {
-        return __all_sync(0xffffffffu, chunk_wait(bar, (uint32_t)phase & 1u, abort_flag, p.err)) != 0;
+        return __all_sync(0xffffffffu, chunk_wait(bar, (uint32_t)phase & 1u, abort_flag)) != 0;
     };
 
     if (warp < 8) {
@@ -540,7 +556,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int c = 0; c < chunks; ++c) {
             const int s = c % ST, n = c + 1 < chunks ? LC : n_last;
             const float *w = (c + 1 < chunks ? w_full : w_last) + q2;
-            uint8_t *stage = sm + s * S::kStageBytes;
+            uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
             if (!wait(&full[s], c / ST)) break;
             if (n < LC) {
                 // rows behind the sequence's end are zeroed (a weight of 0 would not cancel a NaN there)
@@ -675,11 +691,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_wait_st();
             tc_fence_before();
         };
-        if (!LOCAL) {
-            if (real) publish();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(st_ready);
-        }
         bool ok = true;
         const float a_full = decay[LC], a_full_lo = decay[2 * LC + 1];
         const float a_last = decay[n_last], a_last_lo = decay[LC + 1 + n_last];
@@ -687,6 +698,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int c = 0; c < chunks; ++c) {
             const bool full_chunk = c + 1 < chunks;
             const float a = full_chunk ? a_full : a_last, a_lo = full_chunk ? a_full_lo : a_last_lo;
+            if (!LOCAL) {
+                if (c > 0 && !(ok = wait(qs_done, c - 1))) break;
+                tc_fence_after();
+                if (real) publish();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(st_ready);
+            }
             if (!(ok = wait(kv_ready, c))) break;
             tc_fence_after();
             if (real) {
@@ -707,13 +725,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(kv_free);
-            if (!LOCAL && c + 1 < chunks) {
-                if (!(ok = wait(qs_done, c))) break;
-                tc_fence_after();
-                if (real) publish();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(st_ready);
-            }
         }
         float *dst = nullptr;
         if (LOCAL) dst = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
@@ -736,9 +747,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // stmatrix row address: token (lane / 16) * 8 + lane % 8 of its group, dv chunk lane / 8 % 2
             const int row0 = (lane >> 4) * 8 + (lane & 7), ch0 = (lane >> 3) & 1, sw = (row0 >> 1) & 3;
             const uint32_t stg_at = smem_u32(stg) + row0 * 64;
+            // Group 2 first has tokens 32..63 of P against keys 0..31 (lanes 64..95, columns 0..31): all of
+            // them before those tokens, e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}.  It runs a chunk ahead.
+            bool ok = true;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = grp == 2 ? -1 : 0; c < chunks && ok; ++c) {
                 const int n = c + 1 < chunks ? LC : n_last;
+                if (grp == 2 && c + 1 < chunks) {
+                    if (!(ok = wait(s_ready, c + 1))) break;
+                    tc_fence_after();
+                    uint8_t *ph = sm + S::kPOff + ((c + 1) & 1) * 2 * kChunkPanel;
+                    const float f = tab[lane + 1];
+                    uint32_t s[8];
+                    tmem_ld8(lane_base + TC_S, s);
+                    tc_wait_ld();
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + k * 8);
+                        const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + k * 8);
+                        const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
+                            fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), 0.f, 0.f);
+                        }
+                        tmem_ld8(lane_base + TC_S + ((k * 8 + 8) & 31), s);
+                        put_p(ph, 32 + lane, k, x);
+                        tc_wait_ld();
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready);
+                    if (c < 0) continue;
+                }
                 if (!wait(o_ready, c)) break;
                 tc_fence_after();
                 if (!real) {
@@ -800,8 +843,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 28)
         auto load = [&]() {                      // the next chunk's, once its stage is free
             const int c = loaded, s = c % ST;
-            if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag, p.err)) return false;
-            uint8_t *stage = sm + s * S::kStageBytes;
+            if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag)) return false;
+            uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
             const int row = (int)(u.t0 + (int64_t)c * LC);
             mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
 #pragma unroll
@@ -813,90 +856,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             ++loaded;
             return true;
         };
-        if (half == 0 && lane == 0) {
-            const int first = LOCAL ? chunks : min(chunks, ST);
-            while (loaded < first && load()) {
+        if (LOCAL && half == 0 && lane == 0)
+            while (loaded < chunks && load()) {
             }
-        }
         __syncwarp();
         if (!LOCAL) {
-            const int i = half * 32 + lane;
-            const uint32_t lane_base = tmem + ((uint32_t)(half * 32) << 16);
+            // warp 28: tokens 32..63 and keys 32..63 (lanes 0..31, columns 32..63), warp 29: tokens and keys
+            // 0..31 (lanes 32..63, columns 0..31)
+            const int b0 = half == 0 ? 32 : 0, i = b0 + lane;
+            const uint32_t at = tmem + ((uint32_t)(half * 32) << 16) + TC_S + b0;
             uint8_t *pbuf = sm + S::kPOff;
-            if (half == 0) {
+            if (half == 1) {
                 // tokens 0..31 see no key behind 31: those halves of their rows stay zero
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     *reinterpret_cast<uint4 *>(pbuf + (k >> 2) * kChunkPanel + sw128_off(i, 4 + (k & 3))) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
-            // 8 keys of a row -> 16-byte chunk `ch` of both parts
-            auto put = [&](uint8_t *ph, int ch, float (&x)[8]) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    hi[k] = take_bf16(x[2 * k], x[2 * k + 1]);
-                    lo[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-                }
-                const uint32_t at = sw128_off(i, ch);
-                *reinterpret_cast<uint4 *>(ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(ph + kChunkPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            };
-            for (int c = 0; c < chunks; ++c) {
-                uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
-                if (!wait(s_ready, c)) break;
-                tc_fence_after();
-                // 8 keys at a time, the next ones loading meanwhile
-                uint32_t s[8];
-                tmem_ld8(lane_base + TC_S, s);
-                tc_wait_ld();
-                if (half == 1) {
-                    // keys 0..31, all before these tokens: e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}
-                    const float f = tab[lane + 1];
+            // warp 28 first fills the ring
+#pragma unroll 1
+            for (int c = half == 0 ? -min(chunks, ST) : 0; c < chunks; ++c) {
+                if (c >= 0) {
+                    uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
+                    if (!wait(s_ready, c)) break;
+                    tc_fence_after();
+                    // 8 keys at a time, the next ones loading meanwhile
+                    uint32_t s[8];
+                    tmem_ld8(at, s);
+                    tc_wait_ld();
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + k * 8);
-                        const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + k * 8);
-                        const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        const int d = lane - k * 8;
+                        const float *e = tab + d;
                         float x[8];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
-                            fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), 0.f, 0.f);
-                        }
-                        tmem_ld8(lane_base + TC_S + k * 8 + 8, s);
-                        put(ph, k, x);
+                        for (int j = 0; j < 8; ++j)
+                            // masked by choice, not by the table's zeros, which would keep a NaN
+                            x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
+                        tmem_ld8(at + ((k * 8 + 8) & 31), s);
+                        put_p(ph, i, b0 / 8 + k, x);
                         tc_wait_ld();
                     }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready);
                 }
-#pragma unroll 1
-                for (int k = 4 * half; k < 4 * half + 4; ++k) {        // the 32 keys around the diagonal
-                    const int d = i - k * 8;
-                    const float *e = tab + d;
-                    float x[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        // masked by choice, not by the table's zeros, which would keep a NaN
-                        x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
-                    tmem_ld8(lane_base + TC_S + ((k * 8 + 8) & 63), s);
-                    put(ph, k, x);
-                    tc_wait_ld();
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(p_ready);
-                    // the stage of the chunk before comes free about now
-                    if (half == 0 && c > 0 && loaded < chunks) load();
-                }
+                // past the first chunk: the stage of the chunk before comes free about now
+                if (half == 0 && lane == 0 && c != 0 && loaded < chunks) load();
                 __syncwarp();
             }
         }
         // copies still in flight (after a wait that gave up) land before the CTA ends
         if (half == 0 && lane == 0)
             for (int d = max(0, loaded - ST); d < loaded; ++d)
-                chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, nullptr, p.err);
+                chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, &never);
         __syncwarp();
     } else if (warp == 30) {
         // ============================================================ MMA: KV and QS
@@ -906,14 +920,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c % ST;
-            const uint32_t qk = smem_u32(sm + s * S::kStageBytes);
+            const uint32_t qk = smb + S::kStageOff + s * S::kStageBytes;
             ok = (c == 0 || wait(kv_free, c - 1)) && wait(w_ready, c);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
                 const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
-                const uint64_t ld = sw128_desc(smem_u32(sm + S::kLoOff), PAN == 2 ? kChunkPanel : 0, 1024);
+                const uint64_t ld = sw128_desc(smb + S::kLoOff, PAN == 2 ? kChunkPanel : 0, 1024);
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
 #pragma unroll
@@ -951,23 +965,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // nothing of this CTA's is left in the tensor core when TMEM goes back
         if (elect_one()) tc_commit(drain);
         __syncwarp();
-        chunk_wait(drain, 0u, nullptr, p.err);
+        chunk_wait(drain, 0u, &never);
         __syncwarp();
     } else {
         // ============================================================ MMA: QK, a chunk ahead, and PV
         if (!LOCAL) {
             bool ok = true;
             auto issue_qk = [&](int c) {
-                // rows 64..127 of A are K's: a product nobody reads, in exchange for M = 128
-                const uint64_t qd = sw128_desc(smem_u32(sm + (c % ST) * S::kStageBytes), 16, 1024);
-                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+                // The three 32 x 32 blocks of S that are not masked, each in another group of 32 lanes (a warp
+                // reads its own group only, so P's work spreads over three of the SM's four quarters):
+                //   columns 0..31 (keys 0..31), A from 32 rows before Q: tokens 0..31 in lanes 32..63,
+                //                                                        tokens 32..63 in lanes 64..95
+                //   columns 32..63 (keys 32..63), A from Q's row 32:     tokens 32..63 in lanes 0..31
+                // The other rows of A are whatever lies there; nobody reads their products.
+                const uint64_t qd = sw128_desc(smb + S::kStageOff + (c % ST) * S::kStageBytes, 16, 1024);
+                constexpr uint32_t id = idesc_bf16_f32(128, 32, 0);
+                constexpr uint64_t kHalf = kChunkPanel / 2 >> 4;
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int pan = 0; pan < PAN; ++pan) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
-                            tc_mma_ss(tmem + TC_S, d, d + (kChunkPanel >> 4), id, pan + k > 0);
+                            tc_mma_ss(tmem + TC_S, d - kHalf, d + (kChunkPanel >> 4), id, pan + k > 0);
+                            tc_mma_ss(tmem + TC_S + 32, d + kHalf, d + (kChunkPanel >> 4) + kHalf, id, pan + k > 0);
                         }
                     }
                     tc_commit(s_ready);
@@ -990,8 +1011,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
                     // 64..127 repeat the one panel
                     constexpr uint32_t id = idesc_bf16_f32(128, LC, 0) | kAMnMajor;
-                    const uint64_t pd = sw128_desc(smem_u32(sm + S::kPOff + (c & 1) * 2 * kChunkPanel), 16, 1024);
-                    const uint64_t vd = sw128_desc(smem_u32(sm + (c % ST) * S::kStageBytes + S::kVOff),
+                    const uint64_t pd = sw128_desc(smb + S::kPOff + (c & 1) * 2 * kChunkPanel, 16, 1024);
+                    const uint64_t vd = sw128_desc(smb + S::kStageOff + (c % ST) * S::kStageBytes + S::kVOff,
                                                    PAN == 2 ? kChunkPanel : 0, 1024);
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
@@ -1008,7 +1029,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (elect_one()) tc_commit(drain);
         __syncwarp();
-        chunk_wait(drain, 0u, nullptr, p.err);
+        chunk_wait(drain, 0u, &never);
         __syncwarp();
     }
     }
@@ -1016,6 +1037,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0 && (abort_flag[0] | abort_flag[1])) record_error(p.err, ERR_TIMEOUT | SRC_LINEAR);
 }
 
 // kernel<<<grid, block, smem>>> as the programmatic dependent of the launch before it
