@@ -1173,7 +1173,7 @@ static LinearLayout linear_layout(int batch, int num_heads_q, int num_heads_kv, 
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     LinearLayout l;
     l.units = 256;   // the count in front
-    l.decay = l.units + up(sizeof(int4) * ((size_t)batch + linear_extra_segments(num_heads_q)));
+    l.decay = l.units + up((size_t)kLinearUnitBytes * ((size_t)batch + linear_extra_segments(num_heads_q)));
     l.states = l.decay + up(sizeof(float) * (size_t)num_heads_kv * kLinearDecayRow);
     l.bytes = l.states + sizeof(float) * (size_t)linear_state_rows(batch, num_heads_q, num_heads_kv, true) *
                              num_heads_kv * head_dim * head_dim;
@@ -1273,7 +1273,7 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
     const LinearLayout l = linear_layout(batch, num_heads_q, num_heads_kv, head_dim);
     char *ws = reinterpret_cast<char *>(workspace);
     p.unit_count = reinterpret_cast<int *>(ws);
-    p.units = reinterpret_cast<int4 *>(ws + l.units);
+    p.units = ws + l.units;
     p.decay = reinterpret_cast<float *>(ws + l.decay);
     p.states = reinterpret_cast<float *>(ws + l.states);
     CUtensorMap qmap, kmap, vmap;

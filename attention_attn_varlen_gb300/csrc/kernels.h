@@ -155,13 +155,13 @@ struct LinearParams {
     // prompts: the work list and the states at segment starts, in the workspace
     int seg_len;                      // a longer sequence is cut into segments of this many tokens (a multiple of 64)
     int max_units, state_rows;        // entries of units, rows of states
-    int4 *units;                      // (sequence, segment, first row of states or -1, segments)
+    void *units;                      // kLinearUnitBytes each
     int *unit_count;
     float *decay;                     // [Hkv, kLinearDecayRow]
     float *states;                    // [state_rows, Hkv, D, D]
     uint32_t *err;
 };
-constexpr int kLinearDecayRow = 136;
+constexpr int kLinearDecayRow = 136, kLinearUnitBytes = 32;
 cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream);

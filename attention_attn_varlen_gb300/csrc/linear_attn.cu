@@ -196,7 +196,7 @@ struct ChunkSmem {
     // first non-finite token per dv, four chunks
     static constexpr int kTabBytes = 5 * LC * 4 + 4 * 128 * 4;
     static constexpr int kBarOff = kTabOff + kTabBytes;
-    static constexpr int kNumBars = 3 * kStages + 11;
+    static constexpr int kNumBars = 2 * kStages + 10;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -243,7 +243,8 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 }
 
 // Registers of the calling warpgroup.  The kernel is launched with 64 a thread; the eight
-// warpgroups' shares add up to that: V 2, state 4, output rows 1, the others 1.
+// warpgroups' shares add up to that: V 2, state 4 (which keep what they have), output rows 1,
+// the others 1.
 constexpr int kVRegs = 56, kStateRegs = 72, kOutRegs = 64, kRestRegs = 48;
 static_assert(2 * kVRegs + 4 * kStateRegs + kOutRegs + kRestRegs == 8 * 64, "register shares");
 template <int N> __device__ __forceinline__ void more_regs() {
@@ -305,30 +306,20 @@ __device__ __forceinline__ void put_p(uint8_t *ph, int i, int ch, float (&x)[8])
     *reinterpret_cast<uint4 *>(ph + kChunkPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-// Tokens of unit `u` and the segment's place in its sequence.
-struct ChunkUnit {
-    int b, n, row;      // n tokens, state row in the workspace (-1: none)
-    int64_t t0;
-    bool last;          // holds the sequence's last token
+// A unit's entry in the work list, as the plan writes it.
+struct alignas(16) ChunkUnit {
+    int t0, n;          // first token, tokens
+    int row;            // its start in the workspace's states (-1: none)
+    int last;           // holds the sequence's last token
+    int slot, from;     // state slot (-1: none), whether the sequence starts from it
+    int head;           // first segment: the sequence's segments, else 0
+    int more;           // has a successor
 };
-
-__device__ __forceinline__ ChunkUnit chunk_unit(const LinearParams &p, const int4 e) {
-    ChunkUnit u;
-    int len;
-    linear_rows(p, e.x, u.t0, len, false);
-    u.b = e.x;
-    u.row = e.z < 0 ? -1 : e.z + e.y;
-    const int at = e.y * p.seg_len;
-    u.t0 += at;
-    u.n = min(len - at, p.seg_len);
-    u.last = at + u.n == len;
-    return u;
-}
+static_assert(sizeof(ChunkUnit) == kLinearUnitBytes, "workspace layout");
 
 // The work list: a unit is a sequence, or a segment of seg_len tokens of a longer
 // one; units with the most chunks come first (the hardware starts CTAs in order,
-// so the long ones do not end up alone at the end).  Entry: (sequence, segment,
-// state rows in the workspace or -1, segments).  CTA 0 writes the list, the others
+// so the long ones do not end up alone at the end).  CTA 0 writes the list, the others
 // the heads' decay tables.
 __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
@@ -375,7 +366,8 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p)
                 atomicAdd(&count[bucket(tail)], 1);
             } else {
                 bool from;
-                linear_state(p, b, 0, from, true);
+                const float *state = linear_state(p, b, 0, from, true);
+                const int slot = state ? __ldg(p.slots + b) : -1;
                 // a state of its own for every segment's start; heads that share a state
                 // read a copy, since one of them writes the new one
                 const bool rows = segs > 1 || (from && p.G > 1);
@@ -385,7 +377,11 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p)
                 if (!fits) row = -1;
                 for (int i = 0; i < segs; ++i) {
                     const int at = atomicAdd(&count[bucket(i < segs - 1 ? p.seg_len : tail)], 1);
-                    if (at < p.max_units) p.units[at] = make_int4(b, i, row, segs);
+                    const bool end = i == segs - 1;
+                    if (at < p.max_units)
+                        reinterpret_cast<ChunkUnit *>(p.units)[at] =
+                            ChunkUnit{(int)t0 + i * p.seg_len, end ? tail : p.seg_len, row < 0 ? -1 : row + i, end,
+                                      slot, from, i == 0 ? segs : 0, !end};
                     else fits = false;
                 }
                 if (!fits) record_error(p.err, ERR_INDEX | SRC_LINEAR);
@@ -418,28 +414,27 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p)
 __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x >= *p.unit_count) return;
-    const int4 e = p.units[blockIdx.x];
-    if (e.y != 0 || e.z < 0) return;
+    const ChunkUnit e = reinterpret_cast<const ChunkUnit *>(p.units)[blockIdx.x];
+    if (e.head == 0 || e.row < 0) return;
     const int h = blockIdx.y, D2 = p.D * p.D;
-    bool from;
-    const float *state = linear_state(p, e.x, h, from, false);
+    const float *state = p.state + ((int64_t)e.slot * p.Hkv + h) * D2;   // read only if e.from
     const float *t = p.decay + (int64_t)h * kDecayRow + 2 * LC + 2;
     const float hi = t[0], lo = t[1];
     const int x = (blockIdx.z * 256 + threadIdx.x) * 4;
     if (x >= D2) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (from) run = *reinterpret_cast<const float4 *>(state + x);
-    float *at = p.states + ((int64_t)e.z * p.Hkv + h) * D2 + x;
+    if (e.from) run = *reinterpret_cast<const float4 *>(state + x);
+    float *at = p.states + ((int64_t)e.row * p.Hkv + h) * D2 + x;
     const int64_t step = (int64_t)p.Hkv * D2;
     constexpr int kAhead = 8;   // loads in flight per thread: the sums are read before starts replace them
-    for (int s0 = 0; s0 < e.w; s0 += kAhead) {
+    for (int s0 = 0; s0 < e.head; s0 += kAhead) {
         float4 own[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (s0 + k + 1 < e.w) own[k] = *reinterpret_cast<const float4 *>(at + (s0 + k) * step);
+            if (s0 + k + 1 < e.head) own[k] = *reinterpret_cast<const float4 *>(at + (s0 + k) * step);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            if (s0 + k >= e.w) break;
+            if (s0 + k >= e.head) break;
             *reinterpret_cast<float4 *>(at + (s0 + k) * step) = run;
             run.x = fmaf(hi, run.x, fmaf(lo, run.x, own[k].x));
             run.y = fmaf(hi, run.y, fmaf(lo, run.y, own[k].y));
@@ -466,9 +461,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int heads = LOCAL ? p.Hkv : p.Hq;
     const int at = blockIdx.x / heads, h = blockIdx.x - at * heads;
     if (at >= *p.unit_count) return;
-    const int4 entry = p.units[at];
-    if (LOCAL && entry.y + 1 >= entry.w) return;
-    const ChunkUnit u = chunk_unit(p, entry);
+    const ChunkUnit u = reinterpret_cast<const ChunkUnit *>(p.units)[at];
+    if (LOCAL && !u.more) return;
     const int hk = LOCAL ? h : h / p.G;
     const int chunks = uni((u.n + LC - 1) / LC);
     const int n_last = uni(u.n - (chunks - 1) * LC);
@@ -477,19 +471,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint8_t *sm = lsmem_raw + (smb - smem_u32(lsmem_raw));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *full = bars, *empty = bars + ST;
-    uint64_t *v_ready = bars + 2 * ST;       // [ST]: the stage's V may be read by PV (tail rows and non-finite
-                                             //   entries are zeroed); per stage, as PV may lag behind KV
-    uint64_t *w_ready = bars + 3 * ST;       // (w V)^T of the chunk is in TMEM
-    uint64_t *w_free = w_ready + 1;          // ... and KV has read it
-    uint64_t *s_ready = w_ready + 2;         // QK done
-    uint64_t *p_ready = w_ready + 3;         // P in shared memory, QK's columns free
-    uint64_t *o_ready = w_ready + 4;         // QS and PV done
-    uint64_t *o_free = w_ready + 5;          // the output warps have read both
-    uint64_t *qs_done = w_ready + 6;         // QS has read S_0
-    uint64_t *st_ready = w_ready + 7;        // the next S_0 is in TMEM
-    uint64_t *kv_ready = w_ready + 8;        // KV done
-    uint64_t *kv_free = w_ready + 9;         // the state warps have read it
-    uint64_t *drain = w_ready + 10;          // every MMA done
+    uint64_t *kv_go = bars + 2 * ST;         // (w V)^T of the chunk is in place (and V's tail and non-finite entries
+                                             //   are zeroed), the KV before has been read
+    uint64_t *w_free = kv_go + 1;            // KV has read (w V)^T
+    uint64_t *kv_ready = kv_go + 2;          // KV done
+    uint64_t *qs_go = kv_go + 3;             // S_0 is in TMEM, the output warps have read the chunk before
+    uint64_t *qs_done = kv_go + 4;           // QS has read S_0
+    uint64_t *s_ready = kv_go + 5;           // QK done
+    uint64_t *p_ready = kv_go + 6;           // P in shared memory, QK's columns free
+    uint64_t *pv_go = kv_go + 7;             // QS is issued: what it waited for holds for PV too
+    uint64_t *o_ready = kv_go + 8;           // QS and PV done
+    uint64_t *drain = kv_go + 9;             // every MMA done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *tab = reinterpret_cast<float *>(sm + S::kTabOff) + LC;   // scale e^{m g}, zeros in front
@@ -497,26 +489,44 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float *w_full = tab1 + LC, *w_last = w_full + LC;
     int *bad_at = reinterpret_cast<int *>(w_last + LC);             // [4][128]
 
-    if (threadIdx.x == 0) {
+    // the loader sets the barriers up, and its first copies are on their way before the others are ready
+    if (warp == 28 && lane == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&v_ready[i], 8);
             mbar_init(&empty[i], LOCAL ? 9 : 10);   // each MMA thread, the eight V warps
         }
-        mbar_init(w_ready, 8);
+        mbar_init(kv_go, 8 + 16);            // V, state
         mbar_init(w_free, 1);
+        mbar_init(kv_ready, 1);
+        mbar_init(qs_go, 16 + 4);            // state, output
+        mbar_init(qs_done, 1);
         mbar_init(s_ready, 1);
         mbar_init(p_ready, 3);
+        mbar_init(pv_go, 1);
         mbar_init(o_ready, 2);               // QS, PV
-        mbar_init(o_free, 4);
-        mbar_init(kv_ready, 1);
-        mbar_init(kv_free, 16);
-        mbar_init(qs_done, 1);
-        mbar_init(st_ready, 16);
         mbar_init(drain, 2);                 // each MMA thread
         abort_flag[0] = abort_flag[1] = 0;
         fence_mbar_init();
     }
+    int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 28)
+    auto load = [&]() {                      // the next chunk's, once its stage is free
+        const int c = loaded, s = c % ST;
+        if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag)) return false;
+        uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
+        const int row = (int)(u.t0 + (int64_t)c * LC);
+        mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
+#pragma unroll
+        for (int x = 0; x < PAN; ++x) {
+            if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, h, row);
+            tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
+            tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
+        }
+        ++loaded;
+        return true;
+    };
+    if (warp == 28 && lane == 0)
+        for (int c = 0; c < min(chunks, ST); ++c) load();
+    __syncwarp();
     if (warp == 0) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -611,13 +621,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             if (!waited) break;
             fence_proxy_async_smem();
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(w_ready);
-                if (LOCAL) mbar_arrive(&empty[s]);
-            }
             if (!LOCAL) {
                 const bool any_bad = __any_sync(0xffffffffu, !(zero0 + zero1 == 0.f));
                 if (any_bad) {
@@ -644,16 +647,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 } else if (lane < 16) {
                     bad_at[(c & 3) * 128 + grp * 32 + hl * 16 + lane] = LC;
                 }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&v_ready[s]);
-                    mbar_arrive(&empty[s]);
-                }
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(kv_go);
+                mbar_arrive(&empty[s]);
             }
         }
     } else if (warp < 24) {
-        more_regs<kStateRegs>();
         // ============================================================ state: thread = value dimension, a quarter of dk
+        more_regs<kStateRegs>();
         const int grp = warp & 3, part = (warp - 8) >> 2, dv = grp * 32 + lane;
         const bool real = grp * 32 < D;      // warp-uniform
         const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
@@ -661,12 +666,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         float St[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) St[i] = 0.f;
-        bool from = false;
-        float *state = linear_state(p, u.b, hk, from, false);
+        float *state = u.slot < 0 ? nullptr : p.state + ((int64_t)u.slot * p.Hkv + hk) * D * D;
         if (!LOCAL && real) {
             const float *src = nullptr;
             if (u.row >= 0) src = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
-            else if (from) src = state;
+            else if (u.from) src = state;
             if (src) {
 #pragma unroll
                 for (int i = 0; i < N; i += 4) {
@@ -695,36 +699,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const float a_full = decay[LC], a_full_lo = decay[2 * LC + 1];
         const float a_last = decay[n_last], a_last_lo = decay[LC + 1 + n_last];
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const bool full_chunk = c + 1 < chunks;
-            const float a = full_chunk ? a_full : a_last, a_lo = full_chunk ? a_full_lo : a_last_lo;
-            if (!LOCAL) {
-                if (c > 0 && !(ok = wait(qs_done, c - 1))) break;
+        for (int c = -1; c < chunks; ++c) {
+            if (c >= 0) {
+                const bool full_chunk = c + 1 < chunks;
+                const float a = full_chunk ? a_full : a_last, a_lo = full_chunk ? a_full_lo : a_last_lo;
+                if (!(ok = wait(kv_ready, c))) break;
+                tc_fence_after();
+                if (real) {
+#pragma unroll
+                    for (int i = 0; i < N; i += 16) {
+                        uint32_t kv[16];
+                        tmem_ld16(lane_base + TC_KV + part * N + i, kv);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            float x0, x1;
+                            fma2(x0, x1, a_lo, a_lo, St[i + k], St[i + k + 1], __uint_as_float(kv[k]),
+                                 __uint_as_float(kv[k + 1]));
+                            fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
+                        }
+                    }
+                    tc_fence_before();
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv_go);           // first: there is no KV to be read yet
+            if (!LOCAL && c + 1 < chunks) {
+                if (c >= 0 && !(ok = wait(qs_done, c))) break;
                 tc_fence_after();
                 if (real) publish();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(st_ready);
+                if (lane == 0) mbar_arrive(qs_go);
             }
-            if (!(ok = wait(kv_ready, c))) break;
-            tc_fence_after();
-            if (real) {
-#pragma unroll
-                for (int i = 0; i < N; i += 16) {
-                    uint32_t kv[16];
-                    tmem_ld16(lane_base + TC_KV + part * N + i, kv);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        float x0, x1;
-                        fma2(x0, x1, a_lo, a_lo, St[i + k], St[i + k + 1], __uint_as_float(kv[k]),
-                             __uint_as_float(kv[k + 1]));
-                        fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
-                    }
-                }
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(kv_free);
         }
         float *dst = nullptr;
         if (LOCAL) dst = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
@@ -750,6 +756,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // Group 2 first has tokens 32..63 of P against keys 0..31 (lanes 64..95, columns 0..31): all of
             // them before those tokens, e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}.  It runs a chunk ahead.
             bool ok = true;
+            if (lane == 0) mbar_arrive(qs_go);           // nothing to be read yet
 #pragma unroll 1
             for (int c = grp == 2 ? -1 : 0; c < chunks && ok; ++c) {
                 const int n = c + 1 < chunks ? LC : n_last;
@@ -785,7 +792,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!wait(o_ready, c)) break;
                 tc_fence_after();
                 if (!real) {
-                    if (lane == 0) mbar_arrive(o_free);
+                    if (lane == 0) mbar_arrive(qs_go);
                     continue;
                 }
                 const int *bad_row = bad_at + (c & 3) * 128 + grp * 32;
@@ -802,7 +809,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (part == 3) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(o_free);
+                        if (lane == 0) mbar_arrive(qs_go);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {           // tokens 8 (g0 + i / 2) + q2, + 1; dv + 8 (i % 2)
@@ -840,22 +847,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (warp < 30) {
         // ============================================================ loads (warp 28), P: thread = query token
         const int half = warp - 28;
-        int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 28)
-        auto load = [&]() {                      // the next chunk's, once its stage is free
-            const int c = loaded, s = c % ST;
-            if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag)) return false;
-            uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
-            const int row = (int)(u.t0 + (int64_t)c * LC);
-            mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
-#pragma unroll
-            for (int x = 0; x < PAN; ++x) {
-                if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, h, row);
-                tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
-                tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
-            }
-            ++loaded;
-            return true;
-        };
         if (LOCAL && half == 0 && lane == 0)
             while (loaded < chunks && load()) {
             }
@@ -873,10 +864,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     *reinterpret_cast<uint4 *>(pbuf + (k >> 2) * kChunkPanel + sw128_off(i, 4 + (k & 3))) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
-            // warp 28 first fills the ring
 #pragma unroll 1
-            for (int c = half == 0 ? -min(chunks, ST) : 0; c < chunks; ++c) {
-                if (c >= 0) {
+            for (int c = 0; c < chunks; ++c) {
+                {
                     uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
                     if (!wait(s_ready, c)) break;
                     tc_fence_after();
@@ -903,7 +893,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (lane == 0) mbar_arrive(p_ready);
                 }
                 // past the first chunk: the stage of the chunk before comes free about now
-                if (half == 0 && lane == 0 && c != 0 && loaded < chunks) load();
+                if (half == 0 && lane == 0 && c > 0 && loaded < chunks) load();
                 __syncwarp();
             }
         }
@@ -915,14 +905,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     } else if (warp == 30) {
         // ============================================================ MMA: KV and QS
         // Two threads issue, so that one's waits (about 100 clocks each) fall into the other's
-        // products.  w_ready and p_ready come from threads that saw the chunk's copies land.
-        bool ok = true;
+        // products.  kv_go comes from threads that saw the chunk's copies land.
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c % ST;
             const uint32_t qk = smb + S::kStageOff + s * S::kStageBytes;
-            ok = (c == 0 || wait(kv_free, c - 1)) && wait(w_ready, c);
-            if (!ok) break;
+            if (!wait(kv_go, c)) break;
             tc_fence_after();
             if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
@@ -943,8 +931,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
             if (LOCAL) continue;
-            ok = (c == 0 || wait(o_free, c - 1)) && wait(st_ready, c);
-            if (!ok) break;
+            if (!wait(qs_go, c)) break;
             tc_fence_after();
             if (elect_one()) {
                 constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
@@ -959,6 +946,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tc_commit(qs_done);
                 tc_commit(o_ready);
                 tc_commit(&empty[s]);
+                mbar_arrive(pv_go);
             }
             __syncwarp();
         }
@@ -1004,8 +992,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (c + 1 < chunks) issue_qk(c + 1);
-                ok = (c == 0 || wait(o_free, c - 1)) && wait(&v_ready[c % ST], c / ST);
-                if (!ok) break;
+                if (!wait(pv_go, c)) break;
                 tc_fence_after();
                 if (elect_one()) {
                     // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
