@@ -1262,6 +1262,7 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
     p.max_seqlen = max_seqlen;
     p.start_zero = context_lens == nullptr;
     p.err = d->err;
+    p.num_sms = d->num_sms;
     p.seg_len = linear_seg_len(total_tokens, num_heads_q, max_seqlen);
     const bool split = p.seg_len < max_seqlen;
     const int64_t units = (int64_t)batch + (split ? linear_extra_segments(num_heads_q) : 0);

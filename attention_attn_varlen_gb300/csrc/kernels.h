@@ -144,7 +144,7 @@ struct LinearParams {
     const __nv_bfloat16 *q, *k, *v;   // [T, H, D] with row strides
     __nv_bfloat16 *out;
     const float *log_decay;           // [Hkv]
-    const int32_t *cu;                // [batch + 1]; null: one token per sequence (decode)
+    const int32_t *cu;                // [batch + 1] (prompts)
     float *state;                     // [num_slots, Hkv, D, D], rows along the value dimension; null: none kept
     const int32_t *slots;             // [batch]; < 0: no state
     const int32_t *context_lens;      // [batch] or null; 0: the sequence starts from a zero state
@@ -155,6 +155,7 @@ struct LinearParams {
     // prompts: the work list and the states at segment starts, in the workspace
     int seg_len;                      // a longer sequence is cut into segments of this many tokens (a multiple of 64)
     int max_units, state_rows;        // entries of units, rows of states
+    int num_sms;                      // CTAs of the prompt kernel at most
     void *units;                      // kLinearUnitBytes each
     int *unit_count;
     float *decay;                     // [Hkv, kLinearDecayRow]

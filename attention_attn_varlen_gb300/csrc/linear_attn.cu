@@ -11,14 +11,8 @@
 namespace attn {
 namespace {
 
-// Tokens [t0, t0 + n) of sequence b; n = 0 for bad offsets (recorded once by the
-// CTA of head 0).
-__device__ __forceinline__ bool linear_rows(const LinearParams &p, int b, int64_t &t0, int &n, bool report) {
-    if (!p.cu) {
-        t0 = b;
-        n = 1;
-        return true;
-    }
+// Tokens [t0, t0 + n) of sequence b; n = 0 for bad offsets.
+__device__ __forceinline__ void linear_rows(const LinearParams &p, int b, int64_t &t0, int &n, bool report) {
     const int64_t a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1);
     bool ok = a >= 0 && e >= a && e <= p.total_tokens;
     t0 = ok ? a : 0;
@@ -28,7 +22,6 @@ __device__ __forceinline__ bool linear_rows(const LinearParams &p, int b, int64_
         n = p.max_seqlen;
     }
     if (!ok && report) record_error(p.err, ERR_INDEX | SRC_LINEAR);
-    return ok;
 }
 
 // State of sequence b, KV head h: its address (null: none kept) and whether the
@@ -143,12 +136,12 @@ cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
 //   S_n = e^{n g} S_0 + sum_j e^{(n-1-j) g} v_j k_j^T
 // Every exponent is <= 0: nothing overflows whatever the decay.
 //
-// As matrices with the value dimension in the 128 TMEM lanes (so that all but
-// the first have M = 128, and both S and V are A operands read from TMEM):
-//   QK     [i, j]   = Q K^T                 shared x shared
+// As matrices with the value dimension in the 128 TMEM lanes (a product with M = 64
+// takes as long as one with M = 128, and S and w V are then A operands read from TMEM):
+//   QK     [i, j]   = Q K^T                 shared x shared, three of its four 32 x 32 blocks
 //   QS     [dv, i]  = S_0 Q^T               TMEM (S_0 as two bf16 parts) x shared
-//   PV     [dv, i]  = V^T P^T               TMEM (V^T, exact) x shared (P as two bf16 parts)
-//   KV     [dv, dk] = (w_j V)^T K           TMEM (three bf16 parts) x shared
+//   PV     [dv, i]  = V^T P^T               shared (V as loaded, exact) x shared (P as two bf16 parts)
+//   KV     [dv, dk] = (w_j V)^T K           TMEM (two bf16 parts) and shared (the third) x shared
 // with P = scale * e^{(i-j) g} QK (masked) and w_j = e^{(n-1-j) g}.
 //
 // Precision.  q, k and v are bf16 and exact.  P and S_0 only reach the bf16 output:
@@ -157,13 +150,27 @@ cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
 // or two parts would leave 1.7e-3 or 2.8e-6 of it.  S itself stays in fp32 registers;
 // e^{64 g} multiplies it as hi + lo, so its rounding does not add up over chunks.
 //
-// Bound by HBM: 1 KB per token and head at head_dim 128 (q, k, v read, out
-// written), 65,536 / 152 SMs of it per chunk in 1.49 us; the products above are
-// 12.6 MFLOP there, about 1 us of one SM's tensor core.
+// Bound by the tensor core.  Per chunk of head_dim 128: KV 12 steps of 16 tokens (N = 128, 66
+// clocks), QS 16 steps (N = 64, 33), PV 8 (both operands shared, 50), QK 16 (N = 32, about 17):
+// near 2,000 clocks, 1 us, where HBM's 64 KB would take 1.4 us of an SM's share only if it
+// had its inputs to itself; and the chunks of a sequence follow one another: KV -> S -> QS.
+// So everything else is taken off the one warp that issues and spread over
+// roles that run side by side, each a chunk or less apart.
 //
-// Roles (20 warps): V preparation (transposes V into TMEM, plain and weighted),
-// state (fp32 registers; adds KV, writes S_0's two parts), output rows, P, one
-// thread issuing every MMA, one thread issuing the loads.
+// Roles (32 warps, one CTA per SM):
+//   0..7    V preparation: w V, three parts, transposed into TMEM and shared memory
+//   8..23   state: fp32 registers; adds KV, writes S_0's two parts
+//   24..27  output rows (26 also the block of P below the diagonal ones)
+//   28, 29  P's diagonal blocks; 28 issues the loads, 29 writes the units' tables
+//   30, 31  issue the MMAs: KV and QS; QK (a chunk ahead) and PV
+// What counted, each measured on 16 prompts of a step (32 heads of 128): roles side by side
+// instead of in turn 634 -> 387 us; PV's A straight from the loaded V, QK's blocks spread over
+// three lane groups, waits off the issuing threads 387 -> 324; operands
+// warp-uniform and one code site per role's step, 64 -> 38 KB of code (the instruction
+// cache is shared by all roles) 324 -> 294; fewer barriers 294 -> 280.  One CTA per SM that
+// goes over its units, the next one's tables and copies under way while one ends: 96 short
+// sequences 70 -> 51 us, the prompts as they were; one segment per SM pays 5 us
+// of 194 for the code it adds (32,768 tokens).
 // ---------------------------------------------------------------------------
 
 constexpr int LC = 64;                       // tokens of a chunk
@@ -180,6 +187,13 @@ constexpr int kDecayRow = kLinearDecayRow;   // floats of a head's decay table: 
                                              // below fp32 of each, then e^{seg_len g} in two parts
 constexpr int kBuckets = 256;
 
+// A unit as its roles read it, behind its tables.
+struct UnitInfo {
+    int count;                        // tokens; 0: there is no such unit
+    int t0, h, hk, row, slot, from, last;
+    float a_full, a_full_lo, a_last, a_last_lo;   // e^{n g} over a full chunk and over the last one, two parts each
+};
+
 template <int D>
 struct ChunkSmem {
     static constexpr int kPanels = D / 64;
@@ -192,11 +206,12 @@ struct ChunkSmem {
     static constexpr int kLoOff = kPOff + 4 * kChunkPanel;       // the third part of w V, laid out like V
     static constexpr int kOutOff = kLoOff + kPanels * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
     static constexpr int kTabOff = kOutOff + 4 * LC * 64;
-    // scale e^{m g}: zeros for m = -64..-1, then m = 0..63; m = 1..64; w of a full chunk, of the last chunk;
-    // first non-finite token per dv, four chunks
-    static constexpr int kTabBytes = 5 * LC * 4 + 4 * 128 * 4;
+    // two units' tables: scale e^{m g}, zeros for m = -64..-1, then m = 0..63; m = 1..64; w of a full chunk, of
+    // the last chunk.  Then the first non-finite token per dv, four chunks
+    static constexpr int kTabFloats = 5 * LC + 16;               // ... and the unit itself (UnitInfo)
+    static constexpr int kTabBytes = 2 * kTabFloats * 4 + 4 * 128 * 4;
     static constexpr int kBarOff = kTabOff + kTabBytes;
-    static constexpr int kNumBars = 2 * kStages + 10;
+    static constexpr int kNumBars = 2 * kStages + 14;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -243,8 +258,7 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 }
 
 // Registers of the calling warpgroup.  The kernel is launched with 64 a thread; the eight
-// warpgroups' shares add up to that: V 2, state 4 (which keep what they have), output rows 1,
-// the others 1.
+// warpgroups' shares add up to that: V 2, state 4, output rows 1 (which keep theirs), the others 1.
 constexpr int kVRegs = 56, kStateRegs = 72, kOutRegs = 64, kRestRegs = 48;
 static_assert(2 * kVRegs + 4 * kStateRegs + kOutRegs + kRestRegs == 8 * 64, "register shares");
 template <int N> __device__ __forceinline__ void more_regs() {
@@ -318,8 +332,7 @@ struct alignas(16) ChunkUnit {
 static_assert(sizeof(ChunkUnit) == kLinearUnitBytes, "workspace layout");
 
 // The work list: a unit is a sequence, or a segment of seg_len tokens of a longer
-// one; units with the most chunks come first (the hardware starts CTAs in order,
-// so the long ones do not end up alone at the end).  CTA 0 writes the list, the others
+// one; units with the most chunks come first.  CTA 0 writes the list, the others
 // the heads' decay tables.
 __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
@@ -459,20 +472,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int heads = LOCAL ? p.Hkv : p.Hq;
-    const int at = blockIdx.x / heads, h = blockIdx.x - at * heads;
-    if (at >= *p.unit_count) return;
-    const ChunkUnit u = reinterpret_cast<const ChunkUnit *>(p.units)[at];
-    if (LOCAL && !u.more) return;
-    const int hk = LOCAL ? h : h / p.G;
-    const int chunks = uni((u.n + LC - 1) / LC);
-    const int n_last = uni(u.n - (chunks - 1) * LC);
+    // The CTA's units: places blockIdx.x, 2 gridDim.x - 1 - blockIdx.x, 2 gridDim.x + blockIdx.x, ... of the
+    // list (longest first), back and forth so that the CTAs' sums come out alike.  Warp 29 writes each
+    // unit's tables, a unit ahead; the roles go by them.  Chunks are counted on from unit to unit (g), as
+    // are the barriers' phases.
+    const ChunkUnit *units = reinterpret_cast<const ChunkUnit *>(p.units);
+    const int units_n = uni(*p.unit_count), total = units_n * heads, G = gridDim.x;
+    auto place = [&](int k) { return k * G + ((k & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x); };
+    if (place(0) >= total) return;
+    auto chunks_of = [](int n) { return (n + LC - 1) / LC; };
 
     const uint32_t smb = (smem_u32(lsmem_raw) + 1023u) & ~1023u;          // shared-memory address, for descriptors
     uint8_t *sm = lsmem_raw + (smb - smem_u32(lsmem_raw));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *full = bars, *empty = bars + ST;
     uint64_t *kv_go = bars + 2 * ST;         // (w V)^T of the chunk is in place (and V's tail and non-finite entries
-                                             //   are zeroed), the KV before has been read
+    //   are zeroed), the KV before has been read
     uint64_t *w_free = kv_go + 1;            // KV has read (w V)^T
     uint64_t *kv_ready = kv_go + 2;          // KV done
     uint64_t *qs_go = kv_go + 3;             // S_0 is in TMEM, the output warps have read the chunk before
@@ -482,12 +497,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t *pv_go = kv_go + 7;             // QS is issued: what it waited for holds for PV too
     uint64_t *o_ready = kv_go + 8;           // QS and PV done
     uint64_t *drain = kv_go + 9;             // every MMA done
+    uint64_t *tab_full = kv_go + 10;         // [2]: a unit's tables are written
+    uint64_t *tab_free = kv_go + 12;         // [2]: ... and read for the last time
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *tab = reinterpret_cast<float *>(sm + S::kTabOff) + LC;   // scale e^{m g}, zeros in front
-    float *tab1 = tab + LC;                                         // scale e^{(m + 1) g}
-    float *w_full = tab1 + LC, *w_last = w_full + LC;
-    int *bad_at = reinterpret_cast<int *>(w_last + LC);             // [4][128]
+    float *tables = reinterpret_cast<float *>(sm + S::kTabOff);
+    int *bad_at = reinterpret_cast<int *>(tables + 2 * S::kTabFloats);   // [4][128]
+    // of unit number m: scale e^{j g} (zeros in front), scale e^{(j + 1) g}, w of a full and of the last chunk
+    auto tab_of = [&](int m) { return tables + (m & 1) * S::kTabFloats + LC; };
+    auto info_of = [&](int m) { return reinterpret_cast<UnitInfo *>(tables + (m & 1) * S::kTabFloats + 5 * LC); };
 
     // the loader sets the barriers up, and its first copies are on their way before the others are ready
     if (warp == 28 && lane == 0) {
@@ -505,41 +523,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(pv_go, 1);
         mbar_init(o_ready, 2);               // QS, PV
         mbar_init(drain, 2);                 // each MMA thread
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tab_full[i], 1);
+            mbar_init(&tab_free[i], LOCAL ? 8 + 16 + 1 : 32);   // every warp that reads them
+        }
         abort_flag[0] = abort_flag[1] = 0;
         fence_mbar_init();
     }
-    int loaded = 0;                          // chunks whose copies have been issued (lane 0 of warp 28)
-    auto load = [&]() {                      // the next chunk's, once its stage is free
-        const int c = loaded, s = c % ST;
-        if (c >= ST && !chunk_wait(&empty[s], (uint32_t)(c / ST - 1) & 1u, abort_flag)) return false;
-        uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
-        const int row = (int)(u.t0 + (int64_t)c * LC);
-        mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
-#pragma unroll
-        for (int x = 0; x < PAN; ++x) {
-            if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, h, row);
-            tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
-            tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
-        }
-        ++loaded;
-        return true;
-    };
-    if (warp == 28 && lane == 0)
-        for (int c = 0; c < min(chunks, ST); ++c) load();
-    __syncwarp();
     if (warp == 0) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    const float *decay = p.decay + (int64_t)hk * kDecayRow;
-    if (threadIdx.x < LC) {
-        const int j = threadIdx.x;
-        tab[j - LC] = 0.f;
-        tab[j] = p.scale * decay[j];
-        tab1[j] = p.scale * decay[j + 1];
-        w_full[j] = decay[LC - 1 - j];
-        w_last[j] = j < n_last ? decay[n_last - 1 - j] : 0.f;
-    }
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * LC)
+        tables[(threadIdx.x - 64) / LC * S::kTabFloats + (threadIdx.x & (LC - 1))] = 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -562,76 +558,83 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // head_dim 64: lane groups 2 and 3 repeat 0 and 1 (lanes 64..127 reach no output)
         const int d8 = ((grp * 32) & (D - 1)) / 8 + 2 * hl + ((lane >> 3) & 1);
         const uint32_t frag = S::kVOff + (d8 >> 3) * kChunkPanel + sw128_off((lane >> 4) * 8 + (lane & 7), d8 & 7);
+        int g = 0;                               // chunks before unit m
+        bool ok = true;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const int s = c % ST, n = c + 1 < chunks ? LC : n_last;
-            const float *w = (c + 1 < chunks ? w_full : w_last) + q2;
-            uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
-            if (!wait(&full[s], c / ST)) break;
-            if (n < LC) {
-                // rows behind the sequence's end are zeroed (a weight of 0 would not cancel a NaN there)
-                const int per = (LC - n) * 8;
-                for (int x = threadIdx.x; x < per * 2 * PAN; x += 256) {
-                    const int tile = x / per, r = x - tile * per, pan = tile >> 1;
-                    uint8_t *at = tile & 1 ? stage + S::kVOff + pan * kChunkPanel
-                                           : stage + pan * S::kQkPanel + kChunkPanel;
-                    *reinterpret_cast<uint4 *>(at + n * 128 + r * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int m = 0;; ++m) {
+            if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+            const UnitInfo *u = info_of(m);
+            const int count = uni(u->count), chunks = chunks_of(count);
+            if (count == 0) break;
+#pragma unroll 1
+            for (int c = 0; c < chunks && ok; ++c) {
+                const int gc = g + c, s = gc % ST, n = min(LC, count - c * LC);
+                const float *w = tab_of(m) + (c + 1 < chunks ? 2 : 3) * LC + q2;
+                uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
+                if (!(ok = wait(&full[s], gc / ST))) break;
+                if (n < LC) {
+                    // rows behind the sequence's end are zeroed (a weight of 0 would not cancel a NaN there)
+                    const int per = (LC - n) * 8;
+                    for (int x = threadIdx.x; x < per * 2 * PAN; x += 256) {
+                        const int tile = x / per, r = x - tile * per, pan = tile >> 1;
+                        uint8_t *at = tile & 1 ? stage + S::kVOff + pan * kChunkPanel
+                                               : stage + pan * S::kQkPanel + kChunkPanel;
+                        *reinterpret_cast<uint4 *>(at + n * 128 + r * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
-            }
-            // in two steps of 32 tokens; raw[2 g + x]: dv 8 x + lane / 4, tokens 32 step + 8 g + q2, + 1
-            float zero0 = 0.f, zero1 = 0.f;             // NaN once a non-finite v went by
-            bool waited = true;
+                // in two steps of 32 tokens; raw[2 g + x]: dv 8 x + lane / 4, tokens 32 step + 8 g + q2, + 1
+                float zero0 = 0.f, zero1 = 0.f;             // NaN once a non-finite v went by
 #pragma unroll 1
-            for (int step = 0; step < 2; ++step) {
-                uint32_t raw[8], hi[8], mid[8], lo[8];
-                const uint32_t at = smem_u32(stage) + frag + step * 4096;
-                ldsm_x4_t(at, raw[0], raw[1], raw[2], raw[3]);
-                ldsm_x4_t(at + 2048, raw[4], raw[5], raw[6], raw[7]);
-                if (n < LC) {                           // (another warp may still be zeroing these rows)
+                for (int step = 0; step < 2; ++step) {
+                    uint32_t raw[8], hi[8], mid[8], lo[8];
+                    const uint32_t at = smem_u32(stage) + frag + step * 4096;
+                    ldsm_x4_t(at, raw[0], raw[1], raw[2], raw[3]);
+                    ldsm_x4_t(at + 2048, raw[4], raw[5], raw[6], raw[7]);
+                    if (n < LC) {                           // (another warp may still be zeroing these rows)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = step * 32 + (i >> 1) * 8 + q2;
+                            raw[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int j = step * 32 + (i >> 1) * 8 + q2;
-                        raw[i] &= (j < n ? 0xFFFFu : 0u) | (j + 1 < n ? 0xFFFF0000u : 0u);
+                        const float2 wj = *reinterpret_cast<const float2 *>(w + step * 32 + (i >> 1) * 8);
+                        const float v0 = __uint_as_float(raw[i] << 16), v1 = __uint_as_float(raw[i] & 0xFFFF0000u);
+                        float x0, x1;
+                        if (!LOCAL) fma2(zero0, zero1, v0, v1, 0.f, 0.f, zero0, zero1);
+                        fma2(x0, x1, v0, v1, wj.x, wj.y, 0.f, 0.f);
+                        hi[i] = take_bf16(x0, x1);
+                        mid[i] = take_bf16(x0, x1);
+                        lo[i] = pack_bf16x2(x0, x1);
+                    }
+                    if (step == 0 && gc > 0) {
+                        ok = wait(w_free, gc - 1);
+                        tc_fence_after();
+                    }
+                    if (!ok) break;
+                    tmem_st_16x128b_x4(lane_base + TC_W + step * 16, hi);
+                    tmem_st_16x128b_x4(lane_base + TC_W + 32 + step * 16, mid);
+                    if (grp * 32 < D) {
+                        const uint32_t to = smem_u32(sm + S::kLoOff) + (frag - S::kVOff) + step * 4096;
+                        stsm_x4_t(to, lo[0], lo[1], lo[2], lo[3]);
+                        stsm_x4_t(to + 2048, lo[4], lo[5], lo[6], lo[7]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 wj = *reinterpret_cast<const float2 *>(w + step * 32 + (i >> 1) * 8);
-                    const float v0 = __uint_as_float(raw[i] << 16), v1 = __uint_as_float(raw[i] & 0xFFFF0000u);
-                    float x0, x1;
-                    if (!LOCAL) fma2(zero0, zero1, v0, v1, 0.f, 0.f, zero0, zero1);
-                    fma2(x0, x1, v0, v1, wj.x, wj.y, 0.f, 0.f);
-                    hi[i] = take_bf16(x0, x1);
-                    mid[i] = take_bf16(x0, x1);
-                    lo[i] = pack_bf16x2(x0, x1);
-                }
-                if (step == 0 && c > 0) {
-                    waited = wait(w_free, c - 1);
-                    tc_fence_after();
-                }
-                if (!waited) break;
-                tmem_st_16x128b_x4(lane_base + TC_W + step * 16, hi);
-                tmem_st_16x128b_x4(lane_base + TC_W + 32 + step * 16, mid);
-                if (grp * 32 < D) {
-                    const uint32_t to = smem_u32(sm + S::kLoOff) + (frag - S::kVOff) + step * 4096;
-                    stsm_x4_t(to, lo[0], lo[1], lo[2], lo[3]);
-                    stsm_x4_t(to + 2048, lo[4], lo[5], lo[6], lo[7]);
-                }
-            }
-            if (!waited) break;
-            fence_proxy_async_smem();
-            if (!LOCAL) {
-                const bool any_bad = __any_sync(0xffffffffu, !(zero0 + zero1 == 0.f));
-                if (any_bad) {
-                    // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
-                    // zeroed there and the output warps write NaN from its token on
+                if (!ok) break;
+                fence_proxy_async_smem();
+                if (!LOCAL) {
+                    const bool any_bad = __any_sync(0xffffffffu, !(zero0 + zero1 == 0.f));
+                    if (any_bad) {
+                        // a non-finite v: in PV it would reach the chunk's earlier tokens (0 * NaN), so it is
+                        // zeroed there and the output warps write NaN from its token on
 #pragma unroll 1
-                    for (int r = 0; r < 2; ++r) {       // two rows of the fragment: dv 8 r + lane / 4
-                        const int row = grp * 32 + hl * 16 + 8 * r + (lane >> 2);
-                        int first = LC;
-                        if (row < D)
-                            for (int j = q2; j < n; j += (j & 1) ? 7 : 1) {
+                        for (int r = 0; r < 2; ++r) {       // two rows of the fragment: dv 8 r + lane / 4
+                            const int row = grp * 32 + hl * 16 + 8 * r + (lane >> 2);
+                            int first = LC;
+                            if (row < D)
+                                for (int j = q2; j < n; j += (j & 1) ? 7 : 1) {
                                 uint16_t *v = reinterpret_cast<uint16_t *>(
                                     stage + S::kVOff + (row >> 6) * kChunkPanel + sw128_off(j, (row & 63) >> 3) + (row & 7) * 2);
                                 if ((*v & 0x7F80u) == 0x7F80u) {
@@ -639,22 +642,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                     first = min(first, j);
                                 }
                             }
-                        first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
-                        first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
-                        if ((lane & 3) == 0 && row < D) bad_at[(c & 3) * 128 + row] = first;
+                            first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+                            first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
+                            if ((lane & 3) == 0 && row < D) bad_at[(gc & 3) * 128 + row] = first;
+                        }
+                        fence_proxy_async_smem();
+                    } else if (lane < 16) {
+                        bad_at[(gc & 3) * 128 + grp * 32 + hl * 16 + lane] = LC;
                     }
-                    fence_proxy_async_smem();
-                } else if (lane < 16) {
-                    bad_at[(c & 3) * 128 + grp * 32 + hl * 16 + lane] = LC;
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(kv_go);
+                    mbar_arrive(&empty[s]);
                 }
             }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(kv_go);
-                mbar_arrive(&empty[s]);
-            }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&tab_free[m & 1]);
+            g += chunks;
         }
     } else if (warp < 24) {
         // ============================================================ state: thread = value dimension, a quarter of dk
@@ -664,21 +671,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
         constexpr int N = D / 4;             // columns per thread
         float St[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) St[i] = 0.f;
-        float *state = u.slot < 0 ? nullptr : p.state + ((int64_t)u.slot * p.Hkv + hk) * D * D;
-        if (!LOCAL && real) {
-            const float *src = nullptr;
-            if (u.row >= 0) src = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
-            else if (u.from) src = state;
-            if (src) {
-#pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src + dv * D + part * N + i);
-                    St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
-                }
-            }
-        }
         auto publish = [&]() {               // S_0's two parts to TMEM
 #pragma unroll
             for (int i = 0; i < N; i += 16) {
@@ -695,51 +687,69 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_wait_st();
             tc_fence_before();
         };
+        int g = 0;                               // chunks before unit m
         bool ok = true;
-        const float a_full = decay[LC], a_full_lo = decay[2 * LC + 1];
-        const float a_last = decay[n_last], a_last_lo = decay[LC + 1 + n_last];
 #pragma unroll 1
-        for (int c = -1; c < chunks; ++c) {
-            if (c >= 0) {
-                const bool full_chunk = c + 1 < chunks;
-                const float a = full_chunk ? a_full : a_last, a_lo = full_chunk ? a_full_lo : a_last_lo;
-                if (!(ok = wait(kv_ready, c))) break;
-                tc_fence_after();
-                if (real) {
+        for (int m = 0;; ++m) {
+            if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+            const UnitInfo *u = info_of(m);
+            const int count = uni(u->count), chunks = chunks_of(count);
+            if (count == 0) break;
+            float *state = u->slot < 0 ? nullptr : p.state + ((int64_t)u->slot * p.Hkv + u->hk) * D * D;
+            float *own = u->row < 0 ? nullptr : p.states + ((int64_t)u->row * p.Hkv + u->hk) * D * D;
+            const float *src = LOCAL ? nullptr : own ? own : u->from ? state : nullptr;
 #pragma unroll
-                    for (int i = 0; i < N; i += 16) {
-                        uint32_t kv[16];
-                        tmem_ld16(lane_base + TC_KV + part * N + i, kv);
-                        tc_wait_ld();
+            for (int i = 0; i < N; i += 4) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (src && real) x = *reinterpret_cast<const float4 *>(src + dv * D + part * N + i);
+                St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
+            }
+#pragma unroll 1
+            for (int c = -1; c < chunks; ++c) {
+                const int gc = g + c;
+                if (c >= 0) {
+                    const bool mid = c + 1 < chunks;
+                    const float a = mid ? u->a_full : u->a_last, a_lo = mid ? u->a_full_lo : u->a_last_lo;
+                    if (!(ok = wait(kv_ready, gc))) break;
+                    tc_fence_after();
+                    if (real) {
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            float x0, x1;
-                            fma2(x0, x1, a_lo, a_lo, St[i + k], St[i + k + 1], __uint_as_float(kv[k]),
-                                 __uint_as_float(kv[k + 1]));
-                            fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
+                        for (int i = 0; i < N; i += 16) {
+                            uint32_t kv[16];
+                            tmem_ld16(lane_base + TC_KV + part * N + i, kv);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                float x0, x1;
+                                fma2(x0, x1, a_lo, a_lo, St[i + k], St[i + k + 1], __uint_as_float(kv[k]),
+                                     __uint_as_float(kv[k + 1]));
+                                fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
+                            }
                         }
+                        tc_fence_before();
                     }
-                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0 && (c >= 0 || m == 0)) mbar_arrive(kv_go);   // at the very first: no KV to be read yet
+                if (!LOCAL && c + 1 < chunks) {
+                    if (gc >= 0 && !(ok = wait(qs_done, gc))) break;
+                    tc_fence_after();
+                    if (real) publish();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qs_go);
                 }
             }
+            if (!ok) break;
+            float *dst = LOCAL ? own : u->last ? state : nullptr;
             __syncwarp();
-            if (lane == 0) mbar_arrive(kv_go);           // first: there is no KV to be read yet
-            if (!LOCAL && c + 1 < chunks) {
-                if (c >= 0 && !(ok = wait(qs_done, c))) break;
-                tc_fence_after();
-                if (real) publish();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(qs_go);
-            }
-        }
-        float *dst = nullptr;
-        if (LOCAL) dst = p.states + ((int64_t)u.row * p.Hkv + hk) * D * D;
-        else if (u.last && h % p.G == 0) dst = state;
-        if (ok && real && dst && (!LOCAL || u.row >= 0)) {
+            if (lane == 0) mbar_arrive(&tab_free[m & 1]);
+            if (real && dst) {
 #pragma unroll
-            for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4 *>(dst + dv * D + part * N + i) =
-                    make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
+                for (int i = 0; i < N; i += 4)
+                    *reinterpret_cast<float4 *>(dst + dv * D + part * N + i) =
+                        make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
+            }
+            g += chunks;
         }
     } else if (warp < 28) {
         // ============================================================ output rows: a warp per 32 value dimensions
@@ -755,270 +765,414 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const uint32_t stg_at = smem_u32(stg) + row0 * 64;
             // Group 2 first has tokens 32..63 of P against keys 0..31 (lanes 64..95, columns 0..31): all of
             // them before those tokens, e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}.  It runs a chunk ahead.
-            bool ok = true;
             if (lane == 0) mbar_arrive(qs_go);           // nothing to be read yet
+            int g = 0;                               // chunks before unit m
+            bool ok = true;
 #pragma unroll 1
-            for (int c = grp == 2 ? -1 : 0; c < chunks && ok; ++c) {
-                const int n = c + 1 < chunks ? LC : n_last;
-                if (grp == 2 && c + 1 < chunks) {
-                    if (!(ok = wait(s_ready, c + 1))) break;
-                    tc_fence_after();
-                    uint8_t *ph = sm + S::kPOff + ((c + 1) & 1) * 2 * kChunkPanel;
-                    const float f = tab[lane + 1];
-                    uint32_t s[8];
-                    tmem_ld8(lane_base + TC_S, s);
-                    tc_wait_ld();
+            for (int m = 0;; ++m) {
+                if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+                const UnitInfo *u = info_of(m);
+                const int count = uni(u->count), chunks = chunks_of(count);
+                if (count == 0) break;
+                const int t0 = u->t0, h = u->h;
 #pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + k * 8);
-                        const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + k * 8);
-                        const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-                        float x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
-                            fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), 0.f, 0.f);
-                        }
-                        tmem_ld8(lane_base + TC_S + ((k * 8 + 8) & 31), s);
-                        put_p(ph, 32 + lane, k, x);
+                for (int c = grp == 2 && m == 0 ? -1 : 0; c < chunks && ok; ++c) {
+                    const int gc = g + c, n = min(LC, count - c * LC);
+                    const int of = c + 1 < chunks ? m : m + 1;    // the unit of the next chunk
+                    if (grp == 2 && !(ok = wait(&tab_full[of & 1], of >> 1))) break;
+                    if (grp == 2 && info_of(of)->count > 0) {
+                        if (!(ok = wait(s_ready, gc + 1))) break;
+                        const float *tab = tab_of(of), *w_full = tab + 2 * LC;
+                        tc_fence_after();
+                        uint8_t *ph = sm + S::kPOff + ((gc + 1) & 1) * 2 * kChunkPanel;
+                        const float f = tab[lane + 1];
+                        uint32_t s[8];
+                        tmem_ld8(lane_base + TC_S, s);
                         tc_wait_ld();
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready);
-                    if (c < 0) continue;
-                }
-                if (!wait(o_ready, c)) break;
-                tc_fence_after();
-                if (!real) {
-                    if (lane == 0) mbar_arrive(qs_go);
-                    continue;
-                }
-                const int *bad_row = bad_at + (c & 3) * 128 + grp * 32;
-                const bool any_bad = __any_sync(0xffffffffu, bad_row[lane] < LC);
 #pragma unroll 1
-                for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
-                    const int hl = part >> 1, g0 = (part & 1) * 4;
-                    const uint32_t at = lane_base + ((uint32_t)hl << 20) + g0 * 8;
-                    uint32_t x[16], y[16], r[8];
-                    tmem_ld_16x256b_x4(at + TC_INTRA, x);
-                    tmem_ld_16x256b_x4(at + TC_INTER, y);
-                    const float *e = tab1 + g0 * 8 + q2;
-                    tc_wait_ld();
-                    if (part == 3) {
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + k * 8);
+                            const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + k * 8);
+                            const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                            float x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
+                                fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]),
+                                     0.f, 0.f);
+                            }
+                            tmem_ld8(lane_base + TC_S + ((k * 8 + 8) & 31), s);
+                            put_p(ph, 32 + lane, k, x);
+                            tc_wait_ld();
+                        }
+                        fence_proxy_async_smem();
                         tc_fence_before();
                         __syncwarp();
+                        if (lane == 0) mbar_arrive(p_ready);
+                        if (c < 0) continue;
+                    }
+                    if (!(ok = wait(o_ready, gc))) break;
+                    tc_fence_after();
+                    if (!real) {
                         if (lane == 0) mbar_arrive(qs_go);
+                        continue;
                     }
+                    const int *bad_row = bad_at + (gc & 3) * 128 + grp * 32;
+                    const bool any_bad = __any_sync(0xffffffffu, bad_row[lane] < LC);
+#pragma unroll 1
+                    for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
+                        const int hl = part >> 1, g0 = (part & 1) * 4;
+                        const uint32_t at = lane_base + ((uint32_t)hl << 20) + g0 * 8;
+                        uint32_t x[16], y[16], r[8];
+                        tmem_ld_16x256b_x4(at + TC_INTRA, x);
+                        tmem_ld_16x256b_x4(at + TC_INTER, y);
+                        const float *e = tab_of(m) + LC + g0 * 8 + q2;
+                        tc_wait_ld();
+                        if (part == 3) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(qs_go);
+                        }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {           // tokens 8 (g0 + i / 2) + q2, + 1; dv + 8 (i % 2)
-                        const float2 f = *reinterpret_cast<const float2 *>(e + (i / 2) * 8);
-                        float o0, o1;
-                        fma2(o0, o1, f.x, f.y, __uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]),
-                             __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                        r[i] = pack_bf16x2(o0, o1);
+                        for (int i = 0; i < 8; ++i) {           // tokens 8 (g0 + i / 2) + q2, + 1; dv + 8 (i % 2)
+                            const float2 f = *reinterpret_cast<const float2 *>(e + (i / 2) * 8);
+                            float o0, o1;
+                            fma2(o0, o1, f.x, f.y, __uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]),
+                                 __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                            r[i] = pack_bf16x2(o0, o1);
+                        }
+                        const uint32_t to = stg_at + (uint32_t)(g0 * 512) + (((hl * 2 + ch0) ^ sw) << 4);
+                        stsm_x4_t(to, r[0], r[1], r[2], r[3]);
+                        stsm_x4_t(to + 1024, r[4], r[5], r[6], r[7]);
                     }
-                    const uint32_t to = stg_at + (uint32_t)(g0 * 512) + (((hl * 2 + ch0) ^ sw) << 4);
-                    stsm_x4_t(to, r[0], r[1], r[2], r[3]);
-                    stsm_x4_t(to + 1024, r[4], r[5], r[6], r[7]);
-                }
-                __syncwarp();
-                if (any_bad) {
-                    // NaN from a dv's first non-finite token on
-                    const int first = bad_row[lane];
-                    for (int t = first; t < LC; ++t)
-                        *reinterpret_cast<uint16_t *>(stg + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + (lane & 7) * 2) =
-                            0x7FC0;
-                }
-                __syncwarp();
-                __nv_bfloat16 *out = p.out + (u.t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
+                    __syncwarp();
+                    if (any_bad) {
+                        // NaN from a dv's first non-finite token on
+                        const int first = bad_row[lane];
+                        for (int t = first; t < LC; ++t)
+                            *reinterpret_cast<uint16_t *>(stg + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) +
+                                                          (lane & 7) * 2) =
+                                0x7FC0;
+                    }
+                    __syncwarp();
+                    __nv_bfloat16 *out = p.out + (t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
 #pragma unroll 2
-                for (int i = 0; i < LC / 8; ++i) {
-                    const int t = i * 8 + (lane >> 2);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
-                    if (t < n) *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) = v;
+                    for (int i = 0; i < LC / 8; ++i) {
+                        const int t = i * 8 + (lane >> 2);
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                        if (t < n) *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) = v;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&tab_free[m & 1]);
+                g += chunks;
             }
         }
     } else {
         fewer_regs<kRestRegs>();
-    if (warp < 30) {
-        // ============================================================ loads (warp 28), P: thread = query token
-        const int half = warp - 28;
-        if (LOCAL && half == 0 && lane == 0)
-            while (loaded < chunks && load()) {
-            }
-        __syncwarp();
-        if (!LOCAL) {
-            // warp 28: tokens 32..63 and keys 32..63 (lanes 0..31, columns 32..63), warp 29: tokens and keys
-            // 0..31 (lanes 32..63, columns 0..31)
-            const int b0 = half == 0 ? 32 : 0, i = b0 + lane;
-            const uint32_t at = tmem + ((uint32_t)(half * 32) << 16) + TC_S + b0;
-            uint8_t *pbuf = sm + S::kPOff;
-            if (half == 1) {
-                // tokens 0..31 see no key behind 31: those halves of their rows stay zero
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    *reinterpret_cast<uint4 *>(pbuf + (k >> 2) * kChunkPanel + sw128_off(i, 4 + (k & 3))) =
-                        make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                {
-                    uint8_t *ph = pbuf + (c & 1) * 2 * kChunkPanel;
-                    if (!wait(s_ready, c)) break;
-                    tc_fence_after();
-                    // 8 keys at a time, the next ones loading meanwhile
-                    uint32_t s[8];
-                    tmem_ld8(at, s);
-                    tc_wait_ld();
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        const int d = lane - k * 8;
-                        const float *e = tab + d;
-                        float x[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            // masked by choice, not by the table's zeros, which would keep a NaN
-                            x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
-                        tmem_ld8(at + ((k * 8 + 8) & 31), s);
-                        put_p(ph, i, b0 / 8 + k, x);
-                        tc_wait_ld();
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready);
-                }
-                // past the first chunk: the stage of the chunk before comes free about now
-                if (half == 0 && lane == 0 && c > 0 && loaded < chunks) load();
-                __syncwarp();
-            }
-        }
-        // copies still in flight (after a wait that gave up) land before the CTA ends
-        if (half == 0 && lane == 0)
-            for (int d = max(0, loaded - ST); d < loaded; ++d)
-                chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, &never);
-        __syncwarp();
-    } else if (warp == 30) {
-        // ============================================================ MMA: KV and QS
-        // Two threads issue, so that one's waits (about 100 clocks each) fall into the other's
-        // products.  kv_go comes from threads that saw the chunk's copies land.
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const int s = c % ST;
-            const uint32_t qk = smb + S::kStageOff + s * S::kStageBytes;
-            if (!wait(kv_go, c)) break;
-            tc_fence_after();
-            if (elect_one()) {
-                constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
-                const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
-                const uint64_t ld = sw128_desc(smb + S::kLoOff, PAN == 2 ? kChunkPanel : 0, 1024);
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                    for (int k = 0; k < LC / 16; ++k)
-                        tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8, kd + k * (16 * 128 >> 4), id, part + k > 0);
-                }
-#pragma unroll
-                for (int k = 0; k < LC / 16; ++k)
-                    tc_mma_ss(tmem + TC_KV, ld + k * (16 * 128 >> 4), kd + k * (16 * 128 >> 4), id | kAMnMajor, 1);
-                tc_commit(kv_ready);
-                tc_commit(w_free);
-                if (LOCAL) tc_commit(&empty[s]);
-            }
-            __syncwarp();
-            if (LOCAL) continue;
-            if (!wait(qs_go, c)) break;
-            tc_fence_after();
-            if (elect_one()) {
-                constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
-                const uint64_t qd = sw128_desc(qk, 16, 1024);
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + k * 8,
-                                  qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2, id, part + k > 0);
-                }
-                tc_commit(qs_done);
-                tc_commit(o_ready);
-                tc_commit(&empty[s]);
-                mbar_arrive(pv_go);
-            }
-            __syncwarp();
-        }
-        // nothing of this CTA's is left in the tensor core when TMEM goes back
-        if (elect_one()) tc_commit(drain);
-        __syncwarp();
-        chunk_wait(drain, 0u, &never);
-        __syncwarp();
-    } else {
-        // ============================================================ MMA: QK, a chunk ahead, and PV
-        if (!LOCAL) {
-            bool ok = true;
-            auto issue_qk = [&](int c) {
-                // The three 32 x 32 blocks of S that are not masked, each in another group of 32 lanes (a warp
-                // reads its own group only, so P's work spreads over three of the SM's four quarters):
-                //   columns 0..31 (keys 0..31), A from 32 rows before Q: tokens 0..31 in lanes 32..63,
-                //                                                        tokens 32..63 in lanes 64..95
-                //   columns 32..63 (keys 32..63), A from Q's row 32:     tokens 32..63 in lanes 0..31
-                // The other rows of A are whatever lies there; nobody reads their products.
-                const uint64_t qd = sw128_desc(smb + S::kStageOff + (c % ST) * S::kStageBytes, 16, 1024);
-                constexpr uint32_t id = idesc_bf16_f32(128, 32, 0);
-                constexpr uint64_t kHalf = kChunkPanel / 2 >> 4;
-                if (elect_one()) {
-#pragma unroll 1
-                    for (int pan = 0; pan < PAN; ++pan) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
-                            tc_mma_ss(tmem + TC_S, d - kHalf, d + (kChunkPanel >> 4), id, pan + k > 0);
-                            tc_mma_ss(tmem + TC_S + 32, d + kHalf, d + (kChunkPanel >> 4) + kHalf, id, pan + k > 0);
-                        }
-                    }
-                    tc_commit(s_ready);
-                }
-                __syncwarp();
+        if (warp < 30) {
+            // ============================================================ loads (warp 28), P: thread = query token
+            const int half = warp - 28;
+            // Both walk the CTA's places: `at` and `h` are the next one's unit and head, without a division
+            const int up = 2 * (G - 1 - (int)blockIdx.x) + 1, down = 2 * (int)blockIdx.x + 1;   // to the next place
+            // x / y of x < 2^18: off by less than 2^-20 of itself, and half a step away from the next integer
+            auto quotient = [](int x, float inv) { return (int)(((float)x + 0.5f) * inv); };
+            const float inv_heads = __fdividef(1.f, (float)heads), inv_g = __fdividef(1.f, (float)p.G);
+            const int up_q = uni(quotient(up, inv_heads)), up_r = up - up_q * heads;
+            const int down_q = uni(quotient(down, inv_heads)), down_r = down - down_q * heads;
+            int k = 0, at = uni(quotient(blockIdx.x, inv_heads)), h = blockIdx.x - at * heads;
+            auto step = [&]() {
+                at += k & 1 ? down_q : up_q;
+                h += k & 1 ? down_r : up_r;
+                if (h >= heads) h -= heads, ++at;
+                ++k;
             };
-            ok = wait(&full[0], 0);
-            tc_fence_after();
-            if (ok) issue_qk(0);
+            int loaded = 0, left = 0, row = 0, load_h = 0;   // the loader: chunks so far, the unit it is in
+            // the next chunk's copies, once its stage is free (lane 0 of warp 28); false: no more
+            auto load = [&]() {
+                while (left == 0) {
+                    if (at >= units_n) return false;
+                    const ChunkUnit *u = units + at;
+                    if (!LOCAL || u->more) {
+                        load_h = h;
+                        row = u->t0;
+                        left = chunks_of(u->n);
+                    }
+                    step();
+                }
+                const int s = loaded % ST, hk = LOCAL ? load_h : quotient(load_h, inv_g);
+                if (loaded >= ST && !chunk_wait(&empty[s], (uint32_t)(loaded / ST - 1) & 1u, abort_flag)) return false;
+                uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
+                mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
 #pragma unroll 1
-            for (int c = 0; c < chunks && ok; ++c) {
-                ok = (c + 1 >= chunks || wait(&full[(c + 1) % ST], (c + 1) / ST)) && wait(p_ready, c);
-                if (!ok) break;
-                tc_fence_after();
-                if (c + 1 < chunks) issue_qk(c + 1);
-                if (!wait(pv_go, c)) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
-                    // 64..127 repeat the one panel
-                    constexpr uint32_t id = idesc_bf16_f32(128, LC, 0) | kAMnMajor;
-                    const uint64_t pd = sw128_desc(smb + S::kPOff + (c & 1) * 2 * kChunkPanel, 16, 1024);
-                    const uint64_t vd = sw128_desc(smb + S::kStageOff + (c % ST) * S::kStageBytes + S::kVOff,
-                                                   PAN == 2 ? kChunkPanel : 0, 1024);
+                for (int x = 0; x < PAN; ++x) {
+                    if (!LOCAL) tma_load_3d(stage + x * S::kQkPanel, &qmap, &full[s], x * 64, load_h, row);
+                    tma_load_3d(stage + x * S::kQkPanel + kChunkPanel, &kmap, &full[s], x * 64, hk, row);
+                    tma_load_3d(stage + S::kVOff + x * kChunkPanel, &vmap, &full[s], x * 64, hk, row);
+                }
+                ++loaded;
+                --left;
+                row += LC;
+                return true;
+            };
+            if (LOCAL && half == 0 && lane == 0)
+                while (load()) {
+                }
+            __syncwarp();
+            // warp 29 writes the units' tables, a unit ahead; behind the last one an empty unit
+            int written = 0;
+            auto write_tables = [&]() {
+                const int m = written++;
+                if (m >= 2 && !wait(&tab_free[m & 1], (m >> 1) - 1)) return false;
+                while (LOCAL && at < units_n && !units[at].more) step();
+                const bool some = at < units_n;
+                float *t = tab_of(m);
+                UnitInfo *info = info_of(m);
+                if (some) {
+                    const int hk = LOCAL ? h : uni(quotient(h, inv_g));
+                    const ChunkUnit u = units[at];
+                    const int n_last = u.n - (chunks_of(u.n) - 1) * LC;
+                    const float *decay = p.decay + (int64_t)hk * kDecayRow;
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
+                    for (int j = lane; j < LC; j += 32) {
+                        t[j] = p.scale * decay[j];
+                        t[LC + j] = p.scale * decay[j + 1];
+                        t[2 * LC + j] = decay[LC - 1 - j];
+                        t[3 * LC + j] = j < n_last ? decay[n_last - 1 - j] : 0.f;
+                    }
+                    if (lane == 0)
+                        *info = UnitInfo{u.n, u.t0, h, hk, u.row, u.slot, u.from, u.last && (LOCAL || h == hk * p.G),
+                                         decay[LC], decay[2 * LC + 1], decay[n_last], decay[LC + 1 + n_last]};
+                    step();
+                } else if (lane == 0) {
+                    info->count = 0;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tab_full[m & 1]);
+                return some;
+            };
+            if (LOCAL && half == 1)
+                while (write_tables()) {
+                }
+            if (!LOCAL) {
+                // warp 28: tokens 32..63 and keys 32..63 (lanes 0..31, columns 32..63), warp 29: tokens and keys
+                // 0..31 (lanes 32..63, columns 0..31)
+                const int b0 = half == 0 ? 32 : 0, i = b0 + lane;
+                const uint32_t at = tmem + ((uint32_t)(half * 32) << 16) + TC_S + b0;
+                uint8_t *pbuf = sm + S::kPOff;
+                if (half == 1) {
+                    // tokens 0..31 see no key behind 31: those halves of their rows stay zero
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        *reinterpret_cast<uint4 *>(pbuf + (k >> 2) * kChunkPanel + sw128_off(i, 4 + (k & 3))) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+                int g = -1;                                  // chunks before unit m; -1: the first tables and copies
+                bool ok = true;
+#pragma unroll 1
+                for (int m = -1; ok; ++m) {
+                    int chunks = 1;
+                    if (m >= 0) {
+                        if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+                        chunks = uni(chunks_of(info_of(m)->count));
+                        if (chunks == 0) break;
+                    }
+                    const float *tab = tab_of(m);
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        const int gc = g + c;
+                        if (gc >= 0) {
+                            uint8_t *ph = pbuf + (gc & 1) * 2 * kChunkPanel;
+                            if (!(ok = wait(s_ready, gc))) break;
+                            tc_fence_after();
+                            // 8 keys at a time, the next ones loading meanwhile
+                            uint32_t s[8];
+                            tmem_ld8(at, s);
+                            tc_wait_ld();
+#pragma unroll 1
+                            for (int x8 = 0; x8 < 4; ++x8) {
+                                const int d = lane - x8 * 8;
+                                const float *e = tab + d;
+                                float x[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    // masked by choice, not by the table's zeros, which would keep a NaN
+                                    x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
+                                tmem_ld8(at + ((x8 * 8 + 8) & 31), s);
+                                put_p(ph, i, b0 / 8 + x8, x);
+                                tc_wait_ld();
+                            }
+                            fence_proxy_async_smem();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(p_ready);
+                        }
+                        // the stage of the chunk before comes free about now
+                        if (half == 0 && lane == 0)
+                            for (int r = gc < 0 ? ST : gc > 0 ? 1 : 0; r > 0 && load(); --r) {
+                        }
+                        __syncwarp();
+                        if (half == 1 && c == 0) write_tables();   // its wait giving up shows in the next one here
+                    }
+                    if (!ok) break;
+                    g += chunks;
+                    if (m >= 0 && lane == 0) mbar_arrive(&tab_free[m & 1]);
+                }
+            }
+            // copies still in flight (after a wait that gave up) land before the CTA ends
+            if (half == 0 && lane == 0)
+                for (int d = max(0, loaded - ST); d < loaded; ++d)
+                    chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, &never);
+            __syncwarp();
+        } else if (warp == 30) {
+            // ============================================================ MMA: KV and QS
+            // Two threads issue, so that one's waits (about 100 clocks each) fall into the other's
+            // products.  kv_go comes from threads that saw the chunk's copies land.
+            int g = 0;                               // chunks before unit m
+            bool ok = true;
+#pragma unroll 1
+            for (int m = 0;; ++m) {
+                if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+                const UnitInfo *u = info_of(m);
+                const int count = uni(u->count), chunks = chunks_of(count);
+                if (count == 0) break;
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    const int gc = g + c, s = gc % ST;
+                    const uint32_t qk = smb + S::kStageOff + s * S::kStageBytes;
+                    if (!(ok = wait(kv_go, gc))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
+                        const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
+                        const uint64_t ld = sw128_desc(smb + S::kLoOff, PAN == 2 ? kChunkPanel : 0, 1024);
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                            for (int k = 0; k < LC / 16; ++k)
+                                tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8, kd + k * (16 * 128 >> 4), id,
+                                          part + k > 0);
+                        }
 #pragma unroll
                         for (int k = 0; k < LC / 16; ++k)
-                            tc_mma_ss(tmem + TC_INTRA, vd + k * (16 * 128 >> 4), pd + part * (kChunkPanel >> 4) + k * 2, id,
-                                      part + k > 0);
+                            tc_mma_ss(tmem + TC_KV, ld + k * (16 * 128 >> 4), kd + k * (16 * 128 >> 4), id | kAMnMajor,
+                                      1);
+                        tc_commit(kv_ready);
+                        tc_commit(w_free);
+                        if (LOCAL) tc_commit(&empty[s]);
                     }
-                    tc_commit(&empty[c % ST]);
-                    tc_commit(o_ready);
+                    __syncwarp();
+                    if (LOCAL) continue;
+                    if (!(ok = wait(qs_go, gc))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
+                        const uint64_t qd = sw128_desc(qk, 16, 1024);
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k)
+                                tc_mma_ts(tmem + TC_INTER, tmem + TC_STATE + part * 64 + k * 8,
+                                          qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2, id, part + k > 0);
+                        }
+                        tc_commit(qs_done);
+                        tc_commit(o_ready);
+                        tc_commit(&empty[s]);
+                        mbar_arrive(pv_go);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&tab_free[m & 1]);
+                g += chunks;
             }
+            // nothing of this CTA's is left in the tensor core when TMEM goes back
+            if (elect_one()) tc_commit(drain);
+            __syncwarp();
+            chunk_wait(drain, 0u, &never);
+            __syncwarp();
+        } else {
+            // ============================================================ MMA: QK, a chunk ahead, and PV
+            if (!LOCAL) {
+                auto issue_qk = [&](int c) {
+                    // The three 32 x 32 blocks of S that are not masked, each in another group of 32 lanes (a warp
+                    // reads its own group only, so P's work spreads over three of the SM's four quarters):
+                    //   columns 0..31 (keys 0..31), A from 32 rows before Q: tokens 0..31 in lanes 32..63,
+                    //                                                        tokens 32..63 in lanes 64..95
+                    //   columns 32..63 (keys 32..63), A from Q's row 32:     tokens 32..63 in lanes 0..31
+                    // The other rows of A are whatever lies there; nobody reads their products.
+                    const uint64_t qd = sw128_desc(smb + S::kStageOff + (c % ST) * S::kStageBytes, 16, 1024);
+                    constexpr uint32_t id = idesc_bf16_f32(128, 32, 0);
+                    constexpr uint64_t kHalf = kChunkPanel / 2 >> 4;
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int pan = 0; pan < PAN; ++pan) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
+                                tc_mma_ss(tmem + TC_S, d - kHalf, d + (kChunkPanel >> 4), id, pan + k > 0);
+                                tc_mma_ss(tmem + TC_S + 32, d + kHalf, d + (kChunkPanel >> 4) + kHalf, id, pan + k > 0);
+                            }
+                        }
+                        tc_commit(s_ready);
+                    }
+                    __syncwarp();
+                };
+                if (wait(&full[0], 0)) {
+                    tc_fence_after();
+                    issue_qk(0);
+                }
+                int g = 0;                               // chunks before unit m
+                bool ok = true;
+#pragma unroll 1
+                for (int m = 0;; ++m) {
+                    if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+                    const UnitInfo *u = info_of(m);
+                    const int count = uni(u->count), chunks = chunks_of(count);
+                    if (count == 0) break;
+#pragma unroll 1
+                    for (int c = 0; c < chunks && ok; ++c) {
+                        const int gc = g + c;
+                        const int of = c + 1 < chunks ? m : m + 1;    // the unit of the next chunk
+                        if (!(ok = wait(&tab_full[of & 1], of >> 1))) break;
+                        const bool next = uni(info_of(of)->count) > 0;
+                        ok = (!next || wait(&full[(gc + 1) % ST], (gc + 1) / ST)) && wait(p_ready, gc);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (next) issue_qk(gc + 1);
+                        if (!(ok = wait(pv_go, gc))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
+                            // 64..127 repeat the one panel
+                            constexpr uint32_t id = idesc_bf16_f32(128, LC, 0) | kAMnMajor;
+                            const uint64_t pd = sw128_desc(smb + S::kPOff + (gc & 1) * 2 * kChunkPanel, 16, 1024);
+                            const uint64_t vd = sw128_desc(smb + S::kStageOff + (gc % ST) * S::kStageBytes + S::kVOff,
+                                                           PAN == 2 ? kChunkPanel : 0, 1024);
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                                for (int k = 0; k < LC / 16; ++k)
+                                    tc_mma_ss(tmem + TC_INTRA, vd + k * (16 * 128 >> 4),
+                                              pd + part * (kChunkPanel >> 4) + k * 2, id, part + k > 0);
+                            }
+                            tc_commit(&empty[gc % ST]);
+                            tc_commit(o_ready);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&tab_free[m & 1]);
+                    g += chunks;
+                }
+            }
+            if (elect_one()) tc_commit(drain);
+            __syncwarp();
+            chunk_wait(drain, 0u, &never);
+            __syncwarp();
         }
-        if (elect_one()) tc_commit(drain);
-        __syncwarp();
-        chunk_wait(drain, 0u, &never);
-        __syncwarp();
-    }
     }
     tc_fence_before();
     __syncthreads();
@@ -1063,10 +1217,12 @@ cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
     if (attr_err[dev] != cudaSuccess) return attr_err[dev];
     linear_plan_kernel<<<1 + (p.Hkv + 7) / 8, 1024, 0, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // a CTA per SM at most: each goes over several units
+    auto ctas = [&](int heads) { return (unsigned)min((int64_t)p.max_units * heads, (int64_t)p.num_sms); };
     const bool split = p.seg_len < p.max_seqlen;
     if (split) {
-        e = launch_after(linear_chunk_kernel<D, true>, dim3((unsigned)p.max_units * p.Hkv), kChunkThreads, S::kBytes,
-                         stream, qmap, kmap, vmap, p);
+        e = launch_after(linear_chunk_kernel<D, true>, dim3(ctas(p.Hkv)), kChunkThreads, S::kBytes, stream, qmap, kmap,
+                         vmap, p);
         if (e != cudaSuccess) return e;
     }
     if (p.state_rows > 0) {
@@ -1074,8 +1230,8 @@ cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
         if (e != cudaSuccess) return e;
     }
     main_kernel_event_before(stream);
-    e = launch_after(linear_chunk_kernel<D, false>, dim3((unsigned)p.max_units * p.Hq), kChunkThreads, S::kBytes,
-                     stream, qmap, kmap, vmap, p);
+    e = launch_after(linear_chunk_kernel<D, false>, dim3(ctas(p.Hq)), kChunkThreads, S::kBytes, stream, qmap, kmap, vmap,
+                     p);
     main_kernel_event_after(stream);
     return e;
 }

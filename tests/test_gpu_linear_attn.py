@@ -313,3 +313,92 @@ def test_a_non_finite_value_reaches_its_own_token_and_later_ones_only(D, bad):
             assert not out[t:, 1].isfinite().any()
         else:               # q: its own token
             assert not out[t, 1].isfinite().any() and torch.equal(out[t + 1:], clean[t + 1:])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 4, 128), (12, 12, 64)])
+def test_many_sequences_give_the_bits_of_each_alone(Hq, Hkv, D):
+    """Far more (sequence, head) pairs than the GPU has SMs, of mixed lengths: each
+    one's output and state are those of a call with it alone, and NaN and infinities
+    of one do not reach what is computed after it."""
+    lens = [(7 * i * i + 13 * i) % 400 for i in range(50)] + [64, 128, 1, 1, 0, 63, 65]
+    B, T = len(lens), sum(lens)
+    _, dev, gen = _inputs(Hq + D, T, Hq, Hkv, D)
+    cu, g = cu_of(lens), _decay(Hkv).cuda()
+    bad = [b for b in range(B) if b % 5 == 2 and lens[b]]
+    for b in bad:
+        for i, x in enumerate(dev):
+            x[int(cu[b]) + lens[b] // 2, 0, i] = float("inf") if b % 2 else float("nan")
+    state = torch.randn(B, Hkv, D, D, generator=gen).cuda()
+    slots = torch.randperm(B, generator=gen).to(torch.int32).cuda()
+    ctx = torch.tensor([b % 3 for b in range(B)], dtype=torch.int32, device="cuda")
+    sd = state.clone()
+    out = av.linear_attn_varlen_fwd(*dev, g, cu.cuda(), max(lens), state_cache=sd, state_slots=slots, context_lens=ctx)
+    assert av.get_last_device_error()[0] == 0
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+    for b in range(B):
+        a, e = int(cu[b]), int(cu[b + 1])
+        s1, at = state.clone(), int(slots[b])
+        one = av.linear_attn_varlen_fwd(*(x[a:e] for x in dev), g, cu_of([e - a]).cuda(), max(lens), state_cache=s1,
+                                        state_slots=slots[b:b + 1], context_lens=ctx[b:b + 1])
+        assert b in bad or (one.isfinite().all() and s1[at].isfinite().all())
+        assert same(out[a:e], one) if b not in bad else torch.equal(out[a:e].isnan(), one.isnan())
+        assert same(sd[at], s1[at]) if b not in bad else torch.equal(sd[at].isfinite(), s1[at].isfinite())
+    assert av.get_last_device_error()[0] == 0
+
+
+def test_captured_prompts_replay_on_new_lengths_and_share_a_workspace():
+    """Two graphs over one workspace, replayed in turn with other tokens and other
+    lengths within max_seqlen."""
+    B, T, Hq, Hkv, D, most = 5, 900, 4, 2, 128, 700
+    _, dev, _ = _inputs(8, T, Hq, Hkv, D, strided=False)
+    g = _decay(Hkv).cuda()
+    ws = torch.empty(av.linear_attn_workspace_size(B, Hq, Hkv, D, most), dtype=torch.uint8, device="cuda")
+    slots, ctx = torch.arange(B, dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
+    graphs = []
+    for i in range(2):
+        x, cu = [t.clone() for t in dev], torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+        sd, out = torch.zeros(B, Hkv, D, D, device="cuda"), torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+        call = lambda: av.linear_attn_varlen_fwd(*x, g, cu, most, state_cache=sd, state_slots=slots,  # noqa: E731
+                                                 context_lens=ctx, out=out, workspace=ws)
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, x, cu, sd, out))
+    steps = [[10, 0, 64, 65, 700], [1, 1, 1, 1, 1], [300, 300, 300, 0, 0], [0, 0, 0, 0, 129]]
+    want = [torch.zeros(B, Hkv, D, D, device="cuda") for _ in graphs]
+    for n, lens in enumerate(steps):
+        for i, (graph, x, cu, sd, out) in enumerate(graphs):
+            for t, src in zip(x, dev):
+                t.copy_(src.roll(n + 3 * i, 0))
+            cu.copy_(cu_of(lens))
+            graph.replay()
+            got = out[:sum(lens)].clone()
+            ref = av.linear_attn_varlen_fwd(*x, g, cu, most, state_cache=want[i], state_slots=slots, context_lens=ctx)
+            assert torch.equal(got, ref[:sum(lens)]) and torch.equal(sd, want[i])
+    assert av.get_last_device_error()[0] == 0
+
+
+def test_states_and_rows_past_32_bits_of_offset():
+    """A state slot and rows further than 2^31 elements from the first."""
+    Hq, Hkv, D, num = 8, 8, 128, 16400                    # 2^17 elements a slot
+    (q, k, v), dev, gen = _inputs(2, 70, Hq, Hkv, D)
+    g, i32 = _decay(Hkv), lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    sd = torch.empty(num, Hkv, D, D, device="cuda")
+    start = torch.randn(Hkv, D, D, generator=gen)
+    sd[num - 1] = start.cuda()
+    stride = 1 << 25                                      # row 64 is 2^31 elements behind row 0
+    far = [torch.empty(70 * stride, dtype=torch.bfloat16, device="cuda").as_strided((70, Hq, D), (stride, D, 1))
+           for _ in range(2)]
+    far[0].copy_(dev[0])
+    out = av.linear_attn_varlen_fwd(far[0], *dev[1:], g.cuda(), i32(0, 70), 70, state_cache=sd, state_slots=i32(num - 1),
+                                    context_lens=i32(1), out=far[1])
+    ref, finals, weight = linear(q, k, v, g, [0, 70], D ** -0.5, [start.double()])
+    _check(out, ref, weight, "out")
+    _check_state(sd[num - 1], *finals[0], "state")
+    sd[num - 1] = start.cuda()
+    out = av.linear_attn_decode(far[0][65:66], *(x[65:66] for x in dev[1:]), g.cuda(), sd, i32(num - 1), out=far[1][66:67])
+    ref, finals, weight = linear(q[65:66], k[65:66], v[65:66], g, [0, 1], D ** -0.5, [start.double()])
+    _check(out, ref, weight, "out")
+    _check_state(sd[num - 1], *finals[0], "state", 1)
+    assert av.get_last_device_error()[0] == 0

@@ -158,3 +158,21 @@ def test_no_tokens():
     q = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
     a, b = av.rope_store_kvcache(q, q, None, torch.empty(0, dtype=torch.int32, device="cuda"), _inv(32).cuda())
     assert a.shape == q.shape and b.shape == q.shape
+
+
+def test_slots_and_rows_past_32_bits_of_offset():
+    """A slot further than 2^31 elements into the caches, rows of q as far apart."""
+    N, H, D, num = 3, 2, 128, (1 << 23) + 7                # 2^8 elements a slot
+    gen = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn(N, H, D, generator=gen).to(torch.bfloat16) for _ in range(3))
+    stride = 1 << 30
+    qd = torch.empty((N - 1) * stride + H * D, dtype=torch.bfloat16, device="cuda").as_strided((N, H, D), (stride, D, 1))
+    qd.copy_(q.cuda())
+    kc, vc = (torch.empty(num, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos = torch.tensor([0, 7, 2 ** 31 - 1], dtype=torch.int32)
+    slots = torch.tensor([num - 1, 5, num - 6])
+    inv = _inv(D // 2)
+    got, kr = av.rope_store_kvcache(qd, k.cuda(), v.cuda(), pos.cuda(), inv.cuda(), kc, vc, slots.cuda(), return_k=True)
+    _close(got, rope(q, pos, inv, None, False, 1.0), _size(q, D // 2, False, 1.0), "q")
+    assert torch.equal(kc[slots.cuda()], kr) and torch.equal(vc[slots.cuda()].cpu(), v)
+    assert av.get_last_device_error()[0] == 0
