@@ -138,7 +138,7 @@ cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
 //
 // As matrices with the value dimension in the 128 TMEM lanes (a product with M = 64
 // takes as long as one with M = 128, and S and w V are then A operands read from TMEM):
-//   QK     [i, j]   = Q K^T                 shared x shared, three of its four 32 x 32 blocks
+//   QK     [i, j]   = Q K^T                 shared x shared
 //   QS     [dv, i]  = S_0 Q^T               TMEM (S_0 as two bf16 parts) x shared
 //   PV     [dv, i]  = V^T P^T               shared (V as loaded, exact) x shared (P as two bf16 parts)
 //   KV     [dv, dk] = (w_j V)^T K           TMEM (two bf16 parts) and shared (the third) x shared
@@ -150,27 +150,29 @@ cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
 // or two parts would leave 1.7e-3 or 2.8e-6 of it.  S itself stays in fp32 registers;
 // e^{64 g} multiplies it as hi + lo, so its rounding does not add up over chunks.
 //
-// Bound by the tensor core.  Per chunk of head_dim 128: KV 12 steps of 16 tokens (N = 128, 66
-// clocks), QS 16 steps (N = 64, 33), PV 8 (both operands shared, 50), QK 16 (N = 32, about 17):
-// near 2,000 clocks, 1 us, where HBM's 64 KB would take 1.4 us of an SM's share only if it
-// had its inputs to itself; and the chunks of a sequence follow one another: KV -> S -> QS.
-// So everything else is taken off the one warp that issues and spread over
-// roles that run side by side, each a chunk or less apart.
+// Bound by what the chunks of a sequence wait for, KV -> S -> QS -> output rows, and by the shared
+// memory that all roles and the tensor core's operands share: the tensor core is
+// busy half of the time.  Per chunk of head_dim 128: KV 12 steps of 16 tokens (N = 128, 66 clocks
+// each), QS 16 (N = 64, 33), PV and QK 8 each (both operands shared, 50): 2,100 clocks of the 3,750
+// that a chunk takes; HBM's 64 KB would take 2,700 of them.
+// So everything else is off the warps that issue, in roles that run side by side, each a
+// chunk or less apart.
 //
 // Roles (32 warps, one CTA per SM):
 //   0..7    V preparation: w V, three parts, transposed into TMEM and shared memory
-//   8..23   state: fp32 registers; adds KV, writes S_0's two parts
-//   24..27  output rows (26 also the block of P below the diagonal ones)
-//   28, 29  P's diagonal blocks; 28 issues the loads, 29 writes the units' tables
-//   30, 31  issue the MMAs: KV and QS; QK (a chunk ahead) and PV
+//   8..23   state: fp32 registers; adds KV, then (the eight that see tokens' lanes) P of the next chunk, writes
+//           S_0's two parts
+//   24..27  output rows
+//   28, 29  issue the loads; write the units' tables
+//   30, 31  issue the MMAs: KV, QS, PV; QK (a chunk ahead)
 // What counted, each measured on 16 prompts of a step (32 heads of 128): roles side by side
-// instead of in turn 634 -> 387 us; PV's A straight from the loaded V, QK's blocks spread over
-// three lane groups, waits off the issuing threads 387 -> 324; operands
-// warp-uniform and one code site per role's step, 64 -> 38 KB of code (the instruction
-// cache is shared by all roles) 324 -> 294; fewer barriers 294 -> 280.  One CTA per SM that
-// goes over its units, the next one's tables and copies under way while one ends: 96 short
-// sequences 70 -> 51 us, the prompts as they were; one segment per SM pays 5 us
-// of 194 for the code it adds (32,768 tokens).
+// instead of in turn 634 -> 387 us; PV's A straight from the loaded V, waits off the
+// issuing threads 387 -> 324; operands warp-uniform and one code site per role's step, 64 -> 38 KB
+// of code (the instruction cache is shared by all roles) 324 -> 294; fewer barriers 294 -> 280;
+// P by the state's warps in the time between KV and QS, its factors loaded
+// without branches 280 -> 266; waits that rarely read the timer 266 -> 261.  One CTA per SM that goes over
+// its units, the next one's tables and copies under way while one ends: 96 short sequences
+// 70 -> 47.5 us.
 // ---------------------------------------------------------------------------
 
 constexpr int LC = 64;                       // tokens of a chunk
@@ -201,8 +203,7 @@ struct ChunkSmem {
     static constexpr int kVOff = kPanels * kQkPanel;
     static constexpr int kStageBytes = kVOff + kPanels * kChunkPanel;
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kStageOff = kChunkPanel / 2;            // an A operand of QK starts 32 rows before Q
-    static constexpr int kPOff = kStageOff + kStages * kStageBytes;   // two chunks' P: hi, lo
+    static constexpr int kPOff = kStages * kStageBytes;        // two chunks' P: hi, lo
     static constexpr int kLoOff = kPOff + 4 * kChunkPanel;       // the third part of w V, laid out like V
     static constexpr int kOutOff = kLoOff + kPanels * kChunkPanel;      // per output warp [64 tokens][32 dv] bf16
     static constexpr int kTabOff = kOutOff + 4 * LC * 64;
@@ -211,7 +212,7 @@ struct ChunkSmem {
     static constexpr int kTabFloats = 5 * LC + 16;               // ... and the unit itself (UnitInfo)
     static constexpr int kTabBytes = 2 * kTabFloats * 4 + 4 * 128 * 4;
     static constexpr int kBarOff = kTabOff + kTabBytes;
-    static constexpr int kNumBars = 2 * kStages + 14;
+    static constexpr int kNumBars = 2 * kStages + 13;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -295,16 +296,25 @@ __device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) {
 // in it the warpgroups could not have register shares of their own.  Gives up after about a
 // second, or once another role has; the kernel's end reports it.
 __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    uint32_t t0, t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+    uint32_t t0 = 0, t;
 #pragma unroll 1
     do {
-        if (mbar_try_wait(bar, parity)) return true;
+        // the timer only once in a while: its read would hold up what is waited for (16 prompts 266 -> 259 us)
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        if (t0 == 0) t0 = t;
     } while (t - t0 < (uint32_t)kWaitLimitNs && !*abort);
     *abort = 1;
     return false;
+}
+
+// a load that stays a load of its own: the compiler would put one under a condition behind a branch
+__device__ __forceinline__ float lds_f32(const float *p) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(smem_u32(p)));
+    return x;
 }
 
 // 8 keys of token i's row of P -> 16-byte chunk `ch` of both parts
@@ -490,15 +500,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     //   are zeroed), the KV before has been read
     uint64_t *w_free = kv_go + 1;            // KV has read (w V)^T
     uint64_t *kv_ready = kv_go + 2;          // KV done
-    uint64_t *qs_go = kv_go + 3;             // S_0 is in TMEM, the output warps have read the chunk before
+    uint64_t *qs_go = kv_go + 3;             // S_0 is in TMEM, P in shared memory, the chunk before has been read
     uint64_t *qs_done = kv_go + 4;           // QS has read S_0
     uint64_t *s_ready = kv_go + 5;           // QK done
     uint64_t *p_ready = kv_go + 6;           // P in shared memory, QK's columns free
-    uint64_t *pv_go = kv_go + 7;             // QS is issued: what it waited for holds for PV too
-    uint64_t *o_ready = kv_go + 8;           // QS and PV done
-    uint64_t *drain = kv_go + 9;             // every MMA done
-    uint64_t *tab_full = kv_go + 10;         // [2]: a unit's tables are written
-    uint64_t *tab_free = kv_go + 12;         // [2]: ... and read for the last time
+    uint64_t *o_ready = kv_go + 7;           // QS and PV done
+    uint64_t *drain = kv_go + 8;             // every MMA done
+    uint64_t *tab_full = kv_go + 9;          // [2]: a unit's tables are written
+    uint64_t *tab_free = kv_go + 11;         // [2]: ... and read for the last time
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *tables = reinterpret_cast<float *>(sm + S::kTabOff);
@@ -511,7 +520,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (warp == 28 && lane == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], LOCAL ? 9 : 10);   // each MMA thread, the eight V warps
+            mbar_init(&empty[i], 1 + 8);     // the MMAs, the V warps
         }
         mbar_init(kv_go, 8 + 16);            // V, state
         mbar_init(w_free, 1);
@@ -519,13 +528,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(qs_go, 16 + 4);            // state, output
         mbar_init(qs_done, 1);
         mbar_init(s_ready, 1);
-        mbar_init(p_ready, 3);
-        mbar_init(pv_go, 1);
-        mbar_init(o_ready, 2);               // QS, PV
+        mbar_init(p_ready, 8);               // the state warps of the lanes with tokens
+        mbar_init(o_ready, 1);
         mbar_init(drain, 2);                 // each MMA thread
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tab_full[i], 1);
-            mbar_init(&tab_free[i], LOCAL ? 8 + 16 + 1 : 32);   // every warp that reads them
+            mbar_init(&tab_free[i], LOCAL ? 8 + 16 + 1 : 30);   // every warp that reads them
         }
         abort_flag[0] = abort_flag[1] = 0;
         fence_mbar_init();
@@ -533,6 +541,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (warp == 0) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
+    }
+    if (!LOCAL && warp == 29) {
+        // tokens 0..31 see no key behind 31: those halves of their rows of P stay zero
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k)
+            *reinterpret_cast<uint4 *>(sm + S::kPOff + (k >> 2) * kChunkPanel + sw128_off(lane, 4 + (k & 3))) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
     }
     if (threadIdx.x >= 64 && threadIdx.x < 64 + 2 * LC)
         tables[(threadIdx.x - 64) / LC * S::kTabFloats + (threadIdx.x & (LC - 1))] = 0.f;
@@ -570,7 +586,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int c = 0; c < chunks && ok; ++c) {
                 const int gc = g + c, s = gc % ST, n = min(LC, count - c * LC);
                 const float *w = tab_of(m) + (c + 1 < chunks ? 2 : 3) * LC + q2;
-                uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
+                uint8_t *stage = sm + s * S::kStageBytes;
                 if (!(ok = wait(&full[s], gc / ST))) break;
                 if (n < LC) {
                     // rows behind the sequence's end are zeroed (a weight of 0 would not cancel a NaN there)
@@ -636,7 +652,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             if (row < D)
                                 for (int j = q2; j < n; j += (j & 1) ? 7 : 1) {
                                 uint16_t *v = reinterpret_cast<uint16_t *>(
-                                    stage + S::kVOff + (row >> 6) * kChunkPanel + sw128_off(j, (row & 63) >> 3) + (row & 7) * 2);
+                                    stage + S::kVOff + (row >> 6) * kChunkPanel + sw128_off(j, (row & 63) >> 3) +
+                                    (row & 7) * 2);
                                 if ((*v & 0x7F80u) == 0x7F80u) {
                                     *v = 0;
                                     first = min(first, j);
@@ -730,7 +747,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0 && (c >= 0 || m == 0)) mbar_arrive(kv_go);   // at the very first: no KV to be read yet
+                const bool first_or_read = c >= 0 || m == 0;
+                if (lane == 0 && first_or_read) mbar_arrive(kv_go);   // at the very first: no KV to be read yet
+                if (!LOCAL && grp < 2 && first_or_read) {
+                    // P of the next chunk: lane = token (lanes 64..127 hold none), 8 keys at a time, in turn among
+                    // the warps of a lane group; tokens 0..31 see no key behind 31
+                    const int of = c + 1 < chunks ? m : m + 1;        // its unit
+                    if (!(ok = wait(&tab_full[of & 1], of >> 1))) break;
+                    if (uni(info_of(of)->count) > 0) {
+                        if (!(ok = wait(s_ready, gc + 1))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = part; k < 4 + 4 * grp; k += 4) {
+                            const int d = dv - k * 8;
+                            const float *e = tab_of(of) + d;
+                            float f[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) f[j] = lds_f32(e - j);
+                            uint32_t s[8];
+                            float x[8];
+                            tmem_ld8(lane_base + TC_S + k * 8, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                // masked by choice, not by the table's zeros, which would keep a NaN
+                                x[j] = j <= d ? __uint_as_float(s[j]) * f[j] : 0.f;
+                            put_p(sm + S::kPOff + ((gc + 1) & 1) * 2 * kChunkPanel, dv, k, x);
+                        }
+                        fence_proxy_async_smem();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_ready);
+                    }
+                }
                 if (!LOCAL && c + 1 < chunks) {
                     if (gc >= 0 && !(ok = wait(qs_done, gc))) break;
                     tc_fence_after();
@@ -763,8 +812,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // stmatrix row address: token (lane / 16) * 8 + lane % 8 of its group, dv chunk lane / 8 % 2
             const int row0 = (lane >> 4) * 8 + (lane & 7), ch0 = (lane >> 3) & 1, sw = (row0 >> 1) & 3;
             const uint32_t stg_at = smem_u32(stg) + row0 * 64;
-            // Group 2 first has tokens 32..63 of P against keys 0..31 (lanes 64..95, columns 0..31): all of
-            // them before those tokens, e^{(i-j) g} = e^{(i-31) g} e^{(31-j) g}.  It runs a chunk ahead.
             if (lane == 0) mbar_arrive(qs_go);           // nothing to be read yet
             int g = 0;                               // chunks before unit m
             bool ok = true;
@@ -776,41 +823,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (count == 0) break;
                 const int t0 = u->t0, h = u->h;
 #pragma unroll 1
-                for (int c = grp == 2 && m == 0 ? -1 : 0; c < chunks && ok; ++c) {
+                for (int c = 0; c < chunks; ++c) {
                     const int gc = g + c, n = min(LC, count - c * LC);
-                    const int of = c + 1 < chunks ? m : m + 1;    // the unit of the next chunk
-                    if (grp == 2 && !(ok = wait(&tab_full[of & 1], of >> 1))) break;
-                    if (grp == 2 && info_of(of)->count > 0) {
-                        if (!(ok = wait(s_ready, gc + 1))) break;
-                        const float *tab = tab_of(of), *w_full = tab + 2 * LC;
-                        tc_fence_after();
-                        uint8_t *ph = sm + S::kPOff + ((gc + 1) & 1) * 2 * kChunkPanel;
-                        const float f = tab[lane + 1];
-                        uint32_t s[8];
-                        tmem_ld8(lane_base + TC_S, s);
-                        tc_wait_ld();
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 w0 = *reinterpret_cast<const float4 *>(w_full + 32 + k * 8);
-                            const float4 w1 = *reinterpret_cast<const float4 *>(w_full + 36 + k * 8);
-                            const float wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-                            float x[8];
-#pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                fma2(x[e], x[e + 1], wk[e], wk[e + 1], f, f, 0.f, 0.f);
-                                fma2(x[e], x[e + 1], x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]),
-                                     0.f, 0.f);
-                            }
-                            tmem_ld8(lane_base + TC_S + ((k * 8 + 8) & 31), s);
-                            put_p(ph, 32 + lane, k, x);
-                            tc_wait_ld();
-                        }
-                        fence_proxy_async_smem();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_ready);
-                        if (c < 0) continue;
-                    }
                     if (!(ok = wait(o_ready, gc))) break;
                     tc_fence_after();
                     if (!real) {
@@ -873,7 +887,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     } else {
         fewer_regs<kRestRegs>();
         if (warp < 30) {
-            // ============================================================ loads (warp 28), P: thread = query token
+            // ============================================================ loads (warp 28), the units' tables (warp 29)
             const int half = warp - 28;
             // Both walk the CTA's places: `at` and `h` are the next one's unit and head, without a division
             const int up = 2 * (G - 1 - (int)blockIdx.x) + 1, down = 2 * (int)blockIdx.x + 1;   // to the next place
@@ -904,7 +918,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 const int s = loaded % ST, hk = LOCAL ? load_h : quotient(load_h, inv_g);
                 if (loaded >= ST && !chunk_wait(&empty[s], (uint32_t)(loaded / ST - 1) & 1u, abort_flag)) return false;
-                uint8_t *stage = sm + S::kStageOff + s * S::kStageBytes;
+                uint8_t *stage = sm + s * S::kStageBytes;
                 mbar_arrive_expect_tx(&full[s], (LOCAL ? 2 : 3) * PAN * kChunkPanel);
 #pragma unroll 1
                 for (int x = 0; x < PAN; ++x) {
@@ -917,10 +931,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 row += LC;
                 return true;
             };
-            if (LOCAL && half == 0 && lane == 0)
-                while (load()) {
-                }
-            __syncwarp();
             // warp 29 writes the units' tables, a unit ahead; behind the last one an empty unit
             int written = 0;
             auto write_tables = [&]() {
@@ -953,72 +963,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (lane == 0) mbar_arrive(&tab_full[m & 1]);
                 return some;
             };
-            if (LOCAL && half == 1)
+            if (half == 0 && lane == 0) {
+                while (load()) {
+                }
+            }
+            if (half == 1) {
                 while (write_tables()) {
-                }
-            if (!LOCAL) {
-                // warp 28: tokens 32..63 and keys 32..63 (lanes 0..31, columns 32..63), warp 29: tokens and keys
-                // 0..31 (lanes 32..63, columns 0..31)
-                const int b0 = half == 0 ? 32 : 0, i = b0 + lane;
-                const uint32_t at = tmem + ((uint32_t)(half * 32) << 16) + TC_S + b0;
-                uint8_t *pbuf = sm + S::kPOff;
-                if (half == 1) {
-                    // tokens 0..31 see no key behind 31: those halves of their rows stay zero
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        *reinterpret_cast<uint4 *>(pbuf + (k >> 2) * kChunkPanel + sw128_off(i, 4 + (k & 3))) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                }
-                int g = -1;                                  // chunks before unit m; -1: the first tables and copies
-                bool ok = true;
-#pragma unroll 1
-                for (int m = -1; ok; ++m) {
-                    int chunks = 1;
-                    if (m >= 0) {
-                        if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
-                        chunks = uni(chunks_of(info_of(m)->count));
-                        if (chunks == 0) break;
-                    }
-                    const float *tab = tab_of(m);
-#pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
-                        const int gc = g + c;
-                        if (gc >= 0) {
-                            uint8_t *ph = pbuf + (gc & 1) * 2 * kChunkPanel;
-                            if (!(ok = wait(s_ready, gc))) break;
-                            tc_fence_after();
-                            // 8 keys at a time, the next ones loading meanwhile
-                            uint32_t s[8];
-                            tmem_ld8(at, s);
-                            tc_wait_ld();
-#pragma unroll 1
-                            for (int x8 = 0; x8 < 4; ++x8) {
-                                const int d = lane - x8 * 8;
-                                const float *e = tab + d;
-                                float x[8];
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    // masked by choice, not by the table's zeros, which would keep a NaN
-                                    x[j] = j <= d ? __uint_as_float(s[j]) * e[-j] : 0.f;
-                                tmem_ld8(at + ((x8 * 8 + 8) & 31), s);
-                                put_p(ph, i, b0 / 8 + x8, x);
-                                tc_wait_ld();
-                            }
-                            fence_proxy_async_smem();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(p_ready);
-                        }
-                        // the stage of the chunk before comes free about now
-                        if (half == 0 && lane == 0)
-                            for (int r = gc < 0 ? ST : gc > 0 ? 1 : 0; r > 0 && load(); --r) {
-                        }
-                        __syncwarp();
-                        if (half == 1 && c == 0) write_tables();   // its wait giving up shows in the next one here
-                    }
-                    if (!ok) break;
-                    g += chunks;
-                    if (m >= 0 && lane == 0) mbar_arrive(&tab_free[m & 1]);
                 }
             }
             // copies still in flight (after a wait that gave up) land before the CTA ends
@@ -1027,21 +977,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     chunk_wait(&full[d % ST], (uint32_t)(d / ST) & 1u, &never);
             __syncwarp();
         } else if (warp == 30) {
-            // ============================================================ MMA: KV and QS
-            // Two threads issue, so that one's waits (about 100 clocks each) fall into the other's
-            // products.  kv_go comes from threads that saw the chunk's copies land.
+            // ============================================================ MMA: KV, QS, PV
+            // In this order: while the output warps read PV's chunk, the tensor core has the next KV.
+            // kv_go comes from threads that saw the chunk's copies land; qs_go from warps that wrote their part of
+            // P before.
             int g = 0;                               // chunks before unit m
             bool ok = true;
 #pragma unroll 1
             for (int m = 0;; ++m) {
                 if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
-                const UnitInfo *u = info_of(m);
-                const int count = uni(u->count), chunks = chunks_of(count);
+                const int count = uni(info_of(m)->count), chunks = chunks_of(count);
                 if (count == 0) break;
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
                     const int gc = g + c, s = gc % ST;
-                    const uint32_t qk = smb + S::kStageOff + s * S::kStageBytes;
+                    const uint32_t qk = smb + s * S::kStageBytes;
                     if (!(ok = wait(kv_go, gc))) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -1078,9 +1028,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                           qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2, id, part + k > 0);
                         }
                         tc_commit(qs_done);
+                        // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
+                        // 64..127 repeat the one panel
+                        const uint64_t pd = sw128_desc(smb + S::kPOff + (gc & 1) * 2 * kChunkPanel, 16, 1024);
+                        const uint64_t vd = sw128_desc(qk + S::kVOff, PAN == 2 ? kChunkPanel : 0, 1024);
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                            for (int k = 0; k < LC / 16; ++k)
+                                tc_mma_ss(tmem + TC_INTRA, vd + k * (16 * 128 >> 4),
+                                          pd + part * (kChunkPanel >> 4) + k * 2, id | kAMnMajor, part + k > 0);
+                        }
                         tc_commit(o_ready);
                         tc_commit(&empty[s]);
-                        mbar_arrive(pv_go);
                     }
                     __syncwarp();
                 }
@@ -1094,77 +1054,44 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             chunk_wait(drain, 0u, &never);
             __syncwarp();
         } else {
-            // ============================================================ MMA: QK, a chunk ahead, and PV
+            // ============================================================ MMA: QK, a chunk ahead
             if (!LOCAL) {
-                auto issue_qk = [&](int c) {
-                    // The three 32 x 32 blocks of S that are not masked, each in another group of 32 lanes (a warp
-                    // reads its own group only, so P's work spreads over three of the SM's four quarters):
-                    //   columns 0..31 (keys 0..31), A from 32 rows before Q: tokens 0..31 in lanes 32..63,
-                    //                                                        tokens 32..63 in lanes 64..95
-                    //   columns 32..63 (keys 32..63), A from Q's row 32:     tokens 32..63 in lanes 0..31
-                    // The other rows of A are whatever lies there; nobody reads their products.
-                    const uint64_t qd = sw128_desc(smb + S::kStageOff + (c % ST) * S::kStageBytes, 16, 1024);
-                    constexpr uint32_t id = idesc_bf16_f32(128, 32, 0);
-                    constexpr uint64_t kHalf = kChunkPanel / 2 >> 4;
-                    if (elect_one()) {
-#pragma unroll 1
-                        for (int pan = 0; pan < PAN; ++pan) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint64_t d = qd + pan * (S::kQkPanel >> 4) + k * 2;
-                                tc_mma_ss(tmem + TC_S, d - kHalf, d + (kChunkPanel >> 4), id, pan + k > 0);
-                                tc_mma_ss(tmem + TC_S + 32, d + kHalf, d + (kChunkPanel >> 4) + kHalf, id, pan + k > 0);
-                            }
-                        }
-                        tc_commit(s_ready);
-                    }
-                    __syncwarp();
-                };
-                if (wait(&full[0], 0)) {
-                    tc_fence_after();
-                    issue_qk(0);
-                }
-                int g = 0;                               // chunks before unit m
+                int g = -1;                              // chunks before unit m; unit -1: the first chunk's
                 bool ok = true;
 #pragma unroll 1
-                for (int m = 0;; ++m) {
-                    if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
-                    const UnitInfo *u = info_of(m);
-                    const int count = uni(u->count), chunks = chunks_of(count);
-                    if (count == 0) break;
+                for (int m = -1;; ++m) {
+                    int chunks = 1;
+                    if (m >= 0) {
+                        if (!(ok = wait(&tab_full[m & 1], m >> 1))) break;
+                        chunks = uni(chunks_of(info_of(m)->count));
+                        if (chunks == 0) break;
+                    }
 #pragma unroll 1
-                    for (int c = 0; c < chunks && ok; ++c) {
-                        const int gc = g + c;
-                        const int of = c + 1 < chunks ? m : m + 1;    // the unit of the next chunk
-                        if (!(ok = wait(&tab_full[of & 1], of >> 1))) break;
-                        const bool next = uni(info_of(of)->count) > 0;
-                        ok = (!next || wait(&full[(gc + 1) % ST], (gc + 1) / ST)) && wait(p_ready, gc);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (next) issue_qk(gc + 1);
-                        if (!(ok = wait(pv_go, gc))) break;
+                    for (int c = 0; c < chunks; ++c) {
+                        const int next = g + c + 1;
+                        if (next > 0 && !(ok = wait(p_ready, next - 1))) break;
+                        if (c + 1 == chunks && m >= 0) {
+                            // the next chunk belongs to the next unit, if there is one
+                            if (!(ok = wait(&tab_full[(m + 1) & 1], (m + 1) >> 1))) break;
+                            if (uni(info_of(m + 1)->count) == 0) break;
+                        }
+                        if (!(ok = wait(&full[next % ST], next / ST))) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            // A = V^T straight from the loaded tile (dv along its 128-byte rows); head_dim 64: lanes
-                            // 64..127 repeat the one panel
-                            constexpr uint32_t id = idesc_bf16_f32(128, LC, 0) | kAMnMajor;
-                            const uint64_t pd = sw128_desc(smb + S::kPOff + (gc & 1) * 2 * kChunkPanel, 16, 1024);
-                            const uint64_t vd = sw128_desc(smb + S::kStageOff + (gc % ST) * S::kStageBytes + S::kVOff,
-                                                           PAN == 2 ? kChunkPanel : 0, 1024);
+                            // A = Q's 64 rows and the 64 behind them, whose products nobody reads
+                            const uint64_t qd = sw128_desc(smb + (next % ST) * S::kStageBytes, 16, 1024);
+                            constexpr uint32_t id = idesc_bf16_f32(128, LC, 0);
 #pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                                for (int k = 0; k < LC / 16; ++k)
-                                    tc_mma_ss(tmem + TC_INTRA, vd + k * (16 * 128 >> 4),
-                                              pd + part * (kChunkPanel >> 4) + k * 2, id, part + k > 0);
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint64_t d = qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2;
+                                tc_mma_ss(tmem + TC_S, d, d + (kChunkPanel >> 4), id, k > 0);
                             }
-                            tc_commit(&empty[gc % ST]);
-                            tc_commit(o_ready);
+                            tc_commit(s_ready);
                         }
                         __syncwarp();
                     }
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive(&tab_free[m & 1]);
+                    if (m >= 0 && lane == 0) mbar_arrive(&tab_free[m & 1]);
                     g += chunks;
                 }
             }
@@ -1230,8 +1157,8 @@ cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
         if (e != cudaSuccess) return e;
     }
     main_kernel_event_before(stream);
-    e = launch_after(linear_chunk_kernel<D, false>, dim3(ctas(p.Hq)), kChunkThreads, S::kBytes, stream, qmap, kmap, vmap,
-                     p);
+    e = launch_after(linear_chunk_kernel<D, false>, dim3(ctas(p.Hq)), kChunkThreads, S::kBytes, stream, qmap, kmap,
+                     vmap, p);
     main_kernel_event_after(stream);
     return e;
 }
