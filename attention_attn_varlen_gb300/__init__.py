@@ -27,6 +27,7 @@ and the layer-shaped dispatcher in :mod:`attention_attn_varlen_gb300.attention`.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -39,7 +40,8 @@ from ._build import build
 
 __all__ = ["attn_varlen_fwd", "attn_varlen_fwd_host", "host_staging", "attn_decode_paged", "attn_with_kvcache",
            "attn_padded_fwd", "softmax_rows", "store_kvcache", "step_tables", "trim_pages", "StepTables",
-           "rope_store_kvcache", "linear_attn_varlen_fwd", "linear_attn_decode", "linear_attn_workspace_size", "get_last_device_error", "selftest_bounded_wait",
+           "rope_store_kvcache", "linear_attn_varlen_fwd", "linear_attn_decode", "linear_attn_workspace_size",
+           "get_last_device_error", "selftest_bounded_wait",
            "lib", "build", "AttnError", "exported_symbols", "set_kernel_events", "decode_num_splits",
            "decode_workspace_size"]
 
@@ -211,6 +213,18 @@ def _device(t: torch.Tensor, name: str) -> int:
 # the current stream's handle without making a Stream object (3 us a call less)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _on_stream(call):
+    """`stream` becomes the current stream for the call, so that the outputs and the workspace it makes
+    belong to that stream: memory of the current one may still be in use there."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on
 
 
 def _address(t):
@@ -581,8 +595,9 @@ def _pool_args(request_rows, lens, seq_lens, page_table, free_pages, num_free, l
     return dev, B
 
 
+@_on_stream
 def step_tables(request_rows, new_lens, seq_lens, page_table, free_pages, num_free, block_size: int,
-                max_tokens: int, out: StepTables | None = None, workspace=None, stream=None) -> StepTables:
+                max_tokens: int, out: StepTables | None = None, workspace=None, *, stream=None) -> StepTables:
     """Grow the requests of a step by their new tokens, taking pages off the
     free list, and build the step's tables on the GPU (no host sync).
 
@@ -612,13 +627,14 @@ def step_tables(request_rows, new_lens, seq_lens, page_table, free_pages, num_fr
                             int(max_tokens), out.block_table.data_ptr(), out.slot_mapping.data_ptr(),
                             out.positions.data_ptr(), out.cu_seqlens_q.data_ptr(), out.cu_seqlens_k.data_ptr(),
                             out.cache_seqlens.data_ptr(), out.context_lens.data_ptr(), ws, ws_bytes,
-                            _raw_stream(dev) if stream is None else stream.cuda_stream)
+                            _raw_stream(dev))
     _check(st, "attn_step_tables")
     return out
 
 
+@_on_stream
 def trim_pages(request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, block_size: int, workspace=None,
-               stream=None) -> None:
+               *, stream=None) -> None:
     """Cut requests to their first keep_lens tokens (int32 [B]; 0 ends a
     request) and give the pages behind them back to the free list."""
     dev, B = _pool_args(request_rows, keep_lens, seq_lens, page_table, free_pages, num_free, "keep_lens")
@@ -627,13 +643,14 @@ def trim_pages(request_rows, keep_lens, seq_lens, page_table, free_pages, num_fr
     workspace, ws, ws_bytes = _bytes(workspace, L.attn_step_tables_workspace_size(B), dev, seq_lens)
     st = L.attn_trim_pages(_address(request_rows), keep_lens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
                            free_pages.data_ptr(), num_free.data_ptr(), B, R, M, int(block_size), free_pages.numel(),
-                           ws, ws_bytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+                           ws, ws_bytes, _raw_stream(dev))
     _check(st, "attn_trim_pages")
 
 
+@_on_stream
 def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None, slot_mapping=None, pair_axis=None,
                        interleaved: bool = False, scale: float = 1.0, q_out=None, k_out=None, return_k: bool = False,
-                       v16_cache=None, stream=None):
+                       v16_cache=None, *, stream=None):
     """Rotary positions on q [N, Hq, D] and k [N, Hkv, D], and the scatter of the
     rotated k and of v into the caches (as store_kvcache), in one pass.
 
@@ -684,7 +701,7 @@ def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None,
         q.data_ptr(), k.data_ptr(), _address(v), positions.data_ptr(), inv_freq.data_ptr(), pair_axis, axes,
         positions.stride(0) if axes > 1 else N, 2 * pairs, 1 if interleaved else 0, float(scale), q_out.data_ptr(),
         _address(k_out), _address(k_cache), _address(v_cache), _address(v16_cache), _address(slot_mapping), N, Hq,
-        Hkv, D, qs, ks, vs, qos, kos, num_slots, _raw_stream(dev) if stream is None else stream.cuda_stream)
+        Hkv, D, qs, ks, vs, qos, kos, num_slots, _raw_stream(dev))
     _check(st, "attn_rope_store_kvcache")
     return (q_out, k_out) if return_k else q_out
 
@@ -719,9 +736,10 @@ def linear_attn_workspace_size(batch: int, num_heads_q: int, num_heads_kv: int, 
     return lib().attn_linear_workspace_size(batch, num_heads_q, num_heads_kv, head_dim, max_seqlen)
 
 
+@_on_stream
 def linear_attn_varlen_fwd(q, k, v, log_decay, cu_seqlens, max_seqlen: int, scale: float | None = None,
                            state_cache=None, state_slots=None, context_lens=None, out=None, workspace=None,
-                           stream=None):
+                           *, stream=None):
     """Linear attention with a decay per head over packed sequences:
     S_t = exp(log_decay) S_{t-1} + v_t k_t^T, o_t = scale * S_t q_t.
 
@@ -741,13 +759,14 @@ def linear_attn_varlen_fwd(q, k, v, log_decay, cu_seqlens, max_seqlen: int, scal
                                   cu_seqlens.data_ptr(), _address(state_cache), _address(state_slots),
                                   _address(context_lens), B, T, max_seqlen, Hq, Hkv, D,
                                   1.0 / math.sqrt(D) if scale is None else scale, slots, *strides, ws, ws_bytes,
-                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
+                                  _raw_stream(dev))
     _check(st, "attn_linear_varlen_fwd")
     return out
 
 
+@_on_stream
 def linear_attn_decode(q, k, v, log_decay, state_cache, state_slots, scale: float | None = None, context_lens=None,
-                       out=None, stream=None):
+                       out=None, *, stream=None):
     """linear_attn_varlen_fwd for one token per sequence: q [B, Hq, D], k/v [B,
     Hkv, D]; the states in state_cache are updated in place.  A slot < 0 stands
     for a zero state that is not kept; context_lens[b] = 0 starts from zero
@@ -757,7 +776,7 @@ def linear_attn_decode(q, k, v, log_decay, state_cache, state_slots, scale: floa
     st = lib().attn_linear_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
                                   _address(state_cache), _address(state_slots), _address(context_lens), B, Hq, Hkv, D,
                                   1.0 / math.sqrt(D) if scale is None else scale, slots, *strides,
-                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
+                                  _raw_stream(dev))
     _check(st, "attn_linear_decode")
     return out
 
