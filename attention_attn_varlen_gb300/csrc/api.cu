@@ -86,18 +86,20 @@ EncodeTiledFn encode_fn() {
 }
 
 // bf16 tensor [rows, heads, dim] with a row stride (elements) viewed as a 3-D
-// TMA map (dim, heads, rows), 128-byte swizzle, box (64, box_heads, box_rows).
+// TMA map (dim, heads, rows), box (box_dim, box_heads, box_rows) with a swizzle as wide as its rows.
 bool make_map(CUtensorMap *map, const void *base, int64_t rows, int heads, int dim, int64_t row_stride,
-              int box_heads, int box_rows, CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+              int box_heads, int box_rows, CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              int box_dim = 64) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t gdim[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
     cuuint64_t gstride[2] = {(cuuint64_t)dim * 2, (cuuint64_t)row_stride * 2};
-    cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t box[3] = {(cuuint32_t)box_dim, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = fn(map, dtype, 3, const_cast<void *>(base), gdim, gstride, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    box_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
@@ -1277,12 +1279,14 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
     p.units = ws + l.units;
     p.decay = reinterpret_cast<float *>(ws + l.decay);
     p.states = reinterpret_cast<float *>(ws + l.states);
-    CUtensorMap qmap, kmap, vmap;
+    CUtensorMap qmap, kmap, vmap, omap;
     if (!make_map(&qmap, q, total_tokens, num_heads_q, head_dim, p.q_stride, 1, 64) ||
         !make_map(&kmap, k, total_tokens, num_heads_kv, head_dim, p.k_stride, 1, 64) ||
-        !make_map(&vmap, v, total_tokens, num_heads_kv, head_dim, p.v_stride, 1, 64))
+        !make_map(&vmap, v, total_tokens, num_heads_kv, head_dim, p.v_stride, 1, 64) ||
+        !make_map(&omap, out, total_tokens, num_heads_q, head_dim, p.out_stride, 1, 64,
+                  CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 32))
         return ATTN_ERR_LAUNCH_FAILED;
-    return launched(launch_linear_varlen(qmap, kmap, vmap, p, reinterpret_cast<cudaStream_t>(stream)));
+    return launched(launch_linear_varlen(qmap, kmap, vmap, omap, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_linear_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,

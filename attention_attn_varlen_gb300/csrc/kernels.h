@@ -164,7 +164,7 @@ struct LinearParams {
 };
 constexpr int kLinearDecayRow = 136, kLinearUnitBytes = 32;
 cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                                 const LinearParams &p, cudaStream_t stream);
+                                 const CUtensorMap &omap, const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream);
 
 cudaError_t launch_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,

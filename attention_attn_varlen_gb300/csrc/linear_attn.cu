@@ -170,7 +170,8 @@ cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
 // issuing threads 387 -> 324; operands warp-uniform and one code site per role's step, 64 -> 38 KB
 // of code (the instruction cache is shared by all roles) 324 -> 294; fewer barriers 294 -> 280;
 // P by the state's warps in the time between KV and QS, its factors loaded
-// without branches 280 -> 266; waits that rarely read the timer 266 -> 261.  One CTA per SM that goes over
+// without branches 280 -> 266; waits that rarely read the timer 266 -> 261; output tiles as
+// one bulk store each 261 -> 249.  One CTA per SM that goes over
 // its units, the next one's tables and copies under way while one ends: 96 short sequences
 // 70 -> 47.5 us.
 // ---------------------------------------------------------------------------
@@ -472,7 +473,8 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearParams p) 
 template <int D, bool LOCAL>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap, const LinearParams p) {
+                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
+                        const LinearParams p) {
     using S = ChunkSmem<D>;
     constexpr int ST = S::kStages, PAN = S::kPanels;
     extern __shared__ __align__(1024) uint8_t lsmem_raw[];
@@ -831,6 +833,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         if (lane == 0) mbar_arrive(qs_go);
                         continue;
                     }
+                    if (lane == 0) bulk_wait_read();             // the tile's last store
+                    __syncwarp();
                     const int *bad_row = bad_at + (gc & 3) * 128 + grp * 32;
                     const bool any_bad = __any_sync(0xffffffffu, bad_row[lane] < LC);
 #pragma unroll 1
@@ -869,20 +873,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                 0x7FC0;
                     }
                     __syncwarp();
-                    __nv_bfloat16 *out = p.out + (t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
-#pragma unroll 2
-                    for (int i = 0; i < LC / 8; ++i) {
-                        const int t = i * 8 + (lane >> 2);
-                        const uint4 v =
-                            *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
-                        if (t < n) *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) = v;
+                    if (n == LC) {
+                        // one store of the tile; its swizzle is the copy engine's for rows of 64 bytes
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&omap, stg, grp * 32, h, t0 + c * LC);
+                            bulk_commit();
+                        }
+                    } else {
+                        // rows behind the sequence stay as they are
+                        __nv_bfloat16 *out = p.out + (t0 + (int64_t)c * LC) * p.out_stride + (int64_t)h * D + grp * 32;
+#pragma unroll 1
+                        for (int t = lane >> 2; t < n; t += 8)
+                            *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) =
+                                *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(&tab_free[m & 1]);
                 g += chunks;
             }
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
         }
     } else {
         fewer_regs<kRestRegs>();
@@ -1126,7 +1140,7 @@ cudaError_t launch_after(void (*k)(K...), dim3 grid, unsigned block, size_t smem
 
 template <int D>
 cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                          const LinearParams &p, cudaStream_t stream) {
+                          const CUtensorMap &omap, const LinearParams &p, cudaStream_t stream) {
     using S = ChunkSmem<D>;
     static std::once_flag once[kMaxDev];
     static cudaError_t attr_err[kMaxDev];
@@ -1149,7 +1163,7 @@ cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
     const bool split = p.seg_len < p.max_seqlen;
     if (split) {
         e = launch_after(linear_chunk_kernel<D, true>, dim3(ctas(p.Hkv)), kChunkThreads, S::kBytes, stream, qmap, kmap,
-                         vmap, p);
+                         vmap, omap, p);
         if (e != cudaSuccess) return e;
     }
     if (p.state_rows > 0) {
@@ -1158,7 +1172,7 @@ cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
     }
     main_kernel_event_before(stream);
     e = launch_after(linear_chunk_kernel<D, false>, dim3(ctas(p.Hq)), kChunkThreads, S::kBytes, stream, qmap, kmap,
-                     vmap, p);
+                     vmap, omap, p);
     main_kernel_event_after(stream);
     return e;
 }
@@ -1166,8 +1180,9 @@ cudaError_t launch_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
 }  // namespace
 
 cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                                 const LinearParams &p, cudaStream_t stream) {
-    return p.D == 128 ? launch_chunks<128>(qmap, kmap, vmap, p, stream) : launch_chunks<64>(qmap, kmap, vmap, p, stream);
+                                 const CUtensorMap &omap, const LinearParams &p, cudaStream_t stream) {
+    return p.D == 128 ? launch_chunks<128>(qmap, kmap, vmap, omap, p, stream)
+                      : launch_chunks<64>(qmap, kmap, vmap, omap, p, stream);
 }
 
 cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream) { return launch_decode_kernel(p, stream); }
