@@ -186,7 +186,9 @@ class PagePool:
     adds a step's new tokens and returns its tables, trim() cuts requests (0
     ends one); neither waits for the GPU.  Pages that cannot be served are
     reported by get_last_device_error (status 9) and leave their request as it
-    was."""
+    was here and in the paged caches.  The step's layers still run over its
+    tokens (attention sees the old context only): drop their output, and put back
+    a linear layer's state before the request is tried again."""
 
     def __init__(self, num_blocks: int, block_size: int, max_requests: int, max_blocks: int, device=None):
         i32 = torch.int32

@@ -27,7 +27,7 @@
  *    cache_seqlens, slot_mapping) is not read on the host.  Kernels never
  *    access memory outside the sizes given here: a bad index is skipped and
  *    recorded in the device error word (attn_get_last_device_error).
- *  - head_dim must be 64 or 128; num_heads_q must be a multiple of
+ *  - head_dim must be 64 or 128 (attn_rope_store_kvcache: any even one); num_heads_q must be a multiple of
  *    num_heads_kv (GQA: query head h reads KV head h / (num_heads_q /
  *    num_heads_kv)).  The prefill kernels (attn_varlen_fwd, attn_padded_fwd,
  *    the prefill route of attn_kvcache_fwd) take a group size
@@ -522,8 +522,14 @@ ATTN_API attn_status attn_rope_store_kvcache(const void *q, const void *k, const
  *                state; 0: the sequence starts from a zero state, whatever the
  *                slot holds.  NULL: every sequence starts from zero
  *   max_seqlen   host-side upper bound of the lengths (a longer sequence is cut
- *                to it and reported as ATTN_ERR_DEVICE_INDEX)
+ *                to it and reported as ATTN_ERR_DEVICE_INDEX); 0: nothing runs
  * A sequence of length 0 leaves its slot as it was.
+ * An infinity or NaN in k or v reaches its own token's output and later ones of
+ * its sequence and head (one in v: its value dimension alone) as NaN, one in q
+ * its own token's; nothing else.  The workspace holds nothing from call to call:
+ * calls that follow one another on a stream may share it, calls that may run at the
+ * same time need one each.
+ * Limits: batch, num_heads_q <= 65535; total_tokens < 2^31 - 1.
  * workspace: attn_linear_workspace_size(...) bytes, 256-byte aligned.
  * ------------------------------------------------------------------------ */
 ATTN_API attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, void *out,
@@ -583,14 +589,16 @@ ATTN_API int attn_abi_version(void);
  * benchmark can time the dominant kernel of a call by itself).  `before` and
  * `after` are the caller's cudaEvent_t handles (cast to void *); the library
  * neither creates nor destroys them.  While both are non-NULL, every later
- * attn_varlen_fwd, attn_decode_paged, attn_decode_paged_noalloc and
- * store_kvcache call made from the same host thread records `before` on its
+ * attn_varlen_fwd, attn_decode_paged, attn_decode_paged_noalloc,
+ * store_kvcache, attn_rope_store_kvcache, attn_linear_varlen_fwd and
+ * attn_linear_decode call made from the same host thread records `before` on its
  * stream just before launching its main kernel (the attention kernel of the
- * prefill; the split-KV kernel of the decode; the scatter kernel of the store)
- * and `after` just after it, so
+ * prefill; the split-KV kernel of the decode; the scatter kernel of the store;
+ * the rotary kernel; the chunk kernel or the recurrent one of the linear
+ * attention) and `after` just after it, so
  * cudaEventElapsedTime(before, after) is that kernel's device time.  The
- * scheduling and V-conversion kernels of the prefill and the combine kernel
- * of the decode fall outside.  Pass NULL, NULL to switch it off (the
+ * scheduling and V-conversion kernels of the prefill, the combine kernel
+ * of the decode and the segment passes of the linear attention fall outside.  Pass NULL, NULL to switch it off (the
  * default).  Event-record errors are not reported. */
 ATTN_API void attn_set_kernel_events(void *before, void *after);
 
