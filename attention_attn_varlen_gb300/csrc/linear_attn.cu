@@ -153,7 +153,7 @@ cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
 // Bound by what the chunks of a sequence wait for, KV -> S -> QS -> output rows, and by the shared
 // memory that all roles and the tensor core's operands share: the tensor core is
 // busy half of the time.  Per chunk of head_dim 128: KV 12 steps of 16 tokens (N = 128, 66 clocks
-// each), QS 16 (N = 64, 33), PV and QK 8 each (both operands shared, 50): 2,100 clocks of the 3,750
+// each), QS 16 (N = 64, 33), PV and QK 8 each (both operands shared, 50): 2,100 clocks of the 3,500
 // that a chunk takes; HBM's 64 KB would take 2,700 of them.
 // So everything else is off the warps that issue, in roles that run side by side, each a
 // chunk or less apart.
@@ -213,7 +213,7 @@ struct ChunkSmem {
     static constexpr int kTabFloats = 5 * LC + 16;               // ... and the unit itself (UnitInfo)
     static constexpr int kTabBytes = 2 * kTabFloats * 4 + 4 * 128 * 4;
     static constexpr int kBarOff = kTabOff + kTabBytes;
-    static constexpr int kNumBars = 2 * kStages + 13;
+    static constexpr int kNumBars = 2 * kStages + 15;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -498,18 +498,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint8_t *sm = lsmem_raw + (smb - smem_u32(lsmem_raw));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *full = bars, *empty = bars + ST;
-    uint64_t *kv_go = bars + 2 * ST;         // (w V)^T of the chunk is in place (and V's tail and non-finite entries
+    uint64_t *kv_go = bars + 2 * ST;         // [2], by chunk: (w V)^T is in place (and V's tail and non-finite entries
     //   are zeroed), the KV before has been read
-    uint64_t *w_free = kv_go + 1;            // KV has read (w V)^T
-    uint64_t *kv_ready = kv_go + 2;          // KV done
-    uint64_t *qs_go = kv_go + 3;             // S_0 is in TMEM, P in shared memory, the chunk before has been read
-    uint64_t *qs_done = kv_go + 4;           // QS has read S_0
-    uint64_t *s_ready = kv_go + 5;           // QK done
-    uint64_t *p_ready = kv_go + 6;           // P in shared memory, QK's columns free
-    uint64_t *o_ready = kv_go + 7;           // QS and PV done
-    uint64_t *drain = kv_go + 8;             // every MMA done
-    uint64_t *tab_full = kv_go + 9;          // [2]: a unit's tables are written
-    uint64_t *tab_free = kv_go + 11;         // [2]: ... and read for the last time
+    uint64_t *w_free = kv_go + 2;            // [2], by chunk: KV has read (w V)^T
+    uint64_t *kv_ready = kv_go + 4;          // KV done
+    uint64_t *qs_go = kv_go + 5;             // S_0 is in TMEM, P in shared memory, the chunk before has been read
+    uint64_t *qs_done = kv_go + 6;           // QS has read S_0
+    uint64_t *s_ready = kv_go + 7;           // QK done
+    uint64_t *p_ready = kv_go + 8;           // P in shared memory, QK's columns free
+    uint64_t *o_ready = kv_go + 9;           // QS and PV done
+    uint64_t *drain = kv_go + 10;            // every MMA done
+    uint64_t *tab_full = kv_go + 11;         // [2]: a unit's tables are written
+    uint64_t *tab_free = kv_go + 13;         // [2]: ... and read for the last time
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *tables = reinterpret_cast<float *>(sm + S::kTabOff);
@@ -524,8 +524,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1 + 8);     // the MMAs, the V warps
         }
-        mbar_init(kv_go, 8 + 16);            // V, state
-        mbar_init(w_free, 1);
+        mbar_init(&kv_go[0], 8 + 16);        // V, state
+        mbar_init(&kv_go[1], 8 + 16);
+        mbar_init(&w_free[0], 1);
+        mbar_init(&w_free[1], 1);
         mbar_init(kv_ready, 1);
         mbar_init(qs_go, 16 + 4);            // state, output
         mbar_init(qs_done, 1);
@@ -558,6 +560,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
+    // Where a chunk's w V goes: the state-only pass has room for two chunks of it (32,768 tokens, 16 heads:
+    // that pass 69 -> 60 us)
+    constexpr int kWBufs = LOCAL ? 2 : 1;
+    auto w_at = [](int gc) { return LOCAL && (gc & 1) ? TC_STATE : TC_W; };
+    auto lo_at = [](int gc) { return LOCAL && (gc & 1) ? S::kPOff : S::kLoOff; };
     // waits for what the hardware finishes by itself run to the limit: their flag is their own
     volatile int &never = *(abort_flag + 1);
     // a warp's wait: every lane gets the same answer
@@ -627,15 +634,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         mid[i] = take_bf16(x0, x1);
                         lo[i] = pack_bf16x2(x0, x1);
                     }
-                    if (step == 0 && gc > 0) {
-                        ok = wait(w_free, gc - 1);
+                    if (step == 0 && gc >= kWBufs) {
+                        ok = wait(&w_free[(gc - kWBufs) & 1], (gc - kWBufs) >> 1);
                         tc_fence_after();
                     }
                     if (!ok) break;
-                    tmem_st_16x128b_x4(lane_base + TC_W + step * 16, hi);
-                    tmem_st_16x128b_x4(lane_base + TC_W + 32 + step * 16, mid);
+                    tmem_st_16x128b_x4(lane_base + w_at(gc) + step * 16, hi);
+                    tmem_st_16x128b_x4(lane_base + w_at(gc) + 32 + step * 16, mid);
                     if (grp * 32 < D) {
-                        const uint32_t to = smem_u32(sm + S::kLoOff) + (frag - S::kVOff) + step * 4096;
+                        const uint32_t to = smem_u32(sm + lo_at(gc)) + (frag - S::kVOff) + step * 4096;
                         stsm_x4_t(to, lo[0], lo[1], lo[2], lo[3]);
                         stsm_x4_t(to + 2048, lo[4], lo[5], lo[6], lo[7]);
                     }
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(kv_go);
+                    mbar_arrive(&kv_go[gc & 1]);
                     mbar_arrive(&empty[s]);
                 }
             }
@@ -750,7 +757,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 __syncwarp();
                 const bool first_or_read = c >= 0 || m == 0;
-                if (lane == 0 && first_or_read) mbar_arrive(kv_go);   // at the very first: no KV to be read yet
+                if (lane == 0 && first_or_read) mbar_arrive(&kv_go[(gc + 1) & 1]);   // before the first: nothing to read
                 if (!LOCAL && grp < 2 && first_or_read) {
                     // P of the next chunk: lane = token (lanes 64..127 hold none), 8 keys at a time, in turn among
                     // the warps of a lane group; tokens 0..31 see no key behind 31
@@ -1006,17 +1013,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int c = 0; c < chunks; ++c) {
                     const int gc = g + c, s = gc % ST;
                     const uint32_t qk = smb + s * S::kStageBytes;
-                    if (!(ok = wait(kv_go, gc))) break;
+                    if (!(ok = wait(&kv_go[gc & 1], gc >> 1))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         constexpr uint32_t id = idesc_bf16_f32(128, D, 1);
                         const uint64_t kd = sw128_desc(qk + kChunkPanel, S::kQkPanel, 1024);
-                        const uint64_t ld = sw128_desc(smb + S::kLoOff, PAN == 2 ? kChunkPanel : 0, 1024);
+                        const uint64_t ld = sw128_desc(smb + lo_at(gc), PAN == 2 ? kChunkPanel : 0, 1024);
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part) {
 #pragma unroll
                             for (int k = 0; k < LC / 16; ++k)
-                                tc_mma_ts(tmem + TC_KV, tmem + TC_W + part * 32 + k * 8, kd + k * (16 * 128 >> 4), id,
+                                tc_mma_ts(tmem + TC_KV, tmem + w_at(gc) + part * 32 + k * 8, kd + k * (16 * 128 >> 4), id,
                                           part + k > 0);
                         }
 #pragma unroll
@@ -1024,7 +1031,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             tc_mma_ss(tmem + TC_KV, ld + k * (16 * 128 >> 4), kd + k * (16 * 128 >> 4), id | kAMnMajor,
                                       1);
                         tc_commit(kv_ready);
-                        tc_commit(w_free);
+                        tc_commit(&w_free[gc & 1]);
                         if (LOCAL) tc_commit(&empty[s]);
                     }
                     __syncwarp();
