@@ -402,3 +402,35 @@ def test_states_and_rows_past_32_bits_of_offset():
     _check(out, ref, weight, "out")
     _check_state(sd[num - 1], *finals[0], "state", 1)
     assert av.get_last_device_error()[0] == 0
+
+
+def test_the_largest_batch_and_a_wide_group():
+    """65,535 sequences of one token or none; 48 query heads on one state."""
+    B, D = 65535, 64
+    gen = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, 2, (B,), generator=gen)
+    T = int(lens.sum())
+    q, k, v = (torch.randn(T, 1, D, generator=gen).to(torch.bfloat16) for _ in range(3))
+    slots = torch.full((B,), -1, dtype=torch.int32)
+    slots[::1000] = torch.arange(len(slots[::1000]), dtype=torch.int32)
+    sd = torch.full((70, 1, D, D), 3.0, device="cuda")
+    g = torch.tensor([-0.5], device="cuda")
+    out = av.linear_attn_varlen_fwd(q.cuda(), k.cuda(), v.cuda(), g, cu_of(lens.tolist()).cuda(), 1, 0.5, state_cache=sd,
+                                    state_slots=slots.cuda())
+    qk = 0.5 * (q.double() * k.double()).sum(-1, keepdim=True)
+    _check(out[:, 0], (qk * v.double())[:, 0], (0.5 * (q.double() * k.double()).abs().sum(-1, keepdim=True)
+                                                * v.double().abs())[:, 0], "one token each")
+    at = torch.cumsum(lens, 0) - 1
+    for b in range(0, B, 1000):
+        got = sd[slots[b], 0].double().cpu()
+        want = torch.outer(v[at[b], 0].double(), k[at[b], 0].double()) if lens[b] else torch.full((D, D), 3.0).double()
+        assert ((got - want).abs() <= 2.0 ** -22 * want.abs()).all()
+    (q, k, v), dev, _ = _inputs(7, 100, 48, 1, 64)
+    s1 = torch.randn(1, 1, 64, 64, generator=gen)
+    sd = s1.cuda()
+    zero, one = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    out = av.linear_attn_varlen_fwd(*dev, g, cu_of([100]).cuda(), 100, state_cache=sd, state_slots=zero, context_lens=one)
+    ref, finals, weight = linear(q, k, v, g.cpu(), [0, 100], 64 ** -0.5, [s1[0].double()])
+    _check(out, ref, weight, "48 heads")
+    _check_state(sd[0], *finals[0], "48 heads", 100)
+    assert av.get_last_device_error()[0] == 0

@@ -93,3 +93,53 @@ def test_serving_steps(axes):
     step([2, 1], [33, 64], "prompt")
     step([0, 1, 2, 3], [1, 1, 1, 1], "decode")
     assert av.get_last_device_error()[0] == 0
+
+
+def test_a_captured_step_is_the_eager_one():
+    """Tables, rotary store, attention and linear attention of a decode step in one graph,
+    replayed while the requests grow, with a padded batch entry: the bits of eager steps."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    inv = torch.rand(D // 2, generator=gen, device="cuda")
+    g = torch.tensor([-0.3, -0.01], device="cuda")
+    rows, new, slots, start = i32([3, 0, 1, 2]), i32([1, 1, 1, 0]), i32([3, 0, 1, -1]), i32([40, BS - 2, 0, 0])
+
+    def build():
+        pool = PagePool(80, BS, R, 30)
+        pool.grow(start, 200, request_rows=rows)
+        att = Attention(Hq, D, D ** -0.5, Hkv, rotary=Rotary(inv))
+        att.k_cache, att.v_cache = (torch.zeros(80, BS, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lin = LinearAttention(Hq, D, D ** -0.5, Hkv, g)
+        lin.state_cache = torch.ones(R, Hkv, D, D, device="cuda")
+        x = [torch.zeros(4, h, D, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv)]
+
+        def step():
+            t = pool.grow(new, 4, request_rows=rows)
+            ctx = pool.context(t, False, 1, 30 * BS, state_slots=slots)
+            return att(*x, ctx), lin(*x, ctx), t
+        return pool, att, lin, x, step
+
+    a, b = build(), build()
+    torch.cuda.synchronize()
+    keep = [t.clone() for t in (b[0].seq_lens, b[0].page_table, b[0].num_free, b[2].state_cache)]
+    b[4]()                                               # once eagerly, then back to the start
+    torch.cuda.synchronize()
+    for t, old in zip((b[0].seq_lens, b[0].page_table, b[0].num_free, b[2].state_cache), keep):
+        t.copy_(old)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = b[4]()
+    av.get_last_device_error()
+    for n in range(BS + 3):                              # past a page's end
+        q = [rnd(*t.shape) for t in a[3]]
+        for t, u, v in zip(a[3], b[3], q):
+            t.copy_(v)
+            u.copy_(v)
+        want = a[4]()
+        graph.replay()
+        assert torch.equal(got[0][:3], want[0][:3]) and torch.equal(got[1][:3], want[1][:3])
+        assert all(torch.equal(x, y) for x, y in zip(got[2], want[2]))
+    assert torch.equal(a[2].state_cache, b[2].state_cache) and torch.equal(a[1].k_cache, b[1].k_cache)
+    assert a[0].seq_lens.tolist()[:4] == b[0].seq_lens.tolist()[:4] == [BS - 2 + BS + 3, BS + 3, 0, 40 + BS + 3]
+    assert av.get_last_device_error()[0] == 0
