@@ -217,9 +217,12 @@ class PagePool:
         """The step's AttentionContext.  paged=False: a prefill of fresh prompts,
         whose attention reads the step's own k and v.  positions: instead of the
         tables' (for instance several axes)."""
+        # the step's own k has a row for every new token, also of an entry that was not served and so
+        # counts as empty in cu_seqlens_k
+        cu_k, most_k = (tables.cu_seqlens_k, max_seqlen_k) if paged else (tables.cu_seqlens_q, max_seqlen_q)
         return AttentionContext(
             is_prefill, slot_mapping=tables.slot_mapping, cu_seqlens_q=tables.cu_seqlens_q,
-            cu_seqlens_k=tables.cu_seqlens_k, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
+            cu_seqlens_k=cu_k, max_seqlen_q=max_seqlen_q, max_seqlen_k=most_k,
             context_lens=tables.cache_seqlens, block_tables=tables.block_table if paged else None,
             positions=tables.positions if positions is None else positions, state_slots=state_slots,
             past_lens=tables.context_lens)
