@@ -155,8 +155,11 @@ class LinearAttention:
 
     def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ctx: AttentionContext) -> torch.Tensor:
         """q [N, Hq*D] or [N, Hq, D]; k, v [N, Hkv*D] or [N, Hkv, D].  Returns o
-        with q's shape.  A decode step with one token per sequence takes the
-        recurrent form; any other step runs in chunks over ctx.cu_seqlens_q."""
+        with q's shape.  A step of at most one token per sequence
+        (ctx.max_seqlen_q 1) takes the recurrent form, any other runs in chunks,
+        both over ctx.cu_seqlens_q: sequences may have no token, and rows behind
+        the last one are not computed.  A decode step without offsets has one row
+        for each sequence."""
         shape = q.shape
         q = q.view(-1, self.num_heads, self.head_dim)
         k = k.view(-1, self.num_kv_heads, self.head_dim)
@@ -166,14 +169,19 @@ class LinearAttention:
             raise ValueError("a layer with a state cache needs ctx.state_slots")
         if not ctx.is_prefill and slots is None:
             raise ValueError("decode needs the state cache")
-        if not ctx.is_prefill and q.shape[0] == slots.numel():
-            o = linear_attn_decode(q, k, v, self.log_decay, self.state_cache, slots, self.scale,
-                                   context_lens=ctx.past_lens)
+        offsets, past, most = ctx.cu_seqlens_q, ctx.past_lens, ctx.max_seqlen_q or q.shape[0]
+        # offsets that are not of these sequences say nothing about them
+        if not ctx.is_prefill and (offsets is None or offsets.numel() != slots.numel() + 1):
+            if q.shape[0] != slots.numel():
+                raise ValueError("a decode step of several tokens needs the sequences' offsets (ctx.cu_seqlens_q)")
+            o = linear_attn_decode(q, k, v, self.log_decay, self.state_cache, slots, self.scale, context_lens=past)
         else:
-            if not ctx.is_prefill and ctx.past_lens is None:
-                raise ValueError("a decode step of several tokens needs ctx.past_lens")
-            o = linear_attn_varlen_fwd(q, k, v, self.log_decay, ctx.cu_seqlens_q, ctx.max_seqlen_q, self.scale,
-                                       state_cache=self.state_cache, state_slots=slots, context_lens=ctx.past_lens)
+            if not ctx.is_prefill and past is None:
+                if most > 1:
+                    raise ValueError("a decode step of several tokens needs ctx.past_lens")
+                past = torch.ones_like(slots)            # as without offsets: every slot continues
+            o = linear_attn_varlen_fwd(q, k, v, self.log_decay, offsets, most, self.scale,
+                                       state_cache=self.state_cache, state_slots=slots, context_lens=past)
         return o.view(shape)
 
     __call__ = forward

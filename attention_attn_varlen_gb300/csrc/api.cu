@@ -1187,10 +1187,17 @@ static bool linear_sizes(int batch, int num_heads_q, int num_heads_kv, int head_
            num_heads_q % num_heads_kv == 0 && (head_dim == 64 || head_dim == 128);
 }
 
+// Sequences of at most one token take the recurrent form (while its CTAs, four a state at most, are a
+// grid): no work list, tables or copies of states, so no workspace.
+static bool linear_recurrent(int batch, int num_heads_kv, int max_seqlen) {
+    return max_seqlen <= 1 && (int64_t)batch * num_heads_kv * 4 <= (int64_t)INT32_MAX;
+}
+
 extern "C" {
 
 size_t attn_linear_workspace_size(int batch, int num_heads_q, int num_heads_kv, int head_dim, int max_seqlen) {
     if (!linear_sizes(batch, num_heads_q, num_heads_kv, head_dim) || max_seqlen < 0) return 0;
+    if (linear_recurrent(batch, num_heads_kv, max_seqlen)) return 0;
     return linear_layout(batch, num_heads_q, num_heads_kv, head_dim).bytes;
 }
 
@@ -1264,6 +1271,8 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
     p.max_seqlen = max_seqlen;
     p.start_zero = context_lens == nullptr;
     p.err = d->err;
+    if (linear_recurrent(batch, num_heads_kv, max_seqlen))
+        return launched(launch_linear_decode(p, reinterpret_cast<cudaStream_t>(stream)));
     p.num_sms = d->num_sms;
     p.seg_len = linear_seg_len(total_tokens, num_heads_q, max_seqlen);
     const bool split = p.seg_len < max_seqlen;

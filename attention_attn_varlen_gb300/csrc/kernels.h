@@ -144,7 +144,7 @@ struct LinearParams {
     const __nv_bfloat16 *q, *k, *v;   // [T, H, D] with row strides
     __nv_bfloat16 *out;
     const float *log_decay;           // [Hkv]
-    const int32_t *cu;                // [batch + 1] (prompts)
+    const int32_t *cu;                // [batch + 1], or null (recurrent form): sequence b is row b
     float *state;                     // [num_slots, Hkv, D, D], rows along the value dimension; null: none kept
     const int32_t *slots;             // [batch]; < 0: no state
     const int32_t *context_lens;      // [batch] or null; 0: the sequence starts from a zero state

@@ -54,6 +54,8 @@ __device__ __forceinline__ float linear_log_decay(const LinearParams &p, int h, 
 // row sums of a warp's rows are reduced together (9 shuffles for 8 rows).  256
 // sequences, 32 heads of 128: 151 us in the kernel, 7.1 TB/s; a CTA per state, each row
 // reduced by itself: 275 us.  One sequence: 5 us, a launch and three dependent loads.
+// With offsets (packed sequences of at most one token) sequence b's row is cu[b], and a
+// sequence without a token leaves its state as it was.
 // ---------------------------------------------------------------------------
 constexpr int kDecodeRows = 8;        // loads in flight per lane
 constexpr int kDecodeWarps = 4;
@@ -69,6 +71,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
     const int row0 = ((blockIdx.x - unit * CTAS) * kDecodeWarps + warp) * ROWS + (lane / LPR) * kDecodeRows;
     const int col = (lane & (LPR - 1)) * 4;
     const bool report = h == 0 && threadIdx.x == 0;
+    int64_t t = b;
+    if (p.cu) {
+        int n;
+        linear_rows(p, b, t, n, report);
+        if (n == 0) return;
+    }
     bool from;
     float *state = linear_state(p, b, h, from, report);
     float4 S[kDecodeRows];                              // rows row0 .. row0 + 7, columns col .. col + 3
@@ -77,8 +85,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
         S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (from) S[i] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + i) * D + col));
     }
-    const uint2 kr = *reinterpret_cast<const uint2 *>(p.k + (int64_t)b * p.k_stride + h * D + col);
-    const uint4 vr = *reinterpret_cast<const uint4 *>(p.v + (int64_t)b * p.v_stride + h * D + row0);
+    const uint2 kr = *reinterpret_cast<const uint2 *>(p.k + t * p.k_stride + h * D + col);
+    const uint4 vr = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + h * D + row0);
     const float a = expf(linear_log_decay(p, h, b == 0 && threadIdx.x == 0));
     const float k0 = __uint_as_float(kr.x << 16), k1 = __uint_as_float(kr.x & 0xFFFF0000u);
     const float k2 = __uint_as_float(kr.y << 16), k3 = __uint_as_float(kr.y & 0xFFFF0000u);
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
     }
     for (int g = 0; g < p.G; ++g) {
         const int hq = h * p.G + g;
-        const uint2 qr = *reinterpret_cast<const uint2 *>(p.q + (int64_t)b * p.q_stride + (int64_t)hq * D + col);
+        const uint2 qr = *reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (int64_t)hq * D + col);
         const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
         const float q2 = __uint_as_float(qr.y << 16), q3 = __uint_as_float(qr.y & 0xFFFF0000u);
         float o[kDecodeRows];
@@ -117,7 +125,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
         // row bits: 4, 2, 1 from lane bits LPR / 2, LPR / 4, LPR / 8
         const int row = (lane & (LPR - 1)) / (LPR / 8);
         if ((lane & (LPR / 8 - 1)) == 0)
-            p.out[(int64_t)b * p.out_stride + (int64_t)hq * D + row0 + row] = __float2bfloat16_rn(o[0] * p.scale);
+            p.out[t * p.out_stride + (int64_t)hq * D + row0 + row] = __float2bfloat16_rn(o[0] * p.scale);
     }
 }
 

@@ -522,11 +522,13 @@ ATTN_API attn_status attn_rope_store_kvcache(const void *q, const void *k, const
  *                state; 0: the sequence starts from a zero state, whatever the
  *                slot holds.  NULL: every sequence starts from zero
  *   max_seqlen   host-side upper bound of the lengths (a longer sequence is cut
- *                to it and reported as ATTN_ERR_DEVICE_INDEX); 0: nothing runs
+ *                to it and reported as ATTN_ERR_DEVICE_INDEX); 0: nothing runs;
+ *                1 (a decode step): attn_linear_decode's recurrent form, which
+ *                needs no workspace
  * A sequence of length 0 leaves its slot as it was.
  * An infinity or NaN in k or v reaches its own token's output and later ones of
- * its sequence and head (one in v: its value dimension alone) as NaN, one in q
- * its own token's; nothing else.  The workspace holds nothing from call to call:
+ * its sequence and head (one in v: its value dimension alone) as NaN (in the
+ * recurrent form NaN or an infinity), one in q its own token's; nothing else.  The workspace holds nothing from call to call:
  * calls that follow one another on a stream may share it, calls that may run at the
  * same time need one each.
  * Limits: batch, num_heads_q <= 65535; total_tokens < 2^31 - 1.

@@ -28,3 +28,68 @@ def test_fresh_prompts_read_their_own_rows_whoever_was_served():
     assert ctx.max_seqlen_k == 100 and ctx.block_tables is None
     ctx = at.PagePool.context(t, True, 100, 128)
     assert ctx.cu_seqlens_k is t.cu_seqlens_k and ctx.max_seqlen_k == 128 and ctx.block_tables is t.block_table
+
+
+@pytest.fixture
+def linear(monkeypatch):
+    """A layer with states of four slots, and the calls it makes."""
+    calls = []
+
+    def note(name):
+        def f(q, k, v, g, *a, **kw):
+            calls.append((name, a, kw))
+            return torch.zeros_like(q)
+        return f
+
+    for name in ("linear_attn_decode", "linear_attn_varlen_fwd"):
+        monkeypatch.setattr(at, name, note(name))
+    layer = at.LinearAttention(2, 64, 0.5, 1, torch.zeros(1))
+    layer.state_cache = torch.zeros(4, 1, 64, 64)
+
+    def run(ctx, rows):
+        calls.clear()
+        layer(torch.zeros(rows, 128), torch.zeros(rows, 64), torch.zeros(rows, 64), ctx)
+        return calls[0]
+    return run
+
+
+@pytest.mark.parametrize("new,pad", [([2, 0], 0), ([3, 1, 0, 0], 0), ([1, 0, 1, 1], 1), ([1, 0, 1], 0), ([2, 0, 1], 0),
+                                     ([1, 1, 1], 0), ([1, 1, 0], 2), ([2, 2], 0)])
+def test_a_decode_step_goes_by_its_offsets(linear, new, pad):
+    """As many rows as sequences is no sign of one token each: rows are packed in entry
+    order, so that an entry without a token moves the ones behind it."""
+    B = len(new)
+    t = _tables([5] * B, new, [True] * B)
+    ctx = at.PagePool.context(t, False, max(new), 64, state_slots=torch.arange(B).int())
+    name, a, kw = linear(ctx, sum(new) + pad)
+    assert name == "linear_attn_varlen_fwd" and a[0] is t.cu_seqlens_q and a[1] == max(new)
+    assert kw["state_slots"] is ctx.state_slots and kw["context_lens"] is t.context_lens
+
+
+def test_a_decode_step_without_offsets_has_a_row_for_each_sequence(linear):
+    slots, past = _i32(2, 0, 1), _i32(4, 4, 4)
+    ctx = at.AttentionContext(False, state_slots=slots, past_lens=past)
+    name, a, kw = linear(ctx, 3)
+    assert name == "linear_attn_decode" and a[1] is slots and kw["context_lens"] is past
+    with pytest.raises(ValueError, match="offsets"):
+        linear(ctx, 4)
+    # offsets, and no word on what came before: every slot continues, as without offsets
+    ctx = at.AttentionContext(False, state_slots=slots, cu_seqlens_q=_i32(0, 1, 1, 2), max_seqlen_q=1)
+    name, a, kw = linear(ctx, 3)
+    assert name == "linear_attn_varlen_fwd" and kw["context_lens"].tolist() == [1, 1, 1]
+    # no bound on the counts either
+    ctx = at.AttentionContext(False, state_slots=slots, cu_seqlens_q=_i32(0, 2, 2, 3), past_lens=past)
+    name, a, kw = linear(ctx, 3)
+    assert name == "linear_attn_varlen_fwd" and a[1] == 3
+
+
+def test_sequences_of_at_most_one_token_need_no_workspace():
+    av.build()
+    L = av.lib()
+    assert L.attn_linear_workspace_size(256, 32, 8, 128, 1) == L.attn_linear_workspace_size(256, 32, 8, 128, 0) == 0
+    assert L.attn_linear_workspace_size(256, 32, 8, 128, 2) > 0
+    if torch.cuda.is_available():
+        return                                           # made-up addresses below: they must find no device
+    call = lambda most: L.attn_linear_varlen_fwd(0x1000, 0x1000, 0x1000, 0x1000, 0x1000, 0x1000, None, None, None, 4,  # noqa: E731
+                                                 4, most, 2, 1, 64, 0.1, 0, 0, 0, 0, 0, None, 0, None)
+    assert call(1) == 7 and call(2) == 1 and call(0) == 0
