@@ -158,13 +158,23 @@ def _check(status: int, where: str):
         raise AttnError(status, where)
 
 
+def _row_stride(rows: int, stride: int, packed: int, name: str) -> int:
+    """The stride to pass for rows of `packed` elements.  A smaller one (0: a tensor expanded along its
+    rows) is refused here: the library takes 0 for packed and would read past the tensor."""
+    if rows <= 1:
+        return packed
+    if stride < packed:
+        raise ValueError(f"{name}: rows must not overlap (row stride {stride} of rows of {packed} elements)")
+    return stride
+
+
 def _rows(t: torch.Tensor, name: str, heads: int, dim: int) -> int:
     """Row stride (elements) of a [rows, heads, dim] view whose heads and dim are packed."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name}: expected [rows, {heads}, {dim}], got {tuple(t.shape)}")
     if t.stride(2) != 1 or t.stride(1) != dim:
         raise ValueError(f"{name}: heads and head_dim must be packed (strides {t.stride()})")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return _row_stride(t.shape[0], t.stride(0), heads * dim, name)
 
 
 def _bf16_cuda(*named):
@@ -197,7 +207,9 @@ def _tokens(t, name, dev, rows, heads, dim) -> int:
     if t.shape != (rows, heads, dim) or stride[2] != 1 or stride[1] != dim:
         raise ValueError(f"{name}: expected [{rows}, {heads}, {dim}] with packed heads, got {tuple(t.shape)} "
                          f"(strides {stride})")
-    return stride[0] if rows > 1 else heads * dim
+    if rows > 1 and stride[0] >= heads * dim:
+        return stride[0]
+    return _row_stride(rows, stride[0], heads * dim, name)
 
 
 def _device(t: torch.Tensor, name: str) -> int:
@@ -532,8 +544,9 @@ def softmax_rows(x, out=None, stream=None):
     if o2.data_ptr() != out.data_ptr() or x2.data_ptr() != x.data_ptr():
         raise ValueError("x and out must be viewable as [rows, cols]")
     dtype = 1 if x.dtype == torch.bfloat16 else 0
-    st = lib().attn_softmax_rows(_ptr(x2), _ptr(o2), x2.shape[0], cols, x2.stride(0) if x2.shape[0] > 1 else cols,
-                                 o2.stride(0) if o2.shape[0] > 1 else cols, dtype, _stream(stream))
+    rows = x2.shape[0]
+    st = lib().attn_softmax_rows(_ptr(x2), _ptr(o2), rows, cols, _row_stride(rows, x2.stride(0), cols, "x"),
+                                 _row_stride(rows, o2.stride(0), cols, "out"), dtype, _stream(stream))
     _check(st, "attn_softmax_rows")
     return out
 
