@@ -668,7 +668,7 @@ def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None,
     rotated k and of v into the caches (as store_kvcache), in one pass.
 
     positions int32 [N], or [A, N] with pair_axis (a sequence of A-axis numbers,
-    one per pair); inv_freq float32 [rot_dim / 2].  Pair i is elements (i, i +
+    one per pair; [N] expanded to [A, N] will do); inv_freq float32 [rot_dim / 2].  Pair i is elements (i, i +
     rot_dim / 2), or (2 i, 2 i + 1) if interleaved; elements past rot_dim pass
     through.  Without caches only q and k are rotated (v may be None).  q_out and
     k_out may be q and k.  Returns the rotated q, or (q, k) with return_k."""
@@ -710,9 +710,15 @@ def rope_store_kvcache(q, k, v, positions, inv_freq, k_cache=None, v_cache=None,
             raise ValueError("pair_axis must have one entry per pair (inv_freq)")
     elif axes > 1:
         raise ValueError("positions with several axes need pair_axis")
+    axis_stride = positions.stride(0) if axes > 1 else N
+    if axes > 1 and axis_stride == 0:
+        # one row expanded: all axes are that one
+        if max(pair_axis, default=0) >= axes:
+            raise ValueError(f"pair_axis must name axes below {axes}")
+        axes, pair_axis, axis_stride = 1, None, N
     st = lib().attn_rope_store_kvcache(
         q.data_ptr(), k.data_ptr(), _address(v), positions.data_ptr(), inv_freq.data_ptr(), pair_axis, axes,
-        positions.stride(0) if axes > 1 else N, 2 * pairs, 1 if interleaved else 0, float(scale), q_out.data_ptr(),
+        axis_stride, 2 * pairs, 1 if interleaved else 0, float(scale), q_out.data_ptr(),
         _address(k_out), _address(k_cache), _address(v_cache), _address(v16_cache), _address(slot_mapping), N, Hq,
         Hkv, D, qs, ks, vs, qos, kos, num_slots, _raw_stream(dev))
     _check(st, "attn_rope_store_kvcache")
