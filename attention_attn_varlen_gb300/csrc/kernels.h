@@ -110,7 +110,8 @@ struct TablesParams {
     int32_t *cache_seqlens;      //   [batch]: tokens after the step
     int32_t *context_lens;       //   [batch]: tokens before it
     int vec_rows, vec_tokens;    // grow: table rows, tokens take 16-byte accesses
-    int32_t *before;             // workspace [batch]: length found for the entry, -1: unusable
+    int32_t *before;             // workspace [batch]: length found for the entry, -1: unusable; then (trim)
+                                 // before[0]: the release's CTAs that are done
     int4 *info;                  // workspace [batch] (grow)
     int4 *span;                  // workspace [batch] (trim): kept pages, pages before, place, row
     uint32_t *err;

@@ -242,8 +242,9 @@ __device__ __forceinline__ void fill_tokens(const TablesParams &p, int64_t cta, 
 
 // Pages kept..before of every request go back: the request order and page order
 // that a grow of the same spans took them in, reversed, so growing and trimming
-// by the same amounts restores the list.
-__device__ __forceinline__ void release_rows(const TablesParams &p, int64_t w, int64_t warps, bool &bad) {
+// by the same amounts restores the list.  `lost`: one of them is not one of the
+// pool's; drop_lost takes it out.
+__device__ __forceinline__ void release_rows(const TablesParams &p, int64_t w, int64_t warps, bool &lost) {
     const int lane = threadIdx.x & 31;
     const int top = *p.num_free;
     for (int64_t b = w; b < p.batch; b += warps) {
@@ -251,11 +252,35 @@ __device__ __forceinline__ void release_rows(const TablesParams &p, int64_t w, i
         for (int j = s.x + lane; j < s.y; j += 32) {
             int32_t *at = p.page_table + (int64_t)s.w * p.max_blocks + j;
             const int page = *at;
-            bad |= page < 0 || page >= p.num_pages;
+            lost |= page < 0 || page >= p.num_pages;
             p.free_pages[top - 1 - (s.z + (j - s.x))] = page;
             *at = -1;
         }
     }
+}
+
+// The pages just given back without those outside the pool, in the same order (one
+// CTA, after every release is visible to it).
+__device__ void drop_lost(const TablesParams &p) {
+    __shared__ int moved;
+    if (threadIdx.x == 0) moved = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+        const int4 s = p.span[b];
+        if (s.y > s.x) atomicMax(&moved, s.z + s.y - s.x);
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x, top = __ldcg(p.num_free);
+    int out = top - moved;
+    for (int base = out; base < top; base += 32) {
+        const int page = base + lane < top ? __ldcg(p.free_pages + base + lane) : -1;
+        const bool good = page >= 0 && page < p.num_pages;
+        const unsigned mask = __ballot_sync(0xffffffffu, good);   // everyone has read: out <= base
+        if (good) p.free_pages[out + __popc(mask & ((1u << lane) - 1))] = page;
+        out += __popc(mask);
+    }
+    if (lane == 0) *p.num_free = out;
 }
 
 __device__ __forceinline__ void report(const TablesParams &p, bool bad, bool full) {
@@ -424,6 +449,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tables_plan_kernel(const Tabl
     __syncthreads();
     if (tid == 0) {
         *p.num_free = GROW ? nf - moved_s : nf + moved_s;
+        if (!GROW) p.before[0] = 0;            // from here on the release's count
         if (GROW) p.cu_q[0] = p.cu_k[0] = 0;
     }
     if (fill) {
@@ -432,7 +458,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) tables_plan_kernel(const Tabl
             fill_rows(p, tid >> 5, kPlanThreads / 32, bad);
             fill_tokens<kPlanThreads>(p, 0, 1, cu_s, bad);
         } else {
-            release_rows(p, tid >> 5, kPlanThreads / 32, bad);
+            bool lost = false;
+            release_rows(p, tid >> 5, kPlanThreads / 32, lost);
+            bad |= lost;
+            if (__syncthreads_or(lost)) drop_lost(p);
         }
     }
     report(p, bad, full);
@@ -452,11 +481,25 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesP
 }
 
 __global__ void __launch_bounds__(kFillThreads) tables_release_kernel(const TablesParams p) {
+    __shared__ int last;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    bool bad = false;
+    bool lost = false;
     release_rows(p, (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5),
-                 (int64_t)gridDim.x * (kFillThreads / 32), bad);
-    report(p, bad, false);
+                 (int64_t)gridDim.x * (kFillThreads / 32), lost);
+    report(p, lost, false);
+    // the last CTA to get here takes out what any of them lost (before[0]: CTAs done, those that lost pages
+    // above the 16th bit)
+    const int any = __syncthreads_or(lost);
+    if (threadIdx.x == 0) {
+        __threadfence();
+        const int mine = any ? 0x10001 : 1, all = atomicAdd(p.before, mine) + mine;
+        last = (all & 0xFFFF) == (int)gridDim.x && all > 0xFFFF;
+    }
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        drop_lost(p);
+    }
 }
 
 // Launch `k` as the programmatic dependent of the launch before it.
@@ -503,7 +546,7 @@ cudaError_t launch_trim_pages(const TablesParams &p, int num_sms, cudaStream_t s
     cudaError_t e = plan<false>(p, fill, stream);
     if (e != cudaSuccess || fill) return e;
     int64_t grid = (p.batch + kFillThreads / 32 - 1) / (kFillThreads / 32);
-    if (grid > 4 * num_sms) grid = 4 * num_sms;
+    if (grid > 4 * num_sms) grid = 4 * num_sms;                 // far below 2^15, what the release's count holds
     return launch_dependent(tables_release_kernel, (unsigned)grid, kFillThreads, stream, p);
 }
 

@@ -454,7 +454,8 @@ ATTN_API attn_status attn_step_tables(const int32_t *request_rows, const int32_t
  * is the reverse of attn_step_tables', so growing and trimming by the same
  * amounts restores the list.  Entries with a row out of range or named before,
  * a negative keep_lens (taken as 0) or more pages than the pool has left room
- * for (left as they were) are reported as ATTN_ERR_DEVICE_INDEX.  Same
+ * for (left as they were) are reported as ATTN_ERR_DEVICE_INDEX, and so are
+ * page_table entries outside the pool, which do not enter the free list.  Same
  * workspace as attn_step_tables. */
 ATTN_API attn_status attn_trim_pages(const int32_t *request_rows, const int32_t *keep_lens, int32_t *seq_lens,
                                      int32_t *page_table, int32_t *free_pages, int32_t *num_free, int batch,
