@@ -207,9 +207,9 @@ def _tokens(t, name, dev, rows, heads, dim) -> int:
     if t.shape != (rows, heads, dim) or stride[2] != 1 or stride[1] != dim:
         raise ValueError(f"{name}: expected [{rows}, {heads}, {dim}] with packed heads, got {tuple(t.shape)} "
                          f"(strides {stride})")
-    if rows > 1 and stride[0] >= heads * dim:
-        return stride[0]
-    return _row_stride(rows, stride[0], heads * dim, name)
+    if rows > 1 and stride[0] < heads * dim:
+        return _row_stride(rows, stride[0], heads * dim, name)
+    return stride[0] if rows > 1 else heads * dim
 
 
 def _device(t: torch.Tensor, name: str) -> int:
