@@ -124,6 +124,8 @@ def lib():
     L.attn_rope_store_kvcache.restype = _i32
     L.attn_linear_varlen_fwd.argtypes = [_vp] * 9 + [_i32, _i64, _i32, _i32, _i32, _i32, _f32] + [_i64] * 5 + [_vp, _sz, _vp]
     L.attn_linear_varlen_fwd.restype = _i32
+    L.attn_linear_step_fwd.argtypes = [_vp] * 10 + [_i32, _i64, _i32, _i32, _i32, _i32, _f32] + [_i64] * 5 + [_vp, _sz, _vp]
+    L.attn_linear_step_fwd.restype = _i32
     L.attn_linear_workspace_size.argtypes = [_i32] * 5
     L.attn_linear_workspace_size.restype = _sz
     L.attn_linear_decode.argtypes = [_vp] * 8 + [_i32, _i32, _i32, _i32, _f32] + [_i64] * 5 + [_vp]
@@ -758,7 +760,7 @@ def linear_attn_workspace_size(batch: int, num_heads_q: int, num_heads_kv: int, 
 @_on_stream
 def linear_attn_varlen_fwd(q, k, v, log_decay, cu_seqlens, max_seqlen: int, scale: float | None = None,
                            state_cache=None, state_slots=None, context_lens=None, out=None, workspace=None,
-                           *, stream=None):
+                           cache_seqlens=None, *, stream=None):
     """Linear attention with a decay per head over packed sequences:
     S_t = exp(log_decay) S_{t-1} + v_t k_t^T, o_t = scale * S_t q_t.
 
@@ -766,19 +768,23 @@ def linear_attn_varlen_fwd(q, k, v, log_decay, cu_seqlens, max_seqlen: int, scal
     0, cu_seqlens int32 [B + 1].  state_cache float32 [num_slots, Hkv, Dv, Dk]
     with state_slots int32 [B] receives the final states; a sequence with
     context_lens[b] > 0 (int32 [B]) starts from its slot, any other from zero.
-    scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
+    cache_seqlens (int32 [B], of step_tables): a sequence in which it is not above
+    context_lens was refused, and its state stays as it was.  scale defaults to
+    1 / sqrt(D).  Returns out [T, Hq, D]."""
     B = cu_seqlens.numel() - 1
     dev, out, T, Hq, Hkv, D, slots, strides = _linear_args(q, k, v, log_decay, state_cache, state_slots, context_lens,
                                                            out, B)
-    _cuda(torch.int32, dev, ("cu_seqlens", cu_seqlens))
+    _cuda(torch.int32, dev, ("cu_seqlens", cu_seqlens), ("cache_seqlens", cache_seqlens))
+    if cache_seqlens is not None and cache_seqlens.numel() != B:
+        raise ValueError("cache_seqlens must have one entry per sequence")
     L = lib()
     max_seqlen = int(max_seqlen)
     workspace, ws, ws_bytes = _bytes(workspace, L.attn_linear_workspace_size(B, Hq, Hkv, D, max_seqlen), dev, q)
-    st = L.attn_linear_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
-                                  cu_seqlens.data_ptr(), _address(state_cache), _address(state_slots),
-                                  _address(context_lens), B, T, max_seqlen, Hq, Hkv, D,
-                                  1.0 / math.sqrt(D) if scale is None else scale, slots, *strides, ws, ws_bytes,
-                                  _raw_stream(dev))
+    st = L.attn_linear_step_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
+                                cu_seqlens.data_ptr(), _address(state_cache), _address(state_slots),
+                                _address(context_lens), _address(cache_seqlens), B, T, max_seqlen, Hq, Hkv, D,
+                                1.0 / math.sqrt(D) if scale is None else scale, slots, *strides, ws, ws_bytes,
+                                _raw_stream(dev))
     _check(st, "attn_linear_varlen_fwd")
     return out
 

@@ -45,6 +45,7 @@ class AttentionContext:
     positions: torch.Tensor | None = None        # int32 [N] or [axes, N]: rotary positions of the new tokens
     state_slots: torch.Tensor | None = None      # int32 [B]: state slot of each sequence (linear attention; < 0: none)
     past_lens: torch.Tensor | None = None        # int32 [B]: tokens before this step (linear attention; 0: from zero)
+    cache_seqlens: torch.Tensor | None = None    # int32 [B]: and after it (linear attention; no more: refused, state kept)
 
 
 @dataclass
@@ -181,7 +182,8 @@ class LinearAttention:
                     raise ValueError("a decode step of several tokens needs ctx.past_lens")
                 past = torch.ones_like(slots)            # as without offsets: every slot continues
             o = linear_attn_varlen_fwd(q, k, v, self.log_decay, offsets, most, self.scale,
-                                       state_cache=self.state_cache, state_slots=slots, context_lens=past)
+                                       state_cache=self.state_cache, state_slots=slots, context_lens=past,
+                                       cache_seqlens=ctx.cache_seqlens)
         return o.view(shape)
 
     __call__ = forward
@@ -194,9 +196,10 @@ class PagePool:
     adds a step's new tokens and returns its tables, trim() cuts requests (0
     ends one); neither waits for the GPU.  Pages that cannot be served are
     reported by get_last_device_error (status 9) and leave their request as it
-    was here and in the paged caches.  The step's layers still run over its
-    tokens (attention sees the old context only): drop their output, and put back
-    a linear layer's state before the request is tried again."""
+    was here, in the paged caches and in the state caches.  The step's layers
+    still run over its tokens (attention sees the old context only): drop their
+    output.  A page belongs to one request: requests cannot share a prefix's
+    pages."""
 
     def __init__(self, num_blocks: int, block_size: int, max_requests: int, max_blocks: int, device=None):
         i32 = torch.int32
@@ -233,4 +236,4 @@ class PagePool:
             cu_seqlens_k=cu_k, max_seqlen_q=max_seqlen_q, max_seqlen_k=most_k,
             context_lens=tables.cache_seqlens, block_tables=tables.block_table if paged else None,
             positions=tables.positions if positions is None else positions, state_slots=state_slots,
-            past_lens=tables.context_lens)
+            past_lens=tables.context_lens, cache_seqlens=tables.cache_seqlens)

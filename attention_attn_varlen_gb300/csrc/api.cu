@@ -1255,6 +1255,19 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
                                    int num_heads_q, int num_heads_kv, int head_dim, float scale, int64_t num_slots,
                                    int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
                                    int64_t out_row_stride, void *workspace, size_t workspace_bytes, void *stream) {
+    return attn_linear_step_fwd(q, k, v, out, log_decay, cu_seqlens, state_cache, state_slots, context_lens, nullptr,
+                                batch, total_tokens, max_seqlen, num_heads_q, num_heads_kv, head_dim, scale, num_slots,
+                                q_row_stride, k_row_stride, v_row_stride, out_row_stride, workspace, workspace_bytes,
+                                stream);
+}
+
+attn_status attn_linear_step_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                                 const int32_t *cu_seqlens, float *state_cache, const int32_t *state_slots,
+                                 const int32_t *context_lens, const int32_t *cache_seqlens, int batch,
+                                 int64_t total_tokens, int max_seqlen, int num_heads_q, int num_heads_kv, int head_dim,
+                                 float scale, int64_t num_slots, int64_t q_row_stride, int64_t k_row_stride,
+                                 int64_t v_row_stride, int64_t out_row_stride, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
     if (!cu_seqlens || max_seqlen < 0) return ATTN_ERR_INVALID_ARG;
     LinearParams p;
     attn_status st = linear_params(&p, q, k, v, out, log_decay, state_cache, state_slots, context_lens, batch,
@@ -1270,6 +1283,7 @@ attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, 
     p.cu = cu_seqlens;
     p.max_seqlen = max_seqlen;
     p.start_zero = context_lens == nullptr;
+    p.cache_seqlens = cache_seqlens;
     p.err = d->err;
     if (linear_recurrent(batch, num_heads_kv, max_seqlen))
         return launched(launch_linear_decode(p, reinterpret_cast<cudaStream_t>(stream)));

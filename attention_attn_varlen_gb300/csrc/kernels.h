@@ -149,6 +149,7 @@ struct LinearParams {
     float *state;                     // [num_slots, Hkv, D, D], rows along the value dimension; null: none kept
     const int32_t *slots;             // [batch]; < 0: no state
     const int32_t *context_lens;      // [batch] or null; 0: the sequence starts from a zero state
+    const int32_t *cache_seqlens;     // [batch] or null; not above context_lens: refused, no state
     int64_t q_stride, k_stride, v_stride, out_stride, total_tokens, num_slots;
     int batch, Hq, Hkv, G, D, max_seqlen;
     int start_zero;                   // context_lens is null and every sequence starts from zero

@@ -24,18 +24,19 @@ __device__ __forceinline__ void linear_rows(const LinearParams &p, int b, int64_
     if (!ok && report) record_error(p.err, ERR_INDEX | SRC_LINEAR);
 }
 
-// State of sequence b, KV head h: its address (null: none kept) and whether the
-// sequence starts from it.
+// State of sequence b, KV head h: its address (null: none kept, or the step refused
+// the sequence) and whether the sequence starts from it.
 __device__ __forceinline__ float *linear_state(const LinearParams &p, int b, int h, bool &from, bool report) {
     from = false;
     if (!p.state) return nullptr;
     const int64_t slot = __ldg(p.slots + b);
-    if (slot < 0) return nullptr;
+    const int past = p.context_lens ? __ldg(p.context_lens + b) : 0;
+    if (slot < 0 || (p.cache_seqlens && __ldg(p.cache_seqlens + b) <= past)) return nullptr;
     if (slot >= p.num_slots) {
         if (report) record_error(p.err, ERR_INDEX | SRC_LINEAR);
         return nullptr;
     }
-    from = p.context_lens ? __ldg(p.context_lens + b) > 0 : !p.start_zero;
+    from = p.context_lens ? past > 0 : !p.start_zero;
     return p.state + (slot * p.Hkv + h) * (int64_t)p.D * p.D;
 }
 

@@ -543,7 +543,21 @@ ATTN_API attn_status attn_linear_varlen_fwd(const void *q, const void *k, const 
                                             int64_t k_row_stride, int64_t v_row_stride, int64_t out_row_stride,
                                             void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes attn_linear_varlen_fwd needs (0 for invalid sizes, and where it needs none). */
+/* attn_linear_step_fwd -- attn_linear_varlen_fwd for the entries of a step that
+ * attn_step_tables built, which may have refused some of them: cache_seqlens
+ * (nullable int32 [batch], its output) counts a sequence's tokens after the step.
+ * Where it is not above context_lens (NULL: 0) the state stays as it was; the
+ * tokens still run, from a zero state. */
+ATTN_API attn_status attn_linear_step_fwd(const void *q, const void *k, const void *v, void *out,
+                                          const float *log_decay, const int32_t *cu_seqlens, float *state_cache,
+                                          const int32_t *state_slots, const int32_t *context_lens,
+                                          const int32_t *cache_seqlens, int batch, int64_t total_tokens,
+                                          int max_seqlen, int num_heads_q, int num_heads_kv, int head_dim, float scale,
+                                          int64_t num_slots, int64_t q_row_stride, int64_t k_row_stride,
+                                          int64_t v_row_stride, int64_t out_row_stride, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/* Workspace bytes the two calls above need (0 for invalid sizes, and where it needs none). */
 ATTN_API size_t attn_linear_workspace_size(int batch, int num_heads_q, int num_heads_kv, int head_dim, int max_seqlen);
 
 /* attn_linear_decode -- the recurrent form: one token per sequence, q, out
@@ -593,8 +607,8 @@ ATTN_API int attn_abi_version(void);
  * `after` are the caller's cudaEvent_t handles (cast to void *); the library
  * neither creates nor destroys them.  While both are non-NULL, every later
  * attn_varlen_fwd, attn_decode_paged, attn_decode_paged_noalloc,
- * store_kvcache, attn_rope_store_kvcache, attn_linear_varlen_fwd and
- * attn_linear_decode call made from the same host thread records `before` on its
+ * store_kvcache, attn_rope_store_kvcache, attn_linear_varlen_fwd,
+ * attn_linear_step_fwd and attn_linear_decode call made from the same host thread records `before` on its
  * stream just before launching its main kernel (the attention kernel of the
  * prefill; the split-KV kernel of the decode; the scatter kernel of the store;
  * the rotary kernel; the chunk kernel or the recurrent one of the linear

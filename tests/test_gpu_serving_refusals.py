@@ -6,7 +6,7 @@ import torch
 
 import attention_attn_varlen_gb300 as av
 import oracle
-from attention_attn_varlen_gb300.attention import Attention, PagePool
+from attention_attn_varlen_gb300.attention import Attention, LinearAttention, PagePool
 from _util import assert_close
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +53,45 @@ def test_a_refused_prompt_leaves_the_other_one_its_own_keys(where):
         for cache, want in zip((att.k_cache, att.v_cache), hist):
             assert torch.equal(cache[pages[:-(-n // BS)]].view(-1, Hkv, D)[:n].cpu(), want), kind
     assert pool.seq_lens.tolist() == [0, 0, 27]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 2, 64), (4, 1, 128)])
+@pytest.mark.parametrize("new,refused", [([1, 1, 1, 1], [1, 3]), ([5, 70, 1, 0], [1]), ([2000, 9, 40, 3000], [0]),
+                                         ([2000, 9, 40, 3000], [3]), ([3, 3, 3, 3], [0, 1, 2, 3])])
+def test_a_refused_request_keeps_its_linear_state(Hq, Hkv, D, new, refused):
+    """Its tokens run all the same, and nothing of them is kept.  The others have the bits of a
+    step that serves everyone."""
+    B, T = len(new), sum(new)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v = (rnd(T, h, D).bfloat16() for h in (Hq, Hkv, Hkv))
+    state = rnd(B, Hkv, D, D)
+    g = torch.linspace(-0.5, -0.001, Hkv, device="cuda")
+    slots, rows = _i32(2, 0, 3, 1), _i32(*range(B))
+    past = [3, 0, 40, 7]
+
+    def run(full):
+        pool = PagePool(1000, BS, B, 400)
+        pool.grow(_i32(*past), sum(past))
+        for b in full:                                    # rows as long as they may get
+            pool.seq_lens[b] = 400 * BS
+            pool.page_table[b] = 0
+        t = pool.grow(_i32(*new), T)
+        lin = LinearAttention(Hq, D, D ** -0.5, Hkv, g)
+        lin.state_cache = state.clone()
+        y = lin(q, k, v, pool.context(t, max(new) > 1, max(new), 400 * BS, state_slots=slots))
+        return t, y, lin.state_cache
+
+    av.get_last_device_error()
+    t, y, got = run(refused)
+    assert av.get_last_device_error()[0] == 9
+    _, want_y, want = run([])
+    assert av.get_last_device_error()[0] == 0
+    cu = t.cu_seqlens_q.tolist()
+    for b in range(B):
+        s = slots[b].item()
+        if b in refused or new[b] == 0:
+            assert torch.equal(got[s], state[s]), b
+        else:
+            assert torch.equal(got[s], want[s]) and torch.equal(y[cu[b]:cu[b + 1]], want_y[cu[b]:cu[b + 1]]), b
+            assert not torch.equal(got[s], state[s])

@@ -66,6 +66,18 @@ def test_a_decode_step_goes_by_its_offsets(linear, new, pad):
     assert kw["state_slots"] is ctx.state_slots and kw["context_lens"] is t.context_lens
 
 
+def test_the_linear_layer_hears_who_was_served(linear):
+    t = _tables([5, 0, 7], [1, 1, 1], [True, False, True])
+    for prefill in (False, True):
+        ctx = at.PagePool.context(t, prefill, 1, 64, state_slots=_i32(0, 1, 2))
+        assert ctx.cache_seqlens is t.cache_seqlens
+        name, a, kw = linear(ctx, 3)
+        assert name == "linear_attn_varlen_fwd" and kw["cache_seqlens"] is t.cache_seqlens
+    ctx = at.AttentionContext(True, state_slots=_i32(0, 1, 2), cu_seqlens_q=_i32(0, 1, 1, 2), max_seqlen_q=1,
+                              context_lens=_i32(1, 1, 1))
+    assert linear(ctx, 3)[2]["cache_seqlens"] is None    # contexts made by hand say nothing about it
+
+
 def test_a_decode_step_without_offsets_has_a_row_for_each_sequence(linear):
     slots, past = _i32(2, 0, 1), _i32(4, 4, 4)
     ctx = at.AttentionContext(False, state_slots=slots, past_lens=past)
@@ -93,3 +105,18 @@ def test_sequences_of_at_most_one_token_need_no_workspace():
     call = lambda most: L.attn_linear_varlen_fwd(0x1000, 0x1000, 0x1000, 0x1000, 0x1000, 0x1000, None, None, None, 4,  # noqa: E731
                                                  4, most, 2, 1, 64, 0.1, 0, 0, 0, 0, 0, None, 0, None)
     assert call(1) == 7 and call(2) == 1 and call(0) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="passes made-up device addresses")
+def test_the_entry_for_a_steps_entries_checks_what_the_plain_one_does():
+    av.build()
+    L = av.lib()
+    F = 0x1000
+
+    def call(B=2, Hq=4, Hkv=2, D=64, state=F, slots=F, after=F, most=8, ws_bytes=1 << 40, qs=0, cu=F):
+        return L.attn_linear_step_fwd(F, F, F, F, F, cu, state, slots, None, after, B, 10, most, Hq, Hkv, D, 0.1, 4, qs,
+                                      0, 0, 0, F, ws_bytes, None)
+
+    assert call() == call(after=None) == call(state=None, slots=None) == 7
+    assert call(cu=None) == call(Hq=3) == call(state=None) == call(qs=4) == call(most=-1) == 1
+    assert call(D=96) == 2 and call(ws_bytes=8) == 3 and call(ws_bytes=0, most=1) == 7 and call(most=0) == 0
