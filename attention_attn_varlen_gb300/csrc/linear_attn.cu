@@ -24,14 +24,16 @@ __device__ __forceinline__ void linear_rows(const LinearParams &p, int b, int64_
     if (!ok && report) record_error(p.err, ERR_INDEX | SRC_LINEAR);
 }
 
-// State of sequence b, KV head h: its address (null: none kept, or the step refused
-// the sequence) and whether the sequence starts from it.
+// State of sequence b, KV head h: its address (null: none kept, or, STEP, the step
+// refused the sequence) and whether the sequence starts from it.
+template <bool STEP>
 __device__ __forceinline__ float *linear_state(const LinearParams &p, int b, int h, bool &from, bool report) {
     from = false;
     if (!p.state) return nullptr;
     const int64_t slot = __ldg(p.slots + b);
+    if (slot < 0) return nullptr;
     const int past = p.context_lens ? __ldg(p.context_lens + b) : 0;
-    if (slot < 0 || (p.cache_seqlens && __ldg(p.cache_seqlens + b) <= past)) return nullptr;
+    if (STEP && p.cache_seqlens && __ldg(p.cache_seqlens + b) <= past) return nullptr;
     if (slot >= p.num_slots) {
         if (report) record_error(p.err, ERR_INDEX | SRC_LINEAR);
         return nullptr;
@@ -55,13 +57,13 @@ __device__ __forceinline__ float linear_log_decay(const LinearParams &p, int h, 
 // row sums of a warp's rows are reduced together (9 shuffles for 8 rows).  256
 // sequences, 32 heads of 128: 151 us in the kernel, 7.1 TB/s; a CTA per state, each row
 // reduced by itself: 275 us.  One sequence: 5 us, a launch and three dependent loads.
-// With offsets (packed sequences of at most one token) sequence b's row is cu[b], and a
-// sequence without a token leaves its state as it was.
+// PACKED (packed sequences of at most one token): sequence b's row is cu[b], and a
+// sequence without a token leaves its state as it was.  (One sequence: 0.4 us more.)
 // ---------------------------------------------------------------------------
 constexpr int kDecodeRows = 8;        // loads in flight per lane
 constexpr int kDecodeWarps = 4;
 
-template <int D>
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const LinearParams p) {
     constexpr int LPR = D / 4;                          // lanes per row
     constexpr int RPL = 32 / LPR;                       // rows per load
@@ -73,13 +75,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
     const int col = (lane & (LPR - 1)) * 4;
     const bool report = h == 0 && threadIdx.x == 0;
     int64_t t = b;
-    if (p.cu) {
+    if (PACKED) {
         int n;
         linear_rows(p, b, t, n, report);
         if (n == 0) return;
     }
     bool from;
-    float *state = linear_state(p, b, h, from, report);
+    float *state = linear_state<PACKED>(p, b, h, from, report);
     float4 S[kDecodeRows];                              // rows row0 .. row0 + 7, columns col .. col + 3
 #pragma unroll
     for (int i = 0; i < kDecodeRows; ++i) {
@@ -132,9 +134,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
 
 cudaError_t launch_decode_kernel(const LinearParams &p, cudaStream_t stream) {
     const int64_t states = (int64_t)p.batch * p.Hkv;
+    auto *kernel = p.D == 128 ? p.cu ? linear_decode_kernel<128, true> : linear_decode_kernel<128, false>
+                              : p.cu ? linear_decode_kernel<64, true> : linear_decode_kernel<64, false>;
     main_kernel_event_before(stream);
-    if (p.D == 128) linear_decode_kernel<128><<<(unsigned)(states * 4), kDecodeWarps * 32, 0, stream>>>(p);
-    else linear_decode_kernel<64><<<(unsigned)states, kDecodeWarps * 32, 0, stream>>>(p);
+    kernel<<<(unsigned)(p.D == 128 ? states * 4 : states), kDecodeWarps * 32, 0, stream>>>(p);
     main_kernel_event_after(stream);
     return cudaGetLastError();
 }
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(1024) linear_plan_kernel(const LinearParams p)
                 atomicAdd(&count[bucket(tail)], 1);
             } else {
                 bool from;
-                const float *state = linear_state(p, b, 0, from, true);
+                const float *state = linear_state<true>(p, b, 0, from, true);
                 const int slot = state ? __ldg(p.slots + b) : -1;
                 // a state of its own for every segment's start; heads that share a state
                 // read a copy, since one of them writes the new one
