@@ -31,9 +31,11 @@ __device__ __forceinline__ float *linear_state(const LinearParams &p, int b, int
     from = false;
     if (!p.state) return nullptr;
     const int64_t slot = __ldg(p.slots + b);
-    if (slot < 0) return nullptr;
+    if (!STEP && slot < 0) return nullptr;
     const int past = p.context_lens ? __ldg(p.context_lens + b) : 0;
-    if (STEP && p.cache_seqlens && __ldg(p.cache_seqlens + b) <= past) return nullptr;
+    // one branch behind the three loads: they are in flight together
+    const bool refused = STEP && p.cache_seqlens && __ldg(p.cache_seqlens + b) <= past;
+    if (STEP && (slot < 0 || refused)) return nullptr;
     if (slot >= p.num_slots) {
         if (report) record_error(p.err, ERR_INDEX | SRC_LINEAR);
         return nullptr;
@@ -58,7 +60,8 @@ __device__ __forceinline__ float linear_log_decay(const LinearParams &p, int h, 
 // sequences, 32 heads of 128: 151 us in the kernel, 7.1 TB/s; a CTA per state, each row
 // reduced by itself: 275 us.  One sequence: 5 us, a launch and three dependent loads.
 // PACKED (packed sequences of at most one token): sequence b's row is cu[b], and a
-// sequence without a token leaves its state as it was.  (One sequence: 0.4 us more.)
+// sequence without a token leaves its state as it was; its own instance, since the loads and tests
+// cost 0.2 us of one sequence, 0.5 of 64 with 8 states each (10.2 -> 10.7 us).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeRows = 8;        // loads in flight per lane
 constexpr int kDecodeWarps = 4;
@@ -75,13 +78,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) linear_decode_kernel(const 
     const int col = (lane & (LPR - 1)) * 4;
     const bool report = h == 0 && threadIdx.x == 0;
     int64_t t = b;
-    if (PACKED) {
-        int n;
-        linear_rows(p, b, t, n, report);
-        if (n == 0) return;
-    }
+    int n = 1;
+    if (PACKED) linear_rows(p, b, t, n, report);
     bool from;
-    float *state = linear_state<PACKED>(p, b, h, from, report);
+    float *state = linear_state<PACKED>(p, b, h, from, report && n > 0);
+    if (PACKED && n == 0) return;
     float4 S[kDecodeRows];                              // rows row0 .. row0 + 7, columns col .. col + 3
 #pragma unroll
     for (int i = 0; i < kDecodeRows; ++i) {
