@@ -227,7 +227,9 @@ class PagePool:
                 state_slots: torch.Tensor | None = None, positions: torch.Tensor | None = None) -> AttentionContext:
         """The step's AttentionContext.  paged=False: a prefill of fresh prompts,
         whose attention reads the step's own k and v.  positions: instead of the
-        tables' (for instance several axes)."""
+        tables' (for instance several axes).  A decode step (is_prefill False)
+        gives every entry the same number of tokens where it meets an Attention
+        layer; entries of unequal counts go through a paged prefill."""
         # the step's own k has a row for every new token, also of an entry that was not served and so
         # counts as empty in cu_seqlens_k
         cu_k, most_k = (tables.cu_seqlens_k, max_seqlen_k) if paged else (tables.cu_seqlens_q, max_seqlen_q)

@@ -1144,6 +1144,7 @@ attn_status attn_rope_store_kvcache(const void *q, const void *k, const void *v,
 // that run side by side, after a pass that computes each segment's own state from
 // k and v alone: half the main pass's bytes again, plus about 12 us of launches
 // and setup (a segment of 512 tokens).  Without that pass where it does not pay.
+// (The number of SMs is fixed here: the workspace's size, asked for without a device, goes by it.)
 constexpr int kLinearSms = 152;
 static int64_t round64(int64_t x) { return (x + 63) & ~(int64_t)63; }
 

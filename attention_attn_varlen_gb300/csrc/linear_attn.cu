@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto tab_of = [&](int m) { return tables + (m & 1) * S::kTabFloats + LC; };
     auto info_of = [&](int m) { return reinterpret_cast<UnitInfo *>(tables + (m & 1) * S::kTabFloats + 5 * LC); };
 
-    // the loader sets the barriers up, and its first copies are on their way before the others are ready
+    // the loader sets the barriers up; its copies begin when everyone is past the set-up
     if (warp == 28 && lane == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);

@@ -9,8 +9,9 @@
 // Angles.  In fp32 the product loses the fraction of a turn that matters once
 // pos * inv_freq is large (position 10^6: 0.06 rad).  Here inv_freq / 2 pi is a
 // 64-bit binary fraction of a turn and the product with the integer position
-// wraps modulo one turn by itself: 2^-53 of inv_freq * pos remains.  Its top 32 bits
-// are the angle as a signed fraction of half a turn, handed to sincospif.
+// wraps modulo one turn by itself: an error of 2^-52 of inv_freq * pos remains.  Its
+// top 32 bits are the angle as a signed fraction of half a turn, rounded to fp32 (2^-25
+// of half a turn at most) and handed to sincospif.
 //
 // Bound by HBM: q, k, v are read once, q_out, k and v rows written once.  A CTA
 // takes a tile of tokens; the tile's sines and cosines are computed once into
@@ -88,7 +89,7 @@ __device__ __forceinline__ float2 rope_turn(const RopeParams &p, int64_t t, int 
     return make_float2(c * p.scale, s * p.scale);
 }
 
-// Where an item of a token reads and writes.  kind 0: rotated, 1: copied.
+// An item of a token: its two vectors, and where they are in the row.
 template <int VEC>
 struct RopeItem {
     typedef typename RopeVec<VEC>::type V;

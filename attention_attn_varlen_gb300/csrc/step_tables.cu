@@ -17,8 +17,9 @@
 // scan up to 4,096 of them in one round.  Large ones are bound by writing 12 bytes
 // per token and 4 per table entry: a CTA brings the offsets that its tokens span
 // into shared memory, and a thread writes four neighbouring tokens or entries with
-// 16-byte stores.  4,096 prompts with 4.2 M tokens: plan 18 us, fill 21 (50 MB, 2.4 TB/s, issue-bound), trim
-// 13 + 6.
+// 16-byte stores.  4,096 prompts with 4.2 M tokens: plan 17 us (one SM gathers all rows, lengths and
+// claims, and waits for them most of the time), fill 20 (84 instructions a token, issue slots 56 %
+// busy, stores that mostly stay in L2), trim 12 + 5.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -31,7 +32,8 @@ constexpr int kTokens = 4;                 // neighbouring tokens per thread ...
 constexpr int kGroups = 2;                 // ... twice per round
 constexpr int kRowSeg = 512;               // table columns one warp writes per work item
 // table entries and tokens that the planning CTA writes itself, a few per thread (64 requests of 64
-// pages, one token each, grown and trimmed back: 20.5 us a pass, with a second launch 24)
+// pages, one token each, grown and trimmed back: 21 us a pass, 13.2 in a graph; with second launches 25
+// and 14.3)
 constexpr int64_t kInlineWork = 16384;
 constexpr int kSharedRows = kGroups * kPlanThreads * kTokens;   // request rows whose claims fit shared memory
 constexpr int64_t kI32Max = 0x7fffffffll;

@@ -471,8 +471,10 @@ ATTN_API size_t attn_step_tables_workspace_size(int batch);
  *
  * Pair i of a head turns by angle = positions[axis(i)][token] * inv_freq[i]:
  *   (a, b) -> scale * (a cos - b sin, a sin + b cos),
- * computed in fp32 from an angle exact to 2^-31 of half a turn at any position,
- * rounded once to bf16.
+ * computed in fp32 and rounded once to bf16.  The angle's fraction of a turn comes
+ * from inv_freq / (2 pi) in double and is off by 2^-52 of positions * inv_freq at
+ * most, whatever the position; its sine and cosine are taken of that fraction
+ * rounded to fp32 (2^-25 of half a turn at most).
  *
  *   q, k, v      [num_tokens, num_heads_q | num_heads_kv, head_dim]
  *   positions    int32 [num_axes][num_tokens], axes axis_stride elements apart
@@ -527,13 +529,20 @@ ATTN_API attn_status attn_rope_store_kvcache(const void *q, const void *k, const
  *                1 (a decode step): attn_linear_decode's recurrent form, which
  *                needs no workspace
  * A sequence of length 0 leaves its slot as it was.
+ * Precision: q, k and v are exact bf16 operands and sums are fp32.  The state is
+ * kept and returned in fp32, its new terms as exact to 2^-24 each.  Outputs of the
+ * chunked form (max_seqlen > 1) take the factors e^((i-j) g) q_i . k_j and the state
+ * before a chunk as two bf16 parts each, 2^-16 of a term at most, against the bf16
+ * output's own 2^-8: they are not the bits that fp32 factors would give.
  * An infinity or NaN in k or v reaches its own token's output and later ones of
  * its sequence and head (one in v: its value dimension alone) as NaN (in the
  * recurrent form NaN or an infinity), one in q its own token's; nothing else.  The workspace holds nothing from call to call:
  * calls that follow one another on a stream may share it, calls that may run at the
  * same time need one each.
  * Limits: batch, num_heads_q <= 65535; total_tokens < 2^31 - 1.
- * workspace: attn_linear_workspace_size(...) bytes, 256-byte aligned.
+ * workspace: attn_linear_workspace_size(...) bytes, 256-byte aligned.  With grouped
+ * heads that is a start state for every sequence, 4 x num_heads_kv x head_dim^2
+ * bytes, used or not (2.1 GB of 4,096 sequences with 8 heads of 128).
  * ------------------------------------------------------------------------ */
 ATTN_API attn_status attn_linear_varlen_fwd(const void *q, const void *k, const void *v, void *out,
                                             const float *log_decay, const int32_t *cu_seqlens, float *state_cache,
