@@ -36,7 +36,7 @@ class AttentionContext:
     """Per-step metadata shared by all attention layers of a forward pass."""
     is_prefill: bool
     slot_mapping: torch.Tensor | None = None     # int64 [N]: flat cache slot of each new token (< 0: skip)
-    cu_seqlens_q: torch.Tensor | None = None     # int32 [B+1] (prefill)
+    cu_seqlens_q: torch.Tensor | None = None     # int32 [B+1] (prefill; linear attention: any step)
     cu_seqlens_k: torch.Tensor | None = None     # int32 [B+1] (prefill)
     max_seqlen_q: int = 0
     max_seqlen_k: int = 0
