@@ -20,6 +20,12 @@ Entry points (the C ABI's names):
     rope_store_kvcache      rotary positions (several axes) on q and k, fused with the paged store
     linear_attn_varlen_fwd  linear attention with a decay per head over packed prompts, fp32 state cache
     linear_attn_decode      the same for one token per sequence
+    delta_attn_varlen_fwd   linear attention by the gated delta rule over packed sequences, fp32 state cache
+    delta_attn_decode       the same for one token per sequence
+    beam_select             beam search: the best continuations among beams and vocabulary
+    beam_rows               the request rows of the chosen beams, and which of them are copies
+    copy_states             copies of state slots (beams that are continued more than once)
+    copy_kvcache            copies of cached keys and values between request rows
     get_last_device_error   the device error word (index, range and timeout checks)
     selftest_bounded_wait   the failure-detection self-test
 and the layer-shaped dispatcher in :mod:`attention_attn_varlen_gb300.attention`.
@@ -41,6 +47,8 @@ from ._build import build
 __all__ = ["attn_varlen_fwd", "attn_varlen_fwd_host", "host_staging", "attn_decode_paged", "attn_with_kvcache",
            "attn_padded_fwd", "softmax_rows", "store_kvcache", "step_tables", "trim_pages", "StepTables",
            "rope_store_kvcache", "linear_attn_varlen_fwd", "linear_attn_decode", "linear_attn_workspace_size",
+           "delta_attn_varlen_fwd", "delta_attn_decode", "delta_attn_workspace_size", "beam_select",
+           "beam_select_workspace_size", "beam_rows", "copy_states", "copy_kvcache",
            "get_last_device_error", "selftest_bounded_wait",
            "lib", "build", "AttnError", "exported_symbols", "set_kernel_events", "decode_num_splits",
            "decode_workspace_size"]
@@ -130,6 +138,22 @@ def lib():
     L.attn_linear_workspace_size.restype = _sz
     L.attn_linear_decode.argtypes = [_vp] * 8 + [_i32, _i32, _i32, _i32, _f32] + [_i64] * 5 + [_vp]
     L.attn_linear_decode.restype = _i32
+    L.attn_delta_fwd.argtypes = [_vp] * 11 + [_i32, _i64] + [_i32] * 4 + [_f32, _f32] + [_i64] * 7 + [_vp, _sz, _vp]
+    L.attn_delta_fwd.restype = _i32
+    L.attn_delta_workspace_size.argtypes = [_i32, _i64] + [_i32] * 4
+    L.attn_delta_workspace_size.restype = _sz
+    L.attn_delta_decode.argtypes = [_vp] * 9 + [_i32] * 4 + [_f32, _f32] + [_i64] * 7 + [_vp]
+    L.attn_delta_decode.restype = _i32
+    L.attn_beam_select.argtypes = [_vp, _vp] + [_i32] * 4 + [_i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.attn_beam_select.restype = _i32
+    L.attn_beam_select_workspace_size.argtypes = [_i32] * 4
+    L.attn_beam_select_workspace_size.restype = _sz
+    L.attn_beam_rows.argtypes = [_vp] * 4 + [_i32, _i32, _vp]
+    L.attn_beam_rows.restype = _i32
+    L.attn_copy_states.argtypes = [_vp] * 3 + [_i32, _i64, _i64, _vp]
+    L.attn_copy_states.restype = _i32
+    L.attn_copy_kvcache.argtypes = [_vp] * 5 + [_i32] + [_vp] * 3 + [_i32] * 3 + [_i64, _i32, _i32, _vp]
+    L.attn_copy_kvcache.restype = _i32
     _lib = L
     return L
 
@@ -804,6 +828,212 @@ def linear_attn_decode(q, k, v, log_decay, state_cache, state_slots, scale: floa
                                   _raw_stream(dev))
     _check(st, "attn_linear_decode")
     return out
+
+
+def _token_scalars(t, name, dev, rows, heads) -> int:
+    """Row stride of a float32 [rows, heads] tensor on cuda:dev whose heads are packed."""
+    if t.dtype is not torch.float32 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a float32 tensor on cuda:{dev}")
+    if t.shape != (rows, heads) or (heads > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected [{rows}, {heads}] with packed heads, got {tuple(t.shape)} "
+                         f"(strides {t.stride()})")
+    return _row_stride(rows, t.stride(0), heads, name)
+
+
+def _delta_args(q, k, v, log_decay, beta, state_cache, state_slots, context_lens, out, B, scale, qk_norm_eps):
+    dev = _device(q, "q")
+    T, Hk, D = q.shape
+    Hv = v.shape[1]
+    if out is None:
+        out = torch.empty((T, Hv, D), dtype=q.dtype, device=q.device)
+    strides = (_tokens(q, "q", dev, T, Hk, D), _tokens(k, "k", dev, T, Hk, D), _tokens(v, "v", dev, T, Hv, D),
+               _tokens(out, "out", dev, T, Hv, D), _token_scalars(log_decay, "log_decay", dev, T, Hv),
+               _token_scalars(beta, "beta", dev, T, Hv))
+    _cuda(torch.float32, dev, ("state_cache", state_cache))
+    _cuda(torch.int32, dev, ("state_slots", state_slots), ("context_lens", context_lens))
+    if (state_cache is None) != (state_slots is None):
+        raise ValueError("state_cache and state_slots go together")
+    slots = 0
+    if state_cache is not None:
+        slots = state_cache.shape[0]
+        if state_cache.shape != (slots, Hv, D, D):
+            raise ValueError(f"state_cache must be [num_slots, {Hv}, {D}, {D}]")
+        if state_slots.numel() != B:
+            raise ValueError("state_slots must have one entry per sequence")
+    if context_lens is not None and context_lens.numel() != B:
+        raise ValueError("context_lens must have one entry per sequence")
+    if qk_norm_eps is None:
+        qk_norm_eps = -1.0
+    elif not qk_norm_eps >= 0:
+        raise ValueError("qk_norm_eps must not be negative")
+    return dev, out, T, Hk, Hv, D, 1.0 / math.sqrt(D) if scale is None else scale, qk_norm_eps, slots, strides
+
+
+def delta_attn_workspace_size(batch: int, total_tokens: int, num_heads_k: int, num_heads_v: int, head_dim: int,
+                              max_seqlen: int) -> int:
+    return lib().attn_delta_workspace_size(batch, total_tokens, num_heads_k, num_heads_v, head_dim, max_seqlen)
+
+
+@_on_stream
+def delta_attn_varlen_fwd(q, k, v, log_decay, beta, cu_seqlens, max_seqlen: int, scale: float | None = None,
+                          state_cache=None, state_slots=None, context_lens=None, cache_seqlens=None,
+                          qk_norm_eps: float | None = None, out=None, workspace=None, *, stream=None):
+    """Linear attention by the gated delta rule over packed sequences:
+    u_t = beta_t (v_t - exp(log_decay_t) S_{t-1} k_t),
+    S_t = exp(log_decay_t) S_{t-1} + u_t k_t^T, o_t = scale * S_t q_t.
+
+    q, k [T, Hk, D], v [T, Hv, D] bf16 (D 64 or 128, Hv a multiple of Hk),
+    log_decay (<= 0) and beta float32 [T, Hv], cu_seqlens int32 [B + 1].
+    qk_norm_eps: q and k are divided by sqrt(their sum of squares + eps) on the way
+    (None: taken as they are).  state_cache float32 [num_slots, Hv, Dv, Dk] with
+    state_slots, context_lens and cache_seqlens as for linear_attn_varlen_fwd.  scale
+    defaults to 1 / sqrt(D).  Returns out [T, Hv, D]."""
+    B = cu_seqlens.numel() - 1
+    dev, out, T, Hk, Hv, D, scale, eps, slots, strides = _delta_args(
+        q, k, v, log_decay, beta, state_cache, state_slots, context_lens, out, B, scale, qk_norm_eps)
+    _cuda(torch.int32, dev, ("cu_seqlens", cu_seqlens), ("cache_seqlens", cache_seqlens))
+    if cache_seqlens is not None and cache_seqlens.numel() != B:
+        raise ValueError("cache_seqlens must have one entry per sequence")
+    L = lib()
+    max_seqlen = int(max_seqlen)
+    workspace, ws, ws_bytes = _bytes(workspace, L.attn_delta_workspace_size(B, T, Hk, Hv, D, max_seqlen), dev, q)
+    st = L.attn_delta_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
+                          beta.data_ptr(), cu_seqlens.data_ptr(), _address(state_cache), _address(state_slots),
+                          _address(context_lens), _address(cache_seqlens), B, T, max_seqlen, Hk, Hv, D, scale, eps,
+                          slots, *strides, ws, ws_bytes, _raw_stream(dev))
+    _check(st, "attn_delta_fwd")
+    return out
+
+
+@_on_stream
+def delta_attn_decode(q, k, v, log_decay, beta, state_cache, state_slots, scale: float | None = None,
+                      context_lens=None, qk_norm_eps: float | None = None, out=None, *, stream=None):
+    """delta_attn_varlen_fwd for one token per sequence: q, k [B, Hk, D], v [B, Hv,
+    D], log_decay, beta [B, Hv]; the states in state_cache are updated in place.  A
+    slot < 0 stands for a zero state that is not kept; context_lens[b] = 0 starts
+    from zero (None: every slot continues).  Returns out [B, Hv, D]."""
+    dev, out, B, Hk, Hv, D, scale, eps, slots, strides = _delta_args(
+        q, k, v, log_decay, beta, state_cache, state_slots, context_lens, out, q.shape[0], scale, qk_norm_eps)
+    st = lib().attn_delta_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_decay.data_ptr(),
+                                 beta.data_ptr(), _address(state_cache), _address(state_slots),
+                                 _address(context_lens), B, Hk, Hv, D, scale, eps, slots, *strides, _raw_stream(dev))
+    _check(st, "attn_delta_decode")
+    return out
+
+
+def beam_select_workspace_size(num_groups: int, num_beams: int, vocab: int, num_out: int) -> int:
+    return lib().attn_beam_select_workspace_size(num_groups, num_beams, vocab, num_out)
+
+
+@_on_stream
+def beam_select(logits, scores, num_beams: int, num_out: int, out=None, workspace=None, *, stream=None):
+    """One step of beam search: the num_out best continuations of every request.
+
+    logits [R * num_beams, V] bf16 or float32 (-inf: ruled out), scores float32 [R *
+    num_beams] (-inf: a beam without candidates).  A candidate scores its beam's score
+    + log_softmax(logits); equal ones come by beam, then by token.  Returns (tokens,
+    parents, scores), each [R, num_out] (int32, int32, float32; `out`: buffers for them);
+    -1, -1, -inf where there are no more candidates."""
+    dev = _device(logits, "logits")
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits must be bfloat16 or float32 [rows, vocab]")
+    N, V = logits.shape
+    if num_beams <= 0 or N % num_beams:
+        raise ValueError("logits must have num_beams rows per request")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must be contiguous along the vocabulary")
+    stride = _row_stride(N, logits.stride(0), V, "logits")
+    _cuda(torch.float32, dev, ("scores", scores))
+    if scores.numel() != N:
+        raise ValueError("scores must have one entry per row")
+    R = N // num_beams
+    if out is None:
+        new = lambda dt: torch.empty((R, num_out), dtype=dt, device=logits.device)  # noqa: E731
+        out = new(torch.int32), new(torch.int32), new(torch.float32)
+    tokens, parents, best = out
+    _cuda(torch.int32, dev, ("tokens", tokens), ("parents", parents))
+    _cuda(torch.float32, dev, ("out scores", best))
+    if tokens.shape != (R, num_out) or parents.shape != (R, num_out) or best.shape != (R, num_out):
+        raise ValueError(f"out must be three tensors [{R}, {num_out}]")
+    if R == 0:
+        return tokens, parents, best
+    L = lib()
+    workspace, ws, ws_bytes = _bytes(workspace, L.attn_beam_select_workspace_size(R, num_beams, V, num_out), dev,
+                                     logits)
+    st = L.attn_beam_select(logits.data_ptr(), scores.data_ptr(), R, num_beams, V, num_out, stride,
+                            1 if logits.dtype is torch.bfloat16 else 0, tokens.data_ptr(), parents.data_ptr(),
+                            best.data_ptr(), ws, ws_bytes, _raw_stream(dev))
+    _check(st, "attn_beam_select")
+    return tokens, parents, best
+
+
+@_on_stream
+def beam_rows(parents, rows, out=None, *, stream=None):
+    """The request rows of a search's next beams: parents and rows int32 [R,
+    num_beams] (rows all different).  The lowest beam that goes on from a parent
+    takes its row, the others rows that nobody goes on from.  Returns (rows, source),
+    int32 [R, num_beams] each (`out`: buffers for them): source is -1, or the row
+    that copy_states and copy_kvcache have to copy to the new row."""
+    dev = _device(parents, "parents")
+    if out is None:
+        out = torch.empty_like(rows, memory_format=torch.contiguous_format), torch.empty_like(
+            parents, memory_format=torch.contiguous_format)
+    new, source = out
+    _cuda(torch.int32, dev, ("parents", parents), ("rows", rows), ("out rows", new), ("source", source))
+    if parents.dim() != 2 or rows.shape != parents.shape or new.shape != parents.shape             or source.shape != parents.shape:
+        raise ValueError("parents, rows and out must be [requests, num_beams]")
+    if parents.numel() == 0:
+        return new, source
+    st = lib().attn_beam_rows(parents.data_ptr(), rows.data_ptr(), new.data_ptr(), source.data_ptr(),
+                              *parents.shape, _raw_stream(dev))
+    _check(st, "attn_beam_rows")
+    return new, source
+
+
+def _pairs(src, dst, dev) -> int:
+    _cuda(torch.int32, dev, ("src", src), ("dst", dst))
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    return src.numel()
+
+
+@_on_stream
+def copy_states(cache, src, dst, *, stream=None) -> None:
+    """cache[dst[i]] = cache[src[i]] wherever src[i] >= 0: cache [num_slots, ...] of
+    any type (slots of a multiple of 16 bytes), src and dst int32 of one size.  No
+    destination may be a source or named twice."""
+    dev = _device(cache, "cache")
+    if not cache.is_contiguous() or cache.dim() < 2 or cache.numel() == 0:
+        raise ValueError("cache must be a contiguous [num_slots, ...] tensor")
+    n = _pairs(src, dst, dev)
+    slots = cache.shape[0]
+    st = lib().attn_copy_states(cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, slots,
+                                cache.numel() // slots * cache.element_size(), _raw_stream(dev))
+    _check(st, "attn_copy_states")
+
+
+@_on_stream
+def copy_kvcache(k_cache, v_cache, src, dst, page_table, seq_lens, first_tokens=None, v16_cache=None, *,
+                 stream=None) -> None:
+    """Cached tokens of request row src[i] to the same positions of row dst[i]
+    wherever src[i] >= 0, through the rows' pages: caches [num_blocks, block_size, Hkv,
+    D], page_table int32 [num_rows, max_blocks] and seq_lens int32 [num_rows] as
+    step_tables keeps them.  first_tokens int32 [num_rows]: where copying starts (the
+    rows share a prompt's tokens before it).  No destination may be a source."""
+    dev = _device(k_cache, "k_cache")
+    _cuda(torch.bfloat16, dev, ("k_cache", k_cache), ("v_cache", v_cache))
+    _cuda(torch.float16, dev, ("v16_cache", v16_cache))
+    _cuda(torch.int32, dev, ("page_table", page_table), ("seq_lens", seq_lens), ("first_tokens", first_tokens))
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape             or (v16_cache is not None and v16_cache.shape != k_cache.shape):
+        raise ValueError("the caches must have one shape [num_blocks, block_size, Hkv, D]")
+    if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0]             or (first_tokens is not None and first_tokens.numel() != page_table.shape[0]):
+        raise ValueError("page_table must be [num_rows, max_blocks], seq_lens and first_tokens [num_rows]")
+    n = _pairs(src, dst, dev)
+    blocks, bs, Hkv, D = k_cache.shape
+    st = lib().attn_copy_kvcache(k_cache.data_ptr(), v_cache.data_ptr(), _address(v16_cache), src.data_ptr(),
+                                 dst.data_ptr(), n, page_table.data_ptr(), seq_lens.data_ptr(),
+                                 _address(first_tokens), *page_table.shape, bs, blocks, Hkv, D, _raw_stream(dev))
+    _check(st, "attn_copy_kvcache")
 
 
 def set_kernel_events(before=None, after=None) -> None:

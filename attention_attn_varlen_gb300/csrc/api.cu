@@ -1333,3 +1333,255 @@ attn_status attn_linear_decode(const void *q, const void *k, const void *v, void
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// gated delta rule
+// ---------------------------------------------------------------------------
+
+static bool delta_sizes(int batch, int64_t total_tokens, int num_heads_k, int num_heads_v, int head_dim) {
+    return batch > 0 && batch <= 65535 && total_tokens >= 0 && total_tokens < (int64_t)INT32_MAX && num_heads_k > 0 &&
+           num_heads_v > 0 && num_heads_v <= 65535 && num_heads_v % num_heads_k == 0 &&
+           (head_dim == 64 || head_dim == 128) && (int64_t)batch * num_heads_v * 4 <= (int64_t)INT32_MAX;
+}
+
+extern "C" {
+
+size_t attn_delta_workspace_size(int batch, int64_t total_tokens, int num_heads_k, int num_heads_v, int head_dim,
+                                 int max_seqlen) {
+    if (!delta_sizes(batch, total_tokens, num_heads_k, num_heads_v, head_dim) || max_seqlen < 0) return 0;
+    return 0;
+}
+
+}  // extern "C"
+
+// Host checks shared by the two delta-rule entries.
+static attn_status delta_params(DeltaParams *p, const void *q, const void *k, const void *v, void *out,
+                                const float *log_decay, const float *beta, float *state_cache,
+                                const int32_t *state_slots, const int32_t *context_lens, int batch,
+                                int64_t total_tokens, int num_heads_k, int num_heads_v, int head_dim, float scale,
+                                float qk_norm_eps, int64_t num_slots, int64_t q_row_stride, int64_t k_row_stride,
+                                int64_t v_row_stride, int64_t out_row_stride, int64_t log_decay_row_stride,
+                                int64_t beta_row_stride) {
+    if (batch <= 0 || total_tokens < 0 || num_heads_k <= 0 || num_heads_v <= 0 || num_heads_v % num_heads_k)
+        return ATTN_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !out || !log_decay || !beta)) return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !isfinite(scale) || !isfinite(qk_norm_eps)) return ATTN_ERR_INVALID_ARG;
+    if (state_cache ? !state_slots || num_slots <= 0 : state_slots != nullptr) return ATTN_ERR_INVALID_ARG;
+    if (!delta_sizes(batch, total_tokens, num_heads_k, num_heads_v, head_dim)) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state_cache))
+        return ATTN_ERR_INVALID_ARG;
+    if (!fix_stride(&q_row_stride, (int64_t)num_heads_k * head_dim) ||
+        !fix_stride(&k_row_stride, (int64_t)num_heads_k * head_dim) ||
+        !fix_stride(&v_row_stride, (int64_t)num_heads_v * head_dim) ||
+        !fix_stride(&out_row_stride, (int64_t)num_heads_v * head_dim))
+        return ATTN_ERR_INVALID_ARG;
+    if (log_decay_row_stride == 0) log_decay_row_stride = num_heads_v;
+    if (beta_row_stride == 0) beta_row_stride = num_heads_v;
+    if (log_decay_row_stride < num_heads_v || beta_row_stride < num_heads_v) return ATTN_ERR_INVALID_ARG;
+    memset(p, 0, sizeof *p);
+    p->q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p->k = reinterpret_cast<const __nv_bfloat16 *>(k);
+    p->v = reinterpret_cast<const __nv_bfloat16 *>(v);
+    p->out = reinterpret_cast<__nv_bfloat16 *>(out);
+    p->log_decay = log_decay;
+    p->beta = beta;
+    p->state = state_cache;
+    p->slots = state_slots;
+    p->context_lens = context_lens;
+    p->q_stride = q_row_stride;
+    p->k_stride = k_row_stride;
+    p->v_stride = v_row_stride;
+    p->out_stride = out_row_stride;
+    p->decay_stride = log_decay_row_stride;
+    p->beta_stride = beta_row_stride;
+    p->total_tokens = total_tokens;
+    p->num_slots = num_slots;
+    p->batch = batch;
+    p->Hk = num_heads_k;
+    p->Hv = num_heads_v;
+    p->G = num_heads_v / num_heads_k;
+    p->D = head_dim;
+    p->scale = scale;
+    p->norm = qk_norm_eps >= 0.f;
+    p->eps = qk_norm_eps;
+    return ATTN_OK;
+}
+
+extern "C" {
+
+attn_status attn_delta_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                           const float *beta, const int32_t *cu_seqlens, float *state_cache,
+                           const int32_t *state_slots, const int32_t *context_lens, const int32_t *cache_seqlens,
+                           int batch, int64_t total_tokens, int max_seqlen, int num_heads_k, int num_heads_v,
+                           int head_dim, float scale, float qk_norm_eps, int64_t num_slots, int64_t q_row_stride,
+                           int64_t k_row_stride, int64_t v_row_stride, int64_t out_row_stride,
+                           int64_t log_decay_row_stride, int64_t beta_row_stride, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    if (!cu_seqlens || max_seqlen < 0) return ATTN_ERR_INVALID_ARG;
+    DeltaParams p;
+    attn_status st = delta_params(&p, q, k, v, out, log_decay, beta, state_cache, state_slots, context_lens, batch,
+                                  total_tokens, num_heads_k, num_heads_v, head_dim, scale, qk_norm_eps, num_slots,
+                                  q_row_stride, k_row_stride, v_row_stride, out_row_stride, log_decay_row_stride,
+                                  beta_row_stride);
+    if (st != ATTN_OK) return st;
+    const size_t need = attn_delta_workspace_size(batch, total_tokens, num_heads_k, num_heads_v, head_dim, max_seqlen);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (total_tokens == 0 || max_seqlen == 0) return ATTN_OK;
+    DevInfo *d = nullptr;
+    if ((st = device_for(&d)) != ATTN_OK) return st;
+    p.cu = cu_seqlens;
+    p.max_seqlen = max_seqlen;
+    p.start_zero = context_lens == nullptr;
+    p.cache_seqlens = cache_seqlens;
+    p.err = d->err;
+    return launched(launch_delta_recurrent(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_delta_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                              const float *beta, float *state_cache, const int32_t *state_slots,
+                              const int32_t *context_lens, int batch, int num_heads_k, int num_heads_v, int head_dim,
+                              float scale, float qk_norm_eps, int64_t num_slots, int64_t q_row_stride,
+                              int64_t k_row_stride, int64_t v_row_stride, int64_t out_row_stride,
+                              int64_t log_decay_row_stride, int64_t beta_row_stride, void *stream) {
+    if (!state_cache) return ATTN_ERR_INVALID_ARG;
+    DeltaParams p;
+    attn_status st = delta_params(&p, q, k, v, out, log_decay, beta, state_cache, state_slots, context_lens, batch,
+                                  batch, num_heads_k, num_heads_v, head_dim, scale, qk_norm_eps, num_slots,
+                                  q_row_stride, k_row_stride, v_row_stride, out_row_stride, log_decay_row_stride,
+                                  beta_row_stride);
+    if (st != ATTN_OK) return st;
+    DevInfo *d = nullptr;
+    if ((st = device_for(&d)) != ATTN_OK) return st;
+    p.max_seqlen = 1;
+    p.err = d->err;
+    return launched(launch_delta_recurrent(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// beam search
+// ---------------------------------------------------------------------------
+
+static bool beam_sizes(int num_groups, int num_beams, int vocab, int num_out) {
+    return num_groups > 0 && num_beams > 0 && num_beams <= kBeamMax && vocab > 0 && vocab < (1 << 30) && num_out > 0 &&
+           num_out <= kBeamMax && (int64_t)num_groups * num_beams < (1 << 25);
+}
+
+// Slices of a row: four CTAs per SM over all rows, as far as a row has slices.  (The number of SMs is
+// fixed here: the workspace's size, asked for without a device, goes by it.)
+static int beam_slice_len(int rows, int vocab) {
+    const int most = (vocab + kBeamSliceElems - 1) / kBeamSliceElems;
+    int slices = (4 * kLinearSms + rows - 1) / rows;
+    if (slices > most) slices = most;
+    if (slices > 64) slices = 64;
+    const int each = (vocab + slices - 1) / slices;
+    return (each + kBeamSliceElems - 1) / kBeamSliceElems * kBeamSliceElems;
+}
+
+extern "C" {
+
+size_t attn_beam_select_workspace_size(int num_groups, int num_beams, int vocab, int num_out) {
+    if (!beam_sizes(num_groups, num_beams, vocab, num_out)) return 0;
+    const int len = beam_slice_len(num_groups * num_beams, vocab);
+    return (size_t)num_groups * num_beams * ((vocab + len - 1) / len) * ((size_t)num_out + 1) * 8;
+}
+
+attn_status attn_beam_select(const void *logits, const float *scores, int num_groups, int num_beams, int vocab,
+                             int num_out, int64_t row_stride, int dtype, int32_t *tokens, int32_t *parents,
+                             float *out_scores, void *workspace, size_t workspace_bytes, void *stream) {
+    if (num_groups <= 0 || num_beams <= 0 || vocab <= 0 || num_out <= 0) return ATTN_ERR_INVALID_ARG;
+    if (!logits || !scores || !tokens || !parents || !out_scores || !workspace || !aligned16(workspace))
+        return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_DTYPE_F32 && dtype != ATTN_DTYPE_BF16) return ATTN_ERR_INVALID_ARG;
+    if (row_stride == 0) row_stride = vocab;
+    if (row_stride < vocab) return ATTN_ERR_INVALID_ARG;
+    if (!beam_sizes(num_groups, num_beams, vocab, num_out)) return ATTN_ERR_UNSUPPORTED;
+    if (workspace_bytes < attn_beam_select_workspace_size(num_groups, num_beams, vocab, num_out))
+        return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    DevInfo *d = nullptr;
+    attn_status st = device_for(&d);
+    if (st != ATTN_OK) return st;
+    BeamParams p;
+    memset(&p, 0, sizeof p);
+    p.logits = logits;
+    p.scores = scores;
+    p.row_stride = row_stride;
+    p.groups = num_groups;
+    p.W = num_beams;
+    p.V = vocab;
+    p.k = num_out;
+    p.bf16 = dtype == ATTN_DTYPE_BF16;
+    p.slice_len = beam_slice_len(num_groups * num_beams, vocab);
+    p.slices = (vocab + p.slice_len - 1) / p.slice_len;
+    p.wide = aligned16(logits) && row_stride % (p.bf16 ? 8 : 4) == 0;
+    p.keys = reinterpret_cast<uint64_t *>(workspace);
+    p.sums = reinterpret_cast<float2 *>(p.keys + (size_t)num_groups * num_beams * p.slices * num_out);
+    p.tokens = tokens;
+    p.parents = parents;
+    p.out_scores = out_scores;
+    p.err = d->err;
+    return launched(launch_beam_select(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_beam_rows(const int32_t *parents, const int32_t *rows, int32_t *rows_out, int32_t *source,
+                           int num_groups, int num_beams, void *stream) {
+    if (num_groups <= 0 || num_beams <= 0 || !parents || !rows || !rows_out || !source) return ATTN_ERR_INVALID_ARG;
+    if (num_beams > kBeamMax || (int64_t)num_groups * num_beams >= (1 << 25)) return ATTN_ERR_UNSUPPORTED;
+    DevInfo *d = nullptr;
+    attn_status st = device_for(&d);
+    if (st != ATTN_OK) return st;
+    return launched(launch_beam_rows(parents, rows, rows_out, source, num_groups, num_beams, d->err,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_copy_states(void *cache, const int32_t *src, const int32_t *dst, int n, int64_t num_slots,
+                             int64_t slot_bytes, void *stream) {
+    if (n < 0 || num_slots <= 0 || slot_bytes <= 0 || slot_bytes % 16) return ATTN_ERR_INVALID_ARG;
+    if (n == 0) return ATTN_OK;
+    if (!cache || !src || !dst || !aligned16(cache)) return ATTN_ERR_INVALID_ARG;
+    if (n > (1 << 25)) return ATTN_ERR_UNSUPPORTED;
+    DevInfo *d = nullptr;
+    attn_status st = device_for(&d);
+    if (st != ATTN_OK) return st;
+    return launched(launch_copy_states(cache, src, dst, n, num_slots, slot_bytes, d->num_sms, d->err,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_copy_kvcache(void *k_cache, void *v_cache, void *v16_cache, const int32_t *src, const int32_t *dst,
+                              int n, const int32_t *page_table, const int32_t *seq_lens, const int32_t *first_tokens,
+                              int num_rows, int max_blocks, int block_size, int64_t num_blocks, int num_heads_kv,
+                              int head_dim, void *stream) {
+    if (n < 0 || num_rows <= 0 || max_blocks <= 0 || num_blocks <= 0 || num_heads_kv <= 0 || head_dim <= 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (!pow2(block_size) || block_size < 16) return ATTN_ERR_INVALID_ARG;
+    if (n == 0) return ATTN_OK;
+    if (!k_cache || !v_cache || !src || !dst || !page_table || !seq_lens) return ATTN_ERR_INVALID_ARG;
+    if (n > (1 << 25) || (int64_t)num_heads_kv * head_dim > INT32_MAX / 2 ||
+        (int64_t)max_blocks * block_size >= (int64_t)INT32_MAX || num_blocks * block_size >= (int64_t)INT32_MAX)
+        return ATTN_ERR_UNSUPPORTED;
+    DevInfo *d = nullptr;
+    attn_status st = device_for(&d);
+    if (st != ATTN_OK) return st;
+    CopyRowsParams p;
+    memset(&p, 0, sizeof p);
+    p.cache[0] = reinterpret_cast<char *>(k_cache);
+    p.cache[1] = reinterpret_cast<char *>(v_cache);
+    p.cache[2] = reinterpret_cast<char *>(v16_cache);
+    p.row_bytes = (int64_t)num_heads_kv * head_dim * 2;
+    p.src = src;
+    p.dst = dst;
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.first = first_tokens;
+    p.n = n;
+    p.num_rows = num_rows;
+    p.max_blocks = max_blocks;
+    while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
+    p.num_blocks = num_blocks;
+    p.err = d->err;
+    return launched(launch_copy_kvcache(p, d->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -26,6 +26,8 @@ enum : uint32_t {
     SRC_TABLES = 1u << 14,
     SRC_ROPE = 1u << 15,
     SRC_LINEAR = 1u << 16,
+    SRC_DELTA = 1u << 17,
+    SRC_BEAM = 1u << 18,
 };
 
 __device__ __forceinline__ void record_error(uint32_t *err, uint32_t code) {

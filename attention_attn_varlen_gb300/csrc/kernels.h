@@ -169,6 +169,57 @@ cudaError_t launch_linear_varlen(const CUtensorMap &qmap, const CUtensorMap &kma
                                  const CUtensorMap &omap, const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearParams &p, cudaStream_t stream);
 
+// delta_attn.cu: linear attention by the gated delta rule
+struct DeltaParams {
+    const __nv_bfloat16 *q, *k, *v;   // q, k [T, Hk, D], v [T, Hv, D] with row strides
+    __nv_bfloat16 *out;               // [T, Hv, D]
+    const float *log_decay, *beta;    // [T, Hv] with row strides
+    const int32_t *cu;                // [batch + 1], or null (one token per sequence): sequence b is row b
+    float *state;                     // [num_slots, Hv, D, D], rows along the value dimension; null: none kept
+    const int32_t *slots;             // [batch]; < 0: no state
+    const int32_t *context_lens;      // [batch] or null; 0: the sequence starts from a zero state
+    const int32_t *cache_seqlens;     // [batch] or null; not above context_lens: refused, no state
+    int64_t q_stride, k_stride, v_stride, out_stride, decay_stride, beta_stride, total_tokens, num_slots;
+    int batch, Hk, Hv, G, D, max_seqlen;
+    int start_zero;                   // context_lens is null and every sequence starts from zero
+    int norm;                         // q and k are divided by sqrt(their sum of squares + eps)
+    float scale, eps;
+    uint32_t *err;
+};
+cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream);
+
+// beam.cu: beam search's selection, and what follows it
+constexpr int kBeamMax = 32;          // beams of a group, candidates chosen
+constexpr int kBeamSliceElems = 2048; // a slice of a row is a multiple of this
+struct BeamParams {
+    const void *logits;               // [rows, V], bf16 or fp32, row stride in elements
+    const float *scores;              // [rows]
+    int64_t row_stride;
+    int groups, W, V, k, bf16;
+    int slices, slice_len;            // of a row
+    int wide;                         // rows on 16-byte boundaries
+    uint64_t *keys;                   // workspace [rows, slices, k]: a slice's best, sorted
+    float2 *sums;                     // workspace [rows, slices]: maximum, sum of exponentials
+    int32_t *tokens, *parents;        // [groups, k]
+    float *out_scores;                // [groups, k]
+    uint32_t *err;
+};
+cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
+cudaError_t launch_beam_rows(const int32_t *parents, const int32_t *rows, int32_t *rows_out, int32_t *source,
+                             int groups, int W, uint32_t *err, cudaStream_t stream);
+cudaError_t launch_copy_states(void *cache, const int32_t *src, const int32_t *dst, int n, int64_t num_slots,
+                               int64_t slot_bytes, int num_sms, uint32_t *err, cudaStream_t stream);
+struct CopyRowsParams {
+    char *cache[3];                   // k, v, v16 or null; a token's row is row_bytes in each
+    int64_t row_bytes;
+    const int32_t *src, *dst;         // [n] request rows; src < 0: nothing to copy
+    const int32_t *page_table, *seq_lens, *first;   // [num_rows, max_blocks], [num_rows], [num_rows] or null
+    int n, num_rows, max_blocks, bs_log2;
+    int64_t num_blocks;
+    uint32_t *err;
+};
+cudaError_t launch_copy_kvcache(const CopyRowsParams &p, int num_sms, cudaStream_t stream);
+
 cudaError_t launch_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                            const CUtensorMap &omap, const PrefillParams &p, int head_dim, cudaStream_t stream);
 

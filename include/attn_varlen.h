@@ -581,6 +581,130 @@ ATTN_API attn_status attn_linear_decode(const void *q, const void *k, const void
                                         int64_t v_row_stride, int64_t out_row_stride, void *stream);
 
 /* ------------------------------------------------------------------------
+ * attn_delta_fwd -- linear attention by the gated delta rule over packed sequences
+ * (prompts, chunks of prompts, a few guessed tokens each): a token replaces what the
+ * state holds at its key instead of adding to it,
+ *   u_t = beta_t (v_t - e^{g_t} S_{t-1} k_t)
+ *   S_t = e^{g_t} S_{t-1} + u_t k_t^T,   o_t = scale * S_t q_t
+ * with S [head_dim, head_dim] in fp32, rows along v.  Value head h reads key head
+ * h / (num_heads_v / num_heads_k); every value head has its own state.
+ *
+ *   q, k         [total_tokens, num_heads_k, head_dim]
+ *   v, out       [total_tokens, num_heads_v, head_dim]; sequence b owns rows
+ *                [cu_seqlens[b], cu_seqlens[b + 1]); rows behind the last
+ *                sequence are left as they were
+ *   log_decay    float32 [total_tokens, num_heads_v]: g <= 0 (0: no decay; -inf:
+ *                only the token itself); a positive or NaN value is taken as 0 and
+ *                reported as ATTN_ERR_DEVICE_RANGE
+ *   beta         float32 [total_tokens, num_heads_v], usually in [0, 1]
+ *   qk_norm_eps  >= 0: q and k are divided by sqrt(their sum of squares +
+ *                qk_norm_eps) in fp32, per token and head; < 0: taken as they are.
+ *                Keys longer than 1 (beta |k|^2 > 2) make the rule diverge
+ *   state_cache, state_slots, context_lens, cache_seqlens: as for
+ *                attn_linear_step_fwd, with num_heads_v states per slot
+ *                (cache_seqlens nullable: no entry was refused)
+ *   max_seqlen   host-side upper bound of the lengths (a longer sequence is cut
+ *                to it and reported as ATTN_ERR_DEVICE_INDEX); 0: nothing runs
+ * A sequence of length 0 leaves its slot as it was.
+ * Strides in elements, 0 = packed; rows of q, k, v and out start on 16-byte boundaries.
+ * An infinity or NaN in k, v or beta reaches its own token's output and later ones of
+ * its sequence and head as NaN or an infinity (one in v: its value dimension alone),
+ * one in q its own token's; nothing else.
+ * Limits: head_dim 64 or 128; batch, num_heads_v <= 65535; total_tokens < 2^31 - 1.
+ * workspace: attn_delta_workspace_size(...) bytes, 256-byte aligned; it holds
+ * nothing from call to call.  Calls that may run at the same time need one each.
+ * ------------------------------------------------------------------------ */
+ATTN_API attn_status attn_delta_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                                    const float *beta, const int32_t *cu_seqlens, float *state_cache,
+                                    const int32_t *state_slots, const int32_t *context_lens,
+                                    const int32_t *cache_seqlens, int batch, int64_t total_tokens, int max_seqlen,
+                                    int num_heads_k, int num_heads_v, int head_dim, float scale, float qk_norm_eps,
+                                    int64_t num_slots, int64_t q_row_stride, int64_t k_row_stride,
+                                    int64_t v_row_stride, int64_t out_row_stride, int64_t log_decay_row_stride,
+                                    int64_t beta_row_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes attn_delta_fwd needs (0 for invalid sizes, and where it needs none). */
+ATTN_API size_t attn_delta_workspace_size(int batch, int64_t total_tokens, int num_heads_k, int num_heads_v,
+                                          int head_dim, int max_seqlen);
+
+/* attn_delta_decode -- one token per sequence: q, k [batch, num_heads_k, head_dim],
+ * v, out [batch, num_heads_v, head_dim], log_decay, beta [batch, num_heads_v]; the
+ * states are read and updated in place.  state_slots and context_lens as for
+ * attn_linear_decode. */
+ATTN_API attn_status attn_delta_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,
+                                       const float *beta, float *state_cache, const int32_t *state_slots,
+                                       const int32_t *context_lens, int batch, int num_heads_k, int num_heads_v,
+                                       int head_dim, float scale, float qk_norm_eps, int64_t num_slots,
+                                       int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                                       int64_t out_row_stride, int64_t log_decay_row_stride, int64_t beta_row_stride,
+                                       void *stream);
+
+/* ------------------------------------------------------------------------
+ * attn_beam_select -- one step of beam search for num_groups requests of num_beams
+ * beams each: the num_out best continuations of every request.  A candidate (beam b,
+ * token t) scores
+ *   scores[b] + logits[b][t] - log(sum_j e^{logits[b][j]});
+ * higher scores come first, equal ones by beam, within a beam higher logits and
+ * equal ones by token.  Scores are compared in 64 bits.
+ *
+ *   logits       [num_groups * num_beams, vocab], dtype ATTN_DTYPE_*; row stride in
+ *                elements, 0 = packed.  -inf: the token is ruled out
+ *   scores       float32 [num_groups * num_beams]: the beams' scores so far.  -inf:
+ *                the beam has no candidates (for instance all but the first one at
+ *                the start of a search)
+ *   tokens, parents  int32 [num_groups, num_out]: token, and beam 0 .. num_beams - 1
+ *                of its request; -1 where there are no more candidates
+ *   out_scores   float32 [num_groups, num_out]; -inf there
+ * A NaN or +inf among a row's logits or in its score takes the row's candidates away
+ * and is reported as ATTN_ERR_DEVICE_RANGE.
+ * Limits: num_beams, num_out <= 32; vocab < 2^30; num_groups * num_beams < 2^25.
+ * workspace: attn_beam_select_workspace_size(...) bytes, 16-byte aligned; it holds
+ * nothing from call to call.  Calls that may run at the same time need one each.
+ * ------------------------------------------------------------------------ */
+ATTN_API attn_status attn_beam_select(const void *logits, const float *scores, int num_groups, int num_beams,
+                                      int vocab, int num_out, int64_t row_stride, int dtype, int32_t *tokens,
+                                      int32_t *parents, float *out_scores, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* Workspace bytes of attn_beam_select (0 for invalid sizes). */
+ATTN_API size_t attn_beam_select_workspace_size(int num_groups, int num_beams, int vocab, int num_out);
+
+/* attn_beam_rows -- the request rows (and state slots) of a search's next beams.
+ * parents int32 [num_groups, num_beams]: the beam that each new beam goes on from;
+ * rows int32 [num_groups, num_beams]: the beams' request rows so far, all different.
+ * The lowest beam that goes on from a parent takes its row; the others take, in
+ * order, the rows of beams that nobody goes on from.  Outputs [num_groups,
+ * num_beams]: rows_out, and source: -1, or the row whose content has to be copied to
+ * rows_out's (attn_copy_states, attn_copy_kvcache).  No source is a destination.
+ * A parent of -1 takes a row without content; one >= num_beams is taken as -1 and
+ * reported as ATTN_ERR_DEVICE_INDEX.  rows_out may be rows.  num_beams <= 32. */
+ATTN_API attn_status attn_beam_rows(const int32_t *parents, const int32_t *rows, int32_t *rows_out, int32_t *source,
+                                    int num_groups, int num_beams, void *stream);
+
+/* attn_copy_states -- cache[dst[i]] = cache[src[i]] for every i < n with src[i] >= 0
+ * and src[i] != dst[i]; a cache of num_slots slots of slot_bytes (a multiple of 16)
+ * each, of any type: the states of attn_linear_* or attn_delta_*, or others kept per
+ * slot.  A slot out of range is reported as ATTN_ERR_DEVICE_INDEX and the pair
+ * skipped.  A destination that is also a source, or named twice, is a caller error
+ * (its content is then undefined). */
+ATTN_API attn_status attn_copy_states(void *cache, const int32_t *src, const int32_t *dst, int n, int64_t num_slots,
+                                      int64_t slot_bytes, void *stream);
+
+/* attn_copy_kvcache -- cached tokens [first_tokens[src[i]], seq_lens[src[i]]) of
+ * request row src[i] to the same positions of request row dst[i], through both rows'
+ * pages, for every i < n with src[i] >= 0 and src[i] != dst[i].  seq_lens and
+ * page_table as kept by attn_step_tables; first_tokens nullable int32 [num_rows]
+ * (NULL: 0): tokens before it are the same in both rows (the prompt of a search)
+ * and stay.  caches as for store_kvcache (v16_cache nullable).  Both rows
+ * hold as many tokens and share no page; a pair with another length, a row out of range, or
+ * tokens on pages out of range, which are skipped, are reported as ATTN_ERR_DEVICE_INDEX.
+ * A destination that is also a source, or named twice, is a caller error. */
+ATTN_API attn_status attn_copy_kvcache(void *k_cache, void *v_cache, void *v16_cache, const int32_t *src,
+                                       const int32_t *dst, int n, const int32_t *page_table, const int32_t *seq_lens,
+                                       const int32_t *first_tokens, int num_rows, int max_blocks, int block_size,
+                                       int64_t num_blocks, int num_heads_kv, int head_dim, void *stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics
  * ------------------------------------------------------------------------ */
 
@@ -617,11 +741,12 @@ ATTN_API int attn_abi_version(void);
  * neither creates nor destroys them.  While both are non-NULL, every later
  * attn_varlen_fwd, attn_decode_paged, attn_decode_paged_noalloc,
  * store_kvcache, attn_rope_store_kvcache, attn_linear_varlen_fwd,
- * attn_linear_step_fwd and attn_linear_decode call made from the same host thread records `before` on its
+ * attn_linear_step_fwd, attn_linear_decode, attn_delta_fwd, attn_delta_decode,
+ * attn_beam_select, attn_copy_states and attn_copy_kvcache call made from the same host thread records `before` on its
  * stream just before launching its main kernel (the attention kernel of the
  * prefill; the split-KV kernel of the decode; the scatter kernel of the store;
  * the rotary kernel; the chunk kernel or the recurrent one of the linear
- * attention) and `after` just after it, so
+ * attention and of the delta rule; the scan of the selection; the copy) and `after` just after it, so
  * cudaEventElapsedTime(before, after) is that kernel's device time.  The
  * scheduling and V-conversion kernels of the prefill, the combine kernel
  * of the decode and the segment passes of the linear attention fall outside.  Pass NULL, NULL to switch it off (the
