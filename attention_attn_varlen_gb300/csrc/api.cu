@@ -1349,7 +1349,8 @@ extern "C" {
 size_t attn_delta_workspace_size(int batch, int64_t total_tokens, int num_heads_k, int num_heads_v, int head_dim,
                                  int max_seqlen) {
     if (!delta_sizes(batch, total_tokens, num_heads_k, num_heads_v, head_dim) || max_seqlen < 0) return 0;
-    return 0;
+    if (max_seqlen <= kDeltaShort) return 0;
+    return 256 + (size_t)kDeltaUnitBytes * batch;   // the count in front
 }
 
 }  // extern "C"
@@ -1435,7 +1436,18 @@ attn_status attn_delta_fwd(const void *q, const void *k, const void *v, void *ou
     p.start_zero = context_lens == nullptr;
     p.cache_seqlens = cache_seqlens;
     p.err = d->err;
-    return launched(launch_delta_recurrent(p, reinterpret_cast<cudaStream_t>(stream)));
+    if (max_seqlen <= kDeltaShort) return launched(launch_delta_recurrent(p, reinterpret_cast<cudaStream_t>(stream)));
+    p.num_sms = d->num_sms;
+    p.unit_count = reinterpret_cast<int *>(workspace);
+    p.units = reinterpret_cast<char *>(workspace) + 256;
+    CUtensorMap qmap, kmap, vmap, omap;
+    if (!make_map(&qmap, q, total_tokens, num_heads_k, head_dim, p.q_stride, 1, 64) ||
+        !make_map(&kmap, k, total_tokens, num_heads_k, head_dim, p.k_stride, 1, 64) ||
+        !make_map(&vmap, v, total_tokens, num_heads_v, head_dim, p.v_stride, 1, 64) ||
+        !make_map(&omap, out, total_tokens, num_heads_v, head_dim, p.out_stride, 1, 64,
+                  CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 32))
+        return ATTN_ERR_LAUNCH_FAILED;
+    return launched(launch_delta_varlen(qmap, kmap, vmap, omap, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_delta_decode(const void *q, const void *k, const void *v, void *out, const float *log_decay,

@@ -184,8 +184,16 @@ struct DeltaParams {
     int start_zero;                   // context_lens is null and every sequence starts from zero
     int norm;                         // q and k are divided by sqrt(their sum of squares + eps)
     float scale, eps;
+    // prompts: the work list, in the workspace
+    int num_sms;                      // CTAs of the prompt kernel at most
+    void *units;                      // kDeltaUnitBytes each
+    int *unit_count;
     uint32_t *err;
 };
+constexpr int kDeltaUnitBytes = 16;
+constexpr int kDeltaShort = 16;       // sequences of at most this many tokens take the recurrent form
+cudaError_t launch_delta_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                const CUtensorMap &omap, const DeltaParams &p, cudaStream_t stream);
 cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream);
 
 // beam.cu: beam search's selection, and what follows it
