@@ -73,16 +73,17 @@ __device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r
                  : "memory");
 }
 
-// x0, x1 -> their bf16 part (packed); x0, x1 become what is left (exact): fused multiply-adds
+// x0, x1 -> their bf16 part (packed); r0, r1 become what is left (exact): fused multiply-adds
 // that read the bf16 halves as they are, -1 times them (4 % fewer instructions than with their widening, 248 -> 243 us)
-__device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) {
+__device__ __forceinline__ uint32_t take_bf16(float &r0, float &r1, float x0, float x1) {
     const uint32_t h = pack_bf16x2(x0, x1);
     asm("{\n\t.reg .b16 l, u, m;\n\tmov.b32 {l, u}, %2;\n\tmov.b16 m, 0xBF80;\n\t"    // -1
-        "fma.rn.f32.bf16 %0, l, m, %0;\n\tfma.rn.f32.bf16 %1, u, m, %1;\n\t}"
-        : "+f"(x0), "+f"(x1)
-        : "r"(h));
+        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, u, m, %4;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "r"(h), "f"(x0), "f"(x1));
     return h;
 }
+__device__ __forceinline__ uint32_t take_bf16(float &x0, float &x1) { return take_bf16(x0, x1, x0, x1); }
 
 // mbar_wait in few instructions: the kernel's roles share the instruction cache, and with a call
 // in it the warpgroups could not have register shares of their own.  Gives up after about a

@@ -165,29 +165,31 @@ __global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const D
 // Precision.  q, k and v are bf16 and exact.  The state, R, T and w U~ are fp32 values in three bf16 parts,
 // 2^-24 of each; S itself stays in fp32 registers.  What only reaches the bf16 output (S_0 and U~
 // there, P) is taken as two parts, 2^-16 of a term against the output's own 2^-8.  T is solved for
-// in fp32, its 32 x 32 diagonal blocks row by row, the block below them as -T22 A21 T11.  Sums of decays are in
-// 64 bits and differences of them kept as two fp32 parts.
+// in fp32: its 16 x 16 diagonal blocks column by column, then the blocks below pairs of them, of
+// 16 and of 32, as -T22 A21 T11 (mma.sync waits behind the chain's products: 11,000 clocks a chunk for this role
+// instead of 8,000).  Sums of decays are in 64 bits and differences of them kept as two fp32 parts.
 //
 // What bounds it is a chunk's chain S -> SK -> R -> U -> w U~ -> KV -> S; SQ, KQ and PU run in its gaps.
 //
-// Roles (28 warps, one CTA per SM that goes over (sequence, value head) units):
+// Roles (32 warps, one CTA per SM that goes over (sequence, value head) units):
 //   0..15   the chain: thread = value dimension and a quarter of dk or of the tokens; S in registers
-//   16..19  T and P of the next chunk: lanes are the rows of (Q; K)
-//   20..23  output rows
-//   24, 25  issue the loads; write the chunks' tables
-//   26      issues the MMAs
+//   16..23  T and P of the next chunk
+//   24..27  norms of the next chunk, output rows of the one before
+//   28, 29  issue the loads; write the chunks' tables
+//   30      issues the MMAs
+// All of it is meant to stay in the 32 KB of the SM's instruction cache, which the roles share:
+// hence one code site per kind of step, loops where a step repeats, and waits of a few instructions.
 // ---------------------------------------------------------------------------
 constexpr int DC = 64;                       // tokens of a chunk
-constexpr int kDeltaThreads = 28 * 32;
+constexpr int kDeltaThreads = 32 * 32;
 constexpr int kDeltaPanel = DC * 128;        // 64 rows x 128 bytes
 // TMEM columns.  In turn in the same place: SK, U and then KV; S_0's third part, R and then w U~; S_0's first
 // part and then U~'s two; S_0's second part and then KQ of the next chunk
 constexpr uint32_t TM_KV = 0, TM_SK = 0, TM_U = 64;
-constexpr uint32_t TM_S1 = 128, TM_UO = 128, TM_S2 = 192, TM_KQ = 192;
-constexpr uint32_t TM_S3 = 256, TM_R = 256;  // (R: three parts of 32 columns)
+constexpr uint32_t TM_S1 = 128, TM_UO = 128, TM_KQ = 192;    // (S_0: three parts of 64 columns)
+constexpr uint32_t TM_R = 256;               // (three parts of 32 columns)
 constexpr uint32_t TM_SQ = 352, TM_PU = 416;
-constexpr int kBlockStride = 36;             // floats of a row of a 32 x 32 block in shared memory
-constexpr int kBlockFloats = 32 * kBlockStride;
+constexpr int kAStride = 68, kXStride = 36;  // floats of a row of A^T, and of T's and the products' rows
 constexpr int kDeltaBuckets = 256;
 
 // A chunk as its roles read it, behind its tables.
@@ -196,7 +198,8 @@ struct DeltaChunk {
     int t0, h, first, last;           // first row; head; whether the unit starts or ends with it
     int slot, from;                   // state slot (-1: none), whether the unit starts from it
     float a, a_lo;                    // e^{G_n} in two parts
-    int pad[7];
+    int bad;                          // the first token whose row of A is not finite
+    int unused[6];
 };
 
 template <int D>
@@ -209,21 +212,23 @@ struct DeltaSmem {
     static constexpr int kTOff = kVOff + kVStages * kVBytes;     // T: three parts
     static constexpr int kPOff = kTOff + 3 * kDeltaPanel;        // two chunks' P: two parts
     static constexpr int kOutOff = kPOff + 4 * kDeltaPanel;      // per output warp [64 tokens][32 dv] bf16
-    static constexpr int kBlockOff = kOutOff + 4 * DC * 64;      // A11, then T11; A22, then T22; A21; A21 T11
-    static constexpr int kTabOff = kBlockOff + 4 * kBlockFloats * 4;
-    // two chunks' tables: G (two parts), beta, e^G, w, b, -c, f, and the chunk itself
-    static constexpr int kTabFloats = 8 * DC + 16;
-    static constexpr int kBadOff = kTabOff + 2 * kTabFloats * 4; // first non-finite token per dv, two chunks
+    static constexpr int kAOff = kOutOff + 4 * DC * 64;          // A^T, block by block replaced by T^T
+    static constexpr int kTabOff = kAOff + DC * kAStride * 4;
+    // three chunks' tables: G (two parts), beta, e^G, w, b, -c, f, P's row factors, and the chunk itself
+    static constexpr int kTabs = 3, kTabFloats = 9 * DC + 16;
+    static constexpr int kBadOff = kTabOff + kTabs * kTabFloats * 4;     // first non-finite token per dv, two chunks
     static constexpr int kBarOff = kBadOff + 2 * 128 * 4;
     static constexpr int kNumBars = 30;
-    static constexpr int kBytes = kBarOff + kNumBars * 8 + 16 + 1024 /* alignment slack */;
+    static constexpr int kBytes = kBarOff + kNumBars * 8 + 32 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024 && sizeof(DeltaChunk) == 64, "shared memory");
+    // scratch of the solve, where T goes in the end
+    static_assert((DC + 32) * kXStride * 4 <= 3 * kDeltaPanel, "scratch");
 };
 
-// Registers of the calling warpgroup.  The kernel is launched with 72 a thread; the seven warpgroups'
-// shares add up to that: chain 4, T and P, output rows, the others.
-constexpr int kChainRegs = 80, kSolveRegs = 88, kRowRegs = 56, kOtherRegs = 40;
-static_assert(4 * kChainRegs + kSolveRegs + kRowRegs + kOtherRegs <= 7 * 72, "register shares");
+// Registers of the calling warpgroup.  The kernel is launched with 64 a thread; the eight warpgroups'
+// shares add up to that: chain 4, T and P 2 (which keep theirs), output rows, the others.
+constexpr int kChainRegs = 72, kSolveRegs = 64, kRowRegs = 56, kOtherRegs = 40;
+static_assert(4 * kChainRegs + 2 * kSolveRegs + kRowRegs + kOtherRegs == 8 * 64, "register shares");
 
 // A unit's entry in the work list, as the plan writes it.
 struct alignas(16) DeltaUnit {
@@ -277,26 +282,6 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaParams p) {
     }
 }
 
-// the chunks of a CTA's units, in order; places blockIdx.x, 2 gridDim.x - 1 - blockIdx.x, 2 gridDim.x + blockIdx.x,
-// ... of the list (longest first), back and forth so that the CTAs' sums come out alike
-struct DeltaWalk {
-    int k = 0, h = 0, c = 0, chunks = 0;
-    DeltaUnit u;
-    // the next chunk; false: no more
-    __device__ __forceinline__ bool step(const DeltaUnit *units, int units_n, int heads) {
-        if (++c < chunks) return true;
-        const int G = gridDim.x, place = k * G + ((k & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        const int at = place / heads;
-        if (at >= units_n) return false;
-        h = place - at * heads;
-        u = units[at];
-        chunks = (u.n + DC - 1) / DC;
-        c = 0;
-        ++k;
-        return true;
-    }
-};
-
 // 1 / sqrt(x): the hardware's estimate and one step of Newton's method
 __device__ __forceinline__ float inv_sqrt(float x) {
     float y;
@@ -306,10 +291,59 @@ __device__ __forceinline__ float inv_sqrt(float x) {
 
 // x0, x1 as three bf16 parts
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    hi = take_bf16(x0, x1);
-    mid = take_bf16(x0, x1);
-    lo = pack_bf16x2(x0, x1);
+    float r0, r1;
+    hi = take_bf16(r0, r1, x0, x1);
+    mid = take_bf16(r0, r1);
+    lo = pack_bf16x2(r0, r1);
 }
+
+// A bounded wait in as few instructions as it goes; a try takes the hardware 50 clocks or more, so
+// that it gives up after half a second or so.
+constexpr int kDeltaTries = 1 << 24;
+__device__ __forceinline__ bool delta_wait(uint64_t *bar, uint32_t parity) {
+    int left = kDeltaTries;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (--left == 0) return false;
+    return true;
+}
+
+// x as a value that the compiler takes for a new one: what is computed from it stays where it is used.  Addresses
+// kept from chunk to chunk would leave a phase's own loads too few registers to be in flight together.
+__device__ __forceinline__ int renew(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
+// The chunks of a CTA's units, in order: places blockIdx.x, 2 gridDim.x - 1 - blockIdx.x, 2 gridDim.x + blockIdx.x, ...
+// of the list (longest first), back and forth so that the CTAs' sums come out alike; walked without a division.
+struct DeltaWalk {
+    int heads, units_n, up_q, up_r, down_q, down_r;      // to the next place: unit and head
+    int at, hd, place;                                   // the next unit's
+    int left, row, h, slot, from;                        // this chunk on: tokens of its unit, first row, head, state
+    bool first;
+    __device__ __forceinline__ DeltaWalk(int units_n, int heads) : heads(heads), units_n(units_n) {
+        const int up = 2 * ((int)gridDim.x - 1 - (int)blockIdx.x) + 1, down = 2 * (int)blockIdx.x + 1;
+        up_q = up / heads, up_r = up - up_q * heads, down_q = down / heads, down_r = down - down_q * heads;
+        at = (int)blockIdx.x / heads, hd = (int)blockIdx.x - at * heads, place = left = 0;
+    }
+    // to the next chunk; its tokens, 0: there is none
+    __device__ __forceinline__ int step(const DeltaUnit *units) {
+        if (left > DC) {
+            left -= DC, row += DC, first = false;
+        } else if (at < units_n) {
+            const DeltaUnit u = units[at];
+            left = u.n, row = u.t0, slot = u.slot, from = u.from, h = hd, first = true;
+            at += place & 1 ? down_q : up_q;
+            hd += place & 1 ? down_r : up_r;
+            if (hd >= heads) hd -= heads, ++at;
+            ++place;
+        } else {
+            left = 0;
+        }
+        return min(left, DC);
+    }
+};
 
 // non-finite entries of x become 0; returns the first one's place, 16 if there is none
 __device__ __forceinline__ int drop_non_finite(float (&x)[16]) {
@@ -345,55 +379,52 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kBarOff);
     uint64_t *qk_full = bars, *qk_empty = bars + 3;
     uint64_t *v_full = bars + 6, *v_empty = bars + 8;
-    uint64_t *tab_full = bars + 10, *tab_free = bars + 12;   // [2], by chunk: its tables are written, read for the last time
-    uint64_t *norms = bars + 14;             // [2]: b, c and f are written too
-    uint64_t *o_done = bars + 16;            // [2]: SQ and PU done
-    uint64_t *kq_done = bars + 18;           // KQ done
-    uint64_t *kq_read = bars + 19;           // ... and read
-    uint64_t *t_ready = bars + 20;           // T and P in shared memory
-    uint64_t *s_ready = bars + 21;           // S_0 in TMEM, the KV before read
-    uint64_t *sk_done = bars + 22;
-    uint64_t *r_ready = bars + 23;           // R in TMEM
-    uint64_t *u_done = bars + 24;
-    uint64_t *w_ready = bars + 25;           // U~ and w U~ in TMEM
-    uint64_t *kv_done = bars + 26;
-    uint64_t *o_read = bars + 27;            // SQ and PU read
-    uint64_t *solve = bars + 28;             // among the solving warps
+    uint64_t *tab_full = bars + 10, *tab_free = bars + 13;   // [3], by chunk: its tables are written, read for the last time
+    uint64_t *norms = bars + 16;             // [2]: b, c and f are written too
+    uint64_t *o_done = bars + 18;            // [2]: SQ and PU done
+    uint64_t *kq_done = bars + 20;           // KQ done
+    uint64_t *kq_read = bars + 21;           // ... and read
+    uint64_t *t_ready = bars + 22;           // T and P in shared memory
+    uint64_t *go = bars + 23;                // [2]: SK, then U done
+    uint64_t *s_ready = bars + 25;           // S_0 in TMEM, the KV before read
+    uint64_t *x_ready = bars + 26;           // R, then U~ and w U~ in TMEM
+    uint64_t *kv_done = bars + 27;
+    uint64_t *o_read = bars + 28;            // SQ and PU read
     uint64_t *drain = bars + 29;             // every MMA done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);     // [3]: a role's wait gave up
+    volatile int *late = stop + 3;                                            // any wait did
     float *tables = reinterpret_cast<float *>(sm + S::kTabOff);
     int *bad_at = reinterpret_cast<int *>(sm + S::kBadOff);
-    auto tab_of = [&](int gc) { return tables + (gc & 1) * S::kTabFloats; };
-    auto info_of = [&](int gc) { return reinterpret_cast<DeltaChunk *>(tab_of(gc) + 8 * DC); };
-    enum { T_GHI = 0, T_GLO = DC, T_BETA = 2 * DC, T_GAM = 3 * DC, T_W = 4 * DC, T_B = 5 * DC, T_C = 6 * DC, T_F = 7 * DC };
+    // chunk gc's tables lie at tab = gc % 3, in its turn gc / 3
+    auto tab_of = [&](int tab) { return tables + tab * S::kTabFloats; };
+    auto info_of = [&](int tab) { return reinterpret_cast<DeltaChunk *>(tab_of(tab) + 9 * DC); };
+    enum { T_GHI = 0, T_GLO = DC, T_BETA = 2 * DC, T_GAM = 3 * DC, T_W = 4 * DC, T_B = 5 * DC, T_C = 6 * DC, T_F = 7 * DC,
+           T_P = 8 * DC };
 
-    if (warp == 24 && lane == 0) {
+    if (warp == 28 && lane == 0) {
         for (int i = 0; i < QS; ++i) {
             mbar_init(&qk_full[i], 1);
-            mbar_init(&qk_empty[i], 1 + 4);  // the MMAs, the solving warps
+            mbar_init(&qk_empty[i], 1 + 4);  // the MMAs, the norms
+            mbar_init(&tab_full[i], 1);
+            mbar_init(&tab_free[i], 16 + 8 + 4 + 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 16);
-            mbar_init(&tab_full[i], 1);
-            mbar_init(&tab_free[i], 16 + 4 + 4 + 1);
             mbar_init(&norms[i], 4);
             mbar_init(&o_done[i], 1);
+            mbar_init(&go[i], 1);
         }
         mbar_init(kq_done, 1);
-        mbar_init(kq_read, 4);
-        mbar_init(t_ready, 4);
+        mbar_init(kq_read, 8);
+        mbar_init(t_ready, 8);
         mbar_init(s_ready, 16);
-        mbar_init(sk_done, 1);
-        mbar_init(r_ready, 16);
-        mbar_init(u_done, 1);
-        mbar_init(w_ready, 16);
+        mbar_init(x_ready, 16);
         mbar_init(kv_done, 1);
         mbar_init(o_read, 4);
-        mbar_init(solve, 4);
         mbar_init(drain, 1);
-        abort_flag[0] = abort_flag[1] = 0;
+        for (int i = 0; i < 4; ++i) stop[i] = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -401,203 +432,184 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         tmem_relinquish();
     }
     if (warp >= 16 && warp < 20) {
-        // what lies above the diagonal blocks of T and P stays zero: rows 0..31, tokens 32..63 of every part
-#pragma unroll 1
-        for (int x = warp - 16; x < 7; x += 4) {
+        // P: tokens 0..31 see no key behind 31
 #pragma unroll
-            for (int ch = 4; ch < 8; ++ch)
-                *reinterpret_cast<uint4 *>(sm + S::kTOff + x * kDeltaPanel + sw128_off(lane, ch)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int ch = 4; ch < 8; ++ch)
+            *reinterpret_cast<uint4 *>(sm + S::kPOff + (warp - 16) * kDeltaPanel + sw128_off(lane, ch)) =
+                make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
-    // waits for what the hardware finishes by itself run to the limit: their flag is their own
-    volatile int &never = *(abort_flag + 1);
     // a warp's wait: every lane gets the same answer
     auto wait = [&](uint64_t *bar, int phase) {
-        return __all_sync(0xffffffffu, chunk_wait(bar, (uint32_t)phase & 1u, abort_flag)) != 0;
+        const bool ok = __all_sync(0xffffffffu, delta_wait(bar, (uint32_t)phase & 1u));
+        if (!ok) *late = 1;
+        return ok;
     };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
+    // A role of several warps: its first one waits (the others' polling would take issue slots from those that
+    // work) and the rest behind a barrier of the role.  A wait that gave up stops the role at its next chunk, all
+    // of its warps at once.
+    auto role_wait = [&](int role, uint64_t *bar, int phase) {
+        if (!wait(bar, phase)) stop[role] = 1;
+    };
+    auto role_sync = [](int role, int threads) {
+        asm volatile("bar.sync %0, %1;" ::"r"(role + 1), "r"(threads) : "memory");
+    };
+    auto next_tab = [](int &tab, int &turn) {
+        if (++tab == S::kTabs) tab = 0, ++turn;
+    };
 
     if (warp < 16) {
         // ============================================================ the chain
         more_regs<kChainRegs>();
-        const int grp = warp & 3, part = warp >> 2, dv = grp * 32 + lane;
-        const bool real = grp * 32 < D;      // warp-uniform; head_dim 64: lanes 64..127 reach no output
-        const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
+        const bool real = (warp & 3) * 32 < D;       // warp-uniform; head_dim 64: lanes 64..127 reach no output
         constexpr int N = D / 4;             // columns of S per thread
-        // its value dimension in a V tile, its tokens part * 16 ..
-        const uint32_t v_at = smb + S::kVOff + ((dv & (D - 1)) >> 6) * kDeltaPanel + part * 16 * 128 + (dv & 7) * 2;
-        const uint32_t v_ch = ((dv & 63) >> 3) << 4;
         float St[N];
+        int tab_i = 0, turn = 0;
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
-            if (!wait(&tab_full[gc & 1], gc >> 1)) break;
-            const DeltaChunk *info = info_of(gc);
-            const float *tab = tab_of(gc);
-            const int n = uni(info->n);
-            if (n == 0) break;
-            int *bad_row = bad_at + (gc & 1) * 128 + dv;
-            if (info->first) {
-                const float *src = info->from && info->slot >= 0
-                                       ? p.state + ((int64_t)info->slot * p.Hv + info->h) * D * D + dv * D + part * N
-                                       : nullptr;
-#pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (src && real) x = *reinterpret_cast<const float4 *>(src + i);
-                    St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
+            if (warp == 0) {
+                role_wait(0, &tab_full[tab_i], turn);
+                if (info_of(tab_i)->n) {
+                    role_wait(0, &v_full[gc & 1], gc >> 1);
+                    role_wait(0, &norms[gc & 1], gc >> 1);
+                    role_wait(0, kq_read, gc);
+                    if (gc > 0) role_wait(0, &o_done[(gc - 1) & 1], (gc - 1) >> 1);
                 }
             }
-            // ---- S_0's parts to TMEM; the first one where PU of the chunk before reads U~
-            if (part == 0) *bad_row = DC;
-            if (!wait(kq_read, gc)) break;
+            role_sync(0, 512);
+            tc_fence_after();
+            if (uni(info_of(tab_i)->n) == 0 || stop[0]) break;
             {
-                uint32_t s1[N / 2];
-                if (real) {
+                const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, part = tid >> 7, dv = tid & 127;
+                const DeltaChunk *info = info_of(tab_i);
+                if (info->first) {
+                    const float *own = p.state + ((int64_t)info->slot * p.Hv + info->h) * D * D + dv * D + part * N;
+                    const bool some = info->from && info->slot >= 0 && real;
 #pragma unroll
-                    for (int i = 0; i < N; i += 16) {
-                        uint32_t s2[8], s3[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            split3(St[i + 2 * k], St[i + 2 * k + 1], s1[i / 2 + k], s2[k], s3[k]);
-                        tmem_st8(lane_base + TM_S2 + (part * N + i) / 2, s2);
-                        tmem_st8(lane_base + TM_S3 + (part * N + i) / 2, s3);
+                    for (int i = 0; i < N; i += 4) {
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (some) x = *reinterpret_cast<const float4 *>(own + i);
+                        St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
                     }
                 }
-                if (gc > 0 && !wait(&o_done[(gc - 1) & 1], (gc - 1) >> 1)) break;
-                tc_fence_after();
+                // ---- S_0's parts to TMEM
+                if (part == 0) bad_at[(gc & 1) * 128 + dv] = DC;
                 if (real) {
+                    const uint32_t to = tmem + ((uint32_t)grp << 21) + TM_S1 + part * N / 2;
 #pragma unroll
-                    for (int i = 0; i < N / 2; i += 8) {
-                        uint32_t s[8];
+                    for (int i = 0; i < N; i += 16) {
+                        uint32_t s1[8], s2[8], s3[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) s[k] = s1[i + k];
-                        tmem_st8(lane_base + TM_S1 + part * N / 2 + i, s);
+                        for (int k = 0; k < 8; ++k) split3(St[i + 2 * k], St[i + 2 * k + 1], s1[k], s2[k], s3[k]);
+                        tmem_st8(to + i / 2, s1);
+                        tmem_st8(to + 64 + i / 2, s2);
+                        tmem_st8(to + 128 + i / 2, s3);
                     }
                     tc_wait_st();
                 }
+                tc_fence_before();
+                arrive(s_ready);
             }
-            tc_fence_before();
-            arrive(s_ready);
-            // ---- R = b v - c S_0 k
-            if (!wait(&norms[gc & 1], gc >> 1)) break;
-            if (!wait(&v_full[gc % VS], gc / VS)) break;
-            float x[16];
-            {
-                float v[16];
-                const uint32_t at = v_at + (gc % VS) * S::kVBytes;
+            // ---- R = b v - c S_0 k, then U~ and w U~
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                if (warp == 0) role_wait(0, &go[pass], gc);
+                role_sync(0, 512);
+                tc_fence_after();
+                if (real) {
+                    const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, part = tid >> 7, dv = tid & 127;
+                    const uint32_t lane_base = tmem + ((uint32_t)grp << 21);
+                    uint32_t u[16];
+                    tmem_ld16(lane_base + (pass ? TM_U : TM_SK) + part * 16, u);
+                    const float *tab = tab_of(tab_i) + part * 16;
+                    float x[16];
+                    if (pass) {
+                        tc_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    uint16_t r;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at + j * 128 + (v_ch ^ ((j & 7) << 4))));
-                    v[j] = __uint_as_float((uint32_t)r << 16);
-                }
-                const float4 *b4 = reinterpret_cast<const float4 *>(tab + T_B + part * 16);
+                        for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(u[j]);
+                    } else {
+                        // its value dimension in the V tile, its tokens part * 16 ..
+                        const uint32_t at = smb + S::kVOff + (gc & 1) * S::kVBytes + ((dv & (D - 1)) >> 6) * kDeltaPanel +
+                                            part * 16 * 128 + (dv & 7) * 2, ch = ((dv & 63) >> 3) << 4;
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 b = b4[j / 4];
-                    fma2(x[j], x[j + 1], b.x, b.y, v[j], v[j + 1], 0.f, 0.f);
-                    fma2(x[j + 2], x[j + 3], b.z, b.w, v[j + 2], v[j + 3], 0.f, 0.f);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 b = *reinterpret_cast<const float4 *>(tab + T_B + j);
+                            float v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint16_t r;
+                                asm("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at + (j + k) * 128 + (ch ^ (((j + k) & 7) << 4))));
+                                v[k] = __uint_as_float((uint32_t)r << 16);
+                            }
+                            fma2(x[j], x[j + 1], b.x, b.y, v[0], v[1], 0.f, 0.f);
+                            fma2(x[j + 2], x[j + 3], b.z, b.w, v[2], v[3], 0.f, 0.f);
+                        }
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 c = *reinterpret_cast<const float4 *>(tab + T_C + j);
+                            fma2(x[j], x[j + 1], c.x, c.y, __uint_as_float(u[j]), __uint_as_float(u[j + 1]), x[j], x[j + 1]);
+                            fma2(x[j + 2], x[j + 3], c.z, c.w, __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]),
+                                 x[j + 2], x[j + 3]);
+                        }
+                    }
+                    float z0 = 0.f, z1 = 0.f;        // NaN once something non-finite went by
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) fma2(z0, z1, x[j], x[j + 1], 0.f, 0.f, z0, z1);
+                    if (__any_sync(0xffffffffu, !(z0 + z1 == 0.f))) {
+                        // the triangles' zeros would not keep it from earlier tokens
+                        const int first = drop_non_finite(x);
+                        if (first < 16) atomicMin(bad_at + (gc & 1) * 128 + dv, part * 16 + first);
+                    }
+                    uint32_t r1[8], r2[8], r3[8];
+                    if (pass) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float y0, y1;
+                            r1[k] = take_bf16(y0, y1, x[2 * k], x[2 * k + 1]);
+                            r2[k] = pack_bf16x2(y0, y1);
+                        }
+                        tmem_st8(lane_base + TM_UO + part * 8, r1);
+                        tmem_st8(lane_base + TM_UO + 32 + part * 8, r2);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 w = *reinterpret_cast<const float4 *>(tab + T_W + j);
+                            fma2(x[j], x[j + 1], w.x, w.y, x[j], x[j + 1], 0.f, 0.f);
+                            fma2(x[j + 2], x[j + 3], w.z, w.w, x[j + 2], x[j + 3], 0.f, 0.f);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) split3(x[2 * k], x[2 * k + 1], r1[k], r2[k], r3[k]);
+                    tmem_st8(lane_base + TM_R + part * 8, r1);
+                    tmem_st8(lane_base + TM_R + 32 + part * 8, r2);
+                    tmem_st8(lane_base + TM_R + 64 + part * 8, r3);
+                    tc_wait_st();
                 }
+                tc_fence_before();
+                arrive(x_ready);
+                if (pass == 0) arrive(&v_empty[gc & 1]);
             }
-            arrive(&v_empty[gc % VS]);
-            if (!wait(sk_done, gc)) break;
-            tc_fence_after();
-            if (real) {
-                uint32_t sk[16];
-                tmem_ld16(lane_base + TM_SK + part * 16, sk);
-                const float4 *c4 = reinterpret_cast<const float4 *>(tab + T_C + part * 16);
-                tc_wait_ld();
-                float z0 = 0.f, z1 = 0.f;    // NaN once something non-finite went by
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 c = c4[j / 4];
-                    fma2(x[j], x[j + 1], c.x, c.y, __uint_as_float(sk[j]), __uint_as_float(sk[j + 1]), x[j], x[j + 1]);
-                    fma2(x[j + 2], x[j + 3], c.z, c.w, __uint_as_float(sk[j + 2]), __uint_as_float(sk[j + 3]), x[j + 2],
-                         x[j + 3]);
-                }
-                if (n < DC) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = part * 16 + j < n ? x[j] : 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) fma2(z0, z1, x[j], x[j + 1], 0.f, 0.f, z0, z1);
-                if (__any_sync(0xffffffffu, !(z0 + z1 == 0.f))) {
-                    // T's zeros would not keep it from earlier tokens
-                    const int first = drop_non_finite(x);
-                    if (first < 16) atomicMin(bad_row, part * 16 + first);
-                }
-                uint32_t r1[8], r2[8], r3[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) split3(x[2 * k], x[2 * k + 1], r1[k], r2[k], r3[k]);
-                tmem_st8(lane_base + TM_R + part * 8, r1);
-                tmem_st8(lane_base + TM_R + 32 + part * 8, r2);
-                tmem_st8(lane_base + TM_R + 64 + part * 8, r3);
-                tc_wait_st();
-            }
-            tc_fence_before();
-            arrive(r_ready);
-            // ---- U~ and w U~
-            if (!wait(u_done, gc)) break;
-            tc_fence_after();
-            if (real) {
-                uint32_t u[16];
-                tmem_ld16(lane_base + TM_U + part * 16, u);
-                const float4 *w4 = reinterpret_cast<const float4 *>(tab + T_W + part * 16);
-                tc_wait_ld();
-                float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(u[j]);
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) fma2(z0, z1, x[j], x[j + 1], 0.f, 0.f, z0, z1);
-                if (__any_sync(0xffffffffu, !(z0 + z1 == 0.f))) {
-                    const int first = drop_non_finite(x);
-                    if (first < 16) atomicMin(bad_row, part * 16 + first);
-                }
-                uint32_t r1[8], r2[8], r3[8];
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    const float4 w = w4[k / 2];
-                    float y0, y1;
-                    fma2(y0, y1, x[2 * k], x[2 * k + 1], w.x, w.y, 0.f, 0.f);
-                    split3(y0, y1, r1[k], r2[k], r3[k]);
-                    fma2(y0, y1, x[2 * k + 2], x[2 * k + 3], w.z, w.w, 0.f, 0.f);
-                    split3(y0, y1, r1[k + 1], r2[k + 1], r3[k + 1]);
-                }
-                tmem_st8(lane_base + TM_R + part * 8, r1);
-                tmem_st8(lane_base + TM_R + 32 + part * 8, r2);
-                tmem_st8(lane_base + TM_R + 64 + part * 8, r3);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    r1[k] = take_bf16(x[2 * k], x[2 * k + 1]);
-                    r2[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-                }
-                tmem_st8(lane_base + TM_UO + part * 8, r1);
-                tmem_st8(lane_base + TM_UO + 32 + part * 8, r2);
-                tc_wait_st();
-            }
-            tc_fence_before();
-            arrive(w_ready);
             // ---- S = e^{G_n} S + KV
-            const float a = info->a, a_lo = info->a_lo;
-            const bool last = info->last;
-            float *dst = last && info->slot >= 0 ? p.state + ((int64_t)info->slot * p.Hv + info->h) * D * D + dv * D + part * N
-                                                 : nullptr;
-            if (!wait(kv_done, gc)) break;
+            if (warp == 0) role_wait(0, kv_done, gc);
+            role_sync(0, 512);
             tc_fence_after();
             if (real) {
+                const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, part = tid >> 7, dv = tid & 127;
+                const DeltaChunk *info = info_of(tab_i);
+                const bool bad = min(bad_at[(gc & 1) * 128 + dv], info->bad) < DC;
+                const float a = bad ? __uint_as_float(0x7FC00000u) : info->a, a_lo = info->a_lo;
 #pragma unroll
                 for (int i = 0; i < N; i += 16) {
                     uint32_t kv[16];
-                    tmem_ld16(lane_base + TM_KV + part * N + i, kv);
+                    tmem_ld16(tmem + ((uint32_t)grp << 21) + TM_KV + part * N + i, kv);
                     tc_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
@@ -607,341 +619,370 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
                     }
                 }
-                if (__any_sync(0xffffffffu, *bad_row < DC)) {
-                    const bool bad = *bad_row < DC;
+                if (info->last && info->slot >= 0) {
+                    float *own = p.state + ((int64_t)info->slot * p.Hv + info->h) * D * D + dv * D + part * N;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) St[i] = bad ? __uint_as_float(0x7FC00000u) : St[i];
+                    for (int i = 0; i < N; i += 4)
+                        *reinterpret_cast<float4 *>(own + i) = make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
                 }
             }
             tc_fence_before();
-            arrive(&tab_free[gc & 1]);
-            if (real && dst) {
-#pragma unroll
-                for (int i = 0; i < N; i += 4)
-                    *reinterpret_cast<float4 *>(dst + i) = make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
-            }
+            arrive(&tab_free[tab_i]);
+            next_tab(tab_i, turn);
         }
-    } else if (warp < 20) {
-        // ============================================================ T and P: lane = row of (Q; K)
-        more_regs<kSolveRegs>();
-        const int qd = warp & 3, row = qd * 32 + lane, i = row & 63;
-        const bool keys = qd >= 2;
-        const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
-        float *blocks = reinterpret_cast<float *>(sm + S::kBlockOff);
-        float *blk11 = blocks, *blk22 = blocks + kBlockFloats, *blk21 = blocks + 2 * kBlockFloats,
-              *blkx = blocks + 3 * kBlockFloats;
-        int turn = 0;                        // phases of `solve`
-        auto together = [&]() {
-            arrive(solve);
-            return wait(solve, turn++);
-        };
-        // column `lane` of a 32 x 32 block of T: rows r, r + step of it, as three parts
-        auto put_t = [&](int r, int step, int col, float x0, float x1) {
-            uint32_t h[3];
-            split3(x0, x1, h[0], h[1], h[2]);
-            uint8_t *t = sm + S::kTOff + (col & 7) * 2;
-            const uint32_t a0 = sw128_off(r, col >> 3), a1 = sw128_off(r + step, col >> 3);
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                *reinterpret_cast<uint16_t *>(t + x * kDeltaPanel + a0) = (uint16_t)h[x];
-                *reinterpret_cast<uint16_t *>(t + x * kDeltaPanel + a1) = (uint16_t)(h[x] >> 16);
-            }
-        };
+    } else if (warp < 24) {
+        // ============================================================ T and P
+        const int w8 = warp - 16, qd = warp & 3, half = w8 >> 2;
+        const bool keys = qd >= 2;           // lane = row of (Q; K)
+        float *At = reinterpret_cast<float *>(sm + S::kAOff);            // [j][i]
+        float *Tm = reinterpret_cast<float *>(sm + S::kTOff);            // [i][j % 32], T11 and the diagonal blocks
+        float *X = Tm + DC * kXStride;                                   // [i][j]: A21 T11
+        int tab_i = 0, turn = 0;
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
-            if (!wait(&tab_full[gc & 1], gc >> 1)) break;
-            const DeltaChunk *info = info_of(gc);
-            float *tab = tab_of(gc);
-            const int n = uni(info->n);
-            if (n == 0) break;
-            const int s = gc % QS;
-            if (!wait(&qk_full[s], gc / QS)) break;
-            uint8_t *tile = sm + s * S::kQkBytes + row * 128;
-            if (keys && i >= n) {
-                // rows behind the sequence's end are zeroed (a weight of 0 would not cancel a NaN there)
-#pragma unroll 1
-                for (int x = 0; x < PAN * 8; ++x)
-                    *reinterpret_cast<uint4 *>(tile + (x >> 3) * S::kQkPanel + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (n < DC) fence_proxy_async_smem();
-            float r = 1.f;
-            if (p.norm) {
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll 2
-                for (int x = 0; x < PAN * 8; ++x) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(tile + (x >> 3) * S::kQkPanel +
-                                                                     (((x & 7) ^ (row & 7)) << 4));
-                    const uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float e0 = __uint_as_float(y[k] << 16), e1 = __uint_as_float(y[k] & 0xFFFF0000u);
-                        fma2(s0, s1, e0, e1, e0, e1, s0, s1);
-                    }
+            if (w8 == 0) {
+                role_wait(1, &tab_full[tab_i], turn);
+                if (info_of(tab_i)->n) {
+                    role_wait(1, &norms[gc & 1], gc >> 1);
+                    role_wait(1, kq_done, gc);
                 }
-                r = inv_sqrt(s0 + s1 + p.eps);
             }
-            float factor;                    // of the row of A or P
-            if (keys) {
-                const float beta = tab[T_BETA + i];
-                tab[T_B + i] = beta * r;
-                factor = beta * r * r;
-                tab[T_C + i] = -factor * tab[T_GAM + i];
-            } else {
-                factor = p.scale * r;
-                tab[T_F + i] = factor * tab[T_GAM + i];
-            }
-            arrive(&norms[gc & 1]);
-            arrive(&qk_empty[s]);
-            const float ghi = tab[T_GHI + i], glo = tab[T_GLO + i];
-            if (!wait(kq_done, gc)) break;
-            if (!keys && gc >= 2 && !wait(&o_done[gc & 1], (gc >> 1) - 1)) break;       // P's buffer
+            role_sync(1, 256);
             tc_fence_after();
-            // tokens 0..31 see no key behind 31
-            uint8_t *ph = sm + S::kPOff + (gc & 1) * 2 * kDeltaPanel;
+            const int n = uni(info_of(tab_i)->n);
+            if (n == 0 || stop[1]) break;
+            {
+                const int i = (qd & 1) * 32 + renew(lane);
+                const float *tab = tab_of(tab_i);
+                const float ghi = tab[T_GHI + i], glo = tab[T_GLO + i], factor = tab[(keys ? T_BETA : T_P) + i];
+                const int see = keys ? (i < n ? i : 0) : i + 1;              // columns that count
+                // KQ follows PU of the chunk before the last: P's place is free.
+                // Tokens 0..31 see no key behind 31; two warps share a row's columns, eight at a time
+                const int width = 16 + 16 * (qd & 1);
+                const uint32_t from = tmem + ((uint32_t)(qd * 32) << 16) + TM_KQ;
+                uint32_t next[8];
+                tmem_ld8(from + half * width, next);
 #pragma unroll 1
-            for (int j0 = 0; j0 < 32 + 32 * (qd & 1); j0 += 8) {
-                uint32_t kq[8];
-                tmem_ld8(lane_base + TM_KQ + j0, kq);
-                float x[8], g1[8], g2[8];
+                for (int j0 = half * width; j0 < half * width + width; j0 += 8) {
+                    float x[8], g[8];
 #pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const float4 a = *reinterpret_cast<const float4 *>(tab + T_GHI + j0 + j);
-                    const float4 b = *reinterpret_cast<const float4 *>(tab + T_GLO + j0 + j);
-                    g1[j] = a.x, g1[j + 1] = a.y, g1[j + 2] = a.z, g1[j + 3] = a.w;
-                    g2[j] = b.x, g2[j + 1] = b.y, g2[j + 2] = b.z, g2[j + 3] = b.w;
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 a = *reinterpret_cast<const float4 *>(tab + T_GHI + j0 + j);
+                        const float4 b = *reinterpret_cast<const float4 *>(tab + T_GLO + j0 + j);
+                        x[j] = ghi - a.x, x[j + 1] = ghi - a.y, x[j + 2] = ghi - a.z, x[j + 3] = ghi - a.w;
+                        g[j] = glo - b.x, g[j + 1] = glo - b.y, g[j + 2] = glo - b.z, g[j + 3] = glo - b.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = ex2(x[j] + g[j]) * factor;
+                    tc_wait_ld();
+                    bool bad = false;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        // masked by choice, not by a factor, which would keep a NaN
+                        x[j] = j0 + j < see ? x[j] * __uint_as_float(next[j]) : 0.f;
+                        // a zero of T would not keep it from earlier tokens: 0 here, and NaN from this token on later
+                        const bool drop = keys && !(fabsf(x[j]) < INFINITY);
+                        x[j] = drop ? 0.f : x[j];
+                        bad |= drop;
+                    }
+                    if (bad) atomicMin(&info_of(tab_i)->bad, i);
+                    tmem_ld8(from + ((j0 + 8) & 63), next);              // (behind the last ones: not used)
+                    if (keys) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) At[(j0 + j) * kAStride + i] = x[j];
+                    } else {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            hi[k] = take_bf16(x[2 * k], x[2 * k + 1]);
+                            lo[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                        }
+                        uint8_t *to = sm + S::kPOff + (gc & 1) * 2 * kDeltaPanel + sw128_off(i, j0 >> 3);
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(to + kDeltaPanel) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
-                const int see = keys ? (i < n ? i : 0) : i + 1;      // columns that count
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = ex2((ghi - g1[j]) + (glo - g2[j])) * factor;
                 tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    // masked by choice, not by a factor, which would keep a NaN
-                    x[j] = j0 + j < see ? x[j] * __uint_as_float(kq[j]) : 0.f;
-                if (keys) {
-                    float *to = (qd == 2 ? blk11 : j0 < 32 ? blk21 : blk22) + lane * kBlockStride + (j0 & 31);
-                    *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
-                    *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
-                } else {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        hi[k] = take_bf16(x[2 * k], x[2 * k + 1]);
-                        lo[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-                    }
-                    const uint32_t at = sw128_off(i, j0 >> 3);
-                    *reinterpret_cast<uint4 *>(ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(ph + kDeltaPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
+                tc_fence_before();
+                arrive(kq_read);
             }
-            tc_fence_before();
-            arrive(kq_read);
-            if (!together()) break;
-            if (gc > 0 && !wait(u_done, gc - 1)) break;              // T's place
-            // T11 and T22, a warp each, a lane per column: x_r = [r = lane] - sum_{m < r} A_rm x_m
-            if (qd == 0 || qd == 2) {
-                float *blk = qd == 2 ? blk11 : blk22;
-                const int t0 = qd == 2 ? 0 : 32;
-                float x[32];
-                x[0] = lane == 0 ? 1.f : 0.f;
+            if (w8 == 0 && gc > 0) role_wait(1, &go[1], gc - 1);     // U of the chunk before done: T's place
+            role_sync(1, 256);
+            // the 16 x 16 diagonal blocks, two a warp, a lane per column: x_q = [q = column] - sum_{m < q} A_qm x_m
+            if (w8 == 0 || w8 == 6) {
+                const int l = renew(lane), col = l & 15, jb = 32 * (w8 == 6) + (l & 16);
+                float *blk = At + jb * kAStride + jb;
+                float x[16];
 #pragma unroll
-                for (int q = 1; q < 32; ++q) {
-                    float acc[4] = {lane == q ? 1.f : 0.f, 0.f, 0.f, 0.f};
+                for (int q = 0; q < 16; ++q) x[q] = q == col ? 1.f : 0.f;
 #pragma unroll
-                    for (int m = 0; m < q; m += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(blk + q * kBlockStride + m);
-                        acc[0] = fmaf(-a.x, x[m], acc[0]);
-                        if (m + 1 < q) acc[1] = fmaf(-a.y, x[m + 1], acc[1]);
-                        if (m + 2 < q) acc[2] = fmaf(-a.z, x[m + 2], acc[2]);
-                        if (m + 3 < q) acc[3] = fmaf(-a.w, x[m + 3], acc[3]);
+                for (int m = 0; m < 15; ++m) {
+#pragma unroll
+                    for (int q = (m + 1) & ~3; q < 16; q += 4) {
+                        const float4 a = *reinterpret_cast<const float4 *>(blk + m * kAStride + q);
+                        if (q > m) x[q] = fmaf(-a.x, x[m], x[q]);
+                        if (q + 1 > m) x[q + 1] = fmaf(-a.y, x[m], x[q + 1]);
+                        if (q + 2 > m) x[q + 2] = fmaf(-a.z, x[m], x[q + 2]);
+                        if (q + 3 > m) x[q + 3] = fmaf(-a.w, x[m], x[q + 3]);
                     }
-                    x[q] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
                 }
                 __syncwarp();
 #pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    x[q] = lane <= q ? x[q] : 0.f;
-                    blk[q * kBlockStride + lane] = x[q];
-                }
+                for (int q = 0; q < 16; q += 4)
+                    *reinterpret_cast<float4 *>(blk + col * kAStride + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                float *to = Tm + jb * kXStride + (jb & 16) + col;
 #pragma unroll
-                for (int q = 0; q < 32; q += 2) put_t(t0 + q, 1, t0 + lane, x[q], x[q + 1]);
+                for (int q = 0; q < 16; ++q) to[q * kXStride] = x[q];
             }
-            if (!together()) break;
-            // A21 T11: eight rows a warp, a lane per column
-            {
-                float t[32];
+            role_sync(1, 256);
+            // the blocks below: A21 T11, then -T22 (A21 T11), of 16 x 16 (two side by side, four warps), then of
+            // 32 x 32.  A warp has 8 rows and 16 columns, a lane four rows of a column.
+#pragma unroll 1
+            for (int step = 0; step < 4; ++step) {
+                const bool big = step >= 2, second = step & 1;
+                const int l = renew(lane), c = l & 15;
+                const int pr = big ? 0 : (w8 >> 1) * 32;                 // first token of the pair of blocks
+                const int size = big ? 32 : 16;
+                const int r0 = (big ? w8 >> 1 : w8 & 1) * 8 + (l >> 4) * 4, c0 = big ? (w8 & 1) * 16 : 0;
+                if (big || w8 < 4) {
+                    const float *left = At + (second ? pr + size : pr) * kAStride + pr + size + r0;
+                    const float *right = (second ? X + (pr >> 1) * kXStride : Tm + pr * kXStride) + c0 + c;
+                    // T11's columns begin at the diagonal, T22's rows end there
+                    const int m0 = second ? 0 : c0, m1 = second && big && w8 < 4 ? 16 : size;
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    left += m0 * kAStride, right += m0 * kXStride;
+#pragma unroll 1
+                    for (int m = m0; m < m1; m += 8, left += 8 * kAStride, right += 8 * kXStride) {
+                        float4 a[8];
+                        float b[8];
 #pragma unroll
-                for (int m = 0; m < 32; ++m) t[m] = blk11[m * kBlockStride + lane];
+                        for (int k = 0; k < 8; ++k) {
+                            a[k] = *reinterpret_cast<const float4 *>(left + k * kAStride);
+                            b[k] = right[k * kXStride];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            acc[0] = fmaf(a[k].x, b[k], acc[0]);
+                            acc[1] = fmaf(a[k].y, b[k], acc[1]);
+                            acc[2] = fmaf(a[k].z, b[k], acc[2]);
+                            acc[3] = fmaf(a[k].w, b[k], acc[3]);
+                        }
+                    }
+                    float *to = X + ((pr >> 1) + r0) * kXStride + c0 + c;
+                    if (second) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[k] = -acc[k];
+                        *reinterpret_cast<float4 *>(At + (pr + c0 + c) * kAStride + pr + size + r0) =
+                            make_float4(acc[0], acc[1], acc[2], acc[3]);
+                        to = Tm + (pr + 16 + r0) * kXStride + c;
+                    }
+                    if (step != 3) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) to[k * kXStride] = acc[k];
+                    }
+                }
+                role_sync(1, 256);
+            }
+            // T's three parts: T11, T22, T21, a lane per row, two columns at a time
 #pragma unroll 2
-                for (int q = qd * 8; q < qd * 8 + 8; ++q) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int x = 0; x < 6; ++x) {
+                const int r = (x >= 2 ? 32 : 0) + renew(lane), j = ((x >> 1) == 1 ? 32 : 0) + 2 * (w8 + 8 * (x & 1));
+                uint32_t h[3];
+                split3(At[j * kAStride + r], At[(j + 1) * kAStride + r], h[0], h[1], h[2]);
+                uint8_t *t = sm + S::kTOff + sw128_off(r, j >> 3) + (j & 7) * 2;
 #pragma unroll
-                    for (int m = 0; m < 32; m += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(blk21 + q * kBlockStride + m);
-                        acc[0] = fmaf(a.x, t[m], acc[0]);
-                        acc[1] = fmaf(a.y, t[m + 1], acc[1]);
-                        acc[2] = fmaf(a.z, t[m + 2], acc[2]);
-                        acc[3] = fmaf(a.w, t[m + 3], acc[3]);
-                    }
-                    blkx[q * kBlockStride + lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                }
-            }
-            if (!together()) break;
-            // T21 = -T22 (A21 T11): rows qd, qd + 4, ... a warp, as far as T22's triangle goes
-            {
-                float t[32], y[8];
-#pragma unroll
-                for (int m = 0; m < 32; ++m) t[m] = blkx[m * kBlockStride + lane];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int m = 0; m <= 4 * k; m += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(blk22 + (qd + 4 * k) * kBlockStride + m);
-                        const bool end = m == 4 * k;     // the triangle ends with column qd of these four
-                        acc[0] = fmaf(-a.x, t[m], acc[0]);
-                        acc[1] = fmaf(-a.y, end && qd < 1 ? 0.f : t[m + 1], acc[1]);
-                        acc[2] = fmaf(-a.z, end && qd < 2 ? 0.f : t[m + 2], acc[2]);
-                        acc[3] = fmaf(-a.w, end && qd < 3 ? 0.f : t[m + 3], acc[3]);
-                    }
-                    y[k] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) put_t(32 + qd + 4 * k, 4, lane, y[k], y[k + 1]);
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(t + k * kDeltaPanel) = h[k];
             }
             fence_proxy_async_smem();
             arrive(t_ready);
-            arrive(&tab_free[gc & 1]);
+            arrive(&tab_free[tab_i]);
+            next_tab(tab_i, turn);
         }
-    } else if (warp < 24) {
-        // ============================================================ output rows: a warp per 32 value dimensions
-        // In 8x8 fragments (thread: two neighbouring tokens of one dv), transposed by stmatrix into the warp's
-        // own [64 tokens][32 dv] tile, 16-byte chunks swizzled by token pair.
+    } else if (warp < 28) {
+        // ============================================================ norms, output rows: a warp per 32 rows of (Q; K),
+        // then per 32 value dimensions, in 8x8 fragments (thread: two neighbouring tokens of one dv), transposed by
+        // stmatrix into the warp's own [64 tokens][32 dv] tile, 16-byte chunks swizzled by token pair.
         fewer_regs<kRowRegs>();
         const int grp = warp & 3, q2 = (lane & 3) * 2;
-        const bool real = grp * 32 < D;
+        const int row = grp * 32 + lane, i = row & 63;
+        const bool real = grp * 32 < D, keys = grp >= 2;
         const uint32_t lane_base = tmem + ((uint32_t)(grp * 32) << 16);
         uint8_t *stg = sm + S::kOutOff + grp * DC * 64;
         // stmatrix row address: token (lane / 16) * 8 + lane % 8 of its group, dv chunk lane / 8 % 2
         const int row0 = (lane >> 4) * 8 + (lane & 7), ch0 = (lane >> 3) & 1, sw = (row0 >> 1) & 3;
         const uint32_t stg_at = smem_u32(stg) + row0 * 64;
+        int tab_i = 0, turn = 0, last_tab = 0;
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
-            if (!wait(&tab_full[gc & 1], gc >> 1)) break;
-            const DeltaChunk *info = info_of(gc);
-            const int n = uni(info->n);
-            if (n == 0) break;
-            const int t0 = info->t0, h = info->h;
-            if (!wait(&o_done[gc & 1], gc >> 1)) break;
-            tc_fence_after();
-            if (!real) {
-                arrive(o_read);
-                arrive(&tab_free[gc & 1]);
-                continue;
+            if (grp == 0) {
+                role_wait(2, &tab_full[tab_i], turn);
+                const int n = info_of(tab_i)->n;
+                if (n) role_wait(2, &qk_full[gc % QS], gc / QS);
+                if (n && n < DC) role_wait(2, &v_full[gc & 1], gc >> 1);
             }
-            if (lane == 0) bulk_wait_read();             // the tile's last store
-            __syncwarp();
-            const int first_bad = bad_at[(gc & 1) * 128 + grp * 32 + lane];
-            const bool any_bad = __any_sync(0xffffffffu, first_bad < DC);
+            role_sync(2, 128);
+            const int more = uni(info_of(tab_i)->n);
+            if (stop[2]) break;
+            if (more > 0) {
+                // ---- norms of this chunk
+                const int s = gc % QS;
+                float *tab = tab_of(tab_i);
+                uint8_t *tile = sm + s * S::kQkBytes + row * 128;
+                const bool behind = keys && i >= more;
+                if (more < DC) {
+                    // K's and V's rows behind the sequence's end are zeroed: a weight of 0 would not cancel a NaN there
+                    uint8_t *v = sm + S::kVOff + (gc & 1) * S::kVBytes + i * 128;
 #pragma unroll 1
-            for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
-                const int hl = part >> 1, g0 = (part & 1) * 4;
-                const uint32_t at = lane_base + ((uint32_t)hl << 20) + g0 * 8;
-                uint32_t x[16], y[16], r[8];
-                tmem_ld_16x256b_x4(at + TM_PU, x);
-                tmem_ld_16x256b_x4(at + TM_SQ, y);
-                const float *e = tab_of(gc) + T_F + g0 * 8 + q2;
-                tc_wait_ld();
-                if (part == 3) {
-                    tc_fence_before();
-                    arrive(o_read);
+                    for (int x = 0; x < PAN * 8; ++x) {
+                        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+                        if (behind) {
+                            *reinterpret_cast<uint4 *>(tile + (x >> 3) * S::kQkPanel + (x & 7) * 16) = none;
+                            *reinterpret_cast<uint4 *>(v + (x >> 3) * kDeltaPanel + (x & 7) * 16) = none;
+                        }
+                    }
+                    fence_proxy_async_smem();
                 }
+                float r = 1.f;
+                if (p.norm) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 2
+                    for (int x = 0; x < PAN * 8; ++x) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(tile + (x >> 3) * S::kQkPanel +
+                                                                         (((x & 7) ^ (row & 7)) << 4));
+                        const uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {           // tokens 8 (g0 + k / 2) + q2, + 1; dv + 8 (k % 2)
-                    const float2 f = *reinterpret_cast<const float2 *>(e + (k / 2) * 8);
-                    float o0, o1;
-                    fma2(o0, o1, f.x, f.y, __uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]),
-                         __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-                    r[k] = pack_bf16x2(o0, o1);
+                        for (int k = 0; k < 4; ++k) {
+                            const float e0 = __uint_as_float(y[k] << 16), e1 = __uint_as_float(y[k] & 0xFFFF0000u);
+                            fma2(s0, s1, e0, e1, e0, e1, s0, s1);
+                        }
+                    }
+                    r = inv_sqrt(s0 + s1 + p.eps);
                 }
-                const uint32_t to = stg_at + (uint32_t)(g0 * 512) + (((hl * 2 + ch0) ^ sw) << 4);
-                stsm_x4_t(to, r[0], r[1], r[2], r[3]);
-                stsm_x4_t(to + 1024, r[4], r[5], r[6], r[7]);
+                if (behind) r = 0.f;
+                // rows of K: b, -c, A's row factor (in beta's place); rows of Q: nothing, f, P's
+                const float first = keys ? tab[T_BETA + i] * r : p.scale * r, second = keys ? first * r : first;
+                tab[(keys ? T_B : T_P) + i] = first;
+                tab[(keys ? T_BETA : T_P) + i] = second;
+                tab[(keys ? T_C : T_F) + i] = (keys ? -second : second) * tab[T_GAM + i];
+                arrive(&norms[gc & 1]);
+                arrive(&qk_empty[s]);
             }
-            arrive(&tab_free[gc & 1]);
-            if (any_bad) {
+            if (gc > 0) {
+                // ---- outputs of the one before
+                const int oc = gc - 1;
+                const DeltaChunk *info = info_of(last_tab);
+                const int n = uni(info->n), t0 = info->t0, h = info->h;
+                if (grp == 0) role_wait(2, &o_done[oc & 1], oc >> 1);
+                role_sync(2, 128);
+                tc_fence_after();
+                int first_bad = DC;
+                if (real) {
+                    if (lane == 0) bulk_wait_read();             // the tile's last store
+                    __syncwarp();
+                    first_bad = min(bad_at[(oc & 1) * 128 + grp * 32 + lane], info->bad);
+#pragma unroll 1
+                    for (int part = 0; part < 4; ++part) {      // 16 dv, 32 tokens
+                        const int hl = part >> 1, g0 = (part & 1) * 4;
+                        const uint32_t at = lane_base + ((uint32_t)hl << 20) + g0 * 8;
+                        uint32_t x[16], y[16], r[8];
+                        tmem_ld_16x256b_x4(at + TM_PU, x);
+                        tmem_ld_16x256b_x4(at + TM_SQ, y);
+                        const float *e = tab_of(last_tab) + T_F + g0 * 8 + q2;
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {           // tokens 8 (g0 + k / 2) + q2, + 1; dv + 8 (k % 2)
+                            const float2 f = *reinterpret_cast<const float2 *>(e + (k / 2) * 8);
+                            float o0, o1;
+                            fma2(o0, o1, f.x, f.y, __uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]),
+                                 __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                            r[k] = pack_bf16x2(o0, o1);
+                        }
+                        const uint32_t to = stg_at + (uint32_t)(g0 * 512) + (((hl * 2 + ch0) ^ sw) << 4);
+                        stsm_x4_t(to, r[0], r[1], r[2], r[3]);
+                        stsm_x4_t(to + 1024, r[4], r[5], r[6], r[7]);
+                    }
+                }
+                tc_fence_before();
+                arrive(o_read);
+                arrive(&tab_free[last_tab]);
                 // NaN from a dv's first non-finite token on
                 for (int t = first_bad; t < DC; ++t)
                     *reinterpret_cast<uint16_t *>(stg + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + (lane & 7) * 2) =
                         0x7FC0;
-            }
-            __syncwarp();
-            if (n == DC) {
-                // one store of the tile; its swizzle is the copy engine's for rows of 64 bytes
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    tma_store_3d(&omap, stg, grp * 32, h, t0);
-                    bulk_commit();
-                }
-            } else {
-                // rows behind the sequence stay as they are
-                __nv_bfloat16 *out = p.out + (int64_t)t0 * p.out_stride + (int64_t)h * D + grp * 32;
+                if (real && n == DC) {
+                    // one store of the tile; its swizzle is the copy engine's for rows of 64 bytes
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&omap, stg, grp * 32, h, t0);
+                        bulk_commit();
+                    }
+                } else if (real) {
+                    // rows behind the sequence stay as they are
+                    __nv_bfloat16 *out = p.out + (int64_t)t0 * p.out_stride + (int64_t)h * D + grp * 32;
 #pragma unroll 1
-                for (int t = lane >> 2; t < n; t += 8)
-                    *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) =
-                        *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
-                __syncwarp();
+                    for (int t = lane >> 2; t < n; t += 8)
+                        *reinterpret_cast<uint4 *>(out + t * p.out_stride + (lane & 3) * 8) =
+                            *reinterpret_cast<const uint4 *>(stg + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                    __syncwarp();
+                }
             }
+            if (more == 0) break;
+            last_tab = tab_i;
+            next_tab(tab_i, turn);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     } else {
         fewer_regs<kOtherRegs>();
-        if (warp == 24) {
+        if (warp == 28) {
             // ============================================================ loads
-            if (lane == 0) {
-                DeltaWalk walk;
-                int gc = 0;
-                while (walk.step(units, units_n, p.Hv)) {
-                    const int s = gc % QS, vs = gc % VS, rw = walk.u.t0 + walk.c * DC, hk = walk.h / p.G;
-                    if (gc >= QS && !chunk_wait(&qk_empty[s], (uint32_t)(gc / QS - 1) & 1u, abort_flag)) break;
-                    uint8_t *qk = sm + s * S::kQkBytes, *v = sm + S::kVOff + vs * S::kVBytes;
+            DeltaWalk walk(units_n, p.Hv);
+            // x / y of x < 2^18: off by less than 2^-20 of itself, and half a step away from the next integer
+            const float inv_g = __fdividef(1.f, (float)p.G);
+            int gc = 0, qk_gone = 0;
+#pragma unroll 1
+            while (walk.step(units)) {
+                const int s = gc % QS, hk = (int)(((float)walk.h + 0.5f) * inv_g);
+                if (gc >= QS && !wait(&qk_empty[s], gc / QS - 1)) break;
+                if (elect_one()) {
+                    uint8_t *to = sm + s * S::kQkBytes;
                     mbar_arrive_expect_tx(&qk_full[s], S::kQkBytes);
 #pragma unroll 1
-                    for (int x = 0; x < PAN; ++x) {
-                        tma_load_3d(qk + x * S::kQkPanel + kDeltaPanel, &kmap, &qk_full[s], x * 64, hk, rw);
-                        tma_load_3d(qk + x * S::kQkPanel, &qmap, &qk_full[s], x * 64, hk, rw);
+                    for (int x = 0; x < PAN; ++x, to += S::kQkPanel) {
+                        tma_load_3d(to + kDeltaPanel, &kmap, &qk_full[s], x * 64, hk, walk.row);
+                        tma_load_3d(to, &qmap, &qk_full[s], x * 64, hk, walk.row);
                     }
-                    // (the barriers below count a chunk's Q and K, then its V)
-                    if (gc >= VS && !chunk_wait(&v_empty[vs], (uint32_t)(gc / VS - 1) & 1u, abort_flag)) {
-                        chunk_wait(&qk_full[s], (uint32_t)(gc / QS) & 1u, &never);
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&v_full[vs], S::kVBytes);
+                }
+                __syncwarp();
+                ++qk_gone;
+                if (gc >= VS && !wait(&v_empty[gc & 1], (gc >> 1) - 1)) break;
+                if (elect_one()) {
+                    uint8_t *to = sm + S::kVOff + (gc & 1) * S::kVBytes;
+                    mbar_arrive_expect_tx(&v_full[gc & 1], S::kVBytes);
 #pragma unroll 1
                     for (int x = 0; x < PAN; ++x)
-                        tma_load_3d(v + x * kDeltaPanel, &vmap, &v_full[vs], x * 64, walk.h, rw);
-                    ++gc;
+                        tma_load_3d(to + x * kDeltaPanel, &vmap, &v_full[gc & 1], x * 64, walk.h, walk.row);
                 }
-                // copies still in flight (after a wait that gave up) land before the CTA ends
-                for (int d = max(0, gc - QS); d < gc; ++d) chunk_wait(&qk_full[d % QS], (uint32_t)(d / QS) & 1u, &never);
-                for (int d = max(0, gc - VS); d < gc; ++d) chunk_wait(&v_full[d % VS], (uint32_t)(d / VS) & 1u, &never);
+                __syncwarp();
+                ++gc;
             }
-            __syncwarp();
-        } else if (warp == 25) {
-            // ============================================================ the chunks' tables: two tokens a lane
-            DeltaWalk walk;
+            // copies still in flight (after a wait that gave up) land before the CTA ends
+            for (int d = max(0, qk_gone - QS); d < qk_gone; ++d) wait(&qk_full[d % QS], d / QS);
+            for (int d = max(0, gc - VS); d < gc; ++d) wait(&v_full[d & 1], d >> 1);
+        } else if (warp == 29) {
+            // ============================================================ the chunks' tables, two tokens a lane
+            DeltaWalk walk(units_n, p.Hv);
             const double kLog2e = 1.4426950408889634074;
+            int tab_i = 0, turn = -1;                                    // (turn of the tables' last readers)
 #pragma unroll 1
-            for (int gc = 0;; ++gc) {
-                const bool some = walk.step(units, units_n, p.Hv);
-                const int n = some ? min(DC, walk.u.n - walk.c * DC) : 0;
-                const int64_t t0 = some ? walk.u.t0 + (int64_t)walk.c * DC : 0;
+            while (true) {
+                const int n = walk.step(units);
                 float g[2] = {0.f, 0.f}, beta[2] = {0.f, 0.f};
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int64_t t = t0 + 2 * lane + x;
+                    const int64_t t = walk.row + 2 * lane + x;
                     if (2 * lane + x < n) {
                         g[x] = __ldg(p.log_decay + t * p.decay_stride + walk.h);
                         beta[x] = __ldg(p.beta + t * p.beta_stride + walk.h);
@@ -952,173 +993,152 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 const double x0 = (double)fmaxf(fminf(g[0], 0.f), -256.f) * kLog2e;
                 const double x1 = (double)fmaxf(fminf(g[1], 0.f), -256.f) * kLog2e;
                 double inc = x0 + x1;
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const double y = __shfl_up_sync(0xffffffffu, inc, o);
                     if (lane >= o) inc += y;
                 }
-                const double before = __shfl_up_sync(0xffffffffu, inc, 1);
-                const double G0 = (lane ? before : 0.0) + x0, G1 = G0 + x1;
-                const double all = __shfl_sync(0xffffffffu, G1, 31);
-                if (gc >= 2 && !wait(&tab_free[gc & 1], (gc >> 1) - 1)) break;
-                float *tab = tab_of(gc);
+                const double all = __shfl_sync(0xffffffffu, inc, 31);
+                if (turn >= 0 && !wait(&tab_free[tab_i], turn)) break;
+                float *tab = tab_of(tab_i);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int i = 2 * lane + x;
-                    const double G = x ? G1 : G0;
-                    const float hi = (float)G;
+                    const double Gi = x ? inc : inc - x1;
+                    const float hi = (float)Gi;
                     tab[T_GHI + i] = hi;
-                    tab[T_GLO + i] = (float)(G - (double)hi);
+                    tab[T_GLO + i] = (float)(Gi - (double)hi);
                     tab[T_BETA + i] = beta[x];
-                    tab[T_GAM + i] = exp2f(hi);
-                    tab[T_W + i] = i < n ? exp2f((float)(all - G)) : 0.f;
+                    tab[T_GAM + i] = ex2(hi);
+                    tab[T_W + i] = i < n ? ex2((float)(all - Gi)) : 0.f;
                 }
-                if (lane == 0) {
-                    DeltaChunk *info = info_of(gc);
-                    // near 1, where a state is multiplied many times before it fades, as two parts
-                    const float y = (float)(all * 0.69314718055994530942);
-                    float a = exp2f((float)all), a_lo = 0.f;
-                    if (y > -0.3f) {
-                        const float e = expm1f(y);
-                        a = 1.f + e;
-                        a_lo = e - (a - 1.f);
-                    }
-                    info->n = n;
-                    info->t0 = (int)t0;
-                    info->h = walk.h;
-                    info->first = walk.c == 0;
-                    info->last = some && walk.c + 1 == walk.chunks;
-                    info->slot = some ? walk.u.slot : -1;
-                    info->from = some ? walk.u.from : 0;
-                    info->a = a;
-                    info->a_lo = a_lo;
+                // e^{G_n} near 1, where a state is multiplied many times before it fades, as two parts: e^y - 1 by its
+                // series up to y^9, 2^-33 of it for y >= -0.3
+                const float y = (float)(all * 0.69314718055994530942);
+                float a = ex2((float)all), a_lo = 0.f;
+                if (y > -0.3f) {
+                    float e = 1.f / 362880.f;
+                    e = fmaf(e, y, 1.f / 40320.f), e = fmaf(e, y, 1.f / 5040.f), e = fmaf(e, y, 1.f / 720.f);
+                    e = fmaf(e, y, 1.f / 120.f), e = fmaf(e, y, 1.f / 24.f), e = fmaf(e, y, 1.f / 6.f);
+                    e = fmaf(e, y, 0.5f), e = fmaf(e, y, 1.f) * y;
+                    a = 1.f + e;
+                    a_lo = e - (a - 1.f);
                 }
-                arrive(&tab_full[gc & 1]);
-                if (!some) break;
+                if (lane == 0)
+                    *info_of(tab_i) = DeltaChunk{n, walk.row, walk.h, walk.first, walk.left <= DC, walk.slot, walk.from, a,
+                                                 a_lo, DC};
+                arrive(&tab_full[tab_i]);
+                next_tab(tab_i, turn);
+                if (n == 0) break;
             }
-        } else if (warp == 26) {
+        } else if (warp == 30) {
             // ============================================================ MMAs
-            auto kq = [&](int gc) {
+            // four steps of 16 of K with A in TMEM
+            auto four = [&](uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t d_step, uint32_t b_step,
+                            uint32_t id_step, bool add) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_ts(tmem + d + k * d_step, tmem + a + k * 8, b + k * b_step, id - k * id_step, add || k > 0);
+            };
+            // S_0 times K or Q: parts of S_0 and panels of the tile
+            auto times = [&](uint32_t d, uint32_t tile, int parts) {
+                const uint64_t b = sw128_desc(tile, 16, 1024);
+#pragma unroll 1
+                for (int x = 0; x < parts * PAN; ++x) {
+                    const int part = PAN == 2 ? x >> 1 : x, pan = PAN == 2 ? x & 1 : 0;
+                    four(d, TM_S1 + part * 64 + pan * 32, b + pan * (S::kQkPanel >> 4), idesc_bf16_f32(128, DC, 0), 0, 2, 0,
+                         x > 0);
+                }
+            };
+            // a product whose B is lower triangular (16 tokens j reach rows from theirs on), of parts of A and B in turn,
+            // a digit each
+            auto triangle = [&](uint32_t d, uint32_t a, uint32_t tile, int products, uint32_t of_a, uint32_t of_b) {
+                const uint64_t b = sw128_desc(tile, 16, 1024);
+#pragma unroll 1
+                for (int x = 0; x < products; ++x)
+                    four(d, a + (of_a >> 4 * x & 3) * 32, b + (of_b >> 4 * x & 3) * (kDeltaPanel >> 4),
+                         idesc_bf16_f32(128, DC, 0), 16, 2 + (16 * 128 >> 4), (16u >> 3) << 17, x > 0);
+            };
+            // KQ of chunk gc, if there is one
+            auto kq = [&](int gc, int tab_i, int turn) {
+                if (!wait(&tab_full[tab_i], turn)) return -1;
+                if (uni(info_of(tab_i)->n) == 0) return 0;
+                if (!wait(&qk_full[gc % QS], gc / QS)) return -1;
+                if (gc > 0 && !wait(kq_read, gc - 1)) return -1;
+                tc_fence_after();
                 if (elect_one()) {
                     const uint64_t qd = sw128_desc(smb + (gc % QS) * S::kQkBytes, 16, 1024);
-                    constexpr uint32_t id = idesc_bf16_f32(128, DC, 0);
+#pragma unroll 1
+                    for (int x = 0; x < PAN; ++x) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t d = qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2;
-                        tc_mma_ss(tmem + TM_KQ, d, d + (kDeltaPanel >> 4), id, k > 0);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t d = qd + x * (S::kQkPanel >> 4) + k * 2;
+                            tc_mma_ss(tmem + TM_KQ, d, d + (kDeltaPanel >> 4), idesc_bf16_f32(128, DC, 0), x + k > 0);
+                        }
                     }
                     tc_commit(kq_done);
                 }
                 __syncwarp();
+                return 1;
             };
-            // the chunk's tables, and its Q and K, are there; 0: no such chunk, -1: a wait gave up
-            auto ready = [&](int gc) {
-                if (!wait(&tab_full[gc & 1], gc >> 1)) return -1;
-                if (uni(info_of(gc)->n) == 0) return 0;
-                return wait(&qk_full[gc % QS], gc / QS) ? 1 : -1;
-            };
-            // a product whose B is lower triangular: 16 tokens j reach rows from theirs on
-            auto triangle = [&](uint32_t d, uint32_t a, uint64_t b, bool add) {
-#pragma unroll
-                for (int k = 0; k < DC / 16; ++k)
-                    tc_mma_ts(tmem + d + 16 * k, tmem + a + k * 8, b + k * 2 + (16 * k * 128 >> 4),
-                              idesc_bf16_f32(128, DC - 16 * k, 0), add || k > 0);
-            };
-            int some = ready(0);
-            if (some > 0) {
-                tc_fence_after();
-                kq(0);
-            }
+            int tab_i = 0, turn = 0;
+            // in the order of the chain; KQ a chunk ahead, in the time in which R is made
 #pragma unroll 1
-            for (int gc = 0; some > 0; ++gc) {
-                const int s = gc % QS;
-                const uint32_t qk = smb + s * S::kQkBytes;
-                constexpr uint32_t id = idesc_bf16_f32(128, DC, 0);
-                some = -1;
-                if (!wait(s_ready, gc)) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t kd = sw128_desc(qk + kDeltaPanel, 16, 1024);
-#pragma unroll
-                    for (int part = 0; part < 3; ++part) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tc_mma_ts(tmem + TM_SK, tmem + (part == 0 ? TM_S1 : part == 1 ? TM_S2 : TM_S3) + k * 8,
-                                      kd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2, id, part + k > 0);
-                    }
-                    tc_commit(sk_done);
-                }
-                __syncwarp();
-                if (gc > 0 && !wait(o_read, gc - 1)) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t qd = sw128_desc(qk, 16, 1024);
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tc_mma_ts(tmem + TM_SQ, tmem + (part == 0 ? TM_S1 : TM_S2) + k * 8,
-                                      qd + (k / 4) * (S::kQkPanel >> 4) + (k % 4) * 2, id, part + k > 0);
-                    }
-                }
-                __syncwarp();
-                if (!wait(t_ready, gc)) break;
-                if (!wait(r_ready, gc)) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t td = sw128_desc(smb + S::kTOff, 16, 1024);
-                    triangle(TM_U, TM_R, td, false);
-                    triangle(TM_U, TM_R + 32, td, true);
-                    triangle(TM_U, TM_R, td + (kDeltaPanel >> 4), true);
-                    triangle(TM_U, TM_R + 64, td, true);
-                    triangle(TM_U, TM_R + 32, td + (kDeltaPanel >> 4), true);
-                    triangle(TM_U, TM_R, td + (2 * kDeltaPanel >> 4), true);
-                    tc_commit(u_done);
-                }
-                __syncwarp();
-                // KQ a chunk ahead, in the time in which w U~ is made
-                const int more = ready(gc + 1);
-                if (more < 0) break;
-                if (more > 0) {
-                    if (!wait(kq_read, gc)) break;
+            for (int gc = -1;; ++gc) {
+                const uint32_t qk = smb + (gc % QS) * S::kQkBytes;
+                int old_tab = tab_i;
+                if (gc >= 0) {
+                    next_tab(tab_i, turn);
+                    if (!wait(s_ready, gc)) break;
                     tc_fence_after();
-                    kq(gc + 1);
+                    if (elect_one()) {
+                        times(TM_SK, qk + kDeltaPanel, 3);
+                        tc_commit(&go[0]);
+                    }
+                    __syncwarp();
+                    if (gc > 0 && !wait(o_read, gc - 1)) break;
+                    tc_fence_after();
+                    if (elect_one()) times(TM_SQ, qk, 2);
+                    __syncwarp();
                 }
-                if (!wait(w_ready, gc)) break;
+                const int more = kq(gc + 1, tab_i, turn);
+                if (more < 0 || (gc < 0 && more == 0)) break;
+                if (gc < 0) continue;
+                if (!wait(t_ready, gc) || !wait(x_ready, 2 * gc)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    // parts of R and of T: (1, 1), (2, 1), (1, 2), (3, 1), (2, 2), (1, 3)
+                    triangle(TM_U, TM_R, smb + S::kTOff, 6, 0x012010, 0x210100);
+                    tc_commit(&go[1]);
+                }
+                __syncwarp();
+                if (!wait(x_ready, 2 * gc + 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t kd = sw128_desc(qk + kDeltaPanel, S::kQkPanel, 1024);
-                    constexpr uint32_t idk = idesc_bf16_f32(128, D, 1);
-#pragma unroll
-                    for (int part = 0; part < 3; ++part) {
-#pragma unroll
-                        for (int k = 0; k < DC / 16; ++k)
-                            tc_mma_ts(tmem + TM_KV, tmem + TM_R + part * 32 + k * 8, kd + k * (16 * 128 >> 4), idk,
-                                      part + k > 0);
-                    }
+#pragma unroll 1
+                    for (int x = 0; x < 3; ++x)
+                        four(TM_KV, TM_R + x * 32, kd, idesc_bf16_f32(128, D, 1), 0, 16 * 128 >> 4, 0, x > 0);
                     tc_commit(kv_done);
-                    tc_commit(&qk_empty[s]);
-                    const uint64_t pd = sw128_desc(smb + S::kPOff + (gc & 1) * 2 * kDeltaPanel, 16, 1024);
-                    triangle(TM_PU, TM_UO, pd, false);
-                    triangle(TM_PU, TM_UO + 32, pd, true);
-                    triangle(TM_PU, TM_UO, pd + (kDeltaPanel >> 4), true);
+                    tc_commit(&qk_empty[gc % QS]);
+                    // parts of U~ and of P: (1, 1), (2, 1), (1, 2)
+                    triangle(TM_PU, TM_UO, smb + S::kPOff + (gc & 1) * 2 * kDeltaPanel, 3, 0x010, 0x100);
                     tc_commit(&o_done[gc & 1]);
                 }
-                arrive(&tab_free[gc & 1]);
-                some = more;
+                arrive(&tab_free[old_tab]);
+                if (more == 0) break;
             }
             // nothing of this CTA's is left in the tensor core when TMEM goes back
             if (elect_one()) tc_commit(drain);
             __syncwarp();
-            chunk_wait(drain, 0u, &never);
-            __syncwarp();
+            wait(drain, 0);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
-    if (threadIdx.x == 0 && (abort_flag[0] | abort_flag[1])) record_error(p.err, ERR_TIMEOUT | SRC_DELTA);
+    if (threadIdx.x == 0 && *late) record_error(p.err, ERR_TIMEOUT | SRC_DELTA);
 }
 
 template <int D>
