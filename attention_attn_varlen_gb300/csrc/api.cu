@@ -1481,11 +1481,12 @@ static bool beam_sizes(int num_groups, int num_beams, int vocab, int num_out) {
            num_out <= kBeamMax && (int64_t)num_groups * num_beams < (1 << 25);
 }
 
-// Slices of a row: four CTAs per SM over all rows, as far as a row has slices.  (The number of SMs is
-// fixed here: the workspace's size, asked for without a device, goes by it.)
+// Slices of a row: at most four CTAs per SM over all rows, which is what an SM holds, as far as a row has
+// slices.  (The number of SMs is fixed here: the workspace's size, asked for without a device, goes by it.)
 static int beam_slice_len(int rows, int vocab) {
     const int most = (vocab + kBeamSliceElems - 1) / kBeamSliceElems;
-    int slices = (4 * kLinearSms + rows - 1) / rows;
+    int slices = 4 * kLinearSms / rows;
+    if (slices < 1) slices = 1;
     if (slices > most) slices = most;
     if (slices > 64) slices = 64;
     const int each = (vocab + slices - 1) / slices;

@@ -17,17 +17,18 @@ constexpr float kLowest = -3.4028234663852886e38f;   // the lowest fp32 value, w
 // candidates comes first may hang on the last digits.
 //
 // One pass over the logits (HBM bounds it).  A CTA takes a slice of a row, a warp a
-// share of the slice in vectors of eight neighbours a lane; every lane keeps a running
-// maximum and the sum of exponentials, the warp the k best logits as a sorted list,
-// one a lane.  A key is the logit's bits in an order that compares as unsigned above
+// share of the slice in vectors of eight neighbours a lane; the warp keeps a sum of
+// exponentials below a reference that moves when a logit lies far above it, and its
+// k best logits as a sorted list, one a lane.  A key is the logit's bits in an order that compares as unsigned above
 // the token's complement: distinct, and a larger one comes first.  What exceeds
 // the list's last key goes to a buffer in shared memory, which is merged into the list 32 at a time.
 // A second small launch joins the slices and the beams of a group.
 // Every row is cut and summed in the same way: equal rows give equal sums.
 // ---------------------------------------------------------------------------
 constexpr int kScanWarps = 8;
-constexpr int kScanAhead = 4;                        // vectors of a warp in flight
-constexpr int kScanBuf = 32 + 256;                   // keys waiting: less than 32, and one vector's
+template <typename T> constexpr int kScanAhead = 8 / sizeof(T);   // vectors of a warp in a step (64 bytes a lane)
+constexpr float kFarAbove = 40.f;                    // a logit this far above the sum's reference moves it
+constexpr float kFarBelow = -1e37f;                  // logits times log2(e) stay finite above this
 
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
     const uint32_t b = __float_as_uint(x + 0.f);     // -0 is 0
@@ -42,6 +43,7 @@ __device__ __forceinline__ uint32_t key_token(uint64_t key) { return ~(uint32_t)
 __device__ __forceinline__ uint64_t key_floor() { return key_of(-INFINITY, 0u) | 0xFFFFFFFFull; }
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t x, int from) { return __shfl_sync(0xffffffffu, x, from); }
+__device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int by) { return __shfl_up_sync(0xffffffffu, x, by); }
 
 // one compare-exchange of a descending network over the lanes
 __device__ __forceinline__ uint64_t exchange(uint64_t x, int lane, int stride, bool descending) {
@@ -69,146 +71,249 @@ __device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b, int lane) {
     return x;
 }
 
-// eight neighbouring logits of a row from element i on; -inf behind the end
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T *row, int i, int end, float (&x)[8]) {
-    if (WIDE && i + 8 <= end) {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 w = ldg_stream16(row + i);
-            const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+// Eight neighbouring logits of a row, as loaded: elements i .. i + 7, -inf behind the end.  MODE 0: the rows lie
+// on 16-byte boundaries and come by way of shared memory, but for the row's end; 1: they need not, and 16 bytes come
+// out of the two aligned pieces that hold them
+template <typename T, int MODE> struct Eight {
+    static constexpr int kWords = sizeof(T) * 2;     // 32-bit words
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const T *row, int i, int end) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + i), lo = at & ~(uintptr_t)15;
+        constexpr int kPieces = kWords / 4 + 1;
+        if (MODE == 1 && lo >= reinterpret_cast<uintptr_t>(row) &&
+            lo + kPieces * 16 <= reinterpret_cast<uintptr_t>(row + end)) {
+            // all of what is read is the row's own
+            uint32_t x[kPieces * 4 + 1];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = __uint_as_float(r[j] << 16);
-                x[2 * j + 1] = __uint_as_float(r[j] & 0xFFFF0000u);
+            for (int k = 0; k < kPieces; ++k) {
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(lo) + k);
+                x[4 * k] = y.x, x[4 * k + 1] = y.y, x[4 * k + 2] = y.z, x[4 * k + 3] = y.w;
             }
-        } else {
-            const uint4 w = ldg_stream16(row + i), y = ldg_stream16(row + i + 4);
-            const uint32_t r[8] = {w.x, w.y, w.z, w.w, y.x, y.y, y.z, y.w};
+            x[kPieces * 4] = 0;
+            const uint32_t off = (uint32_t)(at - lo);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[j]);
+            for (int k = 0; k < kWords + 2; ++k) x[k] = off & 8 ? x[k + 2] : x[k];
+#pragma unroll
+            for (int k = 0; k < kWords + 1; ++k) x[k] = off & 4 ? x[k + 1] : x[k];
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) w[k] = sizeof(T) == 2 ? __funnelshift_r(x[k], x[k + 1], (off & 2) * 8) : x[k];
+            return;
         }
-    } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            x[j] = -INFINITY;
-            if (i + j < end) x[j] = (float)row[i + j];
+            uint32_t b = sizeof(T) == 2 ? 0xFF80u : 0xFF800000u;
+            if (i + j < end)
+                b = sizeof(T) == 2 ? reinterpret_cast<const uint16_t *>(row)[i + j] : reinterpret_cast<const uint32_t *>(row)[i + j];
+            if (sizeof(T) == 2) w[j / 2] = j & 1 ? w[j / 2] | b << 16 : b;
+            else w[j] = b;
         }
     }
-}
+    // what copy() put into shared memory
+    __device__ __forceinline__ void take(const uint4 *from) {
+#pragma unroll
+        for (int k = 0; k < kWords; k += 4) {
+            const uint4 x = from[k / 4 * kScanWarps * 32];
+            w[k] = x.x, w[k + 1] = x.y, w[k + 2] = x.z, w[k + 3] = x.w;
+        }
+    }
+    static __device__ __forceinline__ void copy(uint4 *to, const T *from) {
+#pragma unroll
+        for (int k = 0; k < kWords / 4; ++k)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + k * kScanWarps * 32)),
+                         "l"(reinterpret_cast<const uint4 *>(from) + k)
+                         : "memory");
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if (sizeof(T) == 2) return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+        return __uint_as_float(w[j]);
+    }
+    __device__ __forceinline__ float top() const {
+        if (sizeof(T) == 2) {
+            // pairs as they are
+            uint32_t m;
+            asm("{.reg .b32 a, b;\n\tmax.bf16x2 a, %1, %2;\n\tmax.bf16x2 b, %3, %4;\n\tmax.bf16x2 %0, a, b;}"
+                : "=r"(m)
+                : "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]));
+            return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        }
+        return max3f(max3f(get(0), get(1), get(2)), max3f(get(3), get(4), get(5)), fmaxf(get(6), get(7)));
+    }
+};
 
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kScanWarps * 32) beam_scan_kernel(const BeamParams p) {
-    __shared__ uint64_t buf[kScanWarps][kScanBuf];
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kScanWarps * 32, 4) beam_scan_kernel(const BeamParams p) {
+    __shared__ uint64_t buf[kScanWarps][32];
     __shared__ float2 part[kScanWarps];
+    // MODE 0: the next step's vectors arrive while a step's are gone through; a lane reads what it copied itself
+    constexpr int kAhead = kScanAhead<T>, kStep = kAhead * kScanWarps * 256;
+    __shared__ uint4 ring[MODE == 0 ? 2 * 4 * kScanWarps * 32 : 1];
     asm volatile("griddepcontrol.launch_dependents;");
+    auto pick = [](const Eight<T, MODE> (&x)[kAhead], int v) {           // x[v], registers by choice
+        Eight<T, MODE> y = x[0];
+#pragma unroll
+        for (int u = 1; u < kAhead; ++u) {
+#pragma unroll
+            for (int k = 0; k < y.kWords; ++k) y.w[k] = v == u ? x[u].w[k] : y.w[k];
+        }
+        return y;
+    };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x / p.slices, slice = blockIdx.x - row * p.slices;
     const T *x0 = reinterpret_cast<const T *>(p.logits) + (int64_t)row * p.row_stride;
     const int begin = slice * p.slice_len, end = min(p.V, begin + p.slice_len);
     uint64_t *mine = buf[warp];
-    uint64_t list = key_floor(), last = list;            // last: the k-th key so far
-    int waiting = 0;
-    float top = kLowest, sum = 0.f;                      // (finite: -inf - -inf would be NaN)
-    const int per = (p.slice_len / (kScanWarps * 256) + kScanAhead - 1) / kScanAhead;
-    auto flush = [&](int n) {                            // the first n <= 32 waiting keys into the list
-        __syncwarp();
-        const uint64_t k = lane < n ? mine[lane] : key_floor();
-        list = merge32(list, sort32(k, lane), lane);
-        const uint64_t kth = shfl64(list, p.k - 1);
-        last = kth > last ? kth : last;
-        __syncwarp();
+    uint64_t list = key_floor(), last = list;            // last: the k-th key so far, or a bound below it
+    float bound = -INFINITY;                             // its logit
+    float ref = kLowest, sum = 0.f;                      // sum of e^(x - ref); (finite: -inf - -inf would be NaN)
+    // the warps' sorted lists into buf[0]
+    auto best_of_warps = [&](uint64_t own) {
+        mine[lane] = own;
+        __syncthreads();
+#pragma unroll 1
+        for (int half = kScanWarps / 2; half > 0; half /= 2) {
+            if (warp < half) {
+                own = merge32(own, buf[warp + half][lane], lane);
+                mine[lane] = own;
+            }
+            __syncthreads();
+        }
     };
+    // (steps that end before the slice does need no look at each vector)
+    auto slot = [&](int v, int it) { return ring + ((it & 1) * 4 + v * 4 / kAhead) * kScanWarps * 32 + threadIdx.x; };
+    auto fetch = [&](int base, int it) {
+        if (MODE != 0) return;
+        const T *from = x0 + base + warp * 256 + lane * 8;
+        if (base + kStep <= end) {
+#pragma unroll
+            for (int v = 0; v < kAhead; ++v) Eight<T, MODE>::copy(slot(v, it), from + v * kScanWarps * 256);
+        } else {
+#pragma unroll
+            for (int v = 0; v < kAhead; ++v)
+                if (base + (v * kScanWarps + warp) * 256 + lane * 8 + 8 <= end)
+                    Eight<T, MODE>::copy(slot(v, it), from + v * kScanWarps * 256);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(begin, 0);
 #pragma unroll 1
-    for (int it = 0; it < per; ++it) {
-        float x[kScanAhead][8];
-        const int at = begin + (it * kScanAhead * kScanWarps + warp) * 256 + lane * 8;
+    for (int base = begin, it = 0; base < end; base += kStep, ++it) {
+        fetch(base + kStep, it + 1);
+        if (it > 1 && (it & (it - 1)) == 0) {
+            // the CTA's k-th key so far is a bound for every warp, the tighter the further the scan has come
+            best_of_warps(list);
+            const uint64_t t = buf[0][p.k - 1];
+            if (t > last) last = t, bound = key_logit(t);
+            __syncthreads();
+        }
+        const int at = base + warp * 256 + lane * 8;
+        Eight<T, MODE> x[kAhead];
+        if (MODE == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (MODE == 0 && base + kStep <= end) {
 #pragma unroll
-        for (int v = 0; v < kScanAhead; ++v) load8<T, WIDE>(x0, at + v * kScanWarps * 256, end, x[v]);
-        float high[kScanAhead];
+            for (int v = 0; v < kAhead; ++v) x[v].take(slot(v, it));
+        } else {
 #pragma unroll
-        for (int v = 0; v < kScanAhead; ++v)
-            high[v] = max3f(max3f(x[v][0], x[v][1], x[v][2]), max3f(x[v][3], x[v][4], x[v][5]), fmaxf(x[v][6], x[v][7]));
-        const float lane_top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
-        const float new_top = fmaxf(top, lane_top);
-        sum *= ex2((top - new_top) * kLog2e);
-        top = new_top;
+            for (int v = 0; v < kAhead; ++v) {
+                const int i = at + v * kScanWarps * 256;
+                if (MODE == 0 && i + 8 <= end) x[v].take(slot(v, it));
+                else x[v].load(x0, i, end);
+            }
+        }
+        float high[kAhead], top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < kAhead; ++v) {
+            high[v] = x[v].top();
+            top = fmaxf(top, high[v]);
+        }
+        if (__any_sync(0xffffffffu, top > ref + kFarAbove)) {
+            float m = top;
+#pragma unroll
+            for (int w = 16; w > 0; w /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+            m = fmaxf(m, ref);
+            sum *= ex2((ref - m) * kLog2e);
+            ref = m;
+        }
         float s0 = 0.f, s1 = 0.f;
+        if (ref > kFarBelow) {
+            // 2^(x log2(e) - ref log2(e)), and what the second product's rounding leaves, once for all
+            const float r = -__fmul_rn(ref, kLog2e);
 #pragma unroll
-        for (int v = 0; v < kScanAhead; ++v) {
+            for (int v = 0; v < kAhead; ++v) {
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                float a = x[v][j], b = x[v][j + 1];
-                add2(a, b, -top, -top);
-                fma2(a, b, a, b, kLog2e, kLog2e, 0.f, 0.f);
-                add2(s0, s1, ex2(a), ex2(b));
-            }
-        }
-        sum += s0 + s1;
-        if (it == 0) {
-            // k lanes have a logit at or above the k-th largest of the lanes' maxima
-            const uint64_t t = shfl64(sort32(key_of(lane_top, 0u), lane), p.k - 1);
-            const uint64_t bound = (t & 0xFFFFFFFF00000000ull) - 1;
-            last = bound > last ? bound : last;
-        }
-#pragma unroll 1
-        for (int v = 0; v < kScanAhead; ++v) {
-            const float hv = v == 0 ? high[0] : v == 1 ? high[1] : v == 2 ? high[2] : high[3];
-            if (!__any_sync(0xffffffffu, key_of(hv, 0u) > last)) continue;
-            const uint32_t token = (uint32_t)(at + v * kScanWarps * 256);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xj = v == 0 ? x[0][j] : v == 1 ? x[1][j] : v == 2 ? x[2][j] : x[3][j];
-                const uint64_t key = key_of(xj, token + j);
-                const bool in = key > last && xj == xj;
-                const uint32_t who = __ballot_sync(0xffffffffu, in);
-                if (in) mine[waiting + __popc(who & ((1u << lane) - 1u))] = key;
-                waiting += __popc(who);
-            }
-            if (waiting < 32) continue;
-            int done = 0;
-            for (; waiting - done >= 32; done += 32) {
-                flush(32);
-                if (waiting - done > 32) {               // the rest moves up, 32 at a time, front to back
-                    for (int m = 32; m < waiting - done; m += 32) {
-                        const uint64_t k = m + lane < waiting - done ? mine[m + lane] : 0;
-                        __syncwarp();
-                        mine[m - 32 + lane] = k;
-                        __syncwarp();
-                    }
+                for (int j = 0; j < 8; j += 2) {
+                    float a, b;
+                    fma2(a, b, x[v].get(j), x[v].get(j + 1), kLog2e, kLog2e, r, r);
+                    add2(s0, s1, ex2(a), ex2(b));
                 }
             }
-            waiting -= done;
-        }
-    }
-    if (waiting > 0) flush(waiting);
-    // the warps' lists and sums
-#pragma unroll
-    for (int w = 16; w > 0; w /= 2) {
-        const float t = __shfl_xor_sync(0xffffffffu, top, w), s = __shfl_xor_sync(0xffffffffu, sum, w);
-        const float m = fmaxf(top, t);
-        sum = sum * ex2((top - m) * kLog2e) + s * ex2((t - m) * kLog2e);
-        top = m;
-    }
-    __syncthreads();
-    mine[lane] = list;
-    if (lane == 0) part[warp] = make_float2(top, sum);
-    __syncthreads();
+            sum = fmaf(s0 + s1, ex2(-fmaf(ref, kLog2e, r)), sum);
+        } else {
 #pragma unroll 1
-    for (int half = kScanWarps / 2; half > 0; half /= 2) {
-        if (warp < half) {
-            list = merge32(list, buf[warp + half][lane], lane);
-            mine[lane] = list;
-            if (lane == 0) {
-                const float2 a = part[warp], b = part[warp + half];
-                const float m = fmaxf(a.x, b.x);
-                part[warp] = make_float2(m, a.y * ex2((a.x - m) * kLog2e) + b.y * ex2((b.x - m) * kLog2e));
+            for (int v = 0; v < kAhead; ++v) {
+                const Eight<T, MODE> y = pick(x, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s0 += ex2((y.get(j) - ref) * kLog2e);
+            }
+            sum += s0;
+        }
+        if (base == begin) {
+            // k lanes have a logit at or above the k-th largest of the lanes' maxima, here of all of the CTA's lanes: of
+            // what comes after one in 500 exceeds it (k = 16)
+            best_of_warps(sort32(key_of(top, 0u), lane));
+            const uint64_t t = buf[0][p.k - 1];
+            const uint64_t least = (t & 0xFFFFFFFF00000000ull) - 1;
+            if (least > last) last = least, bound = key_logit(t);
+            __syncthreads();
+        }
+        if (!__any_sync(0xffffffffu, top >= bound)) continue;
+        // (rolled: four copies of this would not fit the instruction cache beside the rest)
+#pragma unroll 1
+        for (int v = 0; v < kAhead; ++v) {
+            float hv = high[0];
+#pragma unroll
+            for (int u = 1; u < kAhead; ++u) hv = v == u ? high[u] : hv;
+            if (!__any_sync(0xffffffffu, hv >= bound)) continue;
+            const Eight<T, MODE> y = pick(x, v);
+            const uint32_t token = (uint32_t)(at + v * kScanWarps * 256);
+            uint32_t hit = __ballot_sync(0xffffffffu, key_of(hv, token) > last);
+#pragma unroll 1
+            for (; hit; hit &= hit - 1) {
+                // this lane's eight, one to each of the first eight lanes
+                const int src = __ffs(hit) - 1;
+                Eight<T, MODE> z;
+#pragma unroll
+                for (int k = 0; k < y.kWords; ++k) z.w[k] = __shfl_sync(0xffffffffu, y.w[k], src);
+                float xj = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) xj = lane == j ? z.get(j) : xj;
+                const uint64_t key = key_of(xj, __shfl_sync(0xffffffffu, token, src) + lane);
+                const bool in = lane < 8 && xj >= bound && key > last;           // (a NaN is not)
+#pragma unroll 1
+                for (uint32_t who = __ballot_sync(0xffffffffu, in); who; who &= who - 1) {
+                    const uint64_t one = shfl64(key, __ffs(who) - 1), above = shfl_up64(list, 1);
+                    const int place = __popc(__ballot_sync(0xffffffffu, list > one));
+                    list = lane < place ? list : lane == place ? one : above;
+                }
+                const uint64_t kth = shfl64(list, p.k - 1);
+                if (kth > last) last = kth, bound = key_logit(kth);
             }
         }
-        __syncthreads();
     }
+    // the warps' lists and sums
+#pragma unroll
+    for (int w = 16; w > 0; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    if (lane == 0) part[warp] = make_float2(ref, sum);
+    best_of_warps(list);
     if (warp == 0) {
-        if (lane < p.k) p.keys[(int64_t)blockIdx.x * p.k + lane] = list;
-        if (lane == 0) p.sums[blockIdx.x] = part[0];
+        float2 all = part[0];
+        for (int w = 1; w < kScanWarps; ++w) {
+            const float2 b = part[w];
+            const float m = fmaxf(all.x, b.x);
+            all = make_float2(m, all.y * ex2((all.x - m) * kLog2e) + b.y * ex2((b.x - m) * kLog2e));
+        }
+        if (lane < p.k) p.keys[(int64_t)blockIdx.x * p.k + lane] = mine[lane];
+        if (lane == 0) p.sums[blockIdx.x] = all;
     }
 }
 
@@ -239,63 +344,88 @@ __device__ __forceinline__ Ranked merge_ranked(Ranked a, Ranked b, int lane) {
     return x;
 }
 
-// A CTA per group, a warp per beam.
-__global__ void __launch_bounds__(1024) beam_join_kernel(const BeamParams p) {
+// A CTA per group, `per` warps (a power of two) for each beam: they share its slices.
+__global__ void __launch_bounds__(1024) beam_join_kernel(const BeamParams p, int per) {
+    __shared__ uint64_t slots[32][32];
     __shared__ Ranked lists[kBeamMax][32];
     __shared__ uint32_t token_of[kBeamMax][32];
     __shared__ double norm[kBeamMax];                 // log of the row's sum; NaN: the row has no candidates
     __shared__ float2 total[kBeamMax];
-    const int lane = threadIdx.x & 31, b = threadIdx.x >> 5, g = blockIdx.x;
+    __shared__ float score_of[kBeamMax];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = warp / per, part = warp - b * per, g = blockIdx.x;
     const int row = g * p.W + b;
+    const float score_so_far = __ldg(p.scores + row);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     uint64_t list = key_floor();
     const uint64_t *keys = p.keys + (int64_t)row * p.slices * p.k;
-    for (int s = 0; s < p.slices; ++s) {
-        const uint64_t k = lane < p.k ? keys[s * p.k + lane] : key_floor();
-        list = s == 0 ? k : merge32(list, k, lane);
+    constexpr int kAhead = 4;                         // slices in flight
+    for (int s0 = part; s0 < p.slices; s0 += kAhead * per) {
+        uint64_t k[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            k[x] = s0 + x * per < p.slices && lane < p.k ? keys[(s0 + x * per) * p.k + lane] : key_floor();
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            if (s0 + x * per < p.slices) list = merge32(list, k[x], lane);
     }
     float top = kLowest, sum = 0.f;
-    for (int s = lane; s < p.slices; s += 32) {
-        const float2 x = p.sums[(int64_t)row * p.slices + s];
-        const float m = fmaxf(top, x.x);
-        sum = sum * ex2((top - m) * kLog2e) + x.y * ex2((x.x - m) * kLog2e);
-        top = m;
-    }
+    if (part == 0) {
+        for (int s = lane; s < p.slices; s += 32) {
+            const float2 x = p.sums[(int64_t)row * p.slices + s];
+            const float m = fmaxf(top, x.x);
+            sum = sum * ex2((top - m) * kLog2e) + x.y * ex2((x.x - m) * kLog2e);
+            top = m;
+        }
 #pragma unroll
-    for (int w = 16; w > 0; w /= 2) {
-        const float t = __shfl_xor_sync(0xffffffffu, top, w), s = __shfl_xor_sync(0xffffffffu, sum, w);
-        const float m = fmaxf(top, t);
-        sum = sum * ex2((top - m) * kLog2e) + s * ex2((t - m) * kLog2e);
-        top = m;
+        for (int w = 16; w > 0; w /= 2) {
+            const float t = __shfl_xor_sync(0xffffffffu, top, w), s = __shfl_xor_sync(0xffffffffu, sum, w);
+            const float m = fmaxf(top, t);
+            sum = sum * ex2((top - m) * kLog2e) + s * ex2((t - m) * kLog2e);
+            top = m;
+        }
     }
-    if (lane == 0) total[b] = make_float2(top, sum);
+    for (int half = per / 2; half > 0; half /= 2) {
+        if (part >= half && part < 2 * half) slots[warp][lane] = list;
+        __syncthreads();
+        if (part < half) list = merge32(list, slots[warp + half][lane], lane);
+    }
+    if (part == 0 && lane == 0) {
+        total[b] = make_float2(top, sum);
+        score_of[b] = score_so_far;
+    }
     __syncthreads();
-    if (b == 0 && lane < p.W) {
-        // the logarithms of all beams in one warp: 64-bit units are few
+    if (warp == 0 && lane < p.W) {
         const float2 x = total[lane];
-        const float score = __ldg(p.scores + (int64_t)g * p.W + lane);
+        const float score = score_of[lane];
         const bool some = x.y > 0.f && x.y < INFINITY;
         // a row of -inf alone and a score of -inf are masks, NaN and +inf mistakes
         if ((!some && !(x.y == 0.f)) || !(score < INFINITY)) record_error(p.err, ERR_RANGE | SRC_BEAM);
-        norm[lane] = some && score > -INFINITY && score < INFINITY ? (double)x.x + log((double)x.y)
-                                                                   : __longlong_as_double(0x7FF8000000000000ll);
+        // (the logarithm of the part in [0.7, 1.4) in fp32, off by 2^-25 and less; 64-bit units are few)
+        int e;
+        float m = frexpf(x.y, &e);
+        if (m < 0.70710678f) m *= 2.f, --e;
+        norm[lane] = some && score > -INFINITY && score < INFINITY
+                         ? (double)x.x + ((double)e * 0.69314718055994530942 + (double)logf(m))
+                         : __longlong_as_double(0x7FF8000000000000ll);
     }
     __syncthreads();
-    const double score = (double)__ldg(p.scores + row) + ((double)key_logit(list) - norm[b]);
+    const double score = (double)score_so_far + ((double)key_logit(list) - norm[b]);
     const bool real = list > key_floor() && norm[b] == norm[b];
     Ranked r = {real ? ordered(score) : 0ull, ~(uint32_t)(b * 32 + lane)};
-    lists[b][lane] = r;
-    token_of[b][lane] = key_token(list);
+    if (part == 0) {
+        lists[b][lane] = r;
+        token_of[b][lane] = key_token(list);
+    }
     __syncthreads();
     for (int n = p.W; n > 1; n = (n + 1) / 2) {
         const int half = (n + 1) / 2;
-        if (b + half < n) {
+        if (part == 0 && b + half < n) {
             r = merge_ranked(r, lists[b + half][lane], lane);
             lists[b][lane] = r;
         }
         __syncthreads();
     }
-    if (b == 0 && lane < p.k) {
+    if (warp == 0 && lane < p.k) {
         const uint32_t id = ~r.id;
         const bool some = r.score != 0;
         p.tokens[(int64_t)g * p.k + lane] = some ? (int32_t)token_of[id >> 5][id & 31] : -1;
@@ -420,8 +550,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kvcache_kernel(const CopyRo
 }  // namespace
 
 cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream) {
-    auto *scan = p.bf16 ? p.wide ? beam_scan_kernel<__nv_bfloat16, true> : beam_scan_kernel<__nv_bfloat16, false>
-                        : p.wide ? beam_scan_kernel<float, true> : beam_scan_kernel<float, false>;
+    auto *scan = p.bf16 ? p.wide ? beam_scan_kernel<__nv_bfloat16, 0> : beam_scan_kernel<__nv_bfloat16, 1>
+                        : p.wide ? beam_scan_kernel<float, 0> : beam_scan_kernel<float, 1>;
     main_kernel_event_before(stream);
     scan<<<(unsigned)(p.groups * p.W * p.slices), kScanWarps * 32, 0, stream>>>(p);
     main_kernel_event_after(stream);
@@ -429,14 +559,16 @@ cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.groups);
-    cfg.blockDim = dim3((unsigned)p.W * 32);
+    int per = 1;
+    while (per * 2 * p.W <= 32 && per * 2 <= p.slices) per *= 2;
+    cfg.blockDim = dim3((unsigned)(p.W * per) * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, beam_join_kernel, p);
+    return cudaLaunchKernelEx(&cfg, beam_join_kernel, p, per);
 }
 
 cudaError_t launch_beam_rows(const int32_t *parents, const int32_t *rows, int32_t *rows_out, int32_t *source,
