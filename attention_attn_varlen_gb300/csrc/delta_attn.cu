@@ -28,20 +28,22 @@ template <int LPR> __device__ __forceinline__ float row_sum(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// The recurrent form.  A lane holds four neighbouring columns of eight rows of S in
-// registers, a warp 32 lanes / (D / 4) times eight rows; S is read and written
-// once, whatever the number of tokens, 8 D^2 bytes per sequence and value head,
-// which bounds one token per sequence (HBM).
+// The recurrent form.  S stays in registers and is read and written once, whatever the
+// number of tokens, 8 D^2 bytes per sequence and value head, which bounds it (HBM).
 // With S k and S q of the state before the token,
 //   S_t q = e^g S q + u (k . q),
-// so one reduction per token serves u and the output.  The sums of the eight rows are
-// reduced together (9 shuffles), S k is then handed back to all lanes (7).
+// so one reduction per token serves u and the output.
+//
+// One token: a lane holds four neighbouring columns of eight rows, a warp 32 lanes / (D / 4) times eight
+// rows.  The sums of the eight rows are reduced together (9 shuffles), S k is
+// then handed back to all lanes (7).  PACKED: packed sequences of at most one token; a sequence
+// without one leaves its state as it was.  256 sequences, 32 heads of 128: 159 us, 6.8 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kRecRows = 8;
 constexpr int kRecWarps = 4;
 
 template <int D, bool PACKED>
-__global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(kRecWarps * 32, 5) delta_one_kernel(const DeltaParams p) {
     constexpr int LPR = D / 4;                          // lanes per row
     constexpr int RPL = 32 / LPR;                       // rows per load
     constexpr int ROWS = kRecRows * RPL;                // rows per warp
@@ -63,81 +65,203 @@ __global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const D
         S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (from) S[i] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + i) * D + col));
     }
-#pragma unroll 1
-    for (; n > 0; --n, ++t) {
-        const uint2 kr = *reinterpret_cast<const uint2 *>(p.k + t * p.k_stride + (int64_t)hk * D + col);
-        const uint2 qr = *reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (int64_t)hk * D + col);
-        const uint4 vr = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + (int64_t)h * D + row0);
-        const float beta = __ldg(p.beta + t * p.beta_stride + h);
-        const float a = delta_decay(p, t, h, first_thread);
-        const float k0 = __uint_as_float(kr.x << 16), k1 = __uint_as_float(kr.x & 0xFFFF0000u);
-        const float k2 = __uint_as_float(kr.y << 16), k3 = __uint_as_float(kr.y & 0xFFFF0000u);
-        const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
-        const float q2 = __uint_as_float(qr.y << 16), q3 = __uint_as_float(qr.y & 0xFFFF0000u);
-        float rk = 1.f, rq = 1.f;
+    const uint2 kr = *reinterpret_cast<const uint2 *>(p.k + t * p.k_stride + (int64_t)hk * D + col);
+    const uint2 qr = *reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (int64_t)hk * D + col);
+    const uint4 vr = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + (int64_t)h * D + row0);
+    const float beta = __ldg(p.beta + t * p.beta_stride + h);
+    const float a = delta_decay(p, t, h, first_thread);
+    const float k0 = __uint_as_float(kr.x << 16), k1 = __uint_as_float(kr.x & 0xFFFF0000u);
+    const float k2 = __uint_as_float(kr.y << 16), k3 = __uint_as_float(kr.y & 0xFFFF0000u);
+    const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
+    const float q2 = __uint_as_float(qr.y << 16), q3 = __uint_as_float(qr.y & 0xFFFF0000u);
+    float rk = 1.f, rq = 1.f;
+    if (p.norm) {
+        rk = 1.f / sqrtf(row_sum<LPR>(fmaf(k0, k0, fmaf(k1, k1, fmaf(k2, k2, k3 * k3)))) + p.eps);
+        rq = 1.f / sqrtf(row_sum<LPR>(fmaf(q0, q0, fmaf(q1, q1, fmaf(q2, q2, q3 * q3)))) + p.eps);
+    }
+    const float kq = row_sum<LPR>(fmaf(k0, q0, fmaf(k1, q1, fmaf(k2, q2, k3 * q3))));
+    float sk[kRecRows], sq[kRecRows];
+#pragma unroll
+    for (int i = 0; i < kRecRows; ++i) {
+        sk[i] = fmaf(S[i].x, k0, fmaf(S[i].y, k1, fmaf(S[i].z, k2, S[i].w * k3)));
+        sq[i] = fmaf(S[i].x, q0, fmaf(S[i].y, q1, fmaf(S[i].z, q2, S[i].w * q3)));
+    }
+    // each step halves the rows a lane carries: the lane's bits LPR / 2, LPR / 4, LPR / 8 pick the row
+    int w = LPR / 2;
+#pragma unroll
+    for (int m = kRecRows / 2; m > 0; m /= 2, w /= 2) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            sk[i] = (up ? sk[i + m] : sk[i]) + __shfl_xor_sync(0xffffffffu, up ? sk[i] : sk[i + m], w);
+            sq[i] = (up ? sq[i + m] : sq[i]) + __shfl_xor_sync(0xffffffffu, up ? sq[i] : sq[i + m], w);
+        }
+    }
+#pragma unroll
+    for (; w > 0; w /= 2) {
+        sk[0] += __shfl_xor_sync(0xffffffffu, sk[0], w);
+        sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], w);
+    }
+    w = LPR / 8;
+#pragma unroll
+    for (int m = 1; m < kRecRows; m *= 2, w *= 2) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, sk[i], w);
+            sk[i + m] = up ? sk[i] : other;
+            sk[i] = up ? other : sk[i];
+        }
+    }
+    const uint32_t vw[4] = {vr.x, vr.y, vr.z, vr.w};
+    const float ark = a * rk;
+    float u[kRecRows];
+#pragma unroll
+    for (int i = 0; i < kRecRows; ++i) {
+        const float v = __uint_as_float(i & 1 ? vw[i / 2] & 0xFFFF0000u : vw[i / 2] << 16);
+        u[i] = beta * (v - ark * sk[i]);
+        const float uk = u[i] * rk;
+        S[i].x = fmaf(uk, k0, a * S[i].x);
+        S[i].y = fmaf(uk, k1, a * S[i].y);
+        S[i].z = fmaf(uk, k2, a * S[i].z);
+        S[i].w = fmaf(uk, k3, a * S[i].w);
+        if (state) __stcs(reinterpret_cast<float4 *>(state + (row0 + i) * D + col), S[i]);
+    }
+    // the row whose sum the lane holds
+    const int row = (lane & (LPR - 1)) / (LPR / 8);
+    float own = u[0];
+#pragma unroll
+    for (int i = 1; i < kRecRows; ++i) own = row == i ? u[i] : own;
+    if ((lane & (LPR / 8 - 1)) == 0)
+        p.out[t * p.out_stride + (int64_t)h * D + row0 + row] =
+            __float2bfloat16_rn(p.scale * rq * fmaf(own * rk, kq, a * sq[0]));
+}
+
+// Two to kDeltaShort tokens.  Here the instructions of the tokens count as well, so what the rows of a state share
+// is prepared once per CTA (decay, k . q, the normalised k and q in fp32), a lane has eight columns of
+// four rows (fewer shuffles and choices among rows per product), and products go in pairs.  64 sequences of 5 tokens,
+// 32 heads of 128: 80 us with the one-token kernel's layout and loop.
+template <int D>
+__global__ void __launch_bounds__(kRecWarps * 32, 5) delta_few_kernel(const DeltaParams p) {
+    constexpr int LPR = D / 8, ROWS = 4 * 32 / LPR;     // lanes per row; rows per warp
+    constexpr int CTAS = D / (ROWS * kRecWarps);        // CTAs per state
+    constexpr int OWN = ROWS * kRecWarps;               // rows of a CTA
+    __shared__ float4 k_s[kDeltaShort][D / 4], q_s[kDeltaShort][D / 4], v_s[kDeltaShort][OWN / 4];
+    __shared__ float4 token[kDeltaShort];               // e^g, k . q, beta
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.x / CTAS, b = unit / p.Hv, h = unit - b * p.Hv, hk = h / p.G;
+    const int cta_row = (blockIdx.x - unit * CTAS) * OWN, l = lane & (LPR - 1), own4 = warp * (ROWS / 4) + lane / LPR;
+    const int row0 = cta_row + own4 * 4;
+    const bool first_cta = cta_row == 0, report = h == 0 && first_cta && threadIdx.x == 0;
+    int64_t t0;
+    int n;
+    sequence_rows<SRC_DELTA>(p, b, t0, n, report);
+    bool from;
+    float *state = sequence_state<SRC_DELTA, true>(p, p.Hv, b, h, from, report && n > 0);
+    if (n == 0) return;
+    float4 S[4][2];                                     // columns 4 l .. and D / 2 + 4 l ..
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            S[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (from) S[i][c] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + i) * D + c * (D / 2)) + l);
+        }
+    }
+    for (int i = warp; i < n; i += kRecWarps) {
+        const int64_t t = t0 + i;
+        const int c = lane & (D / 4 - 1);               // four columns a lane
+        const uint2 kr = *(reinterpret_cast<const uint2 *>(p.k + t * p.k_stride + (int64_t)hk * D) + c);
+        const uint2 qr = *(reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (int64_t)hk * D) + c);
+        float4 k = make_float4(__uint_as_float(kr.x << 16), __uint_as_float(kr.x & 0xFFFF0000u),
+                               __uint_as_float(kr.y << 16), __uint_as_float(kr.y & 0xFFFF0000u));
+        float4 q = make_float4(__uint_as_float(qr.x << 16), __uint_as_float(qr.x & 0xFFFF0000u),
+                               __uint_as_float(qr.y << 16), __uint_as_float(qr.y & 0xFFFF0000u));
+        float rk = 1.f, rq = p.scale;
         if (p.norm) {
-            rk = 1.f / sqrtf(row_sum<LPR>(fmaf(k0, k0, fmaf(k1, k1, fmaf(k2, k2, k3 * k3)))) + p.eps);
-            rq = 1.f / sqrtf(row_sum<LPR>(fmaf(q0, q0, fmaf(q1, q1, fmaf(q2, q2, q3 * q3)))) + p.eps);
+            rk = 1.f / sqrtf(row_sum<D / 4>(fmaf(k.x, k.x, fmaf(k.y, k.y, fmaf(k.z, k.z, k.w * k.w)))) + p.eps);
+            rq = p.scale / sqrtf(row_sum<D / 4>(fmaf(q.x, q.x, fmaf(q.y, q.y, fmaf(q.z, q.z, q.w * q.w)))) + p.eps);
         }
-        const float kq = row_sum<LPR>(fmaf(k0, q0, fmaf(k1, q1, fmaf(k2, q2, k3 * q3))));
-        float sk[kRecRows], sq[kRecRows];
+        k.x *= rk, k.y *= rk, k.z *= rk, k.w *= rk;
+        q.x *= rq, q.y *= rq, q.z *= rq, q.w *= rq;
+        const float kq = row_sum<D / 4>(fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, k.w * q.w))));
+        const float a = delta_decay(p, t, h, first_cta && lane == 0), beta = __ldg(p.beta + t * p.beta_stride + h);
+        if (lane < D / 4) k_s[i][c] = k, q_s[i][c] = q;
 #pragma unroll
-        for (int i = 0; i < kRecRows; ++i) {
-            sk[i] = fmaf(S[i].x, k0, fmaf(S[i].y, k1, fmaf(S[i].z, k2, S[i].w * k3)));
-            sq[i] = fmaf(S[i].x, q0, fmaf(S[i].y, q1, fmaf(S[i].z, q2, S[i].w * q3)));
+        for (int x = lane; x < OWN; x += 32)
+            reinterpret_cast<float *>(v_s[i])[x] = __bfloat162float(p.v[t * p.v_stride + (int64_t)h * D + cta_row + x]);
+        if (lane == 0) token[i] = make_float4(a, kq, beta, 0.f);
+    }
+    __syncthreads();
+    __nv_bfloat16 *out = p.out + t0 * p.out_stride + (int64_t)h * D + row0;
+    const bool up0 = lane & (LPR / 2), up1 = lane & (LPR / 4);
+    // the row whose sum the lane comes to hold
+    const int row = 2 * up0 + up1;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, out += p.out_stride) {
+        const float4 k0 = k_s[i][l], k1 = k_s[i][D / 8 + l], q0 = q_s[i][l], q1 = q_s[i][D / 8 + l];
+        const float4 x = token[i], v4 = v_s[i][own4];
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        float sk[4], sq[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float c, d;
+            fma2(c, d, S[r][0].x, S[r][0].y, k0.x, k0.y, 0.f, 0.f);
+            fma2(c, d, S[r][0].z, S[r][0].w, k0.z, k0.w, c, d);
+            fma2(c, d, S[r][1].x, S[r][1].y, k1.x, k1.y, c, d);
+            fma2(c, d, S[r][1].z, S[r][1].w, k1.z, k1.w, c, d);
+            sk[r] = c + d;
+            fma2(c, d, S[r][0].x, S[r][0].y, q0.x, q0.y, 0.f, 0.f);
+            fma2(c, d, S[r][0].z, S[r][0].w, q0.z, q0.w, c, d);
+            fma2(c, d, S[r][1].x, S[r][1].y, q1.x, q1.y, c, d);
+            fma2(c, d, S[r][1].z, S[r][1].w, q1.z, q1.w, c, d);
+            sq[r] = c + d;
         }
-        // each step halves the rows a lane carries: the lane's bits LPR / 2, LPR / 4, LPR / 8 pick the row
-        int w = LPR / 2;
+        // two steps halve the rows a lane carries, the others add up; then S k goes back to all lanes of a row
 #pragma unroll
-        for (int m = kRecRows / 2; m > 0; m /= 2, w /= 2) {
-            const bool up = lane & w;
-#pragma unroll
-            for (int i = 0; i < m; ++i) {
-                sk[i] = (up ? sk[i + m] : sk[i]) + __shfl_xor_sync(0xffffffffu, up ? sk[i] : sk[i + m], w);
-                sq[i] = (up ? sq[i + m] : sq[i]) + __shfl_xor_sync(0xffffffffu, up ? sq[i] : sq[i + m], w);
-            }
+        for (int r = 0; r < 2; ++r) {
+            sk[r] = (up0 ? sk[r + 2] : sk[r]) + __shfl_xor_sync(0xffffffffu, up0 ? sk[r] : sk[r + 2], LPR / 2);
+            sq[r] = (up0 ? sq[r + 2] : sq[r]) + __shfl_xor_sync(0xffffffffu, up0 ? sq[r] : sq[r + 2], LPR / 2);
         }
+        sk[0] = (up1 ? sk[1] : sk[0]) + __shfl_xor_sync(0xffffffffu, up1 ? sk[0] : sk[1], LPR / 4);
+        sq[0] = (up1 ? sq[1] : sq[0]) + __shfl_xor_sync(0xffffffffu, up1 ? sq[0] : sq[1], LPR / 4);
 #pragma unroll
-        for (; w > 0; w /= 2) {
+        for (int w = LPR / 8; w > 0; w /= 2) {
             sk[0] += __shfl_xor_sync(0xffffffffu, sk[0], w);
             sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], w);
         }
-        w = LPR / 8;
+        const float mine = sk[0], y = __shfl_xor_sync(0xffffffffu, mine, LPR / 4);
+        sk[0] = up1 ? y : mine;
+        sk[1] = up1 ? mine : y;
+        const float y0 = __shfl_xor_sync(0xffffffffu, sk[0], LPR / 2), y1 = __shfl_xor_sync(0xffffffffu, sk[1], LPR / 2);
+        sk[2] = up0 ? sk[0] : y0;
+        sk[3] = up0 ? sk[1] : y1;
+        sk[0] = up0 ? y0 : sk[0];
+        sk[1] = up0 ? y1 : sk[1];
+        float own = 0.f;
 #pragma unroll
-        for (int m = 1; m < kRecRows; m *= 2, w *= 2) {
-            const bool up = lane & w;
+        for (int r = 0; r < 4; ++r) {
+            const float u = x.z * (v[r] - x.x * sk[r]);
+            own = row == r ? u : own;
 #pragma unroll
-            for (int i = 0; i < m; ++i) {
-                const float other = __shfl_xor_sync(0xffffffffu, sk[i], w);
-                sk[i + m] = up ? sk[i] : other;
-                sk[i] = up ? other : sk[i];
+            for (int c = 0; c < 2; ++c) {
+                const float4 k = c ? k1 : k0;
+                float4 z;
+                fma2(z.x, z.y, x.x, x.x, S[r][c].x, S[r][c].y, 0.f, 0.f);
+                fma2(z.z, z.w, x.x, x.x, S[r][c].z, S[r][c].w, 0.f, 0.f);
+                fma2(S[r][c].x, S[r][c].y, u, u, k.x, k.y, z.x, z.y);
+                fma2(S[r][c].z, S[r][c].w, u, u, k.z, k.w, z.z, z.w);
             }
         }
-        const uint32_t vw[4] = {vr.x, vr.y, vr.z, vr.w};
-        const float ark = a * rk;
-        float u[kRecRows];
-#pragma unroll
-        for (int i = 0; i < kRecRows; ++i) {
-            const float v = __uint_as_float(i & 1 ? vw[i / 2] & 0xFFFF0000u : vw[i / 2] << 16);
-            u[i] = beta * (v - ark * sk[i]);
-            const float uk = u[i] * rk;
-            S[i].x = fmaf(uk, k0, a * S[i].x);
-            S[i].y = fmaf(uk, k1, a * S[i].y);
-            S[i].z = fmaf(uk, k2, a * S[i].z);
-            S[i].w = fmaf(uk, k3, a * S[i].w);
-        }
-        // the row whose sum the lane holds
-        const int row = (lane & (LPR - 1)) / (LPR / 8);
-        float own = u[0];
-#pragma unroll
-        for (int i = 1; i < kRecRows; ++i) own = row == i ? u[i] : own;
-        if ((lane & (LPR / 8 - 1)) == 0)
-            p.out[t * p.out_stride + (int64_t)h * D + row0 + row] =
-                __float2bfloat16_rn(p.scale * rq * fmaf(own * rk, kq, a * sq[0]));
+        if ((lane & (LPR / 4 - 1)) == 0) out[row] = __float2bfloat16_rn(fmaf(own, x.y, x.x * sq[0]));
     }
     if (state) {
 #pragma unroll
-        for (int i = 0; i < kRecRows; ++i) __stcs(reinterpret_cast<float4 *>(state + (row0 + i) * D + col), S[i]);
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                __stcs(reinterpret_cast<float4 *>(state + (row0 + i) * D + c * (D / 2)) + l, S[i][c]);
+        }
     }
 }
 
@@ -1170,8 +1294,9 @@ cudaError_t launch_delta_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap
 
 cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream) {
     const int64_t states = (int64_t)p.batch * p.Hv;
-    auto *kernel = p.D == 128 ? p.cu ? delta_recurrent_kernel<128, true> : delta_recurrent_kernel<128, false>
-                              : p.cu ? delta_recurrent_kernel<64, true> : delta_recurrent_kernel<64, false>;
+    auto *kernel = p.max_seqlen > 1 ? p.D == 128 ? delta_few_kernel<128> : delta_few_kernel<64>
+                   : p.D == 128     ? p.cu ? delta_one_kernel<128, true> : delta_one_kernel<128, false>
+                                    : p.cu ? delta_one_kernel<64, true> : delta_one_kernel<64, false>;
     main_kernel_event_before(stream);
     kernel<<<(unsigned)(p.D == 128 ? states * 4 : states), kRecWarps * 32, 0, stream>>>(p);
     main_kernel_event_after(stream);
