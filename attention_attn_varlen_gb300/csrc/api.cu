@@ -1344,13 +1344,46 @@ static bool delta_sizes(int batch, int64_t total_tokens, int num_heads_k, int nu
            (head_dim == 64 || head_dim == 128) && (int64_t)batch * num_heads_v * 4 <= (int64_t)INT32_MAX;
 }
 
+// Segments of the prompt form, as for linear attention (linear_seg_len).  Here a segment's state is a linear
+// function of the one it starts from, so the pass before has two states per segment to find, what the segment makes of a
+// zero state and of the identity: about twice the main pass's time for the cut sequences, which pays from four segments on.
+static int delta_seg_len(int64_t total_tokens, int num_heads_v, int max_seqlen) {
+    const int64_t whole = round64(max_seqlen > 0 ? max_seqlen : 1);
+    int64_t share = total_tokens * num_heads_v / kLinearSms;
+    if (share < 1) share = 1;
+    const int64_t n = max_seqlen / share;
+    if (n < 4) return (int)whole;
+    int64_t seg = round64((max_seqlen + n - 1) / n);
+    if (seg < 512) seg = 512;
+    return max_seqlen > seg + 2 * share + 1024 ? (int)seg : (int)whole;
+}
+
+struct DeltaLayout {
+    int seg_len, max_units, state_rows;
+    size_t units, states, bytes;
+};
+static DeltaLayout delta_layout(int batch, int64_t total_tokens, int num_heads_v, int head_dim, int max_seqlen) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    DeltaLayout l;
+    l.seg_len = delta_seg_len(total_tokens, num_heads_v, max_seqlen);
+    const bool split = l.seg_len < max_seqlen;
+    // each segment beyond a sequence's first stands for at least a fair share of the tokens
+    const int extra = split ? kLinearSms / num_heads_v + 1 : 0;
+    l.max_units = batch + extra;
+    l.state_rows = 2 * extra;
+    l.units = 256;   // the count in front
+    l.states = l.units + up((size_t)kDeltaUnitBytes * l.max_units);
+    l.bytes = l.states + sizeof(float) * 2 * l.state_rows * num_heads_v * head_dim * head_dim;
+    return l;
+}
+
 extern "C" {
 
 size_t attn_delta_workspace_size(int batch, int64_t total_tokens, int num_heads_k, int num_heads_v, int head_dim,
                                  int max_seqlen) {
     if (!delta_sizes(batch, total_tokens, num_heads_k, num_heads_v, head_dim) || max_seqlen < 0) return 0;
     if (max_seqlen <= kDeltaShort) return 0;
-    return 256 + (size_t)kDeltaUnitBytes * batch;   // the count in front
+    return delta_layout(batch, total_tokens, num_heads_v, head_dim, max_seqlen).bytes;
 }
 
 }  // extern "C"
@@ -1438,8 +1471,15 @@ attn_status attn_delta_fwd(const void *q, const void *k, const void *v, void *ou
     p.err = d->err;
     if (max_seqlen <= kDeltaShort) return launched(launch_delta_recurrent(p, reinterpret_cast<cudaStream_t>(stream)));
     p.num_sms = d->num_sms;
-    p.unit_count = reinterpret_cast<int *>(workspace);
-    p.units = reinterpret_cast<char *>(workspace) + 256;
+    const DeltaLayout l = delta_layout(batch, total_tokens, num_heads_v, head_dim, max_seqlen);
+    char *ws = reinterpret_cast<char *>(workspace);
+    p.seg_len = l.seg_len;
+    p.max_units = l.max_units;
+    p.state_rows = l.state_rows;
+    p.unit_count = reinterpret_cast<int *>(ws);
+    p.units = ws + l.units;
+    p.states = reinterpret_cast<float *>(ws + l.states);
+    if ((int64_t)p.max_units * 2 * num_heads_v > (int64_t)INT32_MAX) return ATTN_ERR_UNSUPPORTED;
     CUtensorMap qmap, kmap, vmap, omap;
     if (!make_map(&qmap, q, total_tokens, num_heads_k, head_dim, p.q_stride, 1, 64) ||
         !make_map(&kmap, k, total_tokens, num_heads_k, head_dim, p.k_stride, 1, 64) ||

@@ -319,11 +319,12 @@ constexpr int kDeltaBuckets = 256;
 // A chunk as its roles read it, behind its tables.
 struct DeltaChunk {
     int n;                            // tokens; 0: there is no such chunk
-    int t0, h, first, last;           // first row; head; whether the unit starts or ends with it
-    int slot, from;                   // state slot (-1: none), whether the unit starts from it
+    int t0, h, first;                 // first row; head; whether the unit starts with it
     float a, a_lo;                    // e^{G_n} in two parts
     int bad;                          // the first token whose row of A is not finite
-    int unused[6];
+    int ident;                        // the unit starts from the identity and has no values
+    const float *src;                 // first chunk: the unit's state (null: zero, or the identity)
+    float *dst;                       // last chunk: where the state goes (null: nowhere)
 };
 
 template <int D>
@@ -344,7 +345,7 @@ struct DeltaSmem {
     static constexpr int kBarOff = kBadOff + 2 * 128 * 4;
     static constexpr int kNumBars = 30;
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 32 + 1024 /* alignment slack */;
-    static_assert(kBytes <= 227 * 1024 && sizeof(DeltaChunk) == 64, "shared memory");
+    static_assert(kBytes <= 227 * 1024 && sizeof(DeltaChunk) <= 64, "shared memory");
     // scratch of the solve, where T goes in the end
     static_assert((DC + 32) * kXStride * 4 <= 3 * kDeltaPanel, "scratch");
 };
@@ -358,32 +359,55 @@ static_assert(4 * kChainRegs + 2 * kSolveRegs + kRowRegs + kOtherRegs == 8 * 64,
 struct alignas(16) DeltaUnit {
     int t0, n;          // first token, tokens
     int slot, from;     // state slot (-1: none), whether the sequence starts from it
+    int row;            // its place among the workspace's states (-1: none)
+    int last, more;     // holds the sequence's last token; has a successor
+    int head;           // first segment: the sequence's segments, else 0
 };
 static_assert(sizeof(DeltaUnit) == kDeltaUnitBytes, "workspace layout");
 
-// The work list: a unit is a sequence; the longest come first.
+// The work list: a unit is a sequence, or a segment of seg_len tokens of a longer one; the longest come first.
 __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x;
-    __shared__ int count[kDeltaBuckets];
+    __shared__ int count[kDeltaBuckets], rows_s;
     for (int i = tid; i < kDeltaBuckets; i += 1024) count[i] = 0;
+    if (tid == 0) rows_s = 0;
     __syncthreads();
-    auto bucket = [&](int tokens) {
-        return kDeltaBuckets - 1 - (int)((int64_t)tokens * (kDeltaBuckets - 1) / p.max_seqlen);
-    };
+    const int most = max(1, min(p.seg_len, p.max_seqlen));
+    auto bucket = [&](int tokens) { return kDeltaBuckets - 1 - (int)((int64_t)tokens * (kDeltaBuckets - 1) / most); };
     for (int pass = 0; pass < 2; ++pass) {
         for (int b = tid; b < p.batch; b += 1024) {
             int64_t t0;
             int n;
             sequence_rows<SRC_DELTA>(p, b, t0, n, pass == 0);
             if (n == 0) continue;
-            const int at = atomicAdd(&count[bucket(n)], 1);
-            if (pass == 1) {
-                bool from;
-                const float *state = sequence_state<SRC_DELTA, true>(p, p.Hv, b, 0, from, true);
-                reinterpret_cast<DeltaUnit *>(p.units)[at] =
-                    DeltaUnit{(int)t0, n, state ? __ldg(p.slots + b) : -1, from};
+            const int segs = (n + p.seg_len - 1) / p.seg_len, tail = n - (segs - 1) * p.seg_len;
+            if (pass == 0) {
+                if (segs > 1) atomicAdd(&count[bucket(p.seg_len)], segs - 1);
+                atomicAdd(&count[bucket(tail)], 1);
+                continue;
             }
+            bool from;
+            const float *state = sequence_state<SRC_DELTA, true>(p, p.Hv, b, 0, from, true);
+            const int slot = state ? __ldg(p.slots + b) : -1;
+            int row = segs > 1 ? atomicAdd(&rows_s, segs) : -1;
+            // offsets that overlap can ask for more than the workspace was sized for
+            bool fits = row + segs <= p.state_rows || segs == 1;
+            if (!fits) row = -1;
+            for (int i = 0; i < segs; ++i) {
+                const bool end = i == segs - 1;
+                const int at = atomicAdd(&count[bucket(end ? tail : p.seg_len)], 1);
+                if (at < p.max_units && (row >= 0 || segs == 1))
+                    reinterpret_cast<DeltaUnit *>(p.units)[at] =
+                        DeltaUnit{(int)t0 + i * p.seg_len, end ? tail : p.seg_len, slot, from, row < 0 ? -1 : row + i, end,
+                                  !end, i == 0 ? segs : 0};
+                else {
+                    fits = false;
+                    // (left out: an entry without tokens)
+                    if (at < p.max_units) reinterpret_cast<DeltaUnit *>(p.units)[at] = DeltaUnit{0, 0, -1, 0, -1, 0, 0, 0};
+                }
+            }
+            if (!fits) record_error(p.err, ERR_INDEX | SRC_DELTA);
         }
         __syncthreads();
         if (pass == 0 && tid < 32) {
@@ -400,9 +424,54 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaParams p) {
                 count[i + tid] = base + inc - c;
                 base += __shfl_sync(0xffffffffu, inc, 31);
             }
-            if (tid == 0) *p.unit_count = base;
+            if (tid == 0) *p.unit_count = min(base, p.max_units);
         }
         __syncthreads();
+    }
+}
+
+// The states at the starts of a sequence's segments, in place of what the segments make of a zero state
+// (`own`): with `turn` what they make of the identity,
+//   start_0 = the cached state or 0,  start_{s+1} = start_s turn_s + own_s.
+// A CTA has 16 rows of a head's state: rows do not meet.
+template <int D>
+__global__ void __launch_bounds__(256) delta_join_kernel(const DeltaParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if ((int)blockIdx.x >= *p.unit_count) return;
+    const DeltaUnit e = reinterpret_cast<const DeltaUnit *>(p.units)[blockIdx.x];
+    if (e.head == 0 || e.row < 0) return;
+    constexpr int ROWS = 16 * D / 256;                  // of a thread, one column
+    __shared__ float4 start[16][D / 4];
+    const int h = blockIdx.y, col = threadIdx.x & (D - 1), r0 = threadIdx.x / D * ROWS;
+    const int64_t step = (int64_t)p.Hv * D * D;
+    float *own = p.states + ((int64_t)e.row * p.Hv + h) * D * D + (blockIdx.z * 16 + r0) * D + col;
+    const float *turn = p.states + ((int64_t)(p.state_rows + e.row) * p.Hv + h) * D * D + col;
+    float run[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+        run[r] = e.from ? p.state[((int64_t)e.slot * p.Hv + h) * D * D + (blockIdx.z * 16 + r0 + r) * D + col] : 0.f;
+    for (int s = 0;; ++s, own += step, turn += step) {
+        float next[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (s + 1 < e.head) next[r] = own[r * D];
+            own[r * D] = run[r];
+            reinterpret_cast<float *>(start[r0 + r])[col] = run[r];
+        }
+        if (s + 1 == e.head) break;
+        __syncthreads();
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) {
+            const float m0 = turn[k * D], m1 = turn[(k + 1) * D], m2 = turn[(k + 2) * D], m3 = turn[(k + 3) * D];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const float4 x = start[r0 + r][k / 4];
+                next[r] = fmaf(x.x, m0, fmaf(x.y, m1, fmaf(x.z, m2, fmaf(x.w, m3, next[r]))));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) run[r] = next[r];
     }
 }
 
@@ -444,26 +513,29 @@ __device__ __forceinline__ int renew(int x) {
 struct DeltaWalk {
     int heads, units_n, up_q, up_r, down_q, down_r;      // to the next place: unit and head
     int at, hd, place;                                   // the next unit's
-    int left, row, h, slot, from;                        // this chunk on: tokens of its unit, first row, head, state
+    int left, row, h;                                    // this chunk on: tokens of its unit, first row, head
+    const DeltaUnit *unit;                               // its unit
     bool first;
     __device__ __forceinline__ DeltaWalk(int units_n, int heads) : heads(heads), units_n(units_n) {
         const int up = 2 * ((int)gridDim.x - 1 - (int)blockIdx.x) + 1, down = 2 * (int)blockIdx.x + 1;
         up_q = up / heads, up_r = up - up_q * heads, down_q = down / heads, down_r = down - down_q * heads;
         at = (int)blockIdx.x / heads, hd = (int)blockIdx.x - at * heads, place = left = 0;
     }
-    // to the next chunk; its tokens, 0: there is none
-    __device__ __forceinline__ int step(const DeltaUnit *units) {
+    // to the next chunk (local: of the units that have a successor alone); its tokens, 0: there is none
+    __device__ __forceinline__ int step(const DeltaUnit *units, bool local) {
         if (left > DC) {
             left -= DC, row += DC, first = false;
-        } else if (at < units_n) {
-            const DeltaUnit u = units[at];
-            left = u.n, row = u.t0, slot = u.slot, from = u.from, h = hd, first = true;
+            return min(left, DC);
+        }
+        left = 0;
+        while (left == 0 && at < units_n) {
+            unit = units + at;
+            if (!local || unit->more) left = unit->n;
+            row = unit->t0, h = hd, first = true;
             at += place & 1 ? down_q : up_q;
             hd += place & 1 ? down_r : up_r;
             if (hd >= heads) hd -= heads, ++at;
             ++place;
-        } else {
-            left = 0;
         }
         return min(left, DC);
     }
@@ -481,7 +553,9 @@ __device__ __forceinline__ int drop_non_finite(float (&x)[16]) {
     return first;
 }
 
-template <int D>
+// LOCAL: the pass over the segments that have a successor, without outputs: what each makes of a zero state
+// (heads 0 .. Hv - 1) and of the identity without values (heads Hv ..) goes to the workspace.
+template <int D, bool LOCAL>
 __global__ void __launch_bounds__(kDeltaThreads, 1)
     delta_chunk_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
@@ -495,8 +569,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const DeltaUnit *units = reinterpret_cast<const DeltaUnit *>(p.units);
-    const int units_n = uni(*p.unit_count);
-    if ((int)blockIdx.x >= units_n * p.Hv) return;
+    const int units_n = uni(*p.unit_count), heads = LOCAL ? 2 * p.Hv : p.Hv;
+    if ((int)blockIdx.x >= units_n * heads) return;
 
     const uint32_t smb = (smem_u32(dsmem_raw) + 1023u) & ~1023u;          // shared-memory address, for descriptors
     uint8_t *sm = dsmem_raw + (smb - smem_u32(dsmem_raw));
@@ -605,7 +679,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     role_wait(0, &v_full[gc & 1], gc >> 1);
                     role_wait(0, &norms[gc & 1], gc >> 1);
                     role_wait(0, kq_read, gc);
-                    if (gc > 0) role_wait(0, &o_done[(gc - 1) & 1], (gc - 1) >> 1);
+                    if (!LOCAL && gc > 0) role_wait(0, &o_done[(gc - 1) & 1], (gc - 1) >> 1);
                 }
             }
             role_sync(0, 512);
@@ -615,12 +689,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, part = tid >> 7, dv = tid & 127;
                 const DeltaChunk *info = info_of(tab_i);
                 if (info->first) {
-                    const float *own = p.state + ((int64_t)info->slot * p.Hv + info->h) * D * D + dv * D + part * N;
-                    const bool some = info->from && info->slot >= 0 && real;
+                    const float *src = info->src;
+                    const int one = LOCAL && info->ident ? dv - part * N : -1;       // the column of the identity's 1
 #pragma unroll
                     for (int i = 0; i < N; i += 4) {
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (some) x = *reinterpret_cast<const float4 *>(own + i);
+                        float4 x = make_float4(one == i, one == i + 1, one == i + 2, one == i + 3);
+                        if (!LOCAL && src && real) x = *reinterpret_cast<const float4 *>(src + dv * D + part * N + i);
                         St[i] = x.x, St[i + 1] = x.y, St[i + 2] = x.z, St[i + 3] = x.w;
                     }
                 }
@@ -673,6 +747,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                 asm("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at + (j + k) * 128 + (ch ^ (((j + k) & 7) << 4))));
                                 v[k] = __uint_as_float((uint32_t)r << 16);
                             }
+                            if (LOCAL && info_of(tab_i)->ident) v[0] = v[1] = v[2] = v[3] = 0.f;
                             fma2(x[j], x[j + 1], b.x, b.y, v[0], v[1], 0.f, 0.f);
                             fma2(x[j + 2], x[j + 3], b.z, b.w, v[2], v[3], 0.f, 0.f);
                         }
@@ -695,14 +770,16 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     }
                     uint32_t r1[8], r2[8], r3[8];
                     if (pass) {
+                        if (!LOCAL) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float y0, y1;
-                            r1[k] = take_bf16(y0, y1, x[2 * k], x[2 * k + 1]);
-                            r2[k] = pack_bf16x2(y0, y1);
+                            for (int k = 0; k < 8; ++k) {
+                                float y0, y1;
+                                r1[k] = take_bf16(y0, y1, x[2 * k], x[2 * k + 1]);
+                                r2[k] = pack_bf16x2(y0, y1);
+                            }
+                            tmem_st8(lane_base + TM_UO + part * 8, r1);
+                            tmem_st8(lane_base + TM_UO + 32 + part * 8, r2);
                         }
-                        tmem_st8(lane_base + TM_UO + part * 8, r1);
-                        tmem_st8(lane_base + TM_UO + 32 + part * 8, r2);
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 w = *reinterpret_cast<const float4 *>(tab + T_W + j);
@@ -743,11 +820,10 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         fma2(St[i + k], St[i + k + 1], a, a, St[i + k], St[i + k + 1], x0, x1);
                     }
                 }
-                if (info->last && info->slot >= 0) {
-                    float *own = p.state + ((int64_t)info->slot * p.Hv + info->h) * D * D + dv * D + part * N;
+                if (float *dst = info->dst) {
 #pragma unroll
                     for (int i = 0; i < N; i += 4)
-                        *reinterpret_cast<float4 *>(own + i) = make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
+                        *reinterpret_cast<float4 *>(dst + dv * D + part * N + i) = make_float4(St[i], St[i + 1], St[i + 2], St[i + 3]);
                 }
             }
             tc_fence_before();
@@ -775,7 +851,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             tc_fence_after();
             const int n = uni(info_of(tab_i)->n);
             if (n == 0 || stop[1]) break;
-            {
+            if (LOCAL && !keys) {
+                arrive(kq_read);             // no P
+            } else {
                 const int i = (qd & 1) * 32 + renew(lane);
                 const float *tab = tab_of(tab_i);
                 const float ghi = tab[T_GHI + i], glo = tab[T_GLO + i], factor = tab[(keys ? T_BETA : T_P) + i];
@@ -941,7 +1019,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             if (grp == 0) {
                 role_wait(2, &tab_full[tab_i], turn);
                 const int n = info_of(tab_i)->n;
-                if (n) role_wait(2, &qk_full[gc % QS], gc / QS);
+                if (n) role_wait(2, &qk_full[gc % QS], gc / QS);       // (LOCAL: K alone)
                 if (n && n < DC) role_wait(2, &v_full[gc & 1], gc >> 1);
             }
             role_sync(2, 128);
@@ -967,7 +1045,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     fence_proxy_async_smem();
                 }
                 float r = 1.f;
-                if (p.norm) {
+                if (p.norm && (!LOCAL || keys)) {
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll 2
                     for (int x = 0; x < PAN * 8; ++x) {
@@ -990,8 +1068,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 tab[(keys ? T_C : T_F) + i] = (keys ? -second : second) * tab[T_GAM + i];
                 arrive(&norms[gc & 1]);
                 arrive(&qk_empty[s]);
+                if (LOCAL) arrive(&tab_free[tab_i]);
             }
-            if (gc > 0) {
+            if (!LOCAL && gc > 0) {
                 // ---- outputs of the one before
                 const int oc = gc - 1;
                 const DeltaChunk *info = info_of(last_tab);
@@ -1062,21 +1141,22 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         fewer_regs<kOtherRegs>();
         if (warp == 28) {
             // ============================================================ loads
-            DeltaWalk walk(units_n, p.Hv);
+            DeltaWalk walk(units_n, heads);
             // x / y of x < 2^18: off by less than 2^-20 of itself, and half a step away from the next integer
             const float inv_g = __fdividef(1.f, (float)p.G);
             int gc = 0, qk_gone = 0;
 #pragma unroll 1
-            while (walk.step(units)) {
-                const int s = gc % QS, hk = (int)(((float)walk.h + 0.5f) * inv_g);
+            while (walk.step(units, LOCAL)) {
+                const int s = gc % QS, hv = LOCAL && walk.h >= p.Hv ? walk.h - p.Hv : walk.h;
+                const int hk = (int)(((float)hv + 0.5f) * inv_g);
                 if (gc >= QS && !wait(&qk_empty[s], gc / QS - 1)) break;
                 if (elect_one()) {
                     uint8_t *to = sm + s * S::kQkBytes;
-                    mbar_arrive_expect_tx(&qk_full[s], S::kQkBytes);
+                    mbar_arrive_expect_tx(&qk_full[s], LOCAL ? S::kQkBytes / 2 : S::kQkBytes);
 #pragma unroll 1
                     for (int x = 0; x < PAN; ++x, to += S::kQkPanel) {
                         tma_load_3d(to + kDeltaPanel, &kmap, &qk_full[s], x * 64, hk, walk.row);
-                        tma_load_3d(to, &qmap, &qk_full[s], x * 64, hk, walk.row);
+                        if (!LOCAL) tma_load_3d(to, &qmap, &qk_full[s], x * 64, hk, walk.row);
                     }
                 }
                 __syncwarp();
@@ -1087,7 +1167,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     mbar_arrive_expect_tx(&v_full[gc & 1], S::kVBytes);
 #pragma unroll 1
                     for (int x = 0; x < PAN; ++x)
-                        tma_load_3d(to + x * kDeltaPanel, &vmap, &v_full[gc & 1], x * 64, walk.h, walk.row);
+                        tma_load_3d(to + x * kDeltaPanel, &vmap, &v_full[gc & 1], x * 64, hv, walk.row);
                 }
                 __syncwarp();
                 ++gc;
@@ -1097,19 +1177,21 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             for (int d = max(0, gc - VS); d < gc; ++d) wait(&v_full[d & 1], d >> 1);
         } else if (warp == 29) {
             // ============================================================ the chunks' tables, two tokens a lane
-            DeltaWalk walk(units_n, p.Hv);
+            DeltaWalk walk(units_n, heads);
             const double kLog2e = 1.4426950408889634074;
             int tab_i = 0, turn = -1;                                    // (turn of the tables' last readers)
 #pragma unroll 1
             while (true) {
-                const int n = walk.step(units);
+                const int n = walk.step(units, LOCAL);
+                const bool ident = LOCAL && walk.h >= p.Hv;
+                const int h = ident ? walk.h - p.Hv : walk.h;
                 float g[2] = {0.f, 0.f}, beta[2] = {0.f, 0.f};
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int64_t t = walk.row + 2 * lane + x;
                     if (2 * lane + x < n) {
-                        g[x] = __ldg(p.log_decay + t * p.decay_stride + walk.h);
-                        beta[x] = __ldg(p.beta + t * p.beta_stride + walk.h);
+                        g[x] = __ldg(p.log_decay + t * p.decay_stride + h);
+                        beta[x] = __ldg(p.beta + t * p.beta_stride + h);
                     }
                 }
                 if (!(g[0] <= 0.f && g[1] <= 0.f)) record_error(p.err, ERR_RANGE | SRC_DELTA);
@@ -1148,9 +1230,19 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     a = 1.f + e;
                     a_lo = e - (a - 1.f);
                 }
-                if (lane == 0)
-                    *info_of(tab_i) = DeltaChunk{n, walk.row, walk.h, walk.first, walk.left <= DC, walk.slot, walk.from, a,
-                                                 a_lo, DC};
+                if (lane == 0) {
+                    const float *src = nullptr;
+                    float *dst = nullptr;
+                    if (n && (walk.first || walk.left <= DC)) {
+                        const DeltaUnit u = *walk.unit;
+                        float *cached = u.slot < 0 ? nullptr : p.state + ((int64_t)u.slot * p.Hv + h) * D * D;
+                        float *kept = u.row < 0 ? nullptr
+                                                : p.states + ((int64_t)(u.row + (ident ? p.state_rows : 0)) * p.Hv + h) * D * D;
+                        src = kept ? kept : u.from ? cached : nullptr;
+                        if (walk.left <= DC) dst = LOCAL ? kept : u.last ? cached : nullptr;
+                    }
+                    *info_of(tab_i) = DeltaChunk{n, walk.row, walk.h, walk.first, a, a_lo, DC, ident, src, dst};
+                }
                 arrive(&tab_full[tab_i]);
                 next_tab(tab_i, turn);
                 if (n == 0) break;
@@ -1220,10 +1312,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         tc_commit(&go[0]);
                     }
                     __syncwarp();
-                    if (gc > 0 && !wait(o_read, gc - 1)) break;
-                    tc_fence_after();
-                    if (elect_one()) times(TM_SQ, qk, 2);
-                    __syncwarp();
+                    if (!LOCAL) {
+                        if (gc > 0 && !wait(o_read, gc - 1)) break;
+                        tc_fence_after();
+                        if (elect_one()) times(TM_SQ, qk, 2);
+                        __syncwarp();
+                    }
                 }
                 const int more = kq(gc + 1, tab_i, turn);
                 if (more < 0 || (gc < 0 && more == 0)) break;
@@ -1245,9 +1339,11 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         four(TM_KV, TM_R + x * 32, kd, idesc_bf16_f32(128, D, 1), 0, 16 * 128 >> 4, 0, x > 0);
                     tc_commit(kv_done);
                     tc_commit(&qk_empty[gc % QS]);
-                    // parts of U~ and of P: (1, 1), (2, 1), (1, 2)
-                    triangle(TM_PU, TM_UO, smb + S::kPOff + (gc & 1) * 2 * kDeltaPanel, 3, 0x010, 0x100);
-                    tc_commit(&o_done[gc & 1]);
+                    if (!LOCAL) {
+                        // parts of U~ and of P: (1, 1), (2, 1), (1, 2)
+                        triangle(TM_PU, TM_UO, smb + S::kPOff + (gc & 1) * 2 * kDeltaPanel, 3, 0x010, 0x100);
+                        tc_commit(&o_done[gc & 1]);
+                    }
                 }
                 arrive(&tab_free[old_tab]);
                 if (more == 0) break;
@@ -1276,16 +1372,27 @@ cudaError_t launch_delta_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [&] {
-        attr_err[dev] =
-            cudaFuncSetAttribute(delta_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+        attr_err[dev] = cudaFuncSetAttribute(delta_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             S::kBytes);
+        if (attr_err[dev] == cudaSuccess)
+            attr_err[dev] = cudaFuncSetAttribute(delta_chunk_kernel<D, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     });
     if (attr_err[dev] != cudaSuccess) return attr_err[dev];
     delta_plan_kernel<<<1, 1024, 0, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // a CTA per SM at most: each goes over several units
-    const unsigned ctas = (unsigned)min((int64_t)p.batch * p.Hv, (int64_t)p.num_sms);
+    auto ctas = [&](int heads) { return (unsigned)min((int64_t)p.max_units * heads, (int64_t)p.num_sms); };
+    if (p.seg_len < p.max_seqlen) {
+        e = launch_after(delta_chunk_kernel<D, true>, dim3(ctas(2 * p.Hv)), kDeltaThreads, S::kBytes, stream, qmap, kmap,
+                         vmap, omap, p);
+        if (e == cudaSuccess)
+            e = launch_after(delta_join_kernel<D>, dim3(p.max_units, p.Hv, D / 16), 256, 0, stream, p);
+        if (e != cudaSuccess) return e;
+    }
     main_kernel_event_before(stream);
-    e = launch_after(delta_chunk_kernel<D>, dim3(ctas), kDeltaThreads, S::kBytes, stream, qmap, kmap, vmap, omap, p);
+    e = launch_after(delta_chunk_kernel<D, false>, dim3(ctas(p.Hv)), kDeltaThreads, S::kBytes, stream, qmap, kmap, vmap,
+                     omap, p);
     main_kernel_event_after(stream);
     return e;
 }

@@ -184,13 +184,16 @@ struct DeltaParams {
     int start_zero;                   // context_lens is null and every sequence starts from zero
     int norm;                         // q and k are divided by sqrt(their sum of squares + eps)
     float scale, eps;
-    // prompts: the work list, in the workspace
+    // prompts: the work list and the segments' states, in the workspace
+    int seg_len;                      // a longer sequence is cut into segments of this many tokens (a multiple of 64)
+    int max_units, state_rows;        // entries of units; rows of states, each twice
     int num_sms;                      // CTAs of the prompt kernel at most
     void *units;                      // kDeltaUnitBytes each
     int *unit_count;
+    float *states;                    // [2 state_rows, Hv, D, D]: of a zero state (then: starts), of the identity
     uint32_t *err;
 };
-constexpr int kDeltaUnitBytes = 16;
+constexpr int kDeltaUnitBytes = 32;
 constexpr int kDeltaShort = 16;       // sequences of at most this many tokens take the recurrent form
 cudaError_t launch_delta_varlen(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                 const CUtensorMap &omap, const DeltaParams &p, cudaStream_t stream);

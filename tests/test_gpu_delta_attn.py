@@ -314,3 +314,33 @@ def test_captured_replayed_and_repeated(T):
     side.synchronize()
     assert torch.equal(again, want) and torch.equal(state, s0)
     assert av.get_last_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,D", [([3000], 1, 1, 128), ([2100, 70, 1700, 0, 3], 1, 2, 64), ([640, 1800], 1, 1, 64),
+                                          ([20, 2561], 2, 2, 128)])
+@pytest.mark.parametrize("cached", [False, True])
+def test_long_sequences_cut_into_segments(lens, Hk, Hv, D, cached):
+    """Fewer sequences and heads than the GPU has room for: segments run side by side from the
+    states that a pass before finds (a matrix per segment, applied to its start: sums of D terms, whose
+    rounding of D 2^-24 at most per segment the steps' allowance covers: a segment has 512 tokens at least)."""
+    B, T = len(lens), sum(lens)
+    assert av.delta_attn_workspace_size(B, T, Hk, Hv, D, max(lens)) > 1 << 20          # it does cut them
+    host, dev, gen = inputs(T, T, Hk, Hv, D)
+    cu = cu_of(lens)
+    state = torch.randn(B + 1, Hv, D, D, generator=gen)
+    slots = torch.randperm(B + 1, generator=gen)[:B].to(torch.int32)
+    ctx = torch.tensor([7] * B, dtype=torch.int32)
+    sd = state.cuda()
+    av.get_last_device_error()
+    kw = dict(state_cache=sd, state_slots=slots.cuda(), context_lens=ctx.cuda()) if cached else {}
+    out = av.delta_attn_varlen_fwd(*dev, cu.cuda(), max(lens), qk_norm_eps=1e-6, **kw)
+    torch.cuda.synchronize()
+    assert av.get_last_device_error()[0] == 0
+    ref, finals, reach = delta(*host, cu, D ** -0.5, [state[slots[b]].double() if cached else None for b in range(B)], 1e-6)
+    check_out(out, ref, reach, "out")
+    if cached:
+        for b in range(B):
+            if lens[b]:
+                check_state(sd[slots[b]], *finals[b], f"state {b}")
+        free = [s for s in range(B + 1) if s not in slots.tolist()] + [int(slots[b]) for b in range(B) if lens[b] == 0]
+        assert torch.equal(sd.cpu()[free], state[free])
