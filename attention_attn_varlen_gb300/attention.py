@@ -14,10 +14,11 @@ paged cache (store_kvcache at slot_mapping), then
     bottom-right causality among the new tokens.
 
 With a Rotary the rotation of q and k and the store are one call
-(rope_store_kvcache).  LinearAttention is the layer of models that mix attention
-with linear attention: the same step metadata, a state cache instead of a paged
-one.  PagePool keeps the page tables on the GPU and builds each step's metadata
-there from request lengths.
+(rope_store_kvcache).  LinearAttention and DeltaAttention are the layers of models
+that mix attention with linear attention: the same step metadata, a state cache
+instead of a paged one.  PagePool keeps the page tables on the GPU and builds each
+step's metadata there from request lengths; Beams runs a beam search over its
+requests.
 
 Everything runs in the library's kernels; this module only routes tensors.
 """
@@ -27,7 +28,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (StepTables, attn_decode_paged, attn_varlen_fwd, attn_with_kvcache, linear_attn_decode,
+from . import (StepTables, attn_decode_paged, attn_varlen_fwd, attn_with_kvcache, beam_rows, beam_select,
+               copy_kvcache, copy_states, delta_attn_decode, delta_attn_varlen_fwd, linear_attn_decode,
                linear_attn_varlen_fwd, rope_store_kvcache, step_tables, store_kvcache, trim_pages)
 
 
@@ -136,6 +138,28 @@ class Attention:
     __call__ = forward
 
 
+def _state_step(state_cache, ctx: AttentionContext, rows: int):
+    """How a layer with a state cache runs a step of `rows` rows: (slots, offsets,
+    lengths before it, most tokens of a sequence).  No offsets in a decode step: one
+    row for each sequence."""
+    slots = ctx.state_slots if state_cache is not None else None
+    if state_cache is not None and slots is None:
+        raise ValueError("a layer with a state cache needs ctx.state_slots")
+    if not ctx.is_prefill and slots is None:
+        raise ValueError("decode needs the state cache")
+    offsets, past, most = ctx.cu_seqlens_q, ctx.past_lens, ctx.max_seqlen_q or rows
+    # offsets that are not of these sequences say nothing about them
+    if not ctx.is_prefill and (offsets is None or offsets.numel() != slots.numel() + 1):
+        if rows != slots.numel():
+            raise ValueError("a decode step of several tokens needs the sequences' offsets (ctx.cu_seqlens_q)")
+        return slots, None, past, 1
+    if not ctx.is_prefill and past is None:
+        if most > 1:
+            raise ValueError("a decode step of several tokens needs ctx.past_lens")
+        past = torch.ones_like(slots)            # as without offsets: every slot continues
+    return slots, offsets, past, most
+
+
 class LinearAttention:
     """Linear attention of one layer with a decay per head and a cache of fp32
     states: S_t = exp(log_decay) S_{t-1} + v_t k_t^T, o_t = scale * S_t q_t.
@@ -165,25 +189,54 @@ class LinearAttention:
         q = q.view(-1, self.num_heads, self.head_dim)
         k = k.view(-1, self.num_kv_heads, self.head_dim)
         v = v.view(-1, self.num_kv_heads, self.head_dim)
-        slots = ctx.state_slots if self.state_cache is not None else None
-        if self.state_cache is not None and slots is None:
-            raise ValueError("a layer with a state cache needs ctx.state_slots")
-        if not ctx.is_prefill and slots is None:
-            raise ValueError("decode needs the state cache")
-        offsets, past, most = ctx.cu_seqlens_q, ctx.past_lens, ctx.max_seqlen_q or q.shape[0]
-        # offsets that are not of these sequences say nothing about them
-        if not ctx.is_prefill and (offsets is None or offsets.numel() != slots.numel() + 1):
-            if q.shape[0] != slots.numel():
-                raise ValueError("a decode step of several tokens needs the sequences' offsets (ctx.cu_seqlens_q)")
+        slots, offsets, past, most = _state_step(self.state_cache, ctx, q.shape[0])
+        if offsets is None and not ctx.is_prefill:
             o = linear_attn_decode(q, k, v, self.log_decay, self.state_cache, slots, self.scale, context_lens=past)
         else:
-            if not ctx.is_prefill and past is None:
-                if most > 1:
-                    raise ValueError("a decode step of several tokens needs ctx.past_lens")
-                past = torch.ones_like(slots)            # as without offsets: every slot continues
             o = linear_attn_varlen_fwd(q, k, v, self.log_decay, offsets, most, self.scale,
                                        state_cache=self.state_cache, state_slots=slots, context_lens=past,
                                        cache_seqlens=ctx.cache_seqlens)
+        return o.view(shape)
+
+    __call__ = forward
+
+
+class DeltaAttention:
+    """Linear attention of one layer by the gated delta rule (see
+    delta_attn_varlen_fwd), with a cache of fp32 states.
+
+    state_cache ([num_slots, num_v_heads, head_dim, head_dim] float32) is bound by
+    the owner, as LinearAttention's.  qk_norm_eps: q and k are normalised on the way
+    (None: the caller has done it)."""
+
+    def __init__(self, num_k_heads: int, num_v_heads: int, head_dim: int, scale: float,
+                 qk_norm_eps: float | None = 1e-6):
+        if num_v_heads % num_k_heads:
+            raise ValueError("num_v_heads must be a multiple of num_k_heads")
+        self.num_k_heads = num_k_heads
+        self.num_v_heads = num_v_heads
+        self.head_dim = head_dim
+        self.scale = float(scale)
+        self.qk_norm_eps = qk_norm_eps
+        self.state_cache: torch.Tensor | None = None
+
+    def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, beta: torch.Tensor,
+                ctx: AttentionContext) -> torch.Tensor:
+        """q, k [N, Hk*D] or [N, Hk, D]; v [N, Hv*D] or [N, Hv, D]; log_decay, beta
+        float32 [N, Hv].  Returns o with v's shape.  Steps as for LinearAttention; a
+        few tokens per sequence run token by token on the states, more in chunks."""
+        shape = v.shape
+        q = q.view(-1, self.num_k_heads, self.head_dim)
+        k = k.view(-1, self.num_k_heads, self.head_dim)
+        v = v.view(-1, self.num_v_heads, self.head_dim)
+        slots, offsets, past, most = _state_step(self.state_cache, ctx, q.shape[0])
+        if offsets is None and not ctx.is_prefill:
+            o = delta_attn_decode(q, k, v, log_decay, beta, self.state_cache, slots, self.scale, context_lens=past,
+                                  qk_norm_eps=self.qk_norm_eps)
+        else:
+            o = delta_attn_varlen_fwd(q, k, v, log_decay, beta, offsets, most, self.scale,
+                                      state_cache=self.state_cache, state_slots=slots, context_lens=past,
+                                      cache_seqlens=ctx.cache_seqlens, qk_norm_eps=self.qk_norm_eps)
         return o.view(shape)
 
     __call__ = forward
@@ -239,3 +292,51 @@ class PagePool:
             context_lens=tables.cache_seqlens, block_tables=tables.block_table if paged else None,
             positions=tables.positions if positions is None else positions, state_slots=state_slots,
             past_lens=tables.context_lens, cache_seqlens=tables.cache_seqlens)
+
+
+class Beams:
+    """A beam search over requests of a PagePool: `rows` int32 [R, W] are the request
+    rows of R searches with W beams each, all different.  A row is also its beam's state
+    slot in the caches of LinearAttention and DeltaAttention layers.  Nothing here waits
+    for the GPU.
+
+    All beams of a search hold the same number of tokens.  A prompt is stored in its
+    search's first beam, after every beam's row has grown by it; start() hands it to the
+    others.  A step then is: select() on the step's logits (a row per beam, in the
+    order of `rows`), advance() to the chosen parents, and the next step with the
+    tokens and the new `rows`."""
+
+    def __init__(self, pool: PagePool, rows: torch.Tensor):
+        self.pool = pool
+        self.rows = rows
+        self.first_tokens: torch.Tensor | None = None
+        # the search starts from its first beam alone: the others hold the same prompt
+        self.scores = torch.full(rows.shape, float("-inf"), device=rows.device)
+        self.scores[:, 0] = 0
+
+    def select(self, logits: torch.Tensor, num_out: int | None = None):
+        """(tokens, parents, scores) of the best continuations, [R, num_out] each
+        (None: as many as there are beams), best first; see beam_select."""
+        beams = self.rows.shape[1]
+        return beam_select(logits, self.scores.view(-1), beams, beams if num_out is None else num_out)
+
+    def advance(self, parents: torch.Tensor, scores: torch.Tensor, layers=()) -> None:
+        """Beam w of each search becomes a continuation of beam parents[:, w] with
+        scores[:, w] (both [R, W]; -1 and -inf: none): the beams' rows, and in the
+        caches of `layers` (Attention, LinearAttention, DeltaAttention) what beams that go on
+        more than once have cached."""
+        self.rows, source = beam_rows(parents, self.rows)
+        self.scores = scores
+        for layer in layers:
+            if isinstance(layer, Attention):
+                copy_kvcache(layer.k_cache, layer.v_cache, source, self.rows, self.pool.page_table, self.pool.seq_lens,
+                             first_tokens=self.first_tokens, v16_cache=layer.v16_cache)
+            else:
+                copy_states(layer.state_cache, source, self.rows)
+
+    def start(self, layers=()) -> None:
+        """Copy the prompts from the first beams to the others; what is copied later
+        begins behind them."""
+        scores = self.scores
+        self.advance(torch.zeros_like(self.rows), scores, layers)
+        self.first_tokens = self.pool.seq_lens.clone()

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import attention_attn_varlen_gb300 as av
+import attention_attn_varlen_gb300.attention as at
 
 # accepted calls below carry made-up addresses: they must find no device to run on
 needs_no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="passes made-up device addresses")
@@ -104,3 +105,67 @@ def test_the_binding_refuses_cpu_tensors():
         av.copy_states(torch.zeros(2, 4), i32, i32)
     with pytest.raises(ValueError, match="CUDA"):
         av.copy_kvcache(q[None], q[None], i32, i32, i32.view(1, 2), i32[:1])
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def test_the_delta_layer_goes_by_the_steps_tables(monkeypatch):
+    """As LinearAttention: offsets where there are some, one row per sequence without
+    them, and refusals where neither fits."""
+    calls = []
+    for name in ("delta_attn_decode", "delta_attn_varlen_fwd"):
+        monkeypatch.setattr(at, name, lambda q, k, v, g, b, *a, name=name, **kw: (calls.append((name, a, kw)),
+                                                                                  torch.zeros_like(v))[1])
+    layer = at.DeltaAttention(1, 2, 64, 0.5, qk_norm_eps=None)
+
+    def run(ctx, rows):
+        calls.clear()
+        x = torch.zeros(rows, 64)
+        y = layer(x, x, torch.zeros(rows, 128), torch.zeros(rows, 2), torch.zeros(rows, 2), ctx)
+        assert y.shape == (rows, 128)
+        return calls[0]
+
+    # a prompt without a cache starts from zero and keeps nothing
+    name, a, kw = run(at.AttentionContext(True, cu_seqlens_q=_i32(0, 3, 5), max_seqlen_q=3), 5)
+    assert name == "delta_attn_varlen_fwd" and a[0].tolist() == [0, 3, 5] and a[1:] == (3, 0.5)
+    assert kw["state_cache"] is None and kw["state_slots"] is None and kw["qk_norm_eps"] is None
+    with pytest.raises(ValueError, match="state cache"):
+        run(at.AttentionContext(False, state_slots=_i32(0, 1)), 2)
+    layer.state_cache = torch.zeros(4, 2, 64, 64)
+    with pytest.raises(ValueError, match="state_slots"):
+        run(at.AttentionContext(False), 2)
+    name, a, kw = run(at.AttentionContext(False, state_slots=_i32(0, 1), past_lens=_i32(3, 0)), 2)
+    assert name == "delta_attn_decode" and kw["context_lens"].tolist() == [3, 0]
+    with pytest.raises(ValueError, match="offsets"):
+        run(at.AttentionContext(False, state_slots=_i32(0, 1)), 4)
+    with pytest.raises(ValueError, match="past_lens"):
+        run(at.AttentionContext(False, state_slots=_i32(0, 1), cu_seqlens_q=_i32(0, 2, 4), max_seqlen_q=2), 4)
+    name, a, kw = run(at.AttentionContext(False, state_slots=_i32(0, 1), cu_seqlens_q=_i32(0, 2, 4), max_seqlen_q=2,
+                                          past_lens=_i32(9, 9), cache_seqlens=_i32(11, 9)), 4)
+    assert name == "delta_attn_varlen_fwd" and a[1] == 2 and kw["cache_seqlens"].tolist() == [11, 9]
+    with pytest.raises(ValueError, match="multiple"):
+        at.DeltaAttention(2, 3, 64, 0.5)
+
+
+def test_beams_hand_the_same_rows_to_every_cache(monkeypatch):
+    calls = []
+    monkeypatch.setattr(at, "beam_rows", lambda p, r: (r + 100, p))
+    monkeypatch.setattr(at, "copy_kvcache", lambda *a, **kw: calls.append(("kv", a, kw)))
+    monkeypatch.setattr(at, "copy_states", lambda *a: calls.append(("states", a, {})))
+    pool = at.PagePool(8, 16, 6, 2, device="cpu")
+    beams = at.Beams(pool, _i32(0, 1, 2, 3, 4, 5).view(2, 3))
+    assert beams.scores.tolist() == [[0.0, -float("inf"), -float("inf")]] * 2
+    att, rule = at.Attention(2, 64, 0.5, 1), at.DeltaAttention(1, 1, 64, 0.5)
+    att.k_cache = att.v_cache = torch.zeros(8, 16, 1, 64)
+    rule.state_cache = torch.zeros(6, 1, 64, 64)
+    beams.start((att, rule))
+    assert beams.scores[0, 0] == 0 and beams.first_tokens is not pool.seq_lens
+    assert [c[0] for c in calls] == ["kv", "states"] and calls[0][2]["first_tokens"] is None
+    calls.clear()
+    new = torch.zeros(2, 3)
+    beams.advance(_i32(0, 0, 1, 2, 2, 2).view(2, 3), new, (rule, att))
+    assert beams.scores is new and [c[0] for c in calls] == ["states", "kv"]
+    assert calls[0][1][2] is beams.rows and calls[1][2]["first_tokens"] is beams.first_tokens
+    assert beams.rows.tolist() == [[200, 201, 202], [203, 204, 205]]
