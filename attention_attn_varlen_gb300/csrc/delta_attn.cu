@@ -877,17 +877,19 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = ex2(x[j] + g[j]) * factor;
                     tc_wait_ld();
-                    bool bad = false;
+                    float z = 0.f;               // NaN once something non-finite went by
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         // masked by choice, not by a factor, which would keep a NaN
                         x[j] = j0 + j < see ? x[j] * __uint_as_float(next[j]) : 0.f;
-                        // a zero of T would not keep it from earlier tokens: 0 here, and NaN from this token on later
-                        const bool drop = keys && !(fabsf(x[j]) < INFINITY);
-                        x[j] = drop ? 0.f : x[j];
-                        bad |= drop;
+                        z = fmaf(x[j], 0.f, z);
                     }
-                    if (bad) atomicMin(&info_of(tab_i)->bad, i);
+                    if (keys && !(z == 0.f)) {
+                        // a zero of T would not keep it from earlier tokens: 0 here, and NaN from this token on later
+                        atomicMin(&info_of(tab_i)->bad, i);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = fabsf(x[j]) < INFINITY ? x[j] : 0.f;
+                    }
                     tmem_ld8(from + ((j0 + 8) & 63), next);              // (behind the last ones: not used)
                     if (keys) {
 #pragma unroll
@@ -985,15 +987,18 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 }
                 role_sync(1, 256);
             }
-            // T's three parts: T11, T22, T21, a lane per row, two columns at a time
-#pragma unroll 2
-            for (int x = 0; x < 6; ++x) {
-                const int r = (x >= 2 ? 32 : 0) + renew(lane), j = ((x >> 1) == 1 ? 32 : 0) + 2 * (w8 + 8 * (x & 1));
-                uint32_t h[3];
-                split3(At[j * kAStride + r], At[(j + 1) * kAStride + r], h[0], h[1], h[2]);
-                uint8_t *t = sm + S::kTOff + sw128_off(r, j >> 3) + (j & 7) * 2;
+            // T's three parts: T11, T22, T21, a lane per row, eight columns at a time
+#pragma unroll 1
+            for (int x = w8; x < 12; x += 8) {
+                const int r = (x >= 4 ? 32 : 0) + renew(lane), j = (x >> 2 == 1 ? 32 : 0) + 8 * (x & 3);
+                uint32_t h[3][4];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(t + k * kDeltaPanel) = h[k];
+                for (int k = 0; k < 4; ++k)
+                    split3(At[(j + 2 * k) * kAStride + r], At[(j + 2 * k + 1) * kAStride + r], h[0][k], h[1][k], h[2][k]);
+                uint8_t *t = sm + S::kTOff + sw128_off(r, j >> 3);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint4 *>(t + k * kDeltaPanel) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
             }
             fence_proxy_async_smem();
             arrive(t_ready);
