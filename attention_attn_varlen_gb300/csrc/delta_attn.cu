@@ -910,51 +910,85 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 tc_fence_before();
                 arrive(kq_read);
             }
-            if (w8 == 0 && gc > 0) role_wait(1, &go[1], gc - 1);     // U of the chunk before done: T's place
-            role_sync(1, 256);
-            // the 16 x 16 diagonal blocks, two a warp, a lane per column: x_q = [q = column] - sum_{m < q} A_qm x_m
-            if (w8 == 0 || w8 == 6) {
-                const int l = renew(lane), col = l & 15, jb = 32 * (w8 == 6) + (l & 16);
-                float *blk = At + jb * kAStride + jb;
-                float x[16];
+            // T11 by a warp of A's rows 0..31, T22 by the one that made its block of A.  T11 is there first, so that
+            // A21 T11 is made beside T22.
+            if (qd == 2) role_sync(3, 64);
+            if (w8 == 2 || w8 == 7) {
+                if (gc > 0) role_wait(1, &go[1], gc - 1);            // U of the chunk before done: T's place
+                const int jb = w8 == 2 ? 0 : 32;
+                {
+                    // its two 16 x 16 diagonal blocks, a lane per column: x_q = [q = column] - sum_{m < q} A_qm x_m
+                    const int l = renew(lane), col = l & 15, at = jb + (l & 16);
+                    float *blk = At + at * (kAStride + 1);
+                    float x[16];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) x[q] = q == col ? 1.f : 0.f;
+                    for (int q = 0; q < 16; ++q) x[q] = q == col ? 1.f : 0.f;
 #pragma unroll
-                for (int m = 0; m < 15; ++m) {
+                    for (int m = 0; m < 15; ++m) {
 #pragma unroll
-                    for (int q = (m + 1) & ~3; q < 16; q += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(blk + m * kAStride + q);
-                        if (q > m) x[q] = fmaf(-a.x, x[m], x[q]);
-                        if (q + 1 > m) x[q + 1] = fmaf(-a.y, x[m], x[q + 1]);
-                        if (q + 2 > m) x[q + 2] = fmaf(-a.z, x[m], x[q + 2]);
-                        if (q + 3 > m) x[q + 3] = fmaf(-a.w, x[m], x[q + 3]);
+                        for (int q = (m + 1) & ~3; q < 16; q += 4) {
+                            const float4 a = *reinterpret_cast<const float4 *>(blk + m * kAStride + q);
+                            if (q > m) x[q] = fmaf(-a.x, x[m], x[q]);
+                            if (q + 1 > m) x[q + 1] = fmaf(-a.y, x[m], x[q + 1]);
+                            if (q + 2 > m) x[q + 2] = fmaf(-a.z, x[m], x[q + 2]);
+                            if (q + 3 > m) x[q + 3] = fmaf(-a.w, x[m], x[q + 3]);
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4)
+                        *reinterpret_cast<float4 *>(blk + col * kAStride + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                    float *to = Tm + at * kXStride + l;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) to[q * kXStride] = x[q];
+                }
+                // the block below them: A21 T11, in the place where T21 = -T22 (A21 T11) goes; four rows of two columns a lane
+#pragma unroll 1
+                for (int second = 0; second < 2; ++second) {
+                    __syncwarp();
+                    const int l = renew(lane), r0 = (l >> 3) * 4, c = (l & 7) * 2;
+                    const float *left = At + (jb + 16 * second) * kAStride + jb + 16 + r0;
+                    float *right = Tm + (jb + 16 * second) * kXStride + c;
+                    float y[2][4] = {};
+#pragma unroll 8
+                    for (int m = 0; m < 16; ++m) {
+                        const float4 a = *reinterpret_cast<const float4 *>(left + m * kAStride);
+                        const float2 b = *reinterpret_cast<const float2 *>(right + m * kXStride);
+                        fma2(y[0][0], y[0][1], a.x, a.y, b.x, b.x, y[0][0], y[0][1]);
+                        fma2(y[0][2], y[0][3], a.z, a.w, b.x, b.x, y[0][2], y[0][3]);
+                        fma2(y[1][0], y[1][1], a.x, a.y, b.y, b.y, y[1][0], y[1][1]);
+                        fma2(y[1][2], y[1][3], a.z, a.w, b.y, b.y, y[1][2], y[1][3]);
+                    }
+                    __syncwarp();
+                    const float sign = second ? -1.f : 1.f;
+                    float *to = Tm + (jb + 16 + r0) * kXStride + c;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<float2 *>(to + k * kXStride) = make_float2(sign * y[0][k], sign * y[1][k]);
+                    if (second) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float4 *>(At + (jb + c + e) * kAStride + jb + 16 + r0) =
+                                make_float4(-y[e][0], -y[e][1], -y[e][2], -y[e][3]);
                     }
                 }
-                __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 16; q += 4)
-                    *reinterpret_cast<float4 *>(blk + col * kAStride + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
-                float *to = Tm + jb * kXStride + (jb & 16) + col;
-#pragma unroll
-                for (int q = 0; q < 16; ++q) to[q * kXStride] = x[q];
             }
-            role_sync(1, 256);
-            // the blocks below: A21 T11, then -T22 (A21 T11), of 16 x 16 (two side by side, four warps), then of
-            // 32 x 32.  A warp has 8 rows and 16 columns, a lane four rows of a column.
+            if (w8 != 7) role_sync(4, 224);
+            // the block below, of 32 x 32: X = A21 T11, then -T22 X.  A task has 8 rows and 16 columns, a lane four rows of a
+            // column.
 #pragma unroll 1
-            for (int step = 0; step < 4; ++step) {
-                const bool big = step >= 2, second = step & 1;
-                const int l = renew(lane), c = l & 15;
-                const int pr = big ? 0 : (w8 >> 1) * 32;                 // first token of the pair of blocks
-                const int size = big ? 32 : 16;
-                const int r0 = (big ? w8 >> 1 : w8 & 1) * 8 + (l >> 4) * 4, c0 = big ? (w8 & 1) * 16 : 0;
-                if (big || w8 < 4) {
-                    const float *left = At + (second ? pr + size : pr) * kAStride + pr + size + r0;
-                    const float *right = (second ? X + (pr >> 1) * kXStride : Tm + pr * kXStride) + c0 + c;
+            for (int second = 0; second < 2; ++second) {
+                // (first: of columns 0..15 by the warps of P; 16..31, half as long, by those of A)
+                int task = second ? w8 : ((w8 & 1) + (w8 >> 2) * 2) * 2;
+                if (!second && keys) task = w8 == 2 ? 1 : w8 == 3 ? 3 : w8 == 6 ? 7 : 8;
+#pragma unroll 1
+                for (; task < 8; task = !second && task == 3 ? 5 : 8) {
+                    const int l = renew(lane), c = (task & 1) * 16 + (l & 15), r0 = (task >> 1) * 8 + (l >> 4) * 4;
                     // T11's columns begin at the diagonal, T22's rows end there
-                    const int m0 = second ? 0 : c0, m1 = second && big && w8 < 4 ? 16 : size;
+                    const int m0 = second ? 0 : (task & 1) * 16, m1 = second && task < 4 ? 16 : 32;
+                    const float *left = At + (32 * second + m0) * kAStride + 32 + r0;
+                    const float *right = (second ? X : Tm) + m0 * kXStride + c;
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    left += m0 * kAStride, right += m0 * kXStride;
 #pragma unroll 1
                     for (int m = m0; m < m1; m += 8, left += 8 * kAStride, right += 8 * kXStride) {
                         float4 a[8];
@@ -972,17 +1006,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             acc[3] = fmaf(a[k].w, b[k], acc[3]);
                         }
                     }
-                    float *to = X + ((pr >> 1) + r0) * kXStride + c0 + c;
                     if (second) {
+                        *reinterpret_cast<float4 *>(At + c * kAStride + 32 + r0) =
+                            make_float4(-acc[0], -acc[1], -acc[2], -acc[3]);
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) acc[k] = -acc[k];
-                        *reinterpret_cast<float4 *>(At + (pr + c0 + c) * kAStride + pr + size + r0) =
-                            make_float4(acc[0], acc[1], acc[2], acc[3]);
-                        to = Tm + (pr + 16 + r0) * kXStride + c;
-                    }
-                    if (step != 3) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) to[k * kXStride] = acc[k];
+                        for (int k = 0; k < 4; ++k) X[(r0 + k) * kXStride + c] = acc[k];
                     }
                 }
                 role_sync(1, 256);
