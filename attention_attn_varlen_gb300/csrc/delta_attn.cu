@@ -989,22 +989,31 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     const float *left = At + (32 * second + m0) * kAStride + 32 + r0;
                     const float *right = (second ? X : Tm) + m0 * kXStride + c;
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    float4 a[2][4];
+                    float b[2][4];
+                    auto load = [&](int x) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            a[x][k] = *reinterpret_cast<const float4 *>(left + k * kAStride);
+                            b[x][k] = right[k * kXStride];
+                        }
+                        left += 4 * kAStride, right += 4 * kXStride;
+                    };
+                    auto take = [&](int x) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            fma2(acc[0], acc[1], a[x][k].x, a[x][k].y, b[x][k], b[x][k], acc[0], acc[1]);
+                            fma2(acc[2], acc[3], a[x][k].z, a[x][k].w, b[x][k], b[x][k], acc[2], acc[3]);
+                        }
+                    };
+                    load(0);
 #pragma unroll 1
-                    for (int m = m0; m < m1; m += 8, left += 8 * kAStride, right += 8 * kXStride) {
-                        float4 a[8];
-                        float b[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            a[k] = *reinterpret_cast<const float4 *>(left + k * kAStride);
-                            b[k] = right[k * kXStride];
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            acc[0] = fmaf(a[k].x, b[k], acc[0]);
-                            acc[1] = fmaf(a[k].y, b[k], acc[1]);
-                            acc[2] = fmaf(a[k].z, b[k], acc[2]);
-                            acc[3] = fmaf(a[k].w, b[k], acc[3]);
-                        }
+                    for (int m = m0;; m += 8) {
+                        load(1);
+                        take(0);
+                        if (m + 8 < m1) load(0);
+                        take(1);
+                        if (m + 8 >= m1) break;
                     }
                     if (second) {
                         *reinterpret_cast<float4 *>(At + c * kAStride + 32 + r0) =
