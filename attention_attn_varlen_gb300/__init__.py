@@ -980,7 +980,8 @@ def beam_rows(parents, rows, out=None, *, stream=None):
             parents, memory_format=torch.contiguous_format)
     new, source = out
     _cuda(torch.int32, dev, ("parents", parents), ("rows", rows), ("out rows", new), ("source", source))
-    if parents.dim() != 2 or rows.shape != parents.shape or new.shape != parents.shape             or source.shape != parents.shape:
+    if parents.dim() != 2 or rows.shape != parents.shape or new.shape != parents.shape \
+            or source.shape != parents.shape:
         raise ValueError("parents, rows and out must be [requests, num_beams]")
     if parents.numel() == 0:
         return new, source
@@ -1024,9 +1025,11 @@ def copy_kvcache(k_cache, v_cache, src, dst, page_table, seq_lens, first_tokens=
     _cuda(torch.bfloat16, dev, ("k_cache", k_cache), ("v_cache", v_cache))
     _cuda(torch.float16, dev, ("v16_cache", v16_cache))
     _cuda(torch.int32, dev, ("page_table", page_table), ("seq_lens", seq_lens), ("first_tokens", first_tokens))
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape             or (v16_cache is not None and v16_cache.shape != k_cache.shape):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape \
+            or (v16_cache is not None and v16_cache.shape != k_cache.shape):
         raise ValueError("the caches must have one shape [num_blocks, block_size, Hkv, D]")
-    if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0]             or (first_tokens is not None and first_tokens.numel() != page_table.shape[0]):
+    if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0] \
+            or (first_tokens is not None and first_tokens.numel() != page_table.shape[0]):
         raise ValueError("page_table must be [num_rows, max_blocks], seq_lens and first_tokens [num_rows]")
     n = _pairs(src, dst, dev)
     blocks, bs, Hkv, D = k_cache.shape
