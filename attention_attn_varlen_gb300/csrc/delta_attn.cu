@@ -13,11 +13,17 @@
 namespace attn {
 namespace {
 
-// e^{log_decay} of token t and head h: a positive or NaN log_decay counts as 0 and is reported.
-__device__ __forceinline__ float delta_decay(const DeltaParams &p, int64_t t, int h, bool report) {
-    const float g = __ldg(p.log_decay + t * p.decay_stride + h);
+// e^{log_decay}: a positive or NaN log_decay counts as 0 and is reported.
+__device__ __forceinline__ float delta_decay(const DeltaParams &p, float g, bool report) {
     if (report && !(g <= 0.f)) record_error(p.err, ERR_RANGE | SRC_DELTA);
     return expf(fminf(g, 0.f));
+}
+
+// 1 / sqrt(x): the hardware's estimate and one step of Newton's method
+__device__ __forceinline__ float inv_sqrt(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return x > 0.f ? y * fmaf(-0.5f * x * y, y, 1.5f) : y;
 }
 
 // sums over the LPR lanes of a row, in every lane
@@ -69,7 +75,7 @@ __global__ void __launch_bounds__(kRecWarps * 32, 5) delta_one_kernel(const Delt
     const uint2 qr = *reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (int64_t)hk * D + col);
     const uint4 vr = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + (int64_t)h * D + row0);
     const float beta = __ldg(p.beta + t * p.beta_stride + h);
-    const float a = delta_decay(p, t, h, first_thread);
+    const float a = delta_decay(p, __ldg(p.log_decay + t * p.decay_stride + h), first_thread);
     const float k0 = __uint_as_float(kr.x << 16), k1 = __uint_as_float(kr.x & 0xFFFF0000u);
     const float k2 = __uint_as_float(kr.y << 16), k3 = __uint_as_float(kr.y & 0xFFFF0000u);
     const float q0 = __uint_as_float(qr.x << 16), q1 = __uint_as_float(qr.x & 0xFFFF0000u);
@@ -137,21 +143,28 @@ __global__ void __launch_bounds__(kRecWarps * 32, 5) delta_one_kernel(const Delt
             __float2bfloat16_rn(p.scale * rq * fmaf(own * rk, kq, a * sq[0]));
 }
 
-// Two to kDeltaShort tokens.  Here the instructions of the tokens count as well, so what the rows of a state share
-// is prepared once per CTA (decay, k . q, the normalised k and q in fp32), a lane has eight columns of
-// four rows (fewer shuffles and choices among rows per product), and products go in pairs.  64 sequences of 5 tokens,
-// 32 heads of 128: 80 us with the one-token kernel's layout and loop.
+// Two to kDeltaShort tokens, n, without a product that waits for the one before: with k and q normalised (and q scaled),
+// E_i the decay from the start to token i and R_ij the one from j to i,
+//   u_i = beta_i (v_i - E_i S_0 k_i - sum_{j < i} R_ij k_i.k_j u_j),
+//   o_i = E_i S_0 q_i + sum_{j <= i} R_ij q_i.k_j u_j,   S = E_n S_0 + sum_j R_nj u_j k_j^T,
+// the decays as products of the tokens' own, so that small ones cost nothing.  What the rows share (k, q, R k.k, R q.k) is
+// made once per CTA; a lane has eight columns of 2 D / 32 rows, as many rows twice (k and q) as lanes share a row, so
+// that adding up a token's products leaves a lane one sum.  Issue slots bound it (1,850 instructions a warp, 16 rows), then HBM:
+// 64 sequences of 5 tokens, 32 heads of 128: 60 us (72 token after token; 41 for the states alone).
 template <int D>
-__global__ void __launch_bounds__(kRecWarps * 32, 5) delta_few_kernel(const DeltaParams p) {
-    constexpr int LPR = D / 8, ROWS = 4 * 32 / LPR;     // lanes per row; rows per warp
-    constexpr int CTAS = D / (ROWS * kRecWarps);        // CTAs per state
-    constexpr int OWN = ROWS * kRecWarps;               // rows of a CTA
-    __shared__ float4 k_s[kDeltaShort][D / 4], q_s[kDeltaShort][D / 4], v_s[kDeltaShort][OWN / 4];
-    __shared__ float4 token[kDeltaShort];               // e^g, k . q, beta
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const DeltaParams p) {
+    constexpr int LPR = D / 8, RPL = LPR / 2;           // lanes per row, rows per lane
+    constexpr int ROWS = 16, OWN = ROWS * kRecWarps;    // rows of a warp, of a CTA
+    constexpr int CTAS = D / OWN, N = kDeltaShort;
+    static_assert(RPL * 32 / LPR == ROWS && CTAS * OWN == D && N == 16, "layout");
+    __shared__ float4 k_s[N][D / 4], q_s[N][D / 4];
+    __shared__ float v_s[N][OWN], sums[kRecWarps][N][32];       // S_0 k and S_0 q
+    __shared__ float4 kk_s[N][N / 4], qk_s[N][N / 4];           // R k.k, R q.k
+    __shared__ float4 u_s[kRecWarps][N][ROWS / 4];              // R_nj u_j
+    __shared__ float a_s[N], beta_s[N], e_s[N], w_s[N];         // e^g, beta, E, R_n
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), grp = lane / LPR;
     const int unit = blockIdx.x / CTAS, b = unit / p.Hv, h = unit - b * p.Hv, hk = h / p.G;
-    const int cta_row = (blockIdx.x - unit * CTAS) * OWN, l = lane & (LPR - 1), own4 = warp * (ROWS / 4) + lane / LPR;
-    const int row0 = cta_row + own4 * 4;
+    const int cta_row = (blockIdx.x - unit * CTAS) * OWN, row0 = cta_row + warp * ROWS;
     const bool first_cta = cta_row == 0, report = h == 0 && first_cta && threadIdx.x == 0;
     int64_t t0;
     int n;
@@ -159,109 +172,170 @@ __global__ void __launch_bounds__(kRecWarps * 32, 5) delta_few_kernel(const Delt
     bool from;
     float *state = sequence_state<SRC_DELTA, true>(p, p.Hv, b, h, from, report && n > 0);
     if (n == 0) return;
-    float4 S[4][2];                                     // columns 4 l .. and D / 2 + 4 l ..
+    // loads in the order of their use: LPR lanes per token with eight columns each, eight threads per token's values; S
+    uint4 kr, qr, vr = make_uint4(0u, 0u, 0u, 0u);
+    float g, beta;
+    auto load = [&](int i) {
+        const int64_t t = t0 + i;
+        kr = *(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + (int64_t)hk * D) + l);
+        qr = *(reinterpret_cast<const uint4 *>(p.q + t * p.q_stride + (int64_t)hk * D) + l);
+        beta = __ldg(p.beta + t * p.beta_stride + h);
+        g = __ldg(p.log_decay + t * p.decay_stride + h);
+    };
+    load(min(warp * (32 / LPR) + grp, n - 1));
+    static_assert(OWN == 64 && N * 8 == kRecWarps * 32, "values");
+    const int vi = threadIdx.x >> 3, vc = threadIdx.x & 7;
+    if (vi < n) vr = *(reinterpret_cast<const uint4 *>(p.v + (t0 + vi) * p.v_stride + (int64_t)h * D + cta_row) + vc);
+    float4 S[RPL][2];                                   // columns 4 l .. and D / 2 + 4 l ..
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int r = 0; r < RPL; ++r) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            S[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (from) S[i][c] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + i) * D + c * (D / 2)) + l);
+            S[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (from) S[r][c] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + grp * RPL + r) * D + c * (D / 2)) + l);
         }
     }
-    for (int i = warp; i < n; i += kRecWarps) {
-        const int64_t t = t0 + i;
-        const int c = lane & (D / 4 - 1);               // four columns a lane
-        const uint2 kr = *(reinterpret_cast<const uint2 *>(p.k + t * p.k_stride + (int64_t)hk * D) + c);
-        const uint2 qr = *(reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (int64_t)hk * D) + c);
-        float4 k = make_float4(__uint_as_float(kr.x << 16), __uint_as_float(kr.x & 0xFFFF0000u),
-                               __uint_as_float(kr.y << 16), __uint_as_float(kr.y & 0xFFFF0000u));
-        float4 q = make_float4(__uint_as_float(qr.x << 16), __uint_as_float(qr.x & 0xFFFF0000u),
-                               __uint_as_float(qr.y << 16), __uint_as_float(qr.y & 0xFFFF0000u));
+    for (int i0 = warp * (32 / LPR); i0 < n; i0 += kRecWarps * 32 / LPR) {
+        const int i = min(i0 + grp, n - 1);             // (the last one again where there are no more)
+        if (i0 >= kRecWarps * 32 / LPR) load(i);
+        const uint32_t kw[4] = {kr.x, kr.y, kr.z, kr.w}, qw[4] = {qr.x, qr.y, qr.z, qr.w};
+        float k[8], q[8], ks = 0.f, qs = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            k[2 * x] = __uint_as_float(kw[x] << 16), k[2 * x + 1] = __uint_as_float(kw[x] & 0xFFFF0000u);
+            q[2 * x] = __uint_as_float(qw[x] << 16), q[2 * x + 1] = __uint_as_float(qw[x] & 0xFFFF0000u);
+        }
         float rk = 1.f, rq = p.scale;
         if (p.norm) {
-            rk = 1.f / sqrtf(row_sum<D / 4>(fmaf(k.x, k.x, fmaf(k.y, k.y, fmaf(k.z, k.z, k.w * k.w)))) + p.eps);
-            rq = p.scale / sqrtf(row_sum<D / 4>(fmaf(q.x, q.x, fmaf(q.y, q.y, fmaf(q.z, q.z, q.w * q.w)))) + p.eps);
-        }
-        k.x *= rk, k.y *= rk, k.z *= rk, k.w *= rk;
-        q.x *= rq, q.y *= rq, q.z *= rq, q.w *= rq;
-        const float kq = row_sum<D / 4>(fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, k.w * q.w))));
-        const float a = delta_decay(p, t, h, first_cta && lane == 0), beta = __ldg(p.beta + t * p.beta_stride + h);
-        if (lane < D / 4) k_s[i][c] = k, q_s[i][c] = q;
 #pragma unroll
-        for (int x = lane; x < OWN; x += 32)
-            reinterpret_cast<float *>(v_s[i])[x] = __bfloat162float(p.v[t * p.v_stride + (int64_t)h * D + cta_row + x]);
-        if (lane == 0) token[i] = make_float4(a, kq, beta, 0.f);
+            for (int x = 0; x < 8; ++x) ks = fmaf(k[x], k[x], ks), qs = fmaf(q[x], q[x], qs);
+            rk = inv_sqrt(row_sum<LPR>(ks) + p.eps);
+            rq = p.scale * inv_sqrt(row_sum<LPR>(qs) + p.eps);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            k_s[i][2 * l + x] = make_float4(k[4 * x] * rk, k[4 * x + 1] * rk, k[4 * x + 2] * rk, k[4 * x + 3] * rk);
+            q_s[i][2 * l + x] = make_float4(q[4 * x] * rq, q[4 * x + 1] * rq, q[4 * x + 2] * rq, q[4 * x + 3] * rq);
+        }
+        if (l == 0) a_s[i] = delta_decay(p, g, first_cta), beta_s[i] = beta;
+    }
+    if (vi < n) {
+        float4 *to = reinterpret_cast<float4 *>(v_s[vi]) + 2 * vc;
+        to[0] = make_float4(__uint_as_float(vr.x << 16), __uint_as_float(vr.x & 0xFFFF0000u), __uint_as_float(vr.y << 16),
+                            __uint_as_float(vr.y & 0xFFFF0000u));
+        to[1] = make_float4(__uint_as_float(vr.z << 16), __uint_as_float(vr.z & 0xFFFF0000u), __uint_as_float(vr.w << 16),
+                            __uint_as_float(vr.w & 0xFFFF0000u));
     }
     __syncthreads();
-    __nv_bfloat16 *out = p.out + t0 * p.out_stride + (int64_t)h * D + row0;
-    const bool up0 = lane & (LPR / 2), up1 = lane & (LPR / 4);
-    // the row whose sum the lane comes to hold
-    const int row = 2 * up0 + up1;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i, out += p.out_stride) {
-        const float4 k0 = k_s[i][l], k1 = k_s[i][D / 8 + l], q0 = q_s[i][l], q1 = q_s[i][D / 8 + l];
-        const float4 x = token[i], v4 = v_s[i][own4];
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-        float sk[4], sq[4];
+    // k_i.k_j and q_i.k_j, j <= i, eight lanes a pair
+    for (int x0 = warp * 4; x0 < n * (n + 1) / 2; x0 += kRecWarps * 4) {
+        const int x = min(x0 + (lane >> 3), n * (n + 1) / 2 - 1), l8 = lane & 7;
+        int i = 0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int m = 1; m < N; ++m) i += x >= m * (m + 1) / 2;
+        const int j = x - i * (i + 1) / 2;
+        float kk0 = 0.f, kk1 = 0.f, qk0 = 0.f, qk1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const float4 kj = k_s[j][c * 8 + l8], ki = k_s[i][c * 8 + l8], qi = q_s[i][c * 8 + l8];
+            fma2(kk0, kk1, ki.x, ki.y, kj.x, kj.y, kk0, kk1);
+            fma2(kk0, kk1, ki.z, ki.w, kj.z, kj.w, kk0, kk1);
+            fma2(qk0, qk1, qi.x, qi.y, kj.x, kj.y, qk0, qk1);
+            fma2(qk0, qk1, qi.z, qi.w, kj.z, kj.w, qk0, qk1);
+        }
+        const float kk = row_sum<8>(kk0 + kk1), qk = row_sum<8>(qk0 + qk1);
+        float between = 1.f;
+        for (int m = j + 1; m <= i; ++m) between *= a_s[m];
+        if (l8 == 0) {
+            reinterpret_cast<float *>(kk_s[i])[j] = kk * between;
+            reinterpret_cast<float *>(qk_s[i])[j] = qk * between;
+            if (i == n - 1) w_s[j] = between;
+            if (j == 0) e_s[i] = between * a_s[0];
+        }
+    }
+    // S_0 k and S_0 q: half of the values a lane carries go to the other half of the lanes in every step
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const float4 k0 = k_s[i][l], k1 = k_s[i][D / 8 + l], q0 = q_s[i][l], q1 = q_s[i][D / 8 + l];
+        float x[LPR];
+#pragma unroll
+        for (int r = 0; r < RPL; ++r) {
             float c, d;
             fma2(c, d, S[r][0].x, S[r][0].y, k0.x, k0.y, 0.f, 0.f);
             fma2(c, d, S[r][0].z, S[r][0].w, k0.z, k0.w, c, d);
             fma2(c, d, S[r][1].x, S[r][1].y, k1.x, k1.y, c, d);
             fma2(c, d, S[r][1].z, S[r][1].w, k1.z, k1.w, c, d);
-            sk[r] = c + d;
+            x[r] = c + d;
             fma2(c, d, S[r][0].x, S[r][0].y, q0.x, q0.y, 0.f, 0.f);
             fma2(c, d, S[r][0].z, S[r][0].w, q0.z, q0.w, c, d);
             fma2(c, d, S[r][1].x, S[r][1].y, q1.x, q1.y, c, d);
             fma2(c, d, S[r][1].z, S[r][1].w, q1.z, q1.w, c, d);
-            sq[r] = c + d;
+            x[RPL + r] = c + d;
         }
-        // two steps halve the rows a lane carries, the others add up; then S k goes back to all lanes of a row
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            sk[r] = (up0 ? sk[r + 2] : sk[r]) + __shfl_xor_sync(0xffffffffu, up0 ? sk[r] : sk[r + 2], LPR / 2);
-            sq[r] = (up0 ? sq[r + 2] : sq[r]) + __shfl_xor_sync(0xffffffffu, up0 ? sq[r] : sq[r + 2], LPR / 2);
+        for (int w = LPR / 2; w > 0; w /= 2) {
+            const bool up = lane & w;
+#pragma unroll
+            for (int r = 0; r < w; ++r)
+                x[r] = (up ? x[r + w] : x[r]) + __shfl_xor_sync(0xffffffffu, up ? x[r] : x[r + w], w);
         }
-        sk[0] = (up1 ? sk[1] : sk[0]) + __shfl_xor_sync(0xffffffffu, up1 ? sk[0] : sk[1], LPR / 4);
-        sq[0] = (up1 ? sq[1] : sq[0]) + __shfl_xor_sync(0xffffffffu, up1 ? sq[0] : sq[1], LPR / 4);
+        sums[warp][i][lane] = x[0];                     // (value l of lane group grp)
+    }
+    __syncthreads();
+    // a lane per row
+    if (lane < ROWS) {
+        const int at = lane / RPL * LPR + lane % RPL;
+        __nv_bfloat16 *out = p.out + t0 * p.out_stride + (int64_t)h * D + row0 + lane;
+        float u[N];
 #pragma unroll
-        for (int w = LPR / 8; w > 0; w /= 2) {
-            sk[0] += __shfl_xor_sync(0xffffffffu, sk[0], w);
-            sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], w);
-        }
-        const float mine = sk[0], y = __shfl_xor_sync(0xffffffffu, mine, LPR / 4);
-        sk[0] = up1 ? y : mine;
-        sk[1] = up1 ? mine : y;
-        const float y0 = __shfl_xor_sync(0xffffffffu, sk[0], LPR / 2), y1 = __shfl_xor_sync(0xffffffffu, sk[1], LPR / 2);
-        sk[2] = up0 ? sk[0] : y0;
-        sk[3] = up0 ? sk[1] : y1;
-        sk[0] = up0 ? y0 : sk[0];
-        sk[1] = up0 ? y1 : sk[1];
-        float own = 0.f;
+        for (int i = 0; i < N; ++i) {
+            if (i < n) {
+                const float e = e_s[i];
+                float x = fmaf(-e, sums[warp][i][at], v_s[i][warp * ROWS + lane]), o = e * sums[warp][i][at + RPL];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float u = x.z * (v[r] - x.x * sk[r]);
-            own = row == r ? u : own;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float4 k = c ? k1 : k0;
-                float4 z;
-                fma2(z.x, z.y, x.x, x.x, S[r][c].x, S[r][c].y, 0.f, 0.f);
-                fma2(z.z, z.w, x.x, x.x, S[r][c].z, S[r][c].w, 0.f, 0.f);
-                fma2(S[r][c].x, S[r][c].y, u, u, k.x, k.y, z.x, z.y);
-                fma2(S[r][c].z, S[r][c].w, u, u, k.z, k.w, z.z, z.w);
+                for (int j = 0; j < i; ++j) {
+                    x = fmaf(-reinterpret_cast<const float *>(kk_s[i])[j], u[j], x);
+                    o = fmaf(reinterpret_cast<const float *>(qk_s[i])[j], u[j], o);
+                }
+                u[i] = beta_s[i] * x;
+                o = fmaf(reinterpret_cast<const float *>(qk_s[i])[i], u[i], o);
+                out[i * p.out_stride] = __float2bfloat16_rn(o);
+                reinterpret_cast<float *>(u_s[warp][i])[lane] = w_s[i] * u[i];
             }
         }
-        if ((lane & (LPR / 4 - 1)) == 0) out[row] = __float2bfloat16_rn(fmaf(own, x.y, x.x * sq[0]));
     }
-    if (state) {
+    if (!state) return;
+    __syncwarp();
+    const float e = e_s[n - 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int r = 0; r < RPL; ++r) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                __stcs(reinterpret_cast<float4 *>(state + (row0 + i) * D + c * (D / 2)) + l, S[i][c]);
+        for (int c = 0; c < 2; ++c) {
+            fma2(S[r][c].x, S[r][c].y, e, e, S[r][c].x, S[r][c].y, 0.f, 0.f);
+            fma2(S[r][c].z, S[r][c].w, e, e, S[r][c].z, S[r][c].w, 0.f, 0.f);
         }
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const float4 k0 = k_s[i][l], k1 = k_s[i][D / 8 + l];
+#pragma unroll
+        for (int r = 0; r < RPL; r += 4) {
+            const float4 u4 = u_s[warp][i][(grp * RPL + r) / 4];
+            const float u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                fma2(S[r + k][0].x, S[r + k][0].y, u[k], u[k], k0.x, k0.y, S[r + k][0].x, S[r + k][0].y);
+                fma2(S[r + k][0].z, S[r + k][0].w, u[k], u[k], k0.z, k0.w, S[r + k][0].z, S[r + k][0].w);
+                fma2(S[r + k][1].x, S[r + k][1].y, u[k], u[k], k1.x, k1.y, S[r + k][1].x, S[r + k][1].y);
+                fma2(S[r + k][1].z, S[r + k][1].w, u[k], u[k], k1.z, k1.w, S[r + k][1].z, S[r + k][1].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RPL; ++r) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            __stcs(reinterpret_cast<float4 *>(state + (row0 + grp * RPL + r) * D + c * (D / 2)) + l, S[r][c]);
     }
 }
 
@@ -473,13 +547,6 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const DeltaParams p) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) run[r] = next[r];
     }
-}
-
-// 1 / sqrt(x): the hardware's estimate and one step of Newton's method
-__device__ __forceinline__ float inv_sqrt(float x) {
-    float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return x > 0.f ? y * fmaf(-0.5f * x * y, y, 1.5f) : y;
 }
 
 // x0, x1 as three bf16 parts
@@ -1448,7 +1515,7 @@ cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream) {
                    : p.D == 128     ? p.cu ? delta_one_kernel<128, true> : delta_one_kernel<128, false>
                                     : p.cu ? delta_one_kernel<64, true> : delta_one_kernel<64, false>;
     main_kernel_event_before(stream);
-    kernel<<<(unsigned)(p.D == 128 ? states * 4 : states), kRecWarps * 32, 0, stream>>>(p);
+    kernel<<<(unsigned)(p.D == 64 ? states : p.max_seqlen > 1 ? states * 2 : states * 4), kRecWarps * 32, 0, stream>>>(p);
     main_kernel_event_after(stream);
     return cudaGetLastError();
 }
