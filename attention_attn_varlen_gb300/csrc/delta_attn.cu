@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
 //   KQ [i, j]   = (Q; K) K^T     shared x shared
 //   SK [dv, j]  = S_0 K^T        TMEM (three bf16 parts) x shared
 //   SQ [dv, i]  = S_0 Q^T        TMEM (two parts) x shared
-//   U  [dv, i]  = R^T T^T        TMEM (three parts) x shared (three parts): the five products above 2^-16
+//   U  [dv, i]  = R^T T^T        TMEM (three parts) x shared (three parts): the six products above 2^-24
 //   KV [dv, dk] = (w_j U~)^T K   TMEM (three parts) x shared,  w_j = e^{G_n - G_j}
 //   PU [dv, i]  = U~^T P^T       TMEM (two parts) x shared (two parts)
 //
@@ -364,10 +364,15 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
 // 2^-24 of each; S itself stays in fp32 registers.  What only reaches the bf16 output (S_0 and U~
 // there, P) is taken as two parts, 2^-16 of a term against the output's own 2^-8.  T is solved for
 // in fp32: its 16 x 16 diagonal blocks column by column, then the blocks below pairs of them, of
-// 16 and of 32, as -T22 A21 T11 (mma.sync waits behind the chain's products: 11,000 clocks a chunk for this role
-// instead of 8,000).  Sums of decays are in 64 bits and differences of them kept as two fp32 parts.
+// 16 and of 32, as -T22 A21 T11 (by mma.sync, which waits behind the chain's products, slower).  Sums of decays are in 64
+// bits and differences of them kept as two fp32 parts.
 //
-// What bounds it is a chunk's chain S -> SK -> R -> U -> w U~ -> KV -> S; SQ, KQ and PU run in its gaps.
+// What bounds it: a chunk takes 10,200 clocks, the chain S -> SK -> R -> U -> w U~ -> KV -> S about 9,500 of them
+// (2,900 in the products, the rest in the warps that split operands into parts) and the next chunk's T as many
+// beside it; the schedulers they share are busy 59 % of the time and saturated where both run, the tensor core 30 %.
+// SQ, KQ and PU run in the chain's gaps.  36,576 tokens in 16 prompts, 32 heads of 128: 636 us (token after token 10,600);
+// 32,768 tokens of one, 16 heads: 900 us in segments, 2,650 in one piece (35,000); 96 prompts of 1 to 150 tokens, 16
+// heads of 64: 103 us.
 //
 // Roles (32 warps, one CTA per SM that goes over (sequence, value head) units):
 //   0..15   the chain: thread = value dimension and a quarter of dk or of the tokens; S in registers
@@ -375,8 +380,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
 //   24..27  norms of the next chunk, output rows of the one before
 //   28, 29  issue the loads; write the chunks' tables
 //   30      issues the MMAs
-// All of it is meant to stay in the 32 KB of the SM's instruction cache, which the roles share:
-// hence one code site per kind of step, loops where a step repeats, and waits of a few instructions.
+// The roles share the SM's instruction cache, and their code is larger than it: one code site per kind of step, loops
+// where a step repeats, and waits of a few instructions.
 // ---------------------------------------------------------------------------
 constexpr int DC = 64;                       // tokens of a chunk
 constexpr int kDeltaThreads = 32 * 32;

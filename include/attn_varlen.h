@@ -599,20 +599,29 @@ ATTN_API attn_status attn_linear_decode(const void *q, const void *k, const void
  *   beta         float32 [total_tokens, num_heads_v], usually in [0, 1]
  *   qk_norm_eps  >= 0: q and k are divided by sqrt(their sum of squares +
  *                qk_norm_eps) in fp32, per token and head; < 0: taken as they are.
- *                Keys longer than 1 (beta |k|^2 > 2) make the rule diverge
+ *                Those sums must lie between 2^-120 and 2^120 (a key of zeros with
+ *                qk_norm_eps 0 is a NaN).  Keys longer than 1 (beta |k|^2 > 2) make
+ *                the rule diverge
  *   state_cache, state_slots, context_lens, cache_seqlens: as for
  *                attn_linear_step_fwd, with num_heads_v states per slot
  *                (cache_seqlens nullable: no entry was refused)
  *   max_seqlen   host-side upper bound of the lengths (a longer sequence is cut
  *                to it and reported as ATTN_ERR_DEVICE_INDEX); 0: nothing runs
  * A sequence of length 0 leaves its slot as it was.
+ * Up to 16 tokens each (max_seqlen) the states are read and written once and nothing
+ * else is kept; longer ones go in chunks of 64 tokens on the tensor cores, and sequences
+ * much longer than their share of the GPU in segments that run side by side, from states
+ * that a pass before them finds.  States, and all that reaches them, are carried to
+ * 24 bits in every form; chunked outputs take the state before a chunk and the q . k
+ * factors to 16 (the bf16 output has 8).  The form depends on max_seqlen, and the
+ * segments on total_tokens too: other values of them round differently.
  * Strides in elements, 0 = packed; rows of q, k, v and out start on 16-byte boundaries.
  * An infinity or NaN in k, v or beta reaches its own token's output and later ones of
  * its sequence and head as NaN or an infinity (one in v: its value dimension alone),
  * one in q its own token's; nothing else.
  * Limits: head_dim 64 or 128; batch, num_heads_v <= 65535; total_tokens < 2^31 - 1.
- * workspace: attn_delta_workspace_size(...) bytes, 256-byte aligned; it holds
- * nothing from call to call.  Calls that may run at the same time need one each.
+ * workspace: attn_delta_workspace_size(...) bytes for this call's sizes, 256-byte
+ * aligned; it holds nothing from call to call.  Calls that may run at the same time need one each.
  * ------------------------------------------------------------------------ */
 ATTN_API attn_status attn_delta_fwd(const void *q, const void *k, const void *v, void *out, const float *log_decay,
                                     const float *beta, const int32_t *cu_seqlens, float *state_cache,
@@ -656,7 +665,8 @@ ATTN_API attn_status attn_delta_decode(const void *q, const void *k, const void 
  *                of its request; -1 where there are no more candidates
  *   out_scores   float32 [num_groups, num_out]; -inf there
  * A NaN or +inf among a row's logits or in its score takes the row's candidates away
- * and is reported as ATTN_ERR_DEVICE_RANGE.
+ * and is reported as ATTN_ERR_DEVICE_RANGE.  Exponentials are summed in fp32, in an
+ * order that the number of rows and the vocabulary set: equal rows of a call score equal.
  * Limits: num_beams, num_out <= 32; vocab < 2^30; num_groups * num_beams < 2^25.
  * workspace: attn_beam_select_workspace_size(...) bytes, 16-byte aligned; it holds
  * nothing from call to call.  Calls that may run at the same time need one each.

@@ -263,3 +263,23 @@ def test_cached_rows_past_32_bits():
     for x in (kc, vc):
         assert torch.equal(x[1], x[blocks - 1]) and torch.equal(x[0, :4], x[blocks - 2, :4]) and x[0, 4:].eq(0).all()
     assert av.get_last_device_error()[0] == 0
+
+
+def test_more_candidates_than_beams():
+    """Twice as many as beams are chosen, the even ones go on (a caller's own choice among them)."""
+    from attention_attn_varlen_gb300.attention import Beams, PagePool
+    R, W, V = 3, 4, 1000
+    pool = PagePool(R * W * 2, 16, R * W, 2)
+    beams = Beams(pool, torch.arange(R * W, dtype=torch.int32, device="cuda").view(R, W))
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for _ in range(3):
+        x, before, rows = torch.randn(R * W, V, generator=gen, device="cuda"), beams.scores, beams.rows
+        tokens, parents, scores = beams.select(x, 2 * W)
+        beams.advance(parents[:, ::2], scores[:, ::2])
+        assert torch.equal(beams.scores, scores[:, ::2])
+        assert torch.equal(beams.rows.sort(1).values, rows.sort(1).values)
+        all_ = (before.double()[..., None] + torch.log_softmax(x.double(), -1).view(R, W, V)).flatten(1)
+        want = all_.topk(2 * W, 1).values
+        # sums of 1,000 terms in fp32, 2^-24 for each addition, and scores below 64 rounded to fp32
+        assert ((scores.double() - want).abs() <= 1000 * 2.0 ** -24 + 2.0 ** -18).all()
+    assert av.get_last_device_error()[0] == 0
