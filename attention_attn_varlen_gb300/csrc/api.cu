@@ -1525,7 +1525,7 @@ static bool beam_sizes(int num_groups, int num_beams, int vocab, int num_out) {
 // slices.  (The number of SMs is fixed here: the workspace's size, asked for without a device, goes by it.)
 static int beam_slice_len(int rows, int vocab) {
     const int most = (vocab + kBeamSliceElems - 1) / kBeamSliceElems;
-    int slices = 4 * kLinearSms / rows;
+    int slices = 8 * kLinearSms / rows;
     if (slices < 1) slices = 1;
     if (slices > most) slices = most;
     if (slices > 64) slices = 64;

@@ -28,7 +28,7 @@ constexpr float kLowest = -3.4028234663852886e38f;   // the lowest fp32 value, w
 // A second small launch joins the slices and the beams of a group.
 // Every row is cut and summed in the same way: equal rows give equal sums.
 // ---------------------------------------------------------------------------
-constexpr int kScanWarps = 8;
+constexpr int kScanWarps = 4;
 template <typename T> constexpr int kScanAhead = 8 / sizeof(T);   // vectors of a warp in a step (64 bytes a lane)
 constexpr float kFarAbove = 40.f;                    // a logit this far above the sum's reference moves it
 constexpr float kFarBelow = -1e37f;                  // logits times log2(e) stay finite above this
@@ -145,7 +145,7 @@ template <typename T, int MODE> struct Eight {
 };
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kScanWarps * 32, 4) beam_scan_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kScanWarps * 32, 8) beam_scan_kernel(const BeamParams p) {
     __shared__ uint64_t buf[kScanWarps][32];
     __shared__ float2 part[kScanWarps];
     // MODE 0: the next step's vectors arrive while a step's are gone through; a lane reads what it copied itself
