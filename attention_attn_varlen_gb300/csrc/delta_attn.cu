@@ -977,8 +977,15 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             tc_fence_after();
             const int n = uni(info_of(tab_i)->n);
             if (n == 0 || stop[1]) break;
-            if (LOCAL && !keys) {
-                arrive(kq_read);             // no P
+            // up to 32 tokens: the rows behind them are the identity's, in T too
+            const bool low = n <= DC / 2;
+            if ((LOCAL && !keys) || (low && (qd & 1))) {
+                arrive(kq_read);             // no P, or no use of these rows of it
+                if (keys) {
+                    float *to = At + DC / 2 + renew(lane);
+#pragma unroll 8
+                    for (int j = half * 32; j < half * 32 + 32; ++j) to[j * kAStride] = j == DC / 2 + lane ? 1.f : 0.f;
+                }
             } else {
                 const int i = (qd & 1) * 32 + renew(lane);
                 const float *tab = tab_of(tab_i);
@@ -1039,7 +1046,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             // T11 by a warp of A's rows 0..31, T22 by the one that made its block of A.  T11 is there first, so that
             // A21 T11 is made beside T22.
             if (qd == 2) role_sync(3, 64);
-            if (w8 == 2 || w8 == 7) {
+            if (w8 == 2 || (w8 == 7 && !low)) {
                 if (gc > 0) role_wait(1, &go[1], gc - 1);            // U of the chunk before done: T's place
                 const int jb = w8 == 2 ? 0 : 32;
                 {
@@ -1099,11 +1106,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     }
                 }
             }
-            if (w8 != 7) role_sync(4, 224);
+            if (low) role_sync(1, 256);
+            else if (w8 != 7) role_sync(4, 224);
             // the block below, of 32 x 32: X = A21 T11, then -T22 X.  A task has 8 rows and 16 columns, a lane four rows of a
             // column.
 #pragma unroll 1
-            for (int second = 0; second < 2; ++second) {
+            for (int second = low ? 2 : 0; second < 2; ++second) {
                 // (first: of columns 0..15 by the warps of P; 16..31, half as long, by those of A)
                 int task = second ? w8 : ((w8 & 1) + (w8 >> 2) * 2) * 2;
                 if (!second && keys) task = w8 == 2 ? 1 : w8 == 3 ? 3 : w8 == 6 ? 7 : 8;
