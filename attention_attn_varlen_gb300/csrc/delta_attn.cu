@@ -143,26 +143,43 @@ __global__ void __launch_bounds__(kRecWarps * 32, 5) delta_one_kernel(const Delt
             __float2bfloat16_rn(p.scale * rq * fmaf(own * rk, kq, a * sq[0]));
 }
 
+// x0, x1 as three bf16 parts
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    float r0, r1;
+    hi = take_bf16(r0, r1, x0, x1);
+    mid = take_bf16(r0, r1);
+    lo = pack_bf16x2(r0, r1);
+}
+
+// four 8 x 8 matrices of 16-bit elements, their rows' addresses by lane
+__device__ __forceinline__ void four_8x8(uint32_t (&r)[4], const void *at) { ldsm_x4(smem_u32(at), r[0], r[1], r[2], r[3]); }
+// D = A(16x8, row) * B(8x8, col) + D
+__device__ __forceinline__ void mma_bf16_16808(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0));
+}
+
 // Two to kDeltaShort tokens, n, without a product that waits for the one before: with k and q normalised (and q scaled),
 // E_i the decay from the start to token i and R_ij the one from j to i,
 //   u_i = beta_i (v_i - E_i S_0 k_i - sum_{j < i} R_ij k_i.k_j u_j),
 //   o_i = E_i S_0 q_i + sum_{j <= i} R_ij q_i.k_j u_j,   S = E_n S_0 + sum_j R_nj u_j k_j^T,
-// the decays as products of the tokens' own, so that small ones cost nothing.  What the rows share (k, q, R k.k, R q.k) is
-// made once per CTA; a lane has eight columns of 2 D / 32 rows, as many rows twice (k and q) as lanes share a row, so
-// that adding up a token's products leaves a lane one sum.  Issue slots bound it (1,850 instructions a warp, 16 rows), then HBM:
-// 64 sequences of 5 tokens, 32 heads of 128: 60 us (72 token after token; 41 for the states alone).
-template <int D>
+// the decays as products of the tokens' own, so that small ones cost nothing.  The products go through mma.sync, with k
+// and q as they come (bf16, exact; norms and decays are factors of the sums) and S_0 and u as three bf16 parts, 2^-24 of
+// them, S_0 as two for the output.  A warp has 16 rows, S in the fragments' order with the columns of 16 permuted so that
+// a lane's four are neighbours; a lane per row then solves for u.  NT: room for tokens, 8 or 16.  HBM bounds it: 64 sequences
+// of 5 tokens, 32 heads of 128: 52 us (72 token after token, 58 by fp32 products; 41 for the states alone), of 16: 102
+// for 96 of them (216 by fp32 products, 190 as a chunk).
+template <int D, int NT>
 __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const DeltaParams p) {
-    constexpr int LPR = D / 8, RPL = LPR / 2;           // lanes per row, rows per lane
-    constexpr int ROWS = 16, OWN = ROWS * kRecWarps;    // rows of a warp, of a CTA
-    constexpr int CTAS = D / OWN, N = kDeltaShort;
-    static_assert(RPL * 32 / LPR == ROWS && CTAS * OWN == D && N == 16, "layout");
-    __shared__ float4 k_s[N][D / 4], q_s[N][D / 4];
-    __shared__ float v_s[N][OWN], sums[kRecWarps][N][32];       // S_0 k and S_0 q
-    __shared__ float4 kk_s[N][N / 4], qk_s[N][N / 4];           // R k.k, R q.k
-    __shared__ float4 u_s[kRecWarps][N][ROWS / 4];              // R_nj u_j
-    __shared__ float a_s[N], beta_s[N], e_s[N], w_s[N];         // e^g, beta, E, R_n
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1), grp = lane / LPR;
+    constexpr int ROWS = 16, OWN = ROWS * kRecWarps, CTAS = D / OWN;    // rows of a warp, of a CTA; CTAs per state
+    constexpr int KS = D / 16, LPT = D / 8;                             // steps of 16 columns; lanes per token
+    __shared__ __align__(16) uint16_t k_s[NT][D + 8], q_s[NT][D + 8];   // columns permuted
+    __shared__ float v_s[NT][OWN], sk_s[kRecWarps][NT][ROWS], sq_s[kRecWarps][NT][ROWS], u_s[kRecWarps][NT][ROWS];
+    __shared__ float kk_s[NT][NT], qk_s[NT][NT];                        // R k.k, R q.k
+    __shared__ float a_s[NT], beta_s[NT], rk_s[NT], rq_s[NT], ek_s[NT], eq_s[NT], w_s[NT], en_s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPT - 1);
+    const int g = lane >> 2, t = lane & 3;                              // of a fragment: row or token, pair of columns
     const int unit = blockIdx.x / CTAS, b = unit / p.Hv, h = unit - b * p.Hv, hk = h / p.G;
     const int cta_row = (blockIdx.x - unit * CTAS) * OWN, row0 = cta_row + warp * ROWS;
     const bool first_cta = cta_row == 0, report = h == 0 && first_cta && threadIdx.x == 0;
@@ -172,52 +189,57 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
     bool from;
     float *state = sequence_state<SRC_DELTA, true>(p, p.Hv, b, h, from, report && n > 0);
     if (n == 0) return;
-    // loads in the order of their use: LPR lanes per token with eight columns each, eight threads per token's values; S
-    uint4 kr, qr, vr = make_uint4(0u, 0u, 0u, 0u);
-    float g, beta;
+    // loads in the order of their use: LPT lanes per token with eight columns each, eight threads per token's values; S
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 kr, qr, vr = none;
+    float decay, beta;
     auto load = [&](int i) {
-        const int64_t t = t0 + i;
-        kr = *(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + (int64_t)hk * D) + l);
-        qr = *(reinterpret_cast<const uint4 *>(p.q + t * p.q_stride + (int64_t)hk * D) + l);
-        beta = __ldg(p.beta + t * p.beta_stride + h);
-        g = __ldg(p.log_decay + t * p.decay_stride + h);
+        kr = qr = none;
+        decay = beta = 0.f;
+        if (i < n) {
+            const int64_t at = t0 + i;
+            kr = *(reinterpret_cast<const uint4 *>(p.k + at * p.k_stride + (int64_t)hk * D) + l);
+            qr = *(reinterpret_cast<const uint4 *>(p.q + at * p.q_stride + (int64_t)hk * D) + l);
+            beta = __ldg(p.beta + at * p.beta_stride + h);
+            decay = __ldg(p.log_decay + at * p.decay_stride + h);
+        }
     };
-    load(min(warp * (32 / LPR) + grp, n - 1));
-    static_assert(OWN == 64 && N * 8 == kRecWarps * 32, "values");
+    load(warp * (32 / LPT) + lane / LPT);
+    static_assert(OWN == 64 && NT * 8 <= kRecWarps * 32, "values");
     const int vi = threadIdx.x >> 3, vc = threadIdx.x & 7;
     if (vi < n) vr = *(reinterpret_cast<const uint4 *>(p.v + (t0 + vi) * p.v_stride + (int64_t)h * D + cta_row) + vc);
-    float4 S[RPL][2];                                   // columns 4 l .. and D / 2 + 4 l ..
+    float4 S[KS][2];                                    // rows g, g + 8; columns 16 s + 4 t ..
 #pragma unroll
-    for (int r = 0; r < RPL; ++r) {
+    for (int s = 0; s < KS; ++s) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            S[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (from) S[r][c] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + grp * RPL + r) * D + c * (D / 2)) + l);
+        for (int r = 0; r < 2; ++r) {
+            S[s][r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (from) S[s][r] = __ldcs(reinterpret_cast<const float4 *>(state + (row0 + g + 8 * r) * D + 16 * s) + t);
         }
     }
-    for (int i0 = warp * (32 / LPR); i0 < n; i0 += kRecWarps * 32 / LPR) {
-        const int i = min(i0 + grp, n - 1);             // (the last one again where there are no more)
-        if (i0 >= kRecWarps * 32 / LPR) load(i);
-        const uint32_t kw[4] = {kr.x, kr.y, kr.z, kr.w}, qw[4] = {qr.x, qr.y, qr.z, qr.w};
-        float k[8], q[8], ks = 0.f, qs = 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            k[2 * x] = __uint_as_float(kw[x] << 16), k[2 * x + 1] = __uint_as_float(kw[x] & 0xFFFF0000u);
-            q[2 * x] = __uint_as_float(qw[x] << 16), q[2 * x + 1] = __uint_as_float(qw[x] & 0xFFFF0000u);
-        }
+    for (int i0 = warp * (32 / LPT); i0 < NT; i0 += kRecWarps * 32 / LPT) {
+        const int i = i0 + lane / LPT;
+        if (i0 >= kRecWarps * 32 / LPT) load(i);
         float rk = 1.f, rq = p.scale;
         if (p.norm) {
+            const uint32_t kw[4] = {kr.x, kr.y, kr.z, kr.w}, qw[4] = {qr.x, qr.y, qr.z, qr.w};
+            float ks = 0.f, qs = 0.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) ks = fmaf(k[x], k[x], ks), qs = fmaf(q[x], q[x], qs);
-            rk = inv_sqrt(row_sum<LPR>(ks) + p.eps);
-            rq = p.scale * inv_sqrt(row_sum<LPR>(qs) + p.eps);
+            for (int x = 0; x < 4; ++x) {
+                const float k0 = __uint_as_float(kw[x] << 16), k1 = __uint_as_float(kw[x] & 0xFFFF0000u);
+                const float q0 = __uint_as_float(qw[x] << 16), q1 = __uint_as_float(qw[x] & 0xFFFF0000u);
+                ks = fmaf(k0, k0, fmaf(k1, k1, ks)), qs = fmaf(q0, q0, fmaf(q1, q1, qs));
+            }
+            rk = inv_sqrt(row_sum<LPT>(ks) + p.eps);
+            rq = p.scale * inv_sqrt(row_sum<LPT>(qs) + p.eps);
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            k_s[i][2 * l + x] = make_float4(k[4 * x] * rk, k[4 * x + 1] * rk, k[4 * x + 2] * rk, k[4 * x + 3] * rk);
-            q_s[i][2 * l + x] = make_float4(q[4 * x] * rq, q[4 * x + 1] * rq, q[4 * x + 2] * rq, q[4 * x + 3] * rq);
-        }
-        if (l == 0) a_s[i] = delta_decay(p, g, first_cta), beta_s[i] = beta;
+        // columns 4 t, 4 t + 1 of 16 at 2 t, 2 t + 1; 4 t + 2, 4 t + 3 at 8 + 2 t, 8 + 2 t + 1
+        const int at = (l >> 1) * 16 + (l & 1) * 4;
+        *reinterpret_cast<uint2 *>(&k_s[i][at]) = make_uint2(kr.x, kr.z);
+        *reinterpret_cast<uint2 *>(&k_s[i][at + 8]) = make_uint2(kr.y, kr.w);
+        *reinterpret_cast<uint2 *>(&q_s[i][at]) = make_uint2(qr.x, qr.z);
+        *reinterpret_cast<uint2 *>(&q_s[i][at + 8]) = make_uint2(qr.y, qr.w);
+        if (l == 0) a_s[i] = delta_decay(p, decay, first_cta), beta_s[i] = beta, rk_s[i] = rk, rq_s[i] = rq;
     }
     if (vi < n) {
         float4 *to = reinterpret_cast<float4 *>(v_s[vi]) + 2 * vc;
@@ -227,115 +249,143 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
                             __uint_as_float(vr.w & 0xFFFF0000u));
     }
     __syncthreads();
-    // k_i.k_j and q_i.k_j, j <= i, eight lanes a pair
-    for (int x0 = warp * 4; x0 < n * (n + 1) / 2; x0 += kRecWarps * 4) {
-        const int x = min(x0 + (lane >> 3), n * (n + 1) / 2 - 1), l8 = lane & 7;
-        int i = 0;
+    // k_i.k_j (even warps), q_i.k_j (odd ones), eight j a warp
+    if ((warp >> 1) * 8 < NT) {
+        const bool of_q = warp & 1;
+        const int j0 = (warp >> 1) * 8 + 2 * t, lr = lane & 7, lc = (lane >> 3) * 8;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int m = 1; m < N; ++m) i += x >= m * (m + 1) / 2;
-        const int j = x - i * (i + 1) / 2;
-        float kk0 = 0.f, kk1 = 0.f, qk0 = 0.f, qk1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            const float4 kj = k_s[j][c * 8 + l8], ki = k_s[i][c * 8 + l8], qi = q_s[i][c * 8 + l8];
-            fma2(kk0, kk1, ki.x, ki.y, kj.x, kj.y, kk0, kk1);
-            fma2(kk0, kk1, ki.z, ki.w, kj.z, kj.w, kk0, kk1);
-            fma2(qk0, qk1, qi.x, qi.y, kj.x, kj.y, qk0, qk1);
-            fma2(qk0, qk1, qi.z, qi.w, kj.z, kj.w, qk0, qk1);
+        for (int s = 0; s < KS; s += 2) {
+            uint32_t lo[4], hi[4] = {0u, 0u, 0u, 0u}, kj[4];
+            four_8x8(lo, of_q ? &q_s[lr][s * 16 + lc] : &k_s[lr][s * 16 + lc]);
+            if (NT == 16) four_8x8(hi, of_q ? &q_s[NT - 8 + lr][s * 16 + lc] : &k_s[NT - 8 + lr][s * 16 + lc]);
+            four_8x8(kj, &k_s[(warp >> 1) * 8 + lr][s * 16 + lc]);
+            mma_bf16_16816(c, lo[0], hi[0], lo[1], hi[1], kj[0], kj[1]);
+            mma_bf16_16816(c, lo[2], hi[2], lo[3], hi[3], kj[2], kj[3]);
         }
-        const float kk = row_sum<8>(kk0 + kk1), qk = row_sum<8>(qk0 + qk1);
-        float between = 1.f;
-        for (int m = j + 1; m <= i; ++m) between *= a_s[m];
-        if (l8 == 0) {
-            reinterpret_cast<float *>(kk_s[i])[j] = kk * between;
-            reinterpret_cast<float *>(qk_s[i])[j] = qk * between;
-            if (i == n - 1) w_s[j] = between;
-            if (j == 0) e_s[i] = between * a_s[0];
+        const float rj0 = rk_s[j0], rj1 = rk_s[j0 + 1];
+#pragma unroll
+        for (int r = 0; r < NT / 8; ++r) {
+            const int i = g + 8 * r;
+            if (i < n && j0 <= i) {
+                const float ri = of_q ? rq_s[i] : rk_s[i];
+                float *to = of_q ? qk_s[i] : kk_s[i];
+                float x = 1.f;                          // R of j0 + 1, then of j0
+                for (int m = i; m > j0 + 1; --m) x *= a_s[m];
+                if (j0 < i) {
+                    to[j0 + 1] = c[2 * r + 1] * x * ri * rj1;
+                    x *= a_s[j0 + 1];
+                }
+                to[j0] = c[2 * r] * x * ri * rj0;
+            }
         }
     }
-    // S_0 k and S_0 q: half of the values a lane carries go to the other half of the lanes in every step
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        const float4 k0 = k_s[i][l], k1 = k_s[i][D / 8 + l], q0 = q_s[i][l], q1 = q_s[i][D / 8 + l];
-        float x[LPR];
+    if (const int i = (int)threadIdx.x - (kRecWarps * 32 - NT); i >= 0 && i < n) {
+        float e = 1.f, w = 1.f;
+        for (int m = 0; m <= i; ++m) e *= a_s[m];
+        for (int m = i + 1; m < n; ++m) w *= a_s[m];
+        ek_s[i] = e * rk_s[i], eq_s[i] = e * rq_s[i], w_s[i] = w * rk_s[i];
+        if (i == n - 1) en_s = e;
+    }
+    // S_0 k and S_0 q
+    {
+        float ck[NT / 8][4] = {}, cq[NT / 8][4] = {};
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-            float c, d;
-            fma2(c, d, S[r][0].x, S[r][0].y, k0.x, k0.y, 0.f, 0.f);
-            fma2(c, d, S[r][0].z, S[r][0].w, k0.z, k0.w, c, d);
-            fma2(c, d, S[r][1].x, S[r][1].y, k1.x, k1.y, c, d);
-            fma2(c, d, S[r][1].z, S[r][1].w, k1.z, k1.w, c, d);
-            x[r] = c + d;
-            fma2(c, d, S[r][0].x, S[r][0].y, q0.x, q0.y, 0.f, 0.f);
-            fma2(c, d, S[r][0].z, S[r][0].w, q0.z, q0.w, c, d);
-            fma2(c, d, S[r][1].x, S[r][1].y, q1.x, q1.y, c, d);
-            fma2(c, d, S[r][1].z, S[r][1].w, q1.z, q1.w, c, d);
-            x[RPL + r] = c + d;
+        for (int s = 0; s < KS; s += 2) {
+            uint32_t kb[NT / 8][4], qb[NT / 8][4];
+#pragma unroll
+            for (int x = 0; x < NT / 8; ++x) {
+                four_8x8(kb[x], &k_s[8 * x + (lane & 7)][s * 16 + (lane >> 3) * 8]);
+                four_8x8(qb[x], &q_s[8 * x + (lane & 7)][s * 16 + (lane >> 3) * 8]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t a[3][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    split3(S[s + y][r].x, S[s + y][r].y, a[0][r], a[1][r], a[2][r]);
+                    split3(S[s + y][r].z, S[s + y][r].w, a[0][2 + r], a[1][2 + r], a[2][2 + r]);
+                }
+#pragma unroll
+                for (int part = 2; part >= 0; --part) {
+#pragma unroll
+                    for (int x = 0; x < NT / 8; ++x) {
+                        mma_bf16_16816(ck[x], a[part][0], a[part][1], a[part][2], a[part][3], kb[x][2 * y], kb[x][2 * y + 1]);
+                        if (part < 2)
+                            mma_bf16_16816(cq[x], a[part][0], a[part][1], a[part][2], a[part][3], qb[x][2 * y],
+                                           qb[x][2 * y + 1]);
+                    }
+                }
+            }
         }
 #pragma unroll
-        for (int w = LPR / 2; w > 0; w /= 2) {
-            const bool up = lane & w;
+        for (int x = 0; x < NT / 8; ++x) {
 #pragma unroll
-            for (int r = 0; r < w; ++r)
-                x[r] = (up ? x[r + w] : x[r]) + __shfl_xor_sync(0xffffffffu, up ? x[r] : x[r + w], w);
+            for (int y = 0; y < 4; ++y) {
+                sk_s[warp][8 * x + 2 * t + (y & 1)][g + 8 * (y >> 1)] = ck[x][y];
+                sq_s[warp][8 * x + 2 * t + (y & 1)][g + 8 * (y >> 1)] = cq[x][y];
+            }
         }
-        sums[warp][i][lane] = x[0];                     // (value l of lane group grp)
     }
     __syncthreads();
     // a lane per row
     if (lane < ROWS) {
-        const int at = lane / RPL * LPR + lane % RPL;
         __nv_bfloat16 *out = p.out + t0 * p.out_stride + (int64_t)h * D + row0 + lane;
-        float u[N];
+        float u[NT];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < NT; ++i) {
+            float last = 0.f;
             if (i < n) {
-                const float e = e_s[i];
-                float x = fmaf(-e, sums[warp][i][at], v_s[i][warp * ROWS + lane]), o = e * sums[warp][i][at + RPL];
+                float x = fmaf(-ek_s[i], sk_s[warp][i][lane], v_s[i][warp * ROWS + lane]), o = eq_s[i] * sq_s[warp][i][lane];
 #pragma unroll
                 for (int j = 0; j < i; ++j) {
-                    x = fmaf(-reinterpret_cast<const float *>(kk_s[i])[j], u[j], x);
-                    o = fmaf(reinterpret_cast<const float *>(qk_s[i])[j], u[j], o);
+                    x = fmaf(-kk_s[i][j], u[j], x);
+                    o = fmaf(qk_s[i][j], u[j], o);
                 }
                 u[i] = beta_s[i] * x;
-                o = fmaf(reinterpret_cast<const float *>(qk_s[i])[i], u[i], o);
+                o = fmaf(qk_s[i][i], u[i], o);
                 out[i * p.out_stride] = __float2bfloat16_rn(o);
-                reinterpret_cast<float *>(u_s[warp][i])[lane] = w_s[i] * u[i];
+                last = w_s[i] * u[i];
             }
+            u_s[warp][i][lane] = last;
         }
     }
     if (!state) return;
     __syncwarp();
-    const float e = e_s[n - 1];
+    const float e = en_s;
+    uint32_t u[3][NT / 4];                              // rows g, g + 8; tokens 2 t, 2 t + 1, then those behind 8
 #pragma unroll
-    for (int r = 0; r < RPL; ++r) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            fma2(S[r][c].x, S[r][c].y, e, e, S[r][c].x, S[r][c].y, 0.f, 0.f);
-            fma2(S[r][c].z, S[r][c].w, e, e, S[r][c].z, S[r][c].w, 0.f, 0.f);
-        }
+    for (int x = 0; x < NT / 4; ++x) {
+        const int i = 2 * t + 8 * (x >> 1), r = g + 8 * (x & 1);
+        split3(u_s[warp][i][r], u_s[warp][i + 1][r], u[0][x], u[1][x], u[2][x]);
     }
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        const float4 k0 = k_s[i][l], k1 = k_s[i][D / 8 + l];
 #pragma unroll
-        for (int r = 0; r < RPL; r += 4) {
-            const float4 u4 = u_s[warp][i][(grp * RPL + r) / 4];
-            const float u[4] = {u4.x, u4.y, u4.z, u4.w};
+    for (int s = 0; s < KS; s += NT == 8 ? 2 : 1) {
+        uint32_t kb[4];                                 // columns of 8: four of 8 tokens, two of 16
+        if (NT == 8) ldsm_x4_t(smem_u32(&k_s[lane & 7][s * 16 + (lane >> 3) * 8]), kb[0], kb[1], kb[2], kb[3]);
+        else ldsm_x4_t(smem_u32(&k_s[(lane & 15) & (NT - 1)][s * 16 + (lane >> 4) * 8]), kb[0], kb[1], kb[2], kb[3]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                fma2(S[r + k][0].x, S[r + k][0].y, u[k], u[k], k0.x, k0.y, S[r + k][0].x, S[r + k][0].y);
-                fma2(S[r + k][0].z, S[r + k][0].w, u[k], u[k], k0.z, k0.w, S[r + k][0].z, S[r + k][0].w);
-                fma2(S[r + k][1].x, S[r + k][1].y, u[k], u[k], k1.x, k1.y, S[r + k][1].x, S[r + k][1].y);
-                fma2(S[r + k][1].z, S[r + k][1].w, u[k], u[k], k1.z, k1.w, S[r + k][1].z, S[r + k][1].w);
+        for (int x = 0; x < (NT == 8 ? 4 : 2); ++x) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int part = 2; part >= 0; --part) {
+                if (NT == 8) mma_bf16_16808(c, u[part][0], u[part][1], kb[x]);
+                else mma_bf16_16816(c, u[part][0], u[part][1], u[part][NT / 4 - 2], u[part][NT / 4 - 1], kb[(2 * x) & 3],
+                                    kb[(2 * x + 1) & 3]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float4 &y = S[s + x / 2][r];
+                if (x & 1) fma2(y.z, y.w, e, e, y.z, y.w, c[2 * r], c[2 * r + 1]);
+                else fma2(y.x, y.y, e, e, y.x, y.y, c[2 * r], c[2 * r + 1]);
             }
         }
     }
 #pragma unroll
-    for (int r = 0; r < RPL; ++r) {
+    for (int s = 0; s < KS; ++s) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            __stcs(reinterpret_cast<float4 *>(state + (row0 + grp * RPL + r) * D + c * (D / 2)) + l, S[r][c]);
+        for (int r = 0; r < 2; ++r)
+            __stcs(reinterpret_cast<float4 *>(state + (row0 + g + 8 * r) * D + 16 * s) + t, S[s][r]);
     }
 }
 
@@ -607,14 +657,6 @@ __global__ void __launch_bounds__(2 * D) delta_join_kernel(const DeltaParams p) 
     }
 }
 template <int D> constexpr int kJoinBytes = (kJoinStages * kJoinRows + 2 * 16) * D * 4;
-
-// x0, x1 as three bf16 parts
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    float r0, r1;
-    hi = take_bf16(r0, r1, x0, x1);
-    mid = take_bf16(r0, r1);
-    lo = pack_bf16x2(r0, r1);
-}
 
 // A bounded wait in as few instructions as it goes; a try takes the hardware 50 clocks or more, so
 // that it gives up after half a second or so.
@@ -1581,7 +1623,8 @@ cudaError_t launch_delta_chunks(const CUtensorMap &qmap, const CUtensorMap &kmap
 
 cudaError_t launch_delta_recurrent(const DeltaParams &p, cudaStream_t stream) {
     const int64_t states = (int64_t)p.batch * p.Hv;
-    auto *kernel = p.max_seqlen > 1 ? p.D == 128 ? delta_few_kernel<128> : delta_few_kernel<64>
+    auto *kernel = p.max_seqlen > 8   ? p.D == 128 ? delta_few_kernel<128, 16> : delta_few_kernel<64, 16>
+                   : p.max_seqlen > 1 ? p.D == 128 ? delta_few_kernel<128, 8> : delta_few_kernel<64, 8>
                    : p.D == 128     ? p.cu ? delta_one_kernel<128, true> : delta_one_kernel<128, false>
                                     : p.cu ? delta_one_kernel<64, true> : delta_one_kernel<64, false>;
     main_kernel_event_before(stream);

@@ -612,8 +612,8 @@ ATTN_API attn_status attn_linear_decode(const void *q, const void *k, const void
  * else is kept; longer ones go in chunks of 64 tokens on the tensor cores, and sequences
  * much longer than their share of the GPU in segments that run side by side, from states
  * that a pass before them finds.  States, and all that reaches them, are carried to
- * 24 bits in every form; chunked outputs take the state before a chunk and the q . k
- * factors to 16 (the bf16 output has 8).  The form depends on max_seqlen, and the
+ * 24 bits in every form; outputs take the state before a chunk, or before a few tokens,
+ * to 16, as chunked ones the q . k factors (the bf16 output has 8).  The form depends on max_seqlen, and the
  * segments on total_tokens too: other values of them round differently.
  * Strides in elements, 0 = packed; rows of q, k, v and out start on 16-byte boundaries.
  * An infinity or NaN in k, v or beta reaches its own token's output and later ones of
