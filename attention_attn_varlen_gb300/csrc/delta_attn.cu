@@ -1046,19 +1046,29 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     for (int j = 0; j < 8; j += 4) {
                         const float4 a = *reinterpret_cast<const float4 *>(tab + T_GHI + j0 + j);
                         const float4 b = *reinterpret_cast<const float4 *>(tab + T_GLO + j0 + j);
-                        x[j] = ghi - a.x, x[j + 1] = ghi - a.y, x[j + 2] = ghi - a.z, x[j + 3] = ghi - a.w;
-                        g[j] = glo - b.x, g[j + 1] = glo - b.y, g[j + 2] = glo - b.z, g[j + 3] = glo - b.w;
+                        fma2(x[j], x[j + 1], a.x, a.y, -1.f, -1.f, ghi, ghi);
+                        fma2(x[j + 2], x[j + 3], a.z, a.w, -1.f, -1.f, ghi, ghi);
+                        fma2(g[j], g[j + 1], b.x, b.y, -1.f, -1.f, glo, glo);
+                        fma2(g[j + 2], g[j + 3], b.z, b.w, -1.f, -1.f, glo, glo);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = ex2(x[j] + g[j]) * factor;
+                    for (int j = 0; j < 8; j += 2) {
+                        add2(x[j], x[j + 1], g[j], g[j + 1]);
+                        fma2(x[j], x[j + 1], ex2(x[j]), ex2(x[j + 1]), factor, factor, 0.f, 0.f);
+                    }
                     tc_wait_ld();
-                    float z = 0.f;               // NaN once something non-finite went by
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 8; j += 2)
+                        fma2(x[j], x[j + 1], x[j], x[j + 1], __uint_as_float(next[j]), __uint_as_float(next[j + 1]), 0.f, 0.f);
+                    if (!__all_sync(0xffffffffu, j0 + 8 <= see)) {
                         // masked by choice, not by a factor, which would keep a NaN
-                        x[j] = j0 + j < see ? x[j] * __uint_as_float(next[j]) : 0.f;
-                        z = fmaf(x[j], 0.f, z);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = j0 + j < see ? x[j] : 0.f;
                     }
+                    float z = 0.f, z1 = 0.f;     // NaN once something non-finite went by
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) fma2(z, z1, x[j], x[j + 1], 0.f, 0.f, z, z1);
+                    z += z1;
                     if (keys && !(z == 0.f)) {
                         // a zero of T would not keep it from earlier tokens: 0 here, and NaN from this token on later
                         atomicMin(&info_of(tab_i)->bad, i);
