@@ -844,10 +844,11 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             if (warp == 0) {
                 role_wait(0, &tab_full[tab_i], turn);
                 if (info_of(tab_i)->n) {
-                    role_wait(0, &v_full[gc & 1], gc >> 1);
-                    role_wait(0, &norms[gc & 1], gc >> 1);
-                    role_wait(0, kq_read, gc);
-                    if (!LOCAL && gc > 0) role_wait(0, &o_done[(gc - 1) & 1], (gc - 1) >> 1);
+                    // four barriers at once, one a lane
+                    const bool done = !LOCAL && gc > 0 && lane == 2;
+                    const int turn2 = done ? (gc - 1) >> 1 : gc >> 1;
+                    uint64_t *bar = done ? &o_done[(gc - 1) & 1] : lane == 1 ? &norms[gc & 1] : &v_full[gc & 1];
+                    role_wait(0, lane == 3 ? kq_read : bar, lane == 3 ? gc : turn2);
                 }
             }
             role_sync(0, 512);
@@ -1010,10 +1011,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         for (int gc = 0;; ++gc) {
             if (w8 == 0) {
                 role_wait(1, &tab_full[tab_i], turn);
-                if (info_of(tab_i)->n) {
-                    role_wait(1, &norms[gc & 1], gc >> 1);
-                    role_wait(1, kq_done, gc);
-                }
+                if (info_of(tab_i)->n) role_wait(1, lane ? kq_done : &norms[gc & 1], lane ? gc : gc >> 1);
             }
             role_sync(1, 256);
             tc_fence_after();
