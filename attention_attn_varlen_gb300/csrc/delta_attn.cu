@@ -709,14 +709,18 @@ struct DeltaWalk {
     }
 };
 
-// non-finite entries of x become 0; returns the first one's place, 16 if there is none
-__device__ __forceinline__ int drop_non_finite(float (&x)[16]) {
+// non-finite entries among x[from + 4 g], x[from + 4 g + 1] become 0; returns the first one's 4 g or 4 g + 1, 16 if there
+// is none
+__device__ __forceinline__ int drop_non_finite(float (&x)[16], int from) {
     int first = 16;
 #pragma unroll
-    for (int j = 15; j >= 0; --j) {
-        const bool bad = !(fabsf(x[j]) < INFINITY);
-        first = bad ? j : first;
-        x[j] = bad ? 0.f : x[j];
+    for (int g = 12; g >= 0; g -= 4) {
+#pragma unroll
+        for (int e = 1; e >= 0; --e) {
+            const bool bad = !(fabsf(x[from + g + e]) < INFINITY);
+            first = bad ? g + e : first;
+            x[from + g + e] = bad ? 0.f : x[from + g + e];
+        }
     }
     return first;
 }
@@ -892,41 +896,46 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 role_sync(0, 512);
                 tc_fence_after();
                 if (real) {
-                    const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, part = tid >> 7, dv = tid & 127;
-                    const uint32_t lane_base = tmem + ((uint32_t)grp << 21);
+                    // in 8x8 fragments: 16 value dimensions and 32 tokens a warp; pair 2 g + r of a thread: tokens
+                    // 8 g + q2, + 1 of its dimension dv + 8 r
+                    const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, low = (tid >> 7) & 1, th = (tid >> 8) * 32;
+                    const int l = tid & 31, q2 = (l & 3) * 2, dv0 = grp * 32 + low * 16;
+                    const uint32_t lane_base = tmem + ((uint32_t)grp << 21) + ((uint32_t)low << 20);
                     uint32_t u[16];
-                    tmem_ld16(lane_base + (pass ? TM_U : TM_SK) + part * 16, u);
-                    const float *tab = tab_of(tab_i) + part * 16;
+                    tmem_ld_16x256b_x4(lane_base + (pass ? TM_U : TM_SK) + th, u);
+                    const float *tab = tab_of(tab_i) + th + q2;
                     float x[16];
                     if (pass) {
                         tc_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(u[j]);
                     } else {
-                        // its value dimension in the V tile, its tokens part * 16 ..
-                        const uint32_t at = smb + S::kVOff + (gc & 1) * S::kVBytes + ((dv & (D - 1)) >> 6) * kDeltaPanel +
-                                            part * 16 * 128 + (dv & 7) * 2, ch = ((dv & 63) >> 3) << 4;
+                        // V transposed on the way: a matrix is 8 tokens of 8 dimensions, chunks swizzled by token
+                        const uint32_t at = smb + S::kVOff + (gc & 1) * S::kVBytes + ((dv0 & (D - 1)) >> 6) * kDeltaPanel +
+                                            (th + (l >> 4) * 8 + (l & 7)) * 128 +
+                                            (((((dv0 & 63) >> 3) + ((l >> 3) & 1)) ^ (l & 7)) << 4);
+                        uint32_t v[8];
+                        ldsm_x4_t(at, v[0], v[1], v[2], v[3]);
+                        ldsm_x4_t(at + 16 * 128, v[4], v[5], v[6], v[7]);
+                        if (LOCAL && info_of(tab_i)->ident) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 b = *reinterpret_cast<const float4 *>(tab + T_B + j);
-                            float v[4];
+                            for (int k = 0; k < 8; ++k) v[k] = 0u;
+                        }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint16_t r;
-                                asm("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at + (j + k) * 128 + (ch ^ (((j + k) & 7) << 4))));
-                                v[k] = __uint_as_float((uint32_t)r << 16);
-                            }
-                            if (LOCAL && info_of(tab_i)->ident) v[0] = v[1] = v[2] = v[3] = 0.f;
-                            fma2(x[j], x[j + 1], b.x, b.y, v[0], v[1], 0.f, 0.f);
-                            fma2(x[j + 2], x[j + 3], b.z, b.w, v[2], v[3], 0.f, 0.f);
+                        for (int g = 0; g < 4; ++g) {
+                            const float2 b = *reinterpret_cast<const float2 *>(tab + T_B + 8 * g);
+#pragma unroll
+                            for (int k = 2 * g; k < 2 * g + 2; ++k)
+                                fma2(x[2 * k], x[2 * k + 1], b.x, b.y, __uint_as_float(v[k] << 16),
+                                     __uint_as_float(v[k] & 0xFFFF0000u), 0.f, 0.f);
                         }
                         tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 c = *reinterpret_cast<const float4 *>(tab + T_C + j);
-                            fma2(x[j], x[j + 1], c.x, c.y, __uint_as_float(u[j]), __uint_as_float(u[j + 1]), x[j], x[j + 1]);
-                            fma2(x[j + 2], x[j + 3], c.z, c.w, __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]),
-                                 x[j + 2], x[j + 3]);
+                        for (int g = 0; g < 4; ++g) {
+                            const float2 c = *reinterpret_cast<const float2 *>(tab + T_C + 8 * g);
+#pragma unroll
+                            for (int j = 4 * g; j < 4 * g + 4; j += 2)
+                                fma2(x[j], x[j + 1], c.x, c.y, __uint_as_float(u[j]), __uint_as_float(u[j + 1]), x[j], x[j + 1]);
                         }
                     }
                     float z0 = 0.f, z1 = 0.f;        // NaN once something non-finite went by
@@ -934,8 +943,11 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     for (int j = 0; j < 16; j += 2) fma2(z0, z1, x[j], x[j + 1], 0.f, 0.f, z0, z1);
                     if (__any_sync(0xffffffffu, !(z0 + z1 == 0.f))) {
                         // the triangles' zeros would not keep it from earlier tokens
-                        const int first = drop_non_finite(x);
-                        if (first < 16) atomicMin(bad_at + (gc & 1) * 128 + dv, part * 16 + first);
+                        int *bad = bad_at + (gc & 1) * 128 + dv0 + (l >> 2);
+                        const int first[2] = {drop_non_finite(x, 0), drop_non_finite(x, 2)};
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            if (first[r] < 16) atomicMin(bad + 8 * r, th + (first[r] >> 2) * 8 + q2 + (first[r] & 1));
                     }
                     uint32_t r1[8], r2[8], r3[8];
                     if (pass) {
@@ -946,21 +958,21 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                 r1[k] = take_bf16(y0, y1, x[2 * k], x[2 * k + 1]);
                                 r2[k] = pack_bf16x2(y0, y1);
                             }
-                            tmem_st8(lane_base + TM_UO + part * 8, r1);
-                            tmem_st8(lane_base + TM_UO + 32 + part * 8, r2);
+                            tmem_st_16x128b_x4(lane_base + TM_UO + th / 2, r1);
+                            tmem_st_16x128b_x4(lane_base + TM_UO + 32 + th / 2, r2);
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 w = *reinterpret_cast<const float4 *>(tab + T_W + j);
-                            fma2(x[j], x[j + 1], w.x, w.y, x[j], x[j + 1], 0.f, 0.f);
-                            fma2(x[j + 2], x[j + 3], w.z, w.w, x[j + 2], x[j + 3], 0.f, 0.f);
+                        for (int g = 0; g < 4; ++g) {
+                            const float2 w = *reinterpret_cast<const float2 *>(tab + T_W + 8 * g);
+#pragma unroll
+                            for (int j = 4 * g; j < 4 * g + 4; j += 2) fma2(x[j], x[j + 1], w.x, w.y, x[j], x[j + 1], 0.f, 0.f);
                         }
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) split3(x[2 * k], x[2 * k + 1], r1[k], r2[k], r3[k]);
-                    tmem_st8(lane_base + TM_R + part * 8, r1);
-                    tmem_st8(lane_base + TM_R + 32 + part * 8, r2);
-                    tmem_st8(lane_base + TM_R + 64 + part * 8, r3);
+                    tmem_st_16x128b_x4(lane_base + TM_R + th / 2, r1);
+                    tmem_st_16x128b_x4(lane_base + TM_R + 32 + th / 2, r2);
+                    tmem_st_16x128b_x4(lane_base + TM_R + 64 + th / 2, r3);
                     tc_wait_st();
                 }
                 tc_fence_before();
