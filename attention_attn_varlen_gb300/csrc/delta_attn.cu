@@ -1170,8 +1170,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             }
             if (low) role_sync(1, 256);
             else if (w8 != 7) role_sync(4, 224);
-            // the block below, of 32 x 32: X = A21 T11, then -T22 X.  A task has 8 rows and 16 columns, a lane four rows of a
-            // column.
+            // the block below, of 32 x 32: X = A21 T11, then -T22 X.  A task has 8 rows and 16 columns; a lane adds up
+            // every other term for four rows of two columns and comes to hold one of them.
 #pragma unroll 1
             for (int second = low ? 2 : 0; second < 2; ++second) {
                 // (first: of columns 0..15 by the warps of P; 16..31, half as long, by those of A)
@@ -1179,44 +1179,35 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 if (!second && keys) task = w8 == 2 ? 1 : w8 == 3 ? 3 : w8 == 6 ? 7 : 8;
 #pragma unroll 1
                 for (; task < 8; task = !second && task == 3 ? 5 : 8) {
-                    const int l = renew(lane), c = (task & 1) * 16 + (l & 15), r0 = (task >> 1) * 8 + (l >> 4) * 4;
+                    const int l = renew(lane), odd = l >> 4, c = (task & 1) * 16 + (l & 7) * 2;
+                    const int r0 = (task >> 1) * 8 + ((l >> 3) & 1) * 4;
                     // T11's columns begin at the diagonal, T22's rows end there
                     const int m0 = second ? 0 : (task & 1) * 16, m1 = second && task < 4 ? 16 : 32;
-                    const float *left = At + (32 * second + m0) * kAStride + 32 + r0;
-                    const float *right = (second ? X : Tm) + m0 * kXStride + c;
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    float4 a[2][4];
-                    float b[2][4];
-                    auto load = [&](int x) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            a[x][k] = *reinterpret_cast<const float4 *>(left + k * kAStride);
-                            b[x][k] = right[k * kXStride];
-                        }
-                        left += 4 * kAStride, right += 4 * kXStride;
-                    };
-                    auto take = [&](int x) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            fma2(acc[0], acc[1], a[x][k].x, a[x][k].y, b[x][k], b[x][k], acc[0], acc[1]);
-                            fma2(acc[2], acc[3], a[x][k].z, a[x][k].w, b[x][k], b[x][k], acc[2], acc[3]);
-                        }
-                    };
-                    load(0);
+                    const float *left = At + (32 * second + m0 + odd) * kAStride + 32 + r0;
+                    const float *right = (second ? X : Tm) + (m0 + odd) * kXStride + c;
+                    float y[2][4] = {};
 #pragma unroll 1
-                    for (int m = m0;; m += 8) {
-                        load(1);
-                        take(0);
-                        if (m + 8 < m1) load(0);
-                        take(1);
-                        if (m + 8 >= m1) break;
+                    for (int m = m0; m < m1; m += 16, left += 16 * kAStride, right += 16 * kXStride) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const float4 a = *reinterpret_cast<const float4 *>(left + k * kAStride);
+                            const float2 b = *reinterpret_cast<const float2 *>(right + k * kXStride);
+                            fma2(y[0][0], y[0][1], a.x, a.y, b.x, b.x, y[0][0], y[0][1]);
+                            fma2(y[0][2], y[0][3], a.z, a.w, b.x, b.x, y[0][2], y[0][3]);
+                            fma2(y[1][0], y[1][1], a.x, a.y, b.y, b.y, y[1][0], y[1][1]);
+                            fma2(y[1][2], y[1][3], a.z, a.w, b.y, b.y, y[1][2], y[1][3]);
+                        }
                     }
+                    float acc[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[k] = (odd ? y[1][k] : y[0][k]) + __shfl_xor_sync(0xffffffffu, odd ? y[0][k] : y[1][k], 16);
                     if (second) {
-                        *reinterpret_cast<float4 *>(At + c * kAStride + 32 + r0) =
+                        *reinterpret_cast<float4 *>(At + (c + odd) * kAStride + 32 + r0) =
                             make_float4(-acc[0], -acc[1], -acc[2], -acc[3]);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) X[(r0 + k) * kXStride + c] = acc[k];
+                        for (int k = 0; k < 4; ++k) X[(r0 + k) * kXStride + c + odd] = acc[k];
                     }
                 }
                 role_sync(1, 256);
