@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
 // ---------------------------------------------------------------------------
 constexpr int DC = 64;                       // tokens of a chunk
 constexpr int kDeltaThreads = 32 * 32;
+constexpr int kChainSync = 17 * 32;          // the chain's warps and the one that waits for them
 constexpr int kDeltaPanel = DC * 128;        // 64 rows x 128 bytes
 // TMEM columns.  In turn in the same place: SK, U and then KV; S_0's third part, R and then w U~; S_0's first
 // part and then U~'s two; S_0's second part and then KQ of the next chunk
@@ -845,17 +846,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         int tab_i = 0, turn = 0;
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
-            if (warp == 0) {
-                role_wait(0, &tab_full[tab_i], turn);
-                if (info_of(tab_i)->n) {
-                    // four barriers at once, one a lane
-                    const bool done = !LOCAL && gc > 0 && lane == 2;
-                    const int turn2 = done ? (gc - 1) >> 1 : gc >> 1;
-                    uint64_t *bar = done ? &o_done[(gc - 1) & 1] : lane == 1 ? &norms[gc & 1] : &v_full[gc & 1];
-                    role_wait(0, lane == 3 ? kq_read : bar, lane == 3 ? gc : turn2);
-                }
-            }
-            role_sync(0, 512);
+            role_sync(0, kChainSync);
             tc_fence_after();
             if (uni(info_of(tab_i)->n) == 0 || stop[0]) break;
             {
@@ -892,8 +883,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             // ---- R = b v - c S_0 k, then U~ and w U~
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
-                if (warp == 0) role_wait(0, &go[pass], gc);
-                role_sync(0, 512);
+                role_sync(0, kChainSync);
                 tc_fence_after();
                 if (real) {
                     // in 8x8 fragments: 16 value dimensions and 32 tokens a warp; pair 2 g + r of a thread: tokens
@@ -980,8 +970,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 if (pass == 0) arrive(&v_empty[gc & 1]);
             }
             // ---- S = e^{G_n} S + KV
-            if (warp == 0) role_wait(0, kv_done, gc);
-            role_sync(0, 512);
+            role_sync(0, kChainSync);
             tc_fence_after();
             if (real) {
                 const int tid = renew(threadIdx.x), grp = (tid >> 5) & 3, part = tid >> 7, dv = tid & 127;
@@ -1021,7 +1010,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         int tab_i = 0, turn = 0;
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
-            if (w8 == 0) {
+            if (w8 == 7) {                   // (the first one done with a chunk)
                 role_wait(1, &tab_full[tab_i], turn);
                 if (info_of(tab_i)->n) role_wait(1, lane ? kq_done : &norms[gc & 1], lane ? gc : gc >> 1);
             }
@@ -1582,6 +1571,28 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             if (elect_one()) tc_commit(drain);
             __syncwarp();
             wait(drain, 0);
+        } else {
+            // ============================================================ the chain's waits
+            int tab_i = 0, turn = 0;
+#pragma unroll 1
+            for (int gc = 0;; ++gc) {
+                role_wait(0, &tab_full[tab_i], turn);
+                const bool more = info_of(tab_i)->n;
+                if (more) {
+                    // four barriers at once, one a lane
+                    const bool done = !LOCAL && gc > 0 && lane == 2;
+                    uint64_t *bar = done ? &o_done[(gc - 1) & 1] : lane == 1 ? &norms[gc & 1] : &v_full[gc & 1];
+                    role_wait(0, lane == 3 ? kq_read : bar, lane == 3 ? gc : done ? (gc - 1) >> 1 : gc >> 1);
+                }
+                role_sync(0, kChainSync);
+                if (!more || stop[0]) break;
+#pragma unroll 1
+                for (int x = 0; x < 3; ++x) {
+                    role_wait(0, x == 2 ? kv_done : &go[x], gc);
+                    role_sync(0, kChainSync);
+                }
+                next_tab(tab_i, turn);
+            }
         }
     }
     tc_fence_before();
