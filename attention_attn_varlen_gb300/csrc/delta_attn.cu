@@ -443,7 +443,7 @@ constexpr uint32_t TM_KV = 0, TM_SK = 0, TM_U = 64;
 constexpr uint32_t TM_S1 = 128, TM_UO = 128, TM_KQ = 192;    // (S_0: three parts of 64 columns)
 constexpr uint32_t TM_R = 256;               // (three parts of 32 columns)
 constexpr uint32_t TM_SQ = 352, TM_PU = 416;
-constexpr int kAStride = 68, kXStride = 36;  // floats of a row of A^T, and of T's and the products' rows
+constexpr int kAStride = 68;                 // floats of a row of A^T, and of T's and the products' rows
 constexpr int kDeltaBuckets = 256;
 
 // A chunk as its roles read it, behind its tables.
@@ -477,7 +477,7 @@ struct DeltaSmem {
     static constexpr int kBytes = kBarOff + kNumBars * 8 + 32 + 1024 /* alignment slack */;
     static_assert(kBytes <= 227 * 1024 && sizeof(DeltaChunk) <= 64, "shared memory");
     // scratch of the solve, where T goes in the end
-    static_assert((DC + 32) * kXStride * 4 <= 3 * kDeltaPanel, "scratch");
+    static_assert(DC * kAStride * 4 <= 3 * kDeltaPanel, "scratch");
 };
 
 // Registers of the calling warpgroup.  The kernel is launched with 64 a thread; the eight warpgroups'
@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         const bool keys = qd >= 2;           // lane = row of (Q; K)
         float *At = reinterpret_cast<float *>(sm + S::kAOff);            // [j][i]
         float *Tm = reinterpret_cast<float *>(sm + S::kTOff);            // [i][j % 32], T11 and the diagonal blocks
-        float *X = Tm + DC * kXStride;                                   // [i][j]: A21 T11
+        float *X = At + DC / 2 * kAStride;                                  // [i][j]: A21 T11
         int tab_i = 0, turn = 0;
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
@@ -1122,9 +1122,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 16; q += 4)
                         *reinterpret_cast<float4 *>(blk + col * kAStride + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
-                    float *to = Tm + at * kXStride + l;
+                    float *to = Tm + at * kAStride + l;
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) to[q * kXStride] = x[q];
+                    for (int q = 0; q < 16; ++q) to[q * kAStride] = x[q];
                 }
                 // the block below them: A21 T11, in the place where T21 = -T22 (A21 T11) goes; four rows of two columns a lane
 #pragma unroll 1
@@ -1132,12 +1132,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     __syncwarp();
                     const int l = renew(lane), r0 = (l >> 3) * 4, c = (l & 7) * 2;
                     const float *left = At + (jb + 16 * second) * kAStride + jb + 16 + r0;
-                    float *right = Tm + (jb + 16 * second) * kXStride + c;
+                    float *right = Tm + (jb + 16 * second) * kAStride + c;
                     float y[2][4] = {};
 #pragma unroll 8
                     for (int m = 0; m < 16; ++m) {
                         const float4 a = *reinterpret_cast<const float4 *>(left + m * kAStride);
-                        const float2 b = *reinterpret_cast<const float2 *>(right + m * kXStride);
+                        const float2 b = *reinterpret_cast<const float2 *>(right + m * kAStride);
                         fma2(y[0][0], y[0][1], a.x, a.y, b.x, b.x, y[0][0], y[0][1]);
                         fma2(y[0][2], y[0][3], a.z, a.w, b.x, b.x, y[0][2], y[0][3]);
                         fma2(y[1][0], y[1][1], a.x, a.y, b.y, b.y, y[1][0], y[1][1]);
@@ -1145,10 +1145,10 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     }
                     __syncwarp();
                     const float sign = second ? -1.f : 1.f;
-                    float *to = Tm + (jb + 16 + r0) * kXStride + c;
+                    float *to = Tm + (jb + 16 + r0) * kAStride + c;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<float2 *>(to + k * kXStride) = make_float2(sign * y[0][k], sign * y[1][k]);
+                        *reinterpret_cast<float2 *>(to + k * kAStride) = make_float2(sign * y[0][k], sign * y[1][k]);
                     if (second) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
@@ -1165,22 +1165,22 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             for (int second = low ? 2 : 0; second < 2; ++second) {
                 // (first: of columns 0..15 by the warps of P; 16..31, half as long, by those of A)
                 int task = second ? w8 : ((w8 & 1) + (w8 >> 2) * 2) * 2;
-                if (!second && keys) task = w8 == 2 ? 1 : w8 == 3 ? 3 : w8 == 6 ? 7 : 8;
+                if (!second && keys) task = w8 == 2 ? 1 : w8 == 3 ? 3 : w8 == 6 ? 5 : 8;
 #pragma unroll 1
-                for (; task < 8; task = !second && task == 3 ? 5 : 8) {
+                for (; task < 8; task = !second && task == 5 ? 7 : 8) {
                     const int l = renew(lane), odd = l >> 4, c = (task & 1) * 16 + (l & 7) * 2;
                     const int r0 = (task >> 1) * 8 + ((l >> 3) & 1) * 4;
                     // T11's columns begin at the diagonal, T22's rows end there
                     const int m0 = second ? 0 : (task & 1) * 16, m1 = second && task < 4 ? 16 : 32;
                     const float *left = At + (32 * second + m0 + odd) * kAStride + 32 + r0;
-                    const float *right = (second ? X : Tm) + (m0 + odd) * kXStride + c;
+                    const float *right = (second ? X : Tm) + (m0 + odd) * kAStride + c;
                     float y[2][4] = {};
 #pragma unroll 1
-                    for (int m = m0; m < m1; m += 16, left += 16 * kAStride, right += 16 * kXStride) {
+                    for (int m = m0; m < m1; m += 16, left += 16 * kAStride, right += 16 * kAStride) {
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
                             const float4 a = *reinterpret_cast<const float4 *>(left + k * kAStride);
-                            const float2 b = *reinterpret_cast<const float2 *>(right + k * kXStride);
+                            const float2 b = *reinterpret_cast<const float2 *>(right + k * kAStride);
                             fma2(y[0][0], y[0][1], a.x, a.y, b.x, b.x, y[0][0], y[0][1]);
                             fma2(y[0][2], y[0][3], a.z, a.w, b.x, b.x, y[0][2], y[0][3]);
                             fma2(y[1][0], y[1][1], a.x, a.y, b.y, b.y, y[1][0], y[1][1]);
@@ -1196,7 +1196,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             make_float4(-acc[0], -acc[1], -acc[2], -acc[3]);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) X[(r0 + k) * kXStride + c + odd] = acc[k];
+                        for (int k = 0; k < 4; ++k) X[(r0 + k) * kAStride + c + odd] = acc[k];
                     }
                 }
                 role_sync(1, 256);
