@@ -17,7 +17,8 @@ constexpr float kLowest = -3.4028234663852886e38f;   // the lowest fp32 value, w
 // candidates comes first may hang on the last digits.
 //
 // One pass over the logits: 64 groups of 8 beams, 131,072 bf16 logits each (134 MB), take 40 us, 35 of them the
-// scan (HBM alone: 20), which its instructions bound: 78 for eight logits of 32 lanes, the conversions, exponentials and
+// scan (HBM alone: 20), which its instructions bound: 91 for eight logits of 32 lanes (34 without the
+// candidates), the conversions, exponentials and
 // comparisons (issue slots 60 % busy beside the merges' waits).  One group of 4 beams, 32,000 logits: 10.8 us, the
 // two launches' latency.  A CTA takes a slice of a row, a warp a
 // share of the slice in vectors of eight neighbours a lane; the warp keeps a sum of

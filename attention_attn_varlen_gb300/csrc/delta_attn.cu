@@ -417,19 +417,18 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
 // 16 and of 32, as -T22 A21 T11 (by mma.sync, which waits behind the chain's products, slower).  Sums of decays are in 64
 // bits and differences of them kept as two fp32 parts.
 //
-// What bounds it: a chunk takes 10,000 clocks, the chain S -> SK -> R -> U -> w U~ -> KV -> S about 9,500 of them
-// (2,900 in the products, the rest in the warps that split operands into parts) and the next chunk's T as many
-// beside it; the schedulers they share are busy 59 % of the time and saturated where both run, the tensor core 30 %.
-// SQ, KQ and PU run in the chain's gaps.  34,053 tokens in 16 prompts, 32 heads of 128: 636 us (token after token 10,600);
-// 32,768 tokens of one, 16 heads: 900 us in segments, 2,650 in one piece (35,000); 96 prompts of 1 to 150 tokens, 16
-// heads of 64: 103 us.
+// What bounds it: a chunk takes 9,000 to 9,500 clocks, as does the next chunk's T beside the chain S -> SK -> R -> U ->
+// w U~ -> KV -> S (2,900 in its products, the rest in the warps that split operands into parts); the schedulers they share
+// are busy 59 % of the time and saturated where both run, the tensor core 33 %.  SQ, KQ and PU run in the chain's
+// gaps.  34,053 tokens in 16 prompts, 32 heads of 128: 575 us (token after token 10,600); 32,768 tokens of one, 16
+// heads: 786 us in segments, 2,650 in one piece (35,000); 96 prompts of 1 to 150 tokens, 16 heads of 64: 92 us.
 //
 // Roles (32 warps, one CTA per SM that goes over (sequence, value head) units):
 //   0..15   the chain: thread = value dimension and a quarter of dk or of the tokens; S in registers
 //   16..23  T and P of the next chunk
 //   24..27  norms of the next chunk, output rows of the one before
 //   28, 29  issue the loads; write the chunks' tables
-//   30      issues the MMAs
+//   30, 31  issues the MMAs; waits for the chain (a warp of it that polled would take its time and issue slots)
 // The roles share the SM's instruction cache, and their code is larger than it: one code site per kind of step, loops
 // where a step repeats, and waits of a few instructions.
 // ---------------------------------------------------------------------------
