@@ -344,3 +344,50 @@ def test_long_sequences_cut_into_segments(lens, Hk, Hv, D, cached):
                 check_state(sd[slots[b]], *finals[b], f"state {b}")
         free = [s for s in range(B + 1) if s not in slots.tolist()] + [int(slots[b]) for b in range(B) if lens[b] == 0]
         assert torch.equal(sd.cpu()[free], state[free])
+
+
+@pytest.mark.parametrize("lens", [[2, 1, 0, 2], [7, 8, 3], [9, 1, 8], [12, 16, 0, 5, 15], [32, 17, 31, 1], [33, 96, 40]])
+@pytest.mark.parametrize("Hk,Hv,D", [(2, 2, 64), (1, 3, 128), (2, 4, 128)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_lengths_around_the_forms_limits(lens, Hk, Hv, D, strided):
+    """Up to 8 and up to 16 tokens in one pass over the states, up to 32 and more in chunks; decays and strengths at
+    the ends of their range among them.  One pass: products of the state and of u as parts of 2^-24 together, summed in fp32
+    over D terms and up to 16 tokens (the step's 128 x 2^-24 covers both); outputs take the state as two parts, 2^-16
+    of scale |q| M."""
+    B, T = len(lens), sum(lens)
+    host, dev, gen = inputs(7 * T + D, T, Hk, Hv, D, strided, True)
+    g, beta = host[3].clone(), host[4].clone()
+    g[::5, 0], g[3::7, -1], beta[1::4, 0], beta[2::4, -1] = float("-inf"), 0.0, 0.0, 1.0
+    host, dev = (*host[:3], g, beta), (*dev[:3], g.cuda(), beta.cuda())
+    cu, scale = cu_of(lens), D ** -0.5
+    state = torch.randn(B + 1, Hv, D, D, generator=gen)
+    slots = torch.randperm(B + 1, generator=gen)[:B].to(torch.int32)
+    ctx = torch.tensor([0 if b == 1 else 5 for b in range(B)], dtype=torch.int32)
+    sd = state.cuda()
+    av.get_last_device_error()
+    out = av.delta_attn_varlen_fwd(*dev, cu.cuda(), max(lens), scale, state_cache=sd, state_slots=slots.cuda(),
+                                   context_lens=ctx.cuda(), qk_norm_eps=1e-6)
+    torch.cuda.synchronize()
+    assert av.get_last_device_error()[0] == 0
+    starts = [state[slots[b]].double() if ctx[b] > 0 else None for b in range(B)]
+    ref, finals, reach = delta(*host, cu, scale, starts, 1e-6)
+    check_out(out, ref, reach, "out")
+    got = sd.cpu()
+    for b in range(B):
+        if lens[b] == 0:
+            assert torch.equal(got[slots[b]], state[slots[b]])
+        else:
+            check_state(got[slots[b]], *finals[b], f"state {b}")
+    free = [s for s in range(B + 1) if s not in slots.tolist()]
+    assert torch.equal(got[free], state[free])
+    # the same bits each time
+    again = state.cuda()
+    assert torch.equal(out, av.delta_attn_varlen_fwd(*dev, cu.cuda(), max(lens), scale, state_cache=again,
+                                                     state_slots=slots.cuda(), context_lens=ctx.cuda(), qk_norm_eps=1e-6))
+    assert torch.equal(again, sd)
+
+
+@pytest.mark.parametrize("T", [2, 6, 16, 20, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_nan_in_every_form(T, D):
+    test_a_nan_reaches_later_tokens_alone(T, D)
