@@ -32,7 +32,10 @@ constexpr float kLowest = -3.4028234663852886e38f;   // the lowest fp32 value, w
 constexpr int kScanWarps = 4;
 template <typename T> constexpr int kScanAhead = 8 / sizeof(T);   // vectors of a warp in a step (64 bytes a lane)
 constexpr float kFarAbove = 40.f;                    // a logit this far above the sum's reference moves it
-constexpr float kFarBelow = -1e37f;                  // logits times log2(e) stay finite above this
+// Largest reference for which 2^(x log2(e) - rn(ref log2(e))) is summed and what the rounding left, at most half a step
+// of ref log2(e), is made good afterwards: 64 up to 2^31 (1.49e9), so that 2^-64 .. 2^64 times a sum stay finite and
+// normal; from there on one factor may be 0 and the other infinite.  Masks of -1e9 are still below it.
+constexpr float kFarOff = 1e9f;
 
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
     const uint32_t b = __float_as_uint(x + 0.f);     // -0 is 0
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, 8) beam_scan_kernel(const Bea
             ref = m;
         }
         float s0 = 0.f, s1 = 0.f;
-        if (ref > kFarBelow) {
+        if (fabsf(ref) <= kFarOff) {
             // 2^(x log2(e) - ref log2(e)), and what the second product's rounding leaves, once for all
             const float r = -__fmul_rn(ref, kLog2e);
 #pragma unroll
@@ -253,6 +256,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, 8) beam_scan_kernel(const Bea
             }
             sum = fmaf(s0 + s1, ex2(-fmaf(ref, kLog2e, r)), sum);
         } else {
+            // the difference itself is exact where it counts: as near to ref as 40, both are beyond 2^29
 #pragma unroll 1
             for (int v = 0; v < kAhead; ++v) {
                 const Eight<T, MODE> y = pick(x, v);

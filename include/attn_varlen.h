@@ -665,7 +665,8 @@ ATTN_API attn_status attn_delta_decode(const void *q, const void *k, const void 
  *                of its request; -1 where there are no more candidates
  *   out_scores   float32 [num_groups, num_out]; -inf there
  * A NaN or +inf among a row's logits or in its score takes the row's candidates away
- * and is reported as ATTN_ERR_DEVICE_RANGE.  Exponentials are summed in fp32, in an
+ * and is reported as ATTN_ERR_DEVICE_RANGE; every finite logit is an ordinary one, masks of
+ * large negative numbers among them.  Exponentials are summed in fp32, in an
  * order that the number of rows and the vocabulary set: equal rows of a call score equal.
  * Limits: num_beams, num_out <= 32; vocab < 2^30; num_groups * num_beams < 2^25.
  * workspace: attn_beam_select_workspace_size(...) bytes, 16-byte aligned; it holds
