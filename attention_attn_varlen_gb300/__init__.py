@@ -104,6 +104,8 @@ def lib():
     L.attn_abi_version.restype = _i32
     L.attn_selftest_bounded_wait.argtypes = [_vp, _c.POINTER(_c.c_ulonglong)]
     L.attn_selftest_bounded_wait.restype = _i32
+    L.attn_selftest_chunk_wait.argtypes = [_vp, _i32, _c.POINTER(_c.c_ulonglong)]
+    L.attn_selftest_chunk_wait.restype = _i32
     L.attn_kvcache_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                    _i64, _i32, _f32, _i32, _vp, _vp, _sz, _vp]
     L.attn_kvcache_fwd.restype = _i32
@@ -1058,13 +1060,18 @@ def set_kernel_events(before=None, after=None) -> None:
     lib().attn_set_kernel_events(ctypes.c_void_p(before.cuda_event), ctypes.c_void_p(after.cuda_event))
 
 
-def selftest_bounded_wait(stream=None) -> dict:
+def selftest_bounded_wait(stream=None, wait: str = "kernel") -> dict:
     """Run the library's failure-detection self-test (a bounded wait that runs
-    out on purpose; see attn_selftest_bounded_wait).  Returns the two waiters'
-    success flags and waited nanoseconds; the device error word then holds the
-    timeout."""
+    out on purpose; see attn_selftest_bounded_wait and, for wait = "linear" and "delta",
+    attn_selftest_chunk_wait).  Returns the two waiters' success flags and waited
+    nanoseconds; the device error word then holds the timeout."""
+    if wait not in ("kernel", "linear", "delta"):
+        raise ValueError("wait must be kernel, linear or delta")
     res = (ctypes.c_ulonglong * 4)()
-    _check(lib().attn_selftest_bounded_wait(_stream(stream), res), "attn_selftest_bounded_wait")
+    if wait == "kernel":
+        _check(lib().attn_selftest_bounded_wait(_stream(stream), res), "attn_selftest_bounded_wait")
+    else:
+        _check(lib().attn_selftest_chunk_wait(_stream(stream), wait == "delta", res), "attn_selftest_chunk_wait")
     return {"first_ok": bool(res[0]), "first_ns": int(res[1]), "second_ok": bool(res[2]), "second_ns": int(res[3])}
 
 

@@ -14,6 +14,7 @@
 #include <string.h>
 
 #include "../../include/attn_varlen.h"
+#include "chunks.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -281,20 +282,22 @@ attn_status decode_launch(const DecodeCall &c, const DevInfo *d, int splits, int
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Failure-detection self-test (attn_selftest_bounded_wait).  One CTA, two
+// Failure-detection self-test (attn_selftest_bounded_wait, and for the chunk
+// kernels' waits attn_selftest_chunk_wait).  One CTA, two
 // warps.  Lane 0 of warp 0 waits on an mbarrier that nothing completes: its
 // bounded wait gives up after the wait limit, records a timeout in the error
 // word and raises the CTA's abort flag.  Lane 0 of warp 1 first idles for
 // half that limit, then waits on another such mbarrier with the same abort
 // flag: it must give up as soon as it sees the flag, before its own limit.
-// Each records whether its wait succeeded and how long it waited.
+// Each records whether its wait succeeded and how long it waited.  WAIT 1 and 2:
+// the chunk kernels' waits, which leave the report to the kernel's end.
 // ---------------------------------------------------------------------------
 namespace attn {
 namespace {
 constexpr uint32_t SRC_SELFTEST = 1u << 13;
 static __device__ unsigned long long g_selftest_out[4];
 
-__global__ void __launch_bounds__(64) attn_selftest_wait_kernel(uint32_t *err) {
+template <int WAIT> __global__ void __launch_bounds__(64) attn_selftest_wait_kernel(uint32_t *err) {
     __shared__ uint64_t bars[2];
     __shared__ int abort_flag;
     if (threadIdx.x == 0) {
@@ -313,10 +316,15 @@ __global__ void __launch_bounds__(64) attn_selftest_wait_kernel(uint32_t *err) {
         }
         const uint64_t t0 = globaltimer_ns();
         // phase 0 of a fresh barrier never completes: nothing arrives on it
-        const bool ok = mbar_wait(&bars[w], 0u, &abort_flag, err, SRC_SELFTEST);
+        const bool ok = WAIT == 0   ? mbar_wait(&bars[w], 0u, &abort_flag, err, SRC_SELFTEST)
+                        : WAIT == 1 ? chunk_wait(&bars[w], 0u, &abort_flag)
+                                    : chunk_wait_each(&bars[w], 0u, &abort_flag);
         g_selftest_out[2 * w] = ok ? 1ull : 0ull;
         g_selftest_out[2 * w + 1] = globaltimer_ns() - t0;
     }
+    if (WAIT == 0) return;
+    __syncthreads();
+    if (threadIdx.x == 0 && abort_flag) record_error(err, ERR_TIMEOUT | SRC_SELFTEST);
 }
 }  // namespace
 }  // namespace attn
@@ -343,20 +351,28 @@ void attn_set_kernel_events(void *before, void *after) {
 
 int attn_abi_version(void) { return ATTN_ABI_VERSION; }
 
-attn_status attn_selftest_bounded_wait(void *stream, unsigned long long *result) {
+static attn_status selftest_wait(void (*kernel)(uint32_t *), void *stream, unsigned long long *result) {
     if (!result) return ATTN_ERR_INVALID_ARG;
     DevInfo *d = nullptr;
     attn_status st = dev_info(&d);
     if (st != ATTN_OK) return st;
     if ((st = check_arch(d)) != ATTN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    attn_selftest_wait_kernel<<<1, 64, 0, s>>>(d->err);
+    kernel<<<1, 64, 0, s>>>(d->err);
     if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess ||
         cudaMemcpyFromSymbol(result, g_selftest_out, sizeof(g_selftest_out)) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_LAUNCH_FAILED;
     }
     return ATTN_OK;
+}
+
+attn_status attn_selftest_bounded_wait(void *stream, unsigned long long *result) {
+    return selftest_wait(attn_selftest_wait_kernel<0>, stream, result);
+}
+
+attn_status attn_selftest_chunk_wait(void *stream, int delta, unsigned long long *result) {
+    return selftest_wait(delta ? attn_selftest_wait_kernel<2> : attn_selftest_wait_kernel<1>, stream, result);
 }
 
 const char *attn_status_string(attn_status s) {

@@ -103,6 +103,23 @@ __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, volat
     return false;
 }
 
+// The same in fewer instructions, with the timer read at each try, which suits kernels in which a warp of its own
+// does the waiting (the delta rule's prompts: 574 us, 589 with the one above; linear attention's 141, 139 with it).
+// Gives up after 2^30 ns.
+__device__ __forceinline__ bool chunk_wait_each(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        if (((t - t0) >> 30) | *abort) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // kernel<<<grid, block, smem>>> as the programmatic dependent of the launch before it
 template <typename... K, typename... A>
 cudaError_t launch_after(void (*k)(K...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const A &...a) {

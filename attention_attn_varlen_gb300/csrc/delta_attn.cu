@@ -658,17 +658,6 @@ __global__ void __launch_bounds__(2 * D) delta_join_kernel(const DeltaParams p) 
 }
 template <int D> constexpr int kJoinBytes = (kJoinStages * kJoinRows + 2 * 16) * D * 4;
 
-// A bounded wait in as few instructions as it goes; a try takes the hardware 50 clocks or more, so
-// that it gives up after half a second or so.
-constexpr int kDeltaTries = 1 << 24;
-__device__ __forceinline__ bool delta_wait(uint64_t *bar, uint32_t parity) {
-    int left = kDeltaTries;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (--left == 0) return false;
-    return true;
-}
-
 // x as a value that the compiler takes for a new one: what is computed from it stays where it is used.  Addresses
 // kept from chunk to chunk would leave a phase's own loads too few registers to be in flight together.
 __device__ __forceinline__ int renew(int x) {
@@ -762,8 +751,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     uint64_t *o_read = bars + 28;            // SQ and PU read
     uint64_t *drain = bars + 29;             // every MMA done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kNumBars);
-    volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);     // [3]: a role's wait gave up
-    volatile int *late = stop + 3;                                            // any wait did
+    volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);     // [4]: a role stops; 2's in turn by chunk
+    volatile int *late = stop + 4;                                            // a wait gave up: the others do so too
+    volatile int *never = stop + 5;      // ... but for those for what the hardware finishes by itself
     float *tables = reinterpret_cast<float *>(sm + S::kTabOff);
     int *bad_at = reinterpret_cast<int *>(sm + S::kBadOff);
     // chunk gc's tables lie at tab = gc % 3, in its turn gc / 3
@@ -794,7 +784,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         mbar_init(kv_done, 1);
         mbar_init(o_read, 4);
         mbar_init(drain, 1);
-        for (int i = 0; i < 4; ++i) stop[i] = 0;
+        for (int i = 0; i < 6; ++i) stop[i] = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -815,19 +805,18 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     // a warp's wait: every lane gets the same answer
     auto wait = [&](uint64_t *bar, int phase) {
-        const bool ok = __all_sync(0xffffffffu, delta_wait(bar, (uint32_t)phase & 1u));
-        if (!ok) *late = 1;
-        return ok;
+        return __all_sync(0xffffffffu, chunk_wait_each(bar, (uint32_t)phase & 1u, late)) != 0;
     };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // A role of several warps: its first one waits (the others' polling would take issue slots from those that
-    // work) and the rest behind a barrier of the role.  A wait that gave up stops the role at its next chunk, all
-    // of its warps at once.
-    auto role_wait = [&](int role, uint64_t *bar, int phase) {
-        if (!wait(bar, phase)) stop[role] = 1;
+    // A role of several warps: one of them waits (the others' polling would take issue slots from those that
+    // work) and the rest behind a barrier of the role.  A wait that gives up makes those at the role's next chunk
+    // give up at once, and these stop the role, all of its warps together: its flag is written before that barrier alone,
+    // and not again before every warp has read it.
+    auto role_wait = [&](int flag, uint64_t *bar, int phase) {
+        if (!wait(bar, phase)) stop[flag] = 1;
     };
     auto role_sync = [](int role, int threads) {
         asm volatile("bar.sync %0, %1;" ::"r"(role + 1), "r"(threads) : "memory");
@@ -1097,7 +1086,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             // A21 T11 is made beside T22.
             if (qd == 2) role_sync(3, 64);
             if (w8 == 2 || (w8 == 7 && !low)) {
-                if (gc > 0) role_wait(1, &go[1], gc - 1);            // U of the chunk before done: T's place
+                if (gc > 0) wait(&go[1], gc - 1);                    // U of the chunk before done: T's place
                 const int jb = w8 == 2 ? 0 : 32;
                 {
                     // its two 16 x 16 diagonal blocks, a lane per column: x_q = [q = column] - sum_{m < q} A_qm x_m
@@ -1235,14 +1224,14 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll 1
         for (int gc = 0;; ++gc) {
             if (grp == 0) {
-                role_wait(2, &tab_full[tab_i], turn);
+                role_wait(2 + (gc & 1), &tab_full[tab_i], turn);
                 const int n = info_of(tab_i)->n;
-                if (n) role_wait(2, &qk_full[gc % QS], gc / QS);       // (LOCAL: K alone)
-                if (n && n < DC) role_wait(2, &v_full[gc & 1], gc >> 1);
+                if (n) role_wait(2 + (gc & 1), &qk_full[gc % QS], gc / QS);       // (LOCAL: K alone)
+                if (n && n < DC) role_wait(2 + (gc & 1), &v_full[gc & 1], gc >> 1);
             }
             role_sync(2, 128);
             const int more = uni(info_of(tab_i)->n);
-            if (stop[2]) break;
+            if (stop[2 + (gc & 1)]) break;
             if (more > 0) {
                 // ---- norms of this chunk
                 const int s = gc % QS;
@@ -1293,7 +1282,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 const int oc = gc - 1;
                 const DeltaChunk *info = info_of(last_tab);
                 const int n = uni(info->n), t0 = info->t0, h = info->h;
-                if (grp == 0) role_wait(2, &o_done[oc & 1], oc >> 1);
+                if (grp == 0) wait(&o_done[oc & 1], oc >> 1);
                 role_sync(2, 128);
                 tc_fence_after();
                 int first_bad = DC;
@@ -1391,8 +1380,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 ++gc;
             }
             // copies still in flight (after a wait that gave up) land before the CTA ends
-            for (int d = max(0, qk_gone - QS); d < qk_gone; ++d) wait(&qk_full[d % QS], d / QS);
-            for (int d = max(0, gc - VS); d < gc; ++d) wait(&v_full[d & 1], d >> 1);
+#pragma unroll 1
+            for (int d = max(0, qk_gone - QS); d < qk_gone; ++d)
+                chunk_wait_each(&qk_full[d % QS], (uint32_t)(d / QS) & 1u, never);
+#pragma unroll 1
+            for (int d = max(0, gc - VS); d < gc; ++d) chunk_wait_each(&v_full[d & 1], (uint32_t)(d >> 1) & 1u, never);
+            __syncwarp();
         } else if (warp == 29) {
             // ============================================================ the chunks' tables, two tokens a lane
             DeltaWalk walk(units_n, heads);
@@ -1569,7 +1562,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             // nothing of this CTA's is left in the tensor core when TMEM goes back
             if (elect_one()) tc_commit(drain);
             __syncwarp();
-            wait(drain, 0);
+            chunk_wait_each(drain, 0u, never);
+            __syncwarp();
         } else {
             // ============================================================ the chain's waits
             int tab_i = 0, turn = 0;
@@ -1587,7 +1581,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 if (!more || stop[0]) break;
 #pragma unroll 1
                 for (int x = 0; x < 3; ++x) {
-                    role_wait(0, x == 2 ? kv_done : &go[x], gc);
+                    wait(x == 2 ? kv_done : &go[x], gc);
                     role_sync(0, kChainSync);
                 }
                 next_tab(tab_i, turn);
@@ -1598,7 +1592,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
-    if (threadIdx.x == 0 && *late) record_error(p.err, ERR_TIMEOUT | SRC_DELTA);
+    if (threadIdx.x == 0 && (*late | *never)) record_error(p.err, ERR_TIMEOUT | SRC_DELTA);
 }
 
 template <int D>

@@ -743,6 +743,10 @@ ATTN_API attn_status attn_get_last_device_error(void *stream, uint32_t *detail);
  * or ATTN_ERR_LAUNCH_FAILED. */
 ATTN_API attn_status attn_selftest_bounded_wait(void *stream, unsigned long long *result);
 
+/* The same with the wait of a chunk kernel (delta 0: linear attention's, 1: the gated delta rule's),
+ * whose time-out is reported at the kernel's end. */
+ATTN_API attn_status attn_selftest_chunk_wait(void *stream, int delta, unsigned long long *result);
+
 /* ATTN_ABI_VERSION of the loaded library. */
 ATTN_API int attn_abi_version(void);
 
