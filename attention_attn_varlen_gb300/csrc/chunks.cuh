@@ -77,8 +77,9 @@ __device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r
 // that read the bf16 halves as they are, -1 times them (4 % fewer instructions than with their widening, 248 -> 243 us)
 __device__ __forceinline__ uint32_t take_bf16(float &r0, float &r1, float x0, float x1) {
     const uint32_t h = pack_bf16x2(x0, x1);
-    asm("{\n\t.reg .b16 l, u, m;\n\tmov.b32 {l, u}, %2;\n\tmov.b16 m, 0xBF80;\n\t"    // -1
-        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, u, m, %4;\n\t}"
+    // (the outputs last: they may have the inputs' registers)
+    asm("{\n\t.reg .b16 l, u, m;\n\t.reg .f32 a, b;\n\tmov.b32 {l, u}, %2;\n\tmov.b16 m, 0xBF80;\n\t"    // -1
+        "fma.rn.f32.bf16 a, l, m, %3;\n\tfma.rn.f32.bf16 b, u, m, %4;\n\tmov.f32 %0, a;\n\tmov.f32 %1, b;\n\t}"
         : "=f"(r0), "=f"(r1)
         : "r"(h), "f"(x0), "f"(x1));
     return h;
