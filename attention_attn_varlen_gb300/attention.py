@@ -310,9 +310,13 @@ class Beams:
         self.pool = pool
         self.rows = rows
         self.first_tokens: torch.Tensor | None = None
+        self.scores = self._first_scores()
+
+    def _first_scores(self) -> torch.Tensor:
         # the search starts from its first beam alone: the others hold the same prompt
-        self.scores = torch.full(rows.shape, float("-inf"), device=rows.device)
-        self.scores[:, 0] = 0
+        scores = torch.full(self.rows.shape, float("-inf"), device=self.rows.device)
+        scores[:, 0] = 0
+        return scores
 
     def select(self, logits: torch.Tensor, num_out: int | None = None):
         """(tokens, parents, scores) of the best continuations, [R, num_out] each
@@ -337,7 +341,9 @@ class Beams:
 
     def start(self, layers=()) -> None:
         """Copy the prompts from the first beams to the others; what is copied later
-        begins behind them."""
-        scores = self.scores
-        self.advance(torch.zeros_like(self.rows), scores, layers)
+        begins behind them.  Called again, with new prompts in the first beams (and the
+        old tokens trimmed from every row), it starts the next search over the same rows."""
+        if self.first_tokens is not None:
+            self.first_tokens, self.scores = None, self._first_scores()
+        self.advance(torch.zeros_like(self.rows), self.scores, layers)
         self.first_tokens = self.pool.seq_lens.clone()
