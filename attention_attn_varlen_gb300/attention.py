@@ -224,7 +224,12 @@ class DeltaAttention:
                 ctx: AttentionContext) -> torch.Tensor:
         """q, k [N, Hk*D] or [N, Hk, D]; v [N, Hv*D] or [N, Hv, D]; log_decay, beta
         float32 [N, Hv].  Returns o with v's shape.  Steps as for LinearAttention; up
-        to 16 tokens per sequence run in one pass over the states, more in chunks."""
+        to 16 tokens per sequence run in one pass over the states, more in chunks.
+
+        The states then hold all of the step's tokens.  Guessed tokens that are accepted in
+        part: copy_states(state_cache, rows, spares) before the step, and after it
+        copy_states(state_cache, spares, rows) and another step over the accepted ones
+        (a source of -1 leaves out the sequences that keep all of theirs)."""
         shape = v.shape
         q = q.view(-1, self.num_k_heads, self.head_dim)
         k = k.view(-1, self.num_k_heads, self.head_dim)

@@ -607,7 +607,9 @@ ATTN_API attn_status attn_linear_decode(const void *q, const void *k, const void
  *                (cache_seqlens nullable: no entry was refused)
  *   max_seqlen   host-side upper bound of the lengths (a longer sequence is cut
  *                to it and reported as ATTN_ERR_DEVICE_INDEX); 0: nothing runs
- * A sequence of length 0 leaves its slot as it was.
+ * A sequence of length 0 leaves its slot as it was.  What is kept is the state after all of a sequence's tokens:
+ * where guessed ones are accepted in part, put back the state from before (attn_copy_states to spare slots
+ * and back) and call again with the accepted ones.
  * Up to 16 tokens each (max_seqlen) the states are read and written once and nothing
  * else is kept; longer ones go in chunks of 64 tokens on the tensor cores, and sequences
  * much longer than their share of the GPU in segments that run side by side, from states
