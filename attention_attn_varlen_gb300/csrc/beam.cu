@@ -13,13 +13,16 @@ constexpr float kLowest = -3.4028234663852886e38f;   // the lowest fp32 value, w
 // Selection.  A candidate is (beam b, token t) with the score
 //   scores[b] + logits[b][t] - log(sum_j e^{logits[b][j]}),
 // the order: higher score; equal ones by beam; within a beam higher logit, equal ones
-// by token.  The logarithm of the sum and the scores are in 64 bits: which of two
-// candidates comes first may hang on the last digits.
+// by token.  Exponentials, their sums and the sums' mantissas' logarithms are in fp32 (a few 2^-22 of a row's
+// normaliser), which sets how close candidates of different beams can be told apart; the scores are put together and
+// compared in 64 bits, so that nothing is lost to a beam's score or to a large maximum besides, and the order within a
+// beam is the logits' own.
 //
-// One pass over the logits: 64 groups of 8 beams, 131,072 bf16 logits each (134 MB), take 40 us, 35 of them the
-// scan (HBM alone: 20), which its instructions bound: 91 for eight logits of 32 lanes (34 without the
+// One pass over the logits: 64 groups of 8 beams, 131,072 bf16 logits each (134 MB), take 43 us (41 in a graph), 35 of
+// them the scan (HBM alone: 20), which its instructions bound: 91 for eight logits of 32 lanes (34 without the
 // candidates), the conversions, exponentials and
-// comparisons (issue slots 60 % busy beside the merges' waits).  One group of 4 beams, 32,000 logits: 10.8 us, the
+// comparisons (issue slots 60 % busy beside the merges' waits).  All but one logit in 1,000 masked, by -1e9, -1e10 or the
+// type's lowest value alike: 51 us.  One group of 4 beams, 32,000 logits: 10.5 us in a graph, the
 // two launches' latency.  A CTA takes a slice of a row, a warp a
 // share of the slice in vectors of eight neighbours a lane; the warp keeps a sum of
 // exponentials below a reference that moves when a logit lies far above it, and its
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_states_kernel(uint4 *cache,
 }
 
 // Tokens [first, length) of request row src to request row dst, through both rows' pages.
-// VEC: bytes of an access.
+// V: what a thread moves at a time.
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) copy_kvcache_kernel(const CopyRowsParams p, int parts) {
     const int i = blockIdx.x / parts, part = blockIdx.x - i * parts;
@@ -585,7 +588,7 @@ cudaError_t launch_beam_rows(const int32_t *parents, const int32_t *rows, int32_
     return cudaGetLastError();
 }
 
-// CTAs of a pair: enough to fill the GPU (eight a multiprocessor) with the pairs there are, at most one for
+// CTAs of a pair: 32 a multiprocessor with the pairs there are, a few times what one holds, at most one for
 // every `per` units of its work
 static int parts_of(int64_t work, int64_t per, int n, int num_sms) {
     int64_t parts = (work + per - 1) / per;

@@ -167,9 +167,10 @@ __device__ __forceinline__ void mma_bf16_16808(float (&d)[4], uint32_t a0, uint3
 // the decays as products of the tokens' own, so that small ones cost nothing.  The products go through mma.sync, with k
 // and q as they come (bf16, exact; norms and decays are factors of the sums) and S_0 and u as three bf16 parts, 2^-24 of
 // them, S_0 as two for the output.  A warp has 16 rows, S in the fragments' order with the columns of 16 permuted so that
-// a lane's four are neighbours; a lane per row then solves for u.  NT: room for tokens, 8 or 16.  HBM bounds it: 64 sequences
-// of 5 tokens, 32 heads of 128: 52 us (72 token after token, 58 by fp32 products; 41 for the states alone), of 16: 102
-// for 96 of them (216 by fp32 products, 190 as a chunk).
+// a lane's four are neighbours; a lane per row then solves for u.  NT: room for tokens, 8 or 16.  HBM bounds 64 sequences
+// of 5 tokens, 32 heads of 128: 54 us (72 token after token, 60 by fp32 products; 41 for the states alone).  96 of 16
+// tokens, 122 us (224 by fp32 products, 257 as a chunk; 65 for what is read and written): shared memory 68 % busy, DRAM
+// 41 %, four warps a scheduler that wait for both.
 template <int D, int NT>
 __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const DeltaParams p) {
     constexpr int ROWS = 16, OWN = ROWS * kRecWarps, CTAS = D / OWN;    // rows of a warp, of a CTA; CTAs per state
@@ -420,8 +421,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) delta_few_kernel(const Delt
 // What bounds it: a chunk takes 9,000 to 9,500 clocks, as does the next chunk's T beside the chain S -> SK -> R -> U ->
 // w U~ -> KV -> S (2,900 in its products, the rest in the warps that split operands into parts); the schedulers they share
 // are busy 59 % of the time and saturated where both run, the tensor core 33 %.  SQ, KQ and PU run in the chain's
-// gaps.  34,053 tokens in 16 prompts, 32 heads of 128: 575 us (token after token 10,600); 32,768 tokens of one, 16
-// heads: 786 us in segments, 2,650 in one piece (35,000); 96 prompts of 1 to 150 tokens, 16 heads of 64: 92 us.
+// gaps.  34,053 tokens in 16 prompts, 32 heads of 128: 573 us (token after token 10,600); 32,768 tokens of one, 16
+// heads: 787 us in segments, 2,240 in one piece (35,000); 96 prompts of 1 to 150 tokens, 16 heads of 64: 93 us.
 //
 // Roles (32 warps, one CTA per SM that goes over (sequence, value head) units):
 //   0..15   the chain: thread = value dimension and a quarter of dk or of the tokens; S in registers

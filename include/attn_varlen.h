@@ -596,7 +596,8 @@ ATTN_API attn_status attn_linear_decode(const void *q, const void *k, const void
  *   log_decay    float32 [total_tokens, num_heads_v]: g <= 0 (0: no decay; -inf:
  *                only the token itself); a positive or NaN value is taken as 0 and
  *                reported as ATTN_ERR_DEVICE_RANGE
- *   beta         float32 [total_tokens, num_heads_v], usually in [0, 1]
+ *   beta         float32 [total_tokens, num_heads_v], in [0, 1] or, where a token may turn the
+ *                state around along its key, up to 2
  *   qk_norm_eps  >= 0: q and k are divided by sqrt(their sum of squares +
  *                qk_norm_eps) in fp32, per token and head; < 0: taken as they are.
  *                Those sums must lie between 2^-120 and 2^120 (a key of zeros with
@@ -669,7 +670,11 @@ ATTN_API attn_status attn_delta_decode(const void *q, const void *k, const void 
  * A NaN or +inf among a row's logits or in its score takes the row's candidates away
  * and is reported as ATTN_ERR_DEVICE_RANGE; every finite logit is an ordinary one, masks of
  * large negative numbers among them.  Exponentials are summed in fp32, in an
- * order that the number of rows and the vocabulary set: equal rows of a call score equal.
+ * order that the number of rows and the vocabulary set: equal rows of a call score equal, and
+ * candidates of different beams whose scores lie closer than the sums' errors (a few 2^-22,
+ * at the very worst 2^-18) may come in either order.  The logarithm is one 64-bit number: beside a
+ * maximum beyond 2^53 it is the maximum itself, so a row of nothing but one such value scores as if each token
+ * were certain; rule such a beam out by its score or by -inf.
  * Limits: num_beams, num_out <= 32; vocab < 2^30; num_groups * num_beams < 2^25.
  * workspace: attn_beam_select_workspace_size(...) bytes, 16-byte aligned; it holds
  * nothing from call to call.  Calls that may run at the same time need one each.
